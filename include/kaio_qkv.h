@@ -1,6 +1,7 @@
 /*
- * libkaio_qkv -- GB300 (sm_103a) W4A16 fused QKV projection and dense f16
- * tensor-core matmul behind a plain C ABI.
+ * libkaio_qkv -- GB300 (sm_103a) W4A16 fused QKV projection, dense f16
+ * tensor-core matmul, and the attention that follows the projection (rotary
+ * positions, paged cache, paged attention) behind a plain C ABI.
  *
  * Operations follow two docs.rs source pages of the kaio-candle crate:
  *   "kaio-candle -- src/qkv_project_int4.rs" (qkv_project_int4 and its doc
@@ -10,7 +11,8 @@
  *
  * Conventions shared by every entry point
  *   - All tensor pointers are DEVICE memory on the current CUDA device, owned
- *     by the caller, dense, row-major, with no offset or stride of their own.
+ *     by the caller, dense, row-major, with no offset or stride of their own
+ *     (the rotary and attention entries take strides).
  *     The library never allocates or frees them and never keeps them.
  *   - Every tensor pointer must be 16-byte aligned (TMA and 128-bit loads).
  *   - Calls are asynchronous on `stream` (0 = legacy default stream). The
@@ -268,6 +270,154 @@ int kaio_dequantize_per_group_backward(int dtype, int q_dtype, int32_t outer, in
  */
 int kaio_dequantize_per_group(int q_dtype, int dtype, int32_t outer, int32_t axis, int32_t group,
                               const void* q, const void* scale, void* out, kaio_stream_t stream);
+
+/*
+ * Rotary positions with several axes (time, height, width), for one tensor or
+ * for q and k together with the write of k and v into a paged cache.
+ *
+ * Pair i (0 <= i < pairs) belongs to one axis a(i): axis 0 has the first
+ * sections[0] pairs, axis 1 the next sections[1], and so on. With
+ * angle = positions[a(i), t] * inv_freq[i]:
+ *   y0 = x0 cos(angle) - x1 sin(angle),  y1 = x1 cos(angle) + x0 sin(angle)
+ * where (x0, x1) are elements (i, i + pairs), or (2i, 2i + 1) if interleaved.
+ * inverse negates the angle: the inverse rotation, which is also the gradient
+ * (dx = inverse rotation of dy). Elements from 2 * pairs on are copied. f32
+ * products and sums, the angle reduced exactly at any int32 position, one
+ * rounding to the tensors' type.
+ *
+ *   q, q_out  [tokens, heads, dim]      out may be q itself (same strides)
+ *   k, v      [tokens, kv_heads, dim]   (append only)
+ *   k_cache, v_cache [num_pages, page_size, kv_heads, dim]  (append only): the
+ *             rotated k and the unchanged v of token t go to slot slots[t] =
+ *             page * page_size + place in the page; a slot outside the cache
+ *             (such as -1) stores nothing. Two tokens of one call must not
+ *             have the same slot.
+ *   positions i32 [axes, tokens];  inv_freq f32 [pairs] (finite);  slots i32 [tokens]
+ *
+ * dtype F16 or BF16 for every tensor of the rotation. Strides are in elements;
+ * the last dimension is dense; strides of q, k, v, caches and output are
+ * multiples of 8 (16 bytes), those of a written tensor at least dim.
+ * Errors (KAIO_ERR_INVALID_VALUE unless noted): struct_size other than
+ * sizeof(kaio_rope_args); another dtype; dim not a multiple of 8 in 8..256;
+ * pairs < 1 or 2 * pairs > dim; axes not 1..4, a negative section, or sections
+ * that do not sum to pairs; a bad stride; sizes of 2^30 or more; a null
+ * pointer; an output overlapping an input (other than out == q) or k_cache
+ * starting where v_cache does; memory of another device; KAIO_ERR_MISALIGNED
+ * (16 bytes; positions, slots and inv_freq: 4). tokens == 0 returns KAIO_OK.
+ */
+typedef struct {
+  uint32_t struct_size; /* sizeof(kaio_rope_args) */
+  int32_t dtype;        /* KAIO_DTYPE_F16 or KAIO_DTYPE_BF16 */
+  int32_t tokens, heads, kv_heads, dim;
+  int32_t pairs, axes;
+  int32_t sections[4];
+  int32_t interleaved, inverse;
+  int32_t num_pages, page_size;
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  void* k_cache;
+  void* v_cache;
+  const int32_t* positions;
+  const float* inv_freq;
+  const int32_t* slots;
+  int64_t q_token_stride, q_head_stride;
+  int64_t q_out_token_stride, q_out_head_stride;
+  int64_t k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride;
+  int64_t k_page_stride, k_slot_stride, k_cache_head_stride;
+  int64_t v_page_stride, v_slot_stride, v_cache_head_stride;
+  int64_t positions_axis_stride;
+} kaio_rope_args;
+
+/* Rotates q into q_out; the fields of k, v, the caches and slots are not used. */
+int kaio_rope(const kaio_rope_args* args, kaio_stream_t stream);
+
+/* Rotates q into q_out and k into the cache, and writes v into the cache, in
+ * one launch. inverse must be 0. */
+int kaio_rope_append(const kaio_rope_args* args, kaio_stream_t stream);
+
+/*
+ * Attention of the new tokens of a batch of sequences over a paged cache that
+ * already holds their keys and values.
+ *
+ * Sequence b has kv_lens[b] positions in the cache; its new tokens
+ * q[q_starts[b] .. q_starts[b+1]) are the last ones of them, token i standing at
+ * position p = kv_lens[b] - n + i. It sees position j if
+ *   j < kv_lens[b]  and  (not causal or j <= p)  and
+ *   (window == 0 or j > p - window or j < sinks).
+ * For each query head (query head h reads K/V head h / (heads / kv_heads)):
+ *   s_j = scale * sum_d q[d] k_j[d];  out = sum_j exp(s_j) v_j / sum_j exp(s_j)
+ *   lse = ln sum_j exp(s_j)
+ * over the visible positions, f32 scores, statistics and sums, out rounded once
+ * to the tensors' type. A token that sees nothing gets zeros and lse = -inf.
+ *
+ *   q, out    [tokens, heads, dim]                          F16 or BF16
+ *   k_cache, v_cache [num_pages, page_size, kv_heads, dim]  the same type
+ *   page_table i32 [batch, max_pages]: position j of sequence b lies in page
+ *             page_table[b, j / page_size] at j % page_size. Entries of pages
+ *             that no new token sees are not used (they may be anything); an
+ *             entry outside the cache reads as zeros.
+ *   kv_lens   i32 [batch]        (more than max_pages * page_size: cut to it)
+ *   q_starts  i32 [batch + 1]    from 0 to tokens, not decreasing; null: one
+ *             token for each sequence (tokens == batch)
+ *   lse       f32 [tokens, heads], dense; null: not wanted
+ *   max_new   at least the largest number of new tokens of one sequence; it
+ *             chooses the kernel, results do not depend on it
+ *   workspace kaio_paged_attention_workspace() bytes of device memory,
+ *             16-byte aligned, zeroed once before its first use. Every call
+ *             leaves it ready for the next. Calls that share a workspace have
+ *             to be ordered (one stream, or events); concurrent calls need one
+ *             each.
+ *
+ * Cache positions that no new token sees are never used, whatever they hold. A
+ * NaN or infinity in v at a position that some but not all of the new tokens of
+ * one sequence see can also reach those that do not.
+ * Lengths and table stay on the device: the call does not synchronise, and work
+ * is divided by the actual lengths.
+ *
+ * Strides are in elements, multiples of 8; the last dimension is dense.
+ * Errors (KAIO_ERR_INVALID_VALUE unless noted): struct_size; another dtype; dim
+ * not a multiple of 8 in 8..128; heads not a multiple of kv_heads; page_size
+ * not a power of two in 16..1024; q_starts null with tokens != batch; negative
+ * sizes, window or sinks; scale not finite; a bad stride; sizes of 2^30 or more
+ * (tokens * heads too); a null pointer; out or lse overlapping an input or each
+ * other; workspace_bytes too small; memory of another device;
+ * KAIO_ERR_MISALIGNED (16 bytes; tables and lse: 4). tokens == 0 or batch == 0
+ * returns KAIO_OK without a launch.
+ */
+typedef struct {
+  uint32_t struct_size; /* sizeof(kaio_paged_attention_args) */
+  int32_t dtype;        /* KAIO_DTYPE_F16 or KAIO_DTYPE_BF16 */
+  int32_t batch, tokens, heads, kv_heads, dim;
+  int32_t page_size, num_pages, max_pages;
+  int32_t max_new;
+  int32_t causal, window, sinks;
+  float scale;
+  int32_t reserved; /* 0 */
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* page_table;
+  const int32_t* kv_lens;
+  const int32_t* q_starts;
+  void* out;
+  float* lse;
+  void* workspace;
+  uint64_t workspace_bytes;
+  int64_t q_token_stride, q_head_stride;
+  int64_t out_token_stride, out_head_stride;
+  int64_t k_page_stride, k_slot_stride, k_head_stride;
+  int64_t v_page_stride, v_slot_stride, v_head_stride;
+  int64_t table_stride;
+} kaio_paged_attention_args;
+
+int kaio_paged_attention(const kaio_paged_attention_args* args, kaio_stream_t stream);
+
+/* Bytes of workspace that kaio_paged_attention needs on the current device, for
+ * any sizes. Returns KAIO_OK and writes *bytes, or an error status. */
+int kaio_paged_attention_workspace(uint64_t* bytes);
 
 /*
  * Dequantise packed INT4 weights to f16, exactly as the projection kernels do

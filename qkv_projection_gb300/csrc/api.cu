@@ -17,6 +17,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <string>
@@ -615,6 +616,284 @@ int kaio_dequantize_per_group(int q_dtype, int dtype, int32_t outer, int32_t axi
   g_last_error.clear();
   return dequant_group_impl(false, dtype, q_dtype, outer, axis, group, q, scale, out,
                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+constexpr int64_t kMaxSize = 1 << 30;
+
+// Bytes from a strided 16-bit tensor's first element to past its last one.
+size_t extent16(std::initializer_list<std::pair<int64_t, int64_t>> size_stride, int64_t inner) {
+  int64_t last = inner;
+  for (const auto& d : size_stride) last += (d.first - 1) * d.second;
+  return static_cast<size_t>(last) * 2;
+}
+
+// Strides of a 16-bit tensor whose rows are `dim` dense elements: multiples of
+// 16 bytes, not negative; a written tensor's rows must not share elements.
+int check_strides(const char* name, std::initializer_list<std::pair<int64_t, int64_t>> size_stride, int64_t dim,
+                  bool written) {
+  for (const auto& d : size_stride) {
+    if (d.first <= 1) continue;
+    if (d.second < 0 || d.second % 8 != 0 || d.second > (1ll << 38))
+      return fail(KAIO_ERR_INVALID_VALUE, "%s: stride %lld must be a non-negative multiple of 8 elements", name,
+                  static_cast<long long>(d.second));
+    if (written && d.second < dim)
+      return fail(KAIO_ERR_INVALID_VALUE, "%s: stride %lld of a written tensor is below dim (%lld)", name,
+                  static_cast<long long>(d.second), static_cast<long long>(dim));
+  }
+  return KAIO_OK;
+}
+
+int check_sizes(std::initializer_list<std::pair<const char*, int64_t>> sizes) {
+  for (const auto& v : sizes)
+    if (v.second < 0 || v.second >= kMaxSize)
+      return fail(KAIO_ERR_INVALID_VALUE, "%s (%lld) must be in 0..2^30 - 1", v.first,
+                  static_cast<long long>(v.second));
+  return KAIO_OK;
+}
+
+int check_aligned4(const Span* s, int n) {
+  for (int i = 0; i < n; ++i)
+    if (reinterpret_cast<uintptr_t>(s[i].p) % 4 != 0)
+      return fail(KAIO_ERR_MISALIGNED, "%s (%p) is not 4-byte aligned", s[i].name, s[i].p);
+  return KAIO_OK;
+}
+
+int float16_type(int dtype, kaio::FloatType* t) {
+  size_t es;
+  if (!float_type(dtype, t, &es) || es != 2)
+    return fail(KAIO_ERR_INVALID_VALUE, "dtype %d must be F16 or BF16", dtype);
+  return KAIO_OK;
+}
+
+size_t paged_workspace_bytes(const DeviceInfo& info) {
+  return kaio::paged_decode_workspace_bytes(info.sms);
+}
+
+int rope_impl(const kaio_rope_args* a, bool append, cudaStream_t stream) {
+  if (a == nullptr) return fail(KAIO_ERR_INVALID_VALUE, "args is a null pointer");
+  if (a->struct_size != sizeof(*a))
+    return fail(KAIO_ERR_INVALID_VALUE, "struct_size %u is not sizeof(kaio_rope_args) (%zu)", a->struct_size,
+                sizeof(*a));
+  kaio::FloatType t = kaio::FloatType::F16;
+  KAIO_TRY(float16_type(a->dtype, &t));
+  const int64_t T = a->tokens, H = a->heads, KH = append ? a->kv_heads : 0, D = a->dim;
+  const int64_t P = append ? a->num_pages : 0, ps = append ? a->page_size : 1;
+  KAIO_TRY(check_sizes({{"tokens", T}, {"heads", H}, {"kv_heads", KH}, {"num_pages", P}, {"page_size", ps},
+                        {"tokens * heads", T * std::max<int64_t>(1, H + KH)}}));
+  if (D < 8 || D > 256 || D % 8 != 0)
+    return fail(KAIO_ERR_INVALID_VALUE, "dim (%d) must be a multiple of 8 in 8..256", a->dim);
+  if (a->pairs < 1 || 2ll * a->pairs > D)
+    return fail(KAIO_ERR_INVALID_VALUE, "pairs (%d) must be in 1..dim / 2 (%d)", a->pairs, a->dim / 2);
+  if (a->axes < 1 || a->axes > 4) return fail(KAIO_ERR_INVALID_VALUE, "axes (%d) must be in 1..4", a->axes);
+  int64_t sum = 0;
+  for (int i = 0; i < a->axes; ++i) {
+    if (a->sections[i] < 0) return fail(KAIO_ERR_INVALID_VALUE, "sections[%d] (%d) is negative", i, a->sections[i]);
+    sum += a->sections[i];
+  }
+  if (sum != a->pairs)
+    return fail(KAIO_ERR_INVALID_VALUE, "sections sum to %lld, not to pairs (%d)", static_cast<long long>(sum),
+                a->pairs);
+  if (append) {
+    if (a->inverse) return fail(KAIO_ERR_INVALID_VALUE, "inverse must be 0: the cache holds rotated keys");
+    if (KH < 1 || ps < 1) return fail(KAIO_ERR_INVALID_VALUE, "kv_heads and page_size must be positive");
+  }
+  if (H < 1) return fail(KAIO_ERR_INVALID_VALUE, "heads (%d) must be positive", a->heads);
+  KAIO_TRY(check_strides("q", {{T, a->q_token_stride}, {H, a->q_head_stride}}, D, false));
+  KAIO_TRY(check_strides("q_out", {{T, a->q_out_token_stride}, {H, a->q_out_head_stride}}, D, true));
+  if (append) {
+    KAIO_TRY(check_strides("k", {{T, a->k_token_stride}, {KH, a->k_head_stride}}, D, false));
+    KAIO_TRY(check_strides("v", {{T, a->v_token_stride}, {KH, a->v_head_stride}}, D, false));
+    KAIO_TRY(check_strides("k_cache", {{P, a->k_page_stride}, {ps, a->k_slot_stride}, {KH, a->k_cache_head_stride}},
+                           D, true));
+    KAIO_TRY(check_strides("v_cache", {{P, a->v_page_stride}, {ps, a->v_slot_stride}, {KH, a->v_cache_head_stride}},
+                           D, true));
+  }
+  int dev;
+  DeviceInfo info;
+  if (T == 0) return current_device(&dev, &info);
+
+  const int64_t axis_span = (a->axes - 1) * a->positions_axis_stride + T;
+  if (a->axes > 1 && (a->positions_axis_stride < 0 || a->positions_axis_stride >= (1ll << 40)))
+    return fail(KAIO_ERR_INVALID_VALUE, "positions_axis_stride (%lld) is out of range",
+                static_cast<long long>(a->positions_axis_stride));
+  const Span q = {"q", a->q, extent16({{T, a->q_token_stride}, {H, a->q_head_stride}}, D)};
+  const Span qo = {"q_out", a->q_out, extent16({{T, a->q_out_token_stride}, {H, a->q_out_head_stride}}, D)};
+  Span in[6] = {{"positions", a->positions, static_cast<size_t>(axis_span) * 4},
+                {"inv_freq", a->inv_freq, static_cast<size_t>(a->pairs) * 4}};
+  Span out[3] = {qo};
+  int n_in = 2, n_out = 1;
+  if (append) {
+    in[n_in++] = {"slots", a->slots, static_cast<size_t>(T) * 4};
+    in[n_in++] = {"k", a->k, extent16({{T, a->k_token_stride}, {KH, a->k_head_stride}}, D)};
+    in[n_in++] = {"v", a->v, extent16({{T, a->v_token_stride}, {KH, a->v_head_stride}}, D)};
+    if (P) {      // the pointers of an empty cache may be null
+      out[n_out++] = {"k_cache", a->k_cache,
+                      extent16({{P, a->k_page_stride}, {ps, a->k_slot_stride}, {KH, a->k_cache_head_stride}}, D)};
+      out[n_out++] = {"v_cache", a->v_cache,
+                      extent16({{P, a->v_page_stride}, {ps, a->v_slot_stride}, {KH, a->v_cache_head_stride}}, D)};
+    }
+  }
+  const int n_small = append ? 3 : 2;
+  KAIO_TRY(check_not_null(&q, 1));
+  KAIO_TRY(check_not_null(in, n_in));
+  KAIO_TRY(check_not_null(out, n_out));
+  KAIO_TRY(check_aligned(&q, 1));
+  KAIO_TRY(check_aligned4(in, n_small));
+  KAIO_TRY(check_aligned(in + n_small, n_in - n_small));
+  KAIO_TRY(check_aligned(out, n_out));
+  // q_out may be q, exactly. The caches may be interleaved parts of one buffer
+  // (their extents then overlap), but not the same one.
+  const bool in_place = a->q == a->q_out && (T == 1 || a->q_token_stride == a->q_out_token_stride) &&
+                        (H == 1 || a->q_head_stride == a->q_out_head_stride);
+  if (!in_place) KAIO_TRY(check_overlap(&q, 1, out, 1));
+  KAIO_TRY(check_overlap(in, in_place ? n_small : n_in, out, 1));
+  for (int i = 1; i < n_out; ++i) {
+    KAIO_TRY(check_overlap(&q, 1, out + i, 1));
+    KAIO_TRY(check_overlap(in, n_in, out + i, 1));
+    if (overlaps(qo, out[i])) return fail(KAIO_ERR_INVALID_VALUE, "outputs q_out and %s overlap", out[i].name);
+  }
+  if (n_out == 3 && a->k_cache == a->v_cache) return fail(KAIO_ERR_INVALID_VALUE, "outputs k_cache and v_cache overlap");
+  KAIO_TRY(current_device(&dev, &info));
+  KAIO_TRY(check_on_device(&q, 1, dev));
+  KAIO_TRY(check_on_device(in, n_in, dev));
+  KAIO_TRY(check_on_device(out, n_out, dev));
+
+  kaio::RopeParams r{};
+  r.q = a->q, r.qo = a->q_out;
+  r.q_ts = a->q_token_stride, r.q_hs = a->q_head_stride;
+  r.qo_ts = a->q_out_token_stride, r.qo_hs = a->q_out_head_stride;
+  r.positions = a->positions, r.pos_stride = a->positions_axis_stride, r.inv_freq = a->inv_freq;
+  r.tokens = a->tokens, r.q_heads = a->heads, r.dim = a->dim, r.pairs = a->pairs, r.axes = a->axes;
+  r.interleaved = a->interleaved != 0, r.inverse = a->inverse != 0;
+  for (int i = 0, end = 0; i < 4; ++i) r.section_end[i] = end += i < a->axes ? a->sections[i] : 0;
+  if (append) {
+    r.k = a->k, r.v = a->v, r.kc = a->k_cache, r.vc = a->v_cache, r.slots = a->slots;
+    r.k_ts = a->k_token_stride, r.k_hs = a->k_head_stride;
+    r.v_ts = a->v_token_stride, r.v_hs = a->v_head_stride;
+    r.kc_ps = a->k_page_stride, r.kc_ss = a->k_slot_stride, r.kc_hs = a->k_cache_head_stride;
+    r.vc_ps = a->v_page_stride, r.vc_ss = a->v_slot_stride, r.vc_hs = a->v_cache_head_stride;
+    r.kv_heads = a->kv_heads, r.num_pages = a->num_pages, r.page_size = a->page_size;
+  }
+  const cudaError_t e = kaio::launch_rope(t, r, info.sms, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "rotary kernel launch");
+  return KAIO_OK;
+}
+
+}  // namespace
+
+int kaio_rope(const kaio_rope_args* args, kaio_stream_t stream) {
+  g_last_error.clear();
+  return rope_impl(args, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kaio_rope_append(const kaio_rope_args* args, kaio_stream_t stream) {
+  g_last_error.clear();
+  return rope_impl(args, true, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kaio_paged_attention_workspace(uint64_t* bytes) {
+  g_last_error.clear();
+  if (bytes == nullptr) return fail(KAIO_ERR_INVALID_VALUE, "bytes is a null pointer");
+  int dev;
+  DeviceInfo info;
+  KAIO_TRY(current_device(&dev, &info));
+  *bytes = paged_workspace_bytes(info);
+  return KAIO_OK;
+}
+
+int kaio_paged_attention(const kaio_paged_attention_args* a, kaio_stream_t stream_) {
+  g_last_error.clear();
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (a == nullptr) return fail(KAIO_ERR_INVALID_VALUE, "args is a null pointer");
+  if (a->struct_size != sizeof(*a))
+    return fail(KAIO_ERR_INVALID_VALUE, "struct_size %u is not sizeof(kaio_paged_attention_args) (%zu)",
+                a->struct_size, sizeof(*a));
+  kaio::FloatType t = kaio::FloatType::F16;
+  KAIO_TRY(float16_type(a->dtype, &t));
+  const int64_t T = a->tokens, H = a->heads, KH = a->kv_heads, D = a->dim, P = a->num_pages, ps = a->page_size;
+  const int64_t B = a->batch, W = a->max_pages;
+  KAIO_TRY(check_sizes({{"batch", B}, {"tokens", T}, {"heads", H}, {"kv_heads", KH}, {"num_pages", P},
+                        {"max_pages", W}, {"max_new", a->max_new}, {"tokens * heads", T * H}}));
+  if (D < 8 || D > 128 || D % 8 != 0)
+    return fail(KAIO_ERR_INVALID_VALUE, "dim (%d) must be a multiple of 8 in 8..128", a->dim);
+  if (KH < 1 || H < 1 || H % KH != 0)
+    return fail(KAIO_ERR_INVALID_VALUE, "heads (%d) must be a positive multiple of kv_heads (%d)", a->heads,
+                a->kv_heads);
+  if (ps < 16 || ps > 1024 || (ps & (ps - 1)) != 0)
+    return fail(KAIO_ERR_INVALID_VALUE, "page_size (%d) must be a power of two in 16..1024", a->page_size);
+  if (a->window < 0 || a->sinks < 0)
+    return fail(KAIO_ERR_INVALID_VALUE, "window (%d) and sinks (%d) must not be negative", a->window, a->sinks);
+  if (!(a->scale > -3.0e38f && a->scale < 3.0e38f)) return fail(KAIO_ERR_INVALID_VALUE, "scale must be finite");
+  if (a->q_starts == nullptr && T != B)
+    return fail(KAIO_ERR_INVALID_VALUE, "without q_starts there is one token for each sequence: tokens (%d) != batch (%d)",
+                a->tokens, a->batch);
+  KAIO_TRY(check_strides("q", {{T, a->q_token_stride}, {H, a->q_head_stride}}, D, false));
+  KAIO_TRY(check_strides("out", {{T, a->out_token_stride}, {H, a->out_head_stride}}, D, true));
+  KAIO_TRY(check_strides("k_cache", {{P, a->k_page_stride}, {ps, a->k_slot_stride}, {KH, a->k_head_stride}}, D, false));
+  KAIO_TRY(check_strides("v_cache", {{P, a->v_page_stride}, {ps, a->v_slot_stride}, {KH, a->v_head_stride}}, D, false));
+  if (B > 1 && (a->table_stride < 0 || a->table_stride >= (1ll << 40)))
+    return fail(KAIO_ERR_INVALID_VALUE, "table_stride (%lld) is out of range", static_cast<long long>(a->table_stride));
+  int dev;
+  DeviceInfo info;
+  if (T == 0 || B == 0) return current_device(&dev, &info);
+
+  const size_t table = W ? static_cast<size_t>((B - 1) * a->table_stride + W) * 4 : 0;
+  Span in[6] = {{"q", a->q, extent16({{T, a->q_token_stride}, {H, a->q_head_stride}}, D)},
+                {"kv_lens", a->kv_lens, static_cast<size_t>(B) * 4}};
+  int n_in = 2;
+  const int n_lens = a->q_starts ? 2 : 1;
+  if (a->q_starts) in[n_in++] = {"q_starts", a->q_starts, static_cast<size_t>(B + 1) * 4};
+  const int n_fixed = n_in;
+  // an empty cache or table is never read: its pointers may be null
+  if (P && W) {
+    in[n_in++] = {"page_table", a->page_table, table};
+    in[n_in++] = {"k_cache", a->k_cache,
+                  extent16({{P, a->k_page_stride}, {ps, a->k_slot_stride}, {KH, a->k_head_stride}}, D)};
+    in[n_in++] = {"v_cache", a->v_cache,
+                  extent16({{P, a->v_page_stride}, {ps, a->v_slot_stride}, {KH, a->v_head_stride}}, D)};
+  }
+  Span out[3] = {{"out", a->out, extent16({{T, a->out_token_stride}, {H, a->out_head_stride}}, D)},
+                 {"workspace", a->workspace, static_cast<size_t>(a->workspace_bytes)}};
+  int n_out = 2;
+  if (a->lse) out[n_out++] = {"lse", a->lse, static_cast<size_t>(T * H) * 4};
+  KAIO_TRY(check_not_null(in, n_in));
+  KAIO_TRY(check_not_null(out, 2));
+  KAIO_TRY(check_aligned(in, 1));
+  KAIO_TRY(check_aligned4(in + 1, n_lens));
+  if (n_in > n_fixed) {
+    KAIO_TRY(check_aligned4(in + n_fixed, 1));
+    KAIO_TRY(check_aligned(in + n_fixed + 1, 2));
+  }
+  KAIO_TRY(check_aligned(out, 2));
+  KAIO_TRY(check_aligned4(out + 2, n_out - 2));
+  KAIO_TRY(check_overlap(in, n_in, out, n_out));
+  KAIO_TRY(current_device(&dev, &info));
+  const size_t need = paged_workspace_bytes(info);
+  if (a->workspace_bytes < need)
+    return fail(KAIO_ERR_INVALID_VALUE, "workspace_bytes (%llu) is below kaio_paged_attention_workspace() (%zu)",
+                static_cast<unsigned long long>(a->workspace_bytes), need);
+  KAIO_TRY(check_on_device(in, n_in, dev));
+  KAIO_TRY(check_on_device(out, n_out, dev));
+
+  kaio::PagedParams p{};
+  p.q = a->q, p.kc = a->k_cache, p.vc = a->v_cache, p.out = a->out, p.lse = a->lse;
+  p.q_ts = a->q_token_stride, p.q_hs = a->q_head_stride;
+  p.o_ts = a->out_token_stride, p.o_hs = a->out_head_stride;
+  p.k_ps = a->k_page_stride, p.k_ss = a->k_slot_stride, p.k_hs = a->k_head_stride;
+  p.v_ps = a->v_page_stride, p.v_ss = a->v_slot_stride, p.v_hs = a->v_head_stride;
+  p.table = a->page_table, p.table_stride = a->table_stride, p.kv_lens = a->kv_lens, p.q_starts = a->q_starts;
+  p.batch = a->batch, p.tokens = a->tokens, p.heads = a->heads, p.kv_heads = a->kv_heads;
+  p.group = a->heads / a->kv_heads, p.dim = a->dim;
+  while ((1 << p.page_shift) < a->page_size) ++p.page_shift;
+  p.num_pages = a->num_pages, p.max_pages = P ? a->max_pages : 0;
+  p.causal = a->causal != 0;
+  p.window = std::min(a->window, kaio::kPagedMaxLen), p.sinks = std::min(a->sinks, kaio::kPagedMaxLen);
+  p.scale_log2 = a->scale * 1.4426950408889634f;
+  const cudaError_t e = kaio::launch_paged_decode(t, p, a->workspace, info.sms, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "paged attention kernel launch");
+  return KAIO_OK;
 }
 
 int kaio_dequant_int4_debug(const uint32_t* w, const void* s, void* out, uint32_t K, uint32_t N,

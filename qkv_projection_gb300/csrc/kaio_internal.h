@@ -85,6 +85,51 @@ cudaError_t launch_dequant_group_forward(FloatType t, bool q_unsigned, const voi
                                          void* out, int outer, int axis, int group, int num_sms,
                                          cudaStream_t stream);
 
+// ----------------------------------------------- rotary positions, cache write
+// Strides are in elements. kv_heads == 0: q alone (no cache).
+struct RopeParams {
+  const void *q, *k, *v;
+  void *qo, *kc, *vc;
+  long long q_ts, q_hs, qo_ts, qo_hs, k_ts, k_hs, v_ts, v_hs;   // token and head strides
+  long long kc_ps, kc_ss, kc_hs, vc_ps, vc_ss, vc_hs;           // page, slot and head strides
+  const int* slots;           // [tokens] page * page_size + slot; outside the cache: not stored
+  const int* positions;       // [axes][tokens], axis stride pos_stride
+  long long pos_stride;
+  const float* inv_freq;      // [pairs]
+  int tokens, q_heads, kv_heads, dim, pairs, axes;
+  int section_end[4];         // first pair past each axis's section
+  int num_pages, page_size;
+  bool interleaved, inverse;
+};
+cudaError_t launch_rope(FloatType t, const RopeParams& r, int num_sms, cudaStream_t stream);
+
+// ------------------------------------------------------------- paged attention
+// Strides are in elements.
+struct PagedParams {
+  const void *q, *kc, *vc;
+  void* out;
+  float* lse;                 // [tokens][heads], natural logarithm; may be null
+  long long q_ts, q_hs, o_ts, o_hs;
+  long long k_ps, k_ss, k_hs, v_ps, v_ss, v_hs, table_stride;
+  const int *table, *kv_lens, *q_starts;   // q_starts may be null: one token per sequence
+  int batch, tokens, heads, kv_heads, group, dim;
+  int page_shift, num_pages, max_pages;
+  bool causal;
+  int window, sinks;          // window 0: none; both at most kPagedMaxLen
+  float scale_log2;           // softmax scale * log2(e)
+  float* part_o;              // [2 * ctas][rows][dim] partial outputs of split work
+  float* part_l;              // [2 * ctas][rows] their log2-sum-exp2
+  unsigned* counters;         // [ctas], zero between launches
+};
+constexpr int kPagedMaxLen = 1 << 30;
+// Rows (tokens x query heads of one K/V head) that one CTA of the warp-MMA
+// kernel takes at a time.
+constexpr int kPagedDecodeRows = 16;
+// Workspace layout: counters first, then the partial sums.
+constexpr size_t kPagedCounterBytes = 4096;
+size_t paged_decode_workspace_bytes(int num_sms);
+cudaError_t launch_paged_decode(FloatType t, PagedParams p, void* workspace, int num_sms, cudaStream_t stream);
+
 // ------------------------------------------------- tensor-core (tcgen05) paths
 struct GemmShape {
   int M, N, K;              // C[M, N] = sum_k Aop[M, k] * Bop[k, N]

@@ -1,0 +1,189 @@
+// How the attention kernels over a paged cache divide their work.
+//
+// The new tokens of a sequence and the query heads that share a K/V head form
+// the rows of one matrix product against that head's keys: row r is token
+// r / group, query head r % group of the group. An item is one K/V head of one
+// sequence with one tile of kRows rows; its work is counted in units of kKeys
+// keys, over the keys that at least one of its rows can see: a prefix (the sink
+// tokens) and a run that ends at its last token.
+//
+// All units of all items stand in one line (sequence, K/V head, row tile, key
+// tile), and CTA c takes the c-th equal share of it. So a batch of unlike
+// lengths, one long sequence and many short ones all load the GPU evenly, and
+// the lengths are read where they are, on the device. An item that a boundary
+// cuts is finished from partial results: each CTA writes its output (normalised,
+// f32) and log-sum-exp to the workspace, and the CTA that arrives last joins
+// them, always in the order of the keys, so results do not depend on timing.
+#pragma once
+
+#include "kaio_device.cuh"
+#include "kaio_internal.h"
+
+namespace kaio {
+
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLn2 = 0.69314718055994531f;
+
+struct PagedSeq {
+  int q0, n, kv;     // first token, new tokens, positions in the cache
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
+  PagedSeq s;
+  if (p.q_starts) {
+    s.q0 = min(max(p.q_starts[b], 0), p.tokens);
+    s.n = min(max(p.q_starts[b + 1], s.q0), p.tokens) - s.q0;
+  } else {
+    s.q0 = b;
+    s.n = 1;
+  }
+  const long long room = static_cast<long long>(p.max_pages) << p.page_shift;
+  s.kv = static_cast<int>(min(static_cast<long long>(max(p.kv_lens[b], 0)),
+                              min(room, static_cast<long long>(kPagedMaxLen))));
+  return s;
+}
+
+// Keys that the rows [r0, r1) of a sequence see: [0, first) and [lo, hi), and
+// the key tiles that hold them.
+template <int kKeys>
+struct PagedSpan {
+  int lo, hi, first;
+  int sink_tiles, lo_tile, units;   // units: at least 1, so that every item is visited
+  __device__ __forceinline__ PagedSpan(const PagedParams& p, const PagedSeq& s, int r0, int r1) {
+    const int t0 = r0 / p.group, t1 = (r1 - 1) / p.group;
+    hi = p.causal ? min(max(s.kv - s.n + t1 + 1, 0), s.kv) : s.kv;
+    lo = p.window > 0 ? min(max(s.kv - s.n + t0 - p.window + 1, 0), hi) : 0;
+    first = min(p.sinks, lo);
+    lo_tile = lo / kKeys;
+    sink_tiles = min((first + kKeys - 1) / kKeys, lo_tile);
+    units = max(1, sink_tiles + (hi + kKeys - 1) / kKeys - lo_tile);
+  }
+  __device__ __forceinline__ int key0(int unit) const {
+    return (unit < sink_tiles ? unit : unit - sink_tiles + lo_tile) * kKeys;
+  }
+};
+
+// Keys that one row sees: j < hi and (j >= lo or j < sinks).
+struct PagedRow {
+  int lo, hi;
+  __device__ __forceinline__ PagedRow(const PagedParams& p, const PagedSeq& s, int r) {
+    const int pos = s.kv - s.n + r / p.group;
+    hi = p.causal ? min(max(pos + 1, 0), s.kv) : s.kv;
+    lo = p.window > 0 ? min(max(pos - p.window + 1, 0), hi) : 0;
+  }
+};
+
+// A position in the line of units, and the item that it lies in.
+template <int kRows, int kKeys>
+struct PagedWalk {
+  int b, h, tile, tiles;      // item: sequence, K/V head, row tile of `tiles`
+  int unit, units;            // unit within the item
+  long long at;               // index in the whole line
+  PagedSeq s;
+
+  __device__ __forceinline__ static int row_tiles(const PagedParams& p, const PagedSeq& s) {
+    return static_cast<int>((static_cast<long long>(s.n) * p.group + kRows - 1) / kRows);
+  }
+  __device__ __forceinline__ int row0() const { return tile * kRows; }
+  __device__ __forceinline__ int row1(const PagedParams& p) const { return min(tile * kRows + kRows, s.n * p.group); }
+  __device__ __forceinline__ static int item_units(const PagedParams& p, const PagedSeq& s, int tile) {
+    return PagedSpan<kKeys>(p, s, tile * kRows, min(tile * kRows + kRows, s.n * p.group)).units;
+  }
+  __device__ __forceinline__ static long long head_units(const PagedParams& p, const PagedSeq& s) {
+    long long u = 0;
+    const int tiles = row_tiles(p, s);
+    for (int i = 0; i < tiles; ++i) u += item_units(p, s, i);
+    return u;
+  }
+  // To the first unit of the next item (past the line's end: b == batch).
+  __device__ __forceinline__ void next_item(const PagedParams& p) {
+    at += units - unit;
+    unit = 0;
+    if (++tile == tiles) {
+      tile = 0;
+      if (++h == p.kv_heads) {
+        h = 0;
+        do {
+          if (++b >= p.batch) return;
+          s = paged_seq(p, b);
+          tiles = row_tiles(p, s);
+        } while (tiles == 0);
+      }
+    }
+    units = item_units(p, s, tile);
+  }
+};
+
+// One CTA's share [begin, end) of a line of `total` units among `ctas` CTAs.
+struct PagedShare {
+  long long begin, end, total;
+  int ctas;
+  __device__ __forceinline__ int owner(long long u) const {
+    return static_cast<int>(((u + 1) * ctas + total - 1) / total) - 1;
+  }
+};
+
+// Found by all threads of the CTA together: the share of CTA `cta`, and the
+// place of its first unit. Every thread sums a run of sequences; a scan gives
+// the total and the run in which the share begins. `sums` holds kThreads values
+// in shared memory. Returns false if the share is empty.
+template <int kRows, int kKeys, int kThreads>
+__device__ bool paged_share(const PagedParams& p, int cta, int grid, int min_units, long long* sums,
+                            PagedWalk<kRows, kKeys>* place, PagedShare* share) {
+  using Walk = PagedWalk<kRows, kKeys>;
+  const int tid = threadIdx.x;
+  const int per = (p.batch + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += p.kv_heads * Walk::head_units(p, paged_seq(p, b));
+  sums[tid] = mine;
+  __syncthreads();
+  for (int d = 1; d < kThreads; d <<= 1) {
+    const long long add = tid >= d ? sums[tid - d] : 0;
+    __syncthreads();
+    sums[tid] += add;
+    __syncthreads();
+  }
+  const long long total = sums[kThreads - 1];
+  if (total == 0) return false;
+  share->total = total;
+  share->ctas = static_cast<int>(max(1ll, min(static_cast<long long>(grid), total / min_units)));
+  if (cta >= share->ctas) return false;
+  share->begin = cta * total / share->ctas;
+  share->end = (cta + 1) * total / share->ctas;
+  const long long upto = sums[tid], from = upto - mine;
+  if (share->begin >= from && share->begin < upto) {
+    long long left = share->begin - from;
+    Walk w;
+    w.b = b0;
+    for (;; ++w.b) {
+      w.s = paged_seq(p, w.b);
+      const long long head = Walk::head_units(p, w.s);
+      if (left < head * p.kv_heads) {
+        w.tiles = Walk::row_tiles(p, w.s);
+        w.h = static_cast<int>(left / head);
+        left -= w.h * head;
+        break;
+      }
+      left -= head * p.kv_heads;
+    }
+    for (w.tile = 0;; ++w.tile) {
+      w.units = Walk::item_units(p, w.s, w.tile);
+      if (left < w.units) break;
+      left -= w.units;
+    }
+    w.unit = static_cast<int>(left);
+    w.at = share->begin;
+    *place = w;
+  }
+  __syncthreads();
+  return true;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+}  // namespace kaio

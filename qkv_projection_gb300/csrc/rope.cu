@@ -1,0 +1,281 @@
+// Rotary positions with several axes, and the same fused with the write of K
+// and V into a paged cache.
+//
+// Pair i of R pairs belongs to one position axis a(i) (sections of consecutive
+// pairs) and turns by angle = pos[a(i), t] * inv_freq[i]:
+//   y0 = x0 cos - x1 sin,   y1 = x1 cos + x0 sin     (sin negated: the inverse,
+// which is also the gradient, the rotation being orthogonal). Elements past 2R
+// are copied. Products and sums in f32, one rounding to the tensors' type.
+//
+// The angle is reduced exactly in fixed point: inv_freq / 2 pi is held as a
+// fraction of a turn in 64 bits, its product with the integer position wraps
+// modulo one turn by itself, and the top 32 bits of the product are the angle
+// in turns. The error is about 2^-24 turns at every position (an f32 product of
+// position and frequency is off by 0.004 radians at position 100000).
+//
+// What bounds it: bytes. Every value is read once and written once; the sines
+// are computed once per token and pair and shared by all heads through shared
+// memory. A thread moves 32 bytes (both halves of eight pairs) at a time.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "kaio_internal.h"
+
+namespace kaio {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeMaxPairs = 128;
+constexpr int kRopeMaxTokens = 4;    // tokens of one CTA
+constexpr int kRopeBatch = 2;        // units whose loads one thread has in flight
+
+// n / d for 0 <= n < 2^31 by one multiplication (round-up reciprocal).
+struct FastDiv {
+  uint32_t mul, shift, d;
+  __host__ explicit FastDiv(uint32_t div) : d(div) {
+    shift = 0;
+    while ((1ull << shift) < div) ++shift;
+    mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - div)) / div + 1);
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
+struct RopeKernelParams {
+  RopeParams r;
+  FastDiv unit_div, rot_div, copy_div;   // units per token, per rotated head, per copied head
+  int tokens_per_cta;
+};
+
+template <typename T> struct Pack;
+template <> struct Pack<__half> {
+  static __device__ __forceinline__ float2 get(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
+  static __device__ __forceinline__ uint32_t put(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+template <> struct Pack<__nv_bfloat16> {
+  static __device__ __forceinline__ float2 get(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ uint32_t put(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void from_f(float v, __half* o) { *o = __float2half_rn(v); }
+__device__ __forceinline__ void from_f(float v, __nv_bfloat16* o) { *o = __float2bfloat16_rn(v); }
+
+// Two vectors of eight values, rotated: `half` pairs a[e] with b[e]; otherwise
+// neighbours within each vector are pairs (a's first).
+template <typename T>
+__device__ __forceinline__ void rotate_half(uint4& a, uint4& b, const float2* cs) {
+  uint32_t* pa = &a.x;
+  uint32_t* pb = &b.x;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float2 x = Pack<T>::get(pa[w]), y = Pack<T>::get(pb[w]);
+    const float2 c0 = cs[2 * w], c1 = cs[2 * w + 1];
+    pa[w] = Pack<T>::put(x.x * c0.x - y.x * c0.y, x.y * c1.x - y.y * c1.y);
+    pb[w] = Pack<T>::put(y.x * c0.x + x.x * c0.y, y.y * c1.x + x.y * c1.y);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void rotate_adjacent(uint4& a, const float2* cs) {
+  uint32_t* pa = &a.x;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float2 x = Pack<T>::get(pa[w]);
+    const float2 c = cs[w];
+    pa[w] = Pack<T>::put(x.x * c.x - x.y * c.y, x.y * c.x + x.x * c.y);
+  }
+}
+
+// What one unit of work touches: up to two 16-byte vectors (or, in the scalar
+// form, up to two elements) of one head of one token.
+struct Unit {
+  const char* src;
+  char* dst;            // null: nothing to do (past the end, or a token without a slot)
+  int a, b;             // element offsets; b < 0: only a
+  int pair;             // first pair of vector a (half) or of vectors a and b (adjacent); -1: copy
+};
+
+// kVec: pairs are whole 16-byte vectors (R % 8 == 0, or R % 4 == 0 with adjacent
+// pairs). Otherwise pairs are moved element by element: correct for any R, at
+// about a third of the vector form's bandwidth.
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeKernelParams kp) {
+  const RopeParams& p = kp.r;
+  __shared__ float2 cs[kRopeMaxTokens * kRopeMaxPairs];
+  __shared__ long long kbase[kRopeMaxTokens], vbase[kRopeMaxTokens];   // < 0: not stored
+  const int t0 = static_cast<int>(blockIdx.x) * kp.tokens_per_cta;
+  const int nt = min(kp.tokens_per_cta, p.tokens - t0);
+  const int R = p.pairs;
+
+  for (int i = threadIdx.x; i < nt * R; i += kRopeThreads) {
+    const int t = i / R, pair = i - t * R;
+    int axis = 0;
+    while (axis + 1 < p.axes && pair >= p.section_end[axis]) ++axis;
+    // turns per position, modulo one turn, in units of 2^-64
+    double turns = static_cast<double>(p.inv_freq[pair]) * 0.15915494309189533577;
+    turns -= floor(turns);
+    const unsigned long long frac = static_cast<unsigned long long>(turns * 18446744073709551616.0);
+    const long long pos = p.positions[axis * p.pos_stride + t0 + t];
+    const unsigned long long angle = frac * static_cast<unsigned long long>(pos);
+    const float half_turns = static_cast<float>(static_cast<int32_t>(angle >> 32)) * 0x1p-31f;
+    float s, c;
+    sincospif(half_turns, &s, &c);
+    cs[i] = make_float2(c, p.inverse ? -s : s);
+  }
+  if (p.kv_heads > 0 && threadIdx.x < nt) {
+    const long long slot = p.slots[t0 + threadIdx.x];
+    const bool stored = slot >= 0 && slot < static_cast<long long>(p.num_pages) * p.page_size;
+    const long long page = stored ? slot / p.page_size : 0, at = stored ? slot % p.page_size : 0;
+    kbase[threadIdx.x] = stored ? page * p.kc_ps + at * p.kc_ss : -1;
+    vbase[threadIdx.x] = stored ? page * p.vc_ps + at * p.vc_ss : -1;
+  }
+  __syncthreads();
+
+  const uint32_t per_token = kp.unit_div.d, rot = kp.rot_div.d, copy = kp.copy_div.d;
+  const uint32_t total = static_cast<uint32_t>(nt) * per_token;
+  const uint32_t rot_units = static_cast<uint32_t>(p.q_heads + p.kv_heads) * rot;
+
+  auto unit = [&](uint32_t i) {
+    Unit u;
+    u.dst = nullptr;
+    u.src = nullptr;
+    u.a = 0;
+    u.b = -1;
+    u.pair = -1;
+    if (i >= total) return u;
+    const uint32_t t = kp.unit_div.div(i);
+    uint32_t j = i - t * per_token;
+    const long long tok = t0 + t;
+    if (j < rot_units) {
+      const uint32_t h = kp.rot_div.div(j);
+      j -= h * rot;
+      if (h < static_cast<uint32_t>(p.q_heads)) {
+        u.src = reinterpret_cast<const char*>(static_cast<const T*>(p.q) + tok * p.q_ts + h * p.q_hs);
+        u.dst = reinterpret_cast<char*>(static_cast<T*>(p.qo) + tok * p.qo_ts + h * p.qo_hs);
+      } else {
+        const long long kh = h - p.q_heads;
+        if (kbase[t] < 0) return u;
+        u.src = reinterpret_cast<const char*>(static_cast<const T*>(p.k) + tok * p.k_ts + kh * p.k_hs);
+        u.dst = reinterpret_cast<char*>(static_cast<T*>(p.kc) + kbase[t] + kh * p.kc_hs);
+      }
+      const int jj = static_cast<int>(j);
+      if constexpr (kVec) {
+        if (!p.interleaved) {
+          const int nr = R / 8;
+          if (jj < nr) {
+            u.a = 8 * jj;
+            u.b = R + 8 * jj;
+            u.pair = static_cast<int>(t) * R + 8 * jj;
+          } else {
+            u.a = 2 * R + 16 * (jj - nr);
+            u.b = u.a + 8 < p.dim ? u.a + 8 : -1;
+          }
+        } else {
+          u.a = 16 * jj;
+          u.b = u.a + 8 < p.dim ? u.a + 8 : -1;
+          u.pair = u.a < 2 * R ? static_cast<int>(t) * R + 8 * jj : -1;
+        }
+      } else {
+        if (jj < R) {
+          u.a = p.interleaved ? 2 * jj : jj;
+          u.b = p.interleaved ? 2 * jj + 1 : jj + R;
+          u.pair = static_cast<int>(t) * R + jj;
+        } else {
+          u.a = 2 * R + (jj - R);
+        }
+      }
+    } else {
+      j -= rot_units;
+      const uint32_t h = kp.copy_div.div(j);
+      j -= h * copy;
+      if (vbase[t] < 0) return u;
+      u.src = reinterpret_cast<const char*>(static_cast<const T*>(p.v) + tok * p.v_ts + h * p.v_hs);
+      u.dst = reinterpret_cast<char*>(static_cast<T*>(p.vc) + vbase[t] + h * p.vc_hs);
+      u.a = 16 * static_cast<int>(j);
+      u.b = u.a + 8 < p.dim ? u.a + 8 : -1;
+      u.pair = -2;          // whole vectors in both forms
+    }
+    return u;
+  };
+
+  for (uint32_t i0 = threadIdx.x; i0 < total; i0 += kRopeThreads * kRopeBatch) {
+    if constexpr (kVec) {
+      Unit u[kRopeBatch];
+      uint4 a[kRopeBatch], b[kRopeBatch];
+#pragma unroll
+      for (int n = 0; n < kRopeBatch; ++n) {
+        u[n] = unit(i0 + n * kRopeThreads);
+        if (u[n].dst) {
+          a[n] = *reinterpret_cast<const uint4*>(u[n].src + 2 * u[n].a);
+          if (u[n].b >= 0) b[n] = *reinterpret_cast<const uint4*>(u[n].src + 2 * u[n].b);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < kRopeBatch; ++n) {
+        if (!u[n].dst) continue;
+        if (u[n].pair >= 0) {
+          if (!p.interleaved) {
+            rotate_half<T>(a[n], b[n], cs + u[n].pair);
+          } else {
+            rotate_adjacent<T>(a[n], cs + u[n].pair);
+            if (u[n].b >= 0 && u[n].b < 2 * R) rotate_adjacent<T>(b[n], cs + u[n].pair + 4);
+          }
+        }
+        *reinterpret_cast<uint4*>(u[n].dst + 2 * u[n].a) = a[n];
+        if (u[n].b >= 0) *reinterpret_cast<uint4*>(u[n].dst + 2 * u[n].b) = b[n];
+      }
+    } else {
+      for (int n = 0; n < kRopeBatch; ++n) {
+        const Unit u = unit(i0 + n * kRopeThreads);
+        if (!u.dst) continue;
+        if (u.pair == -2) {
+          *reinterpret_cast<uint4*>(u.dst + 2 * u.a) = *reinterpret_cast<const uint4*>(u.src + 2 * u.a);
+          if (u.b >= 0) *reinterpret_cast<uint4*>(u.dst + 2 * u.b) = *reinterpret_cast<const uint4*>(u.src + 2 * u.b);
+          continue;
+        }
+        const T* s = reinterpret_cast<const T*>(u.src);
+        T* d = reinterpret_cast<T*>(u.dst);
+        if (u.pair < 0) {
+          d[u.a] = s[u.a];
+          continue;
+        }
+        const float x = to_f(s[u.a]), y = to_f(s[u.b]);
+        const float2 c = cs[u.pair];
+        from_f(x * c.x - y * c.y, d + u.a);
+        from_f(y * c.x + x * c.y, d + u.b);
+      }
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch(const RopeParams& r, int num_sms, cudaStream_t stream) {
+  const int R = r.pairs, D = r.dim;
+  const bool vec = r.interleaved ? R % 4 == 0 : R % 8 == 0;
+  const int rot = !vec ? R + (D - 2 * R) : r.interleaved ? (D + 15) / 16 : R / 8 + (D - 2 * R + 15) / 16;
+  const int copy = (D + 15) / 16;
+  const int per_token = (r.q_heads + r.kv_heads) * rot + r.kv_heads * copy;
+  const int tokens = r.tokens >= 8 * num_sms * kRopeMaxTokens ? kRopeMaxTokens : 1;
+  const RopeKernelParams kp{r, FastDiv(per_token), FastDiv(rot), FastDiv(copy), tokens};
+  const unsigned grid = static_cast<unsigned>((r.tokens + tokens - 1) / tokens);
+  if (vec) rope_kernel<T, true><<<grid, kRopeThreads, 0, stream>>>(kp);
+  else rope_kernel<T, false><<<grid, kRopeThreads, 0, stream>>>(kp);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_rope(FloatType t, const RopeParams& r, int num_sms, cudaStream_t stream) {
+  return t == FloatType::BF16 ? launch<__nv_bfloat16>(r, num_sms, stream) : launch<__half>(r, num_sms, stream);
+}
+
+}  // namespace kaio

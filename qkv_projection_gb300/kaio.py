@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 from typing import Optional, Tuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -40,11 +41,21 @@ _SIGNATURES = {
     "kaio_dequantize_per_group_backward": ([_i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp], _i32),
     "kaio_dequantize_per_group": ([_i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp], _i32),
     "kaio_qkv_project_int8": ([_vp] * 4 + [ctypes.c_float] * 3 + [_vp] * 3 + [_u32, _u32, _u32, _vp], _i32),
+    "kaio_rope": ([_vp, _vp], _i32),
+    "kaio_rope_append": ([_vp, _vp], _i32),
+    "kaio_paged_attention": ([_vp, _vp], _i32),
+    "kaio_paged_attention_workspace": ([_vp], _i32),
     "kaio_qkv_path": ([_u32], _i32),
     "kaio_last_error": ([], ctypes.c_char_p),
     "kaio_device_status": ([], _i32),
     "kaio_status_string": ([_i32], ctypes.c_char_p),
 }
+
+
+# Argument blocks of the entries that take one (the structs of include/kaio_qkv.h,
+# field by field), filled by one pack() each.
+_ROPE_ARGS = struct.Struct("@I7i4i4i9P15q")
+_PAGED_ARGS = struct.Struct("@I13ifi9PQ11q")
 
 
 class KaioError(RuntimeError):
@@ -308,3 +319,190 @@ def dequantize_per_group(q, scale, group: int, out=None, stream=None):
     check(lib().kaio_dequantize_per_group(qcode, _float_code(scale.dtype), outer, axis, group,
                                           q.data_ptr(), scale.data_ptr(), out.data_ptr(), _stream_ptr(stream)))
     return out
+
+
+# ------------------------------------------- rotary positions, paged attention
+_F16_CODES = None
+
+
+def _f16_code(dtype, name):
+    global _F16_CODES
+    if _F16_CODES is None:
+        torch = _torch()
+        _F16_CODES = {torch.float16: KAIO_DTYPE_F16, torch.bfloat16: KAIO_DTYPE_BF16}
+    code = _F16_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"{name} has dtype {dtype}, expected torch.float16 or torch.bfloat16")
+    return code
+
+
+def _need_strided(t, name, dtype, shape):
+    """Checks a tensor that may have strides of its own (a dense last dimension);
+    None in ``shape`` takes any size. Returns its strides."""
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device (no CPU fallback)")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    got = t.shape
+    if len(got) != len(shape):
+        raise ValueError(f"{name} must be rank {len(shape)}, got shape {tuple(got)}")
+    if got != shape:
+        for g, want in zip(got, shape):
+            if want is not None and g != want:
+                raise ValueError(f"{name} has shape {tuple(got)}, expected {tuple(shape)}")
+    if t.requires_grad:
+        raise ValueError(f"{name} has gradient tracking enabled; these ops are forward-only: detach() it")
+    strides = t.stride()
+    if strides[-1] != 1 and got[-1] > 1:
+        raise ValueError(f"{name} must have a dense last dimension (strides {strides})")
+    return strides
+
+
+def _rope_axes(positions, tokens, sections, pairs):
+    """(axes, axis stride, sections padded to four) of a positions tensor [T] or [axes, T]."""
+    if isinstance(positions, _torch().Tensor) and positions.dim() == 1:
+        _need_strided(positions, "positions", _torch().int32, (tokens,))
+        axes, stride = 1, 0
+    else:
+        stride = _need_strided(positions, "positions", _torch().int32, (None, tokens))[0]
+        axes = positions.shape[0]
+    if sections is None:
+        if axes != 1:
+            raise ValueError(f"positions has {axes} axes: sections has to say how many pairs each one turns")
+        sections = (pairs,)
+    if len(sections) != axes or axes > 4:
+        raise ValueError(f"sections {tuple(sections)} does not fit positions with {axes} axes (1 to 4)")
+    return axes, stride, (*sections, 0, 0, 0)[:4]
+
+
+def rope(x, positions, inv_freq, sections=None, interleaved: bool = False, inverse: bool = False, out=None,
+         stream=None):
+    """Rotary positions: returns x [T, H, D] (f16 or bf16) with its first 2 * R
+    columns turned by positions[a(i), t] * inv_freq[i], pair by pair.
+
+    positions int32 [T] or [axes, T]; inv_freq f32 [R]; sections: how many
+    consecutive pairs each axis turns (default: all by the one axis). Pairs are
+    columns (i, i + R), or (2i, 2i + 1) if interleaved. inverse turns the other
+    way: the gradient of the rotation with respect to x, given that of its
+    result. out may be x itself.
+    """
+    torch = _torch()
+    code = _f16_code(x.dtype, "x")
+    xs = _need_strided(x, "x", x.dtype, (None, None, None))
+    t, h, d = x.shape
+    _need_strided(inv_freq, "inv_freq", torch.float32, (None,))
+    pairs = inv_freq.shape[0]
+    axes, axis_stride, sec = _rope_axes(positions, t, sections, pairs)
+    if out is None:
+        out = torch.empty((t, h, d), dtype=x.dtype, device=x.device)
+    os_ = _need_strided(out, "out", x.dtype, (t, h, d))
+    args = _ROPE_ARGS.pack(_ROPE_ARGS.size, code, t, h, 0, d, pairs, axes, *sec, interleaved, inverse, 0, 0,
+                           x.data_ptr(), 0, 0, out.data_ptr(), 0, 0, positions.data_ptr(), inv_freq.data_ptr(), 0,
+                           xs[0], xs[1], os_[0], os_[1], 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, axis_stride)
+    check(lib().kaio_rope(args, _stream_ptr(stream)))
+    return out
+
+
+def rope_append(q, k, v, positions, inv_freq, k_cache, v_cache, slots, sections=None, interleaved: bool = False,
+                q_out=None, stream=None):
+    """Rotates q and k as ``rope`` does and writes the rotated k and the unchanged
+    v into a paged cache, in one launch. Returns the rotated q.
+
+    q [T, H, D], k and v [T, KH, D]; k_cache and v_cache [pages, page_size, KH, D]
+    (any strides with a dense last dimension, such as a transposed [pages, KH,
+    page_size, D]); slots int32 [T]: page * page_size + place in the page for each
+    token, or -1 to store nothing. q_out may be q itself.
+    """
+    torch = _torch()
+    dtype = q.dtype
+    code = _f16_code(dtype, "q")
+    qs = _need_strided(q, "q", dtype, (None, None, None))
+    t, h, d = q.shape
+    ks = _need_strided(k, "k", dtype, (t, None, d))
+    kh = k.shape[1]
+    vs = _need_strided(v, "v", dtype, (t, kh, d))
+    kc = _need_strided(k_cache, "k_cache", dtype, (None, None, kh, d))
+    pages, page_size = k_cache.shape[:2]
+    vc = _need_strided(v_cache, "v_cache", dtype, (pages, page_size, kh, d))
+    _need_strided(inv_freq, "inv_freq", torch.float32, (None,))
+    _need_strided(slots, "slots", torch.int32, (t,))
+    pairs = inv_freq.shape[0]
+    axes, axis_stride, sec = _rope_axes(positions, t, sections, pairs)
+    if q_out is None:
+        q_out = torch.empty((t, h, d), dtype=dtype, device=q.device)
+    os_ = _need_strided(q_out, "q_out", dtype, (t, h, d))
+    args = _ROPE_ARGS.pack(_ROPE_ARGS.size, code, t, h, kh, d, pairs, axes, *sec, interleaved, 0, pages, page_size,
+                           q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(),
+                           v_cache.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), slots.data_ptr(),
+                           qs[0], qs[1], os_[0], os_[1], ks[0], ks[1], vs[0], vs[1], kc[0], kc[1], kc[2],
+                           vc[0], vc[1], vc[2], axis_stride)
+    check(lib().kaio_rope_append(args, _stream_ptr(stream)))
+    return q_out
+
+
+def paged_attention_workspace(device=None):
+    """A workspace for ``paged_attention`` on a device: allocate it once and keep
+    it. Calls that use the same one must be ordered (one stream, or events)."""
+    torch = _torch()
+    n = ctypes.c_uint64()
+    with torch.cuda.device(device):
+        check(lib().kaio_paged_attention_workspace(ctypes.byref(n)))
+        return torch.zeros(n.value, dtype=torch.uint8, device="cuda")
+
+
+def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max_new: Optional[int] = None,
+                    scale: Optional[float] = None, causal: bool = True, window: int = 0, sinks: int = 0,
+                    workspace=None, out=None, return_lse: bool = False, lse=None, stream=None):
+    """Attention of new tokens over a paged cache that already holds their keys
+    and values. Returns out [T, H, D], or (out, lse f32 [T, H]) with return_lse.
+
+    q [T, H, D] (f16 or bf16): the new tokens of all sequences, those of sequence
+    b at q_starts[b]:q_starts[b + 1] (int32 [B + 1]; default: one token each);
+    they are the last ones of its kv_lens[b] (int32 [B]) positions. k_cache and
+    v_cache [pages, page_size, KH, D], any strides with a dense last dimension,
+    page_size a power of two from 16 to 1024, H a multiple of KH; page_table
+    int32 [B, P]. max_new: at least the largest number of new tokens of one
+    sequence (default: T). scale defaults to D ** -0.5. causal: a token sees
+    positions up to its own; window: only the last `window` of them, and the
+    first `sinks` positions besides. A token that sees nothing gets zeros
+    and lse = -inf. workspace: from ``paged_attention_workspace``; without one
+    the call makes its own.
+    """
+    torch = _torch()
+    dtype = q.dtype
+    code = _f16_code(dtype, "q")
+    qs = _need_strided(q, "q", dtype, (None, None, None))
+    t, h, d = q.shape
+    kc = _need_strided(k_cache, "k_cache", dtype, (None, None, None, d))
+    pages, page_size, kh = k_cache.shape[:3]
+    vc = _need_strided(v_cache, "v_cache", dtype, (pages, page_size, kh, d))
+    _need_strided(kv_lens, "kv_lens", torch.int32, (None,))
+    b = kv_lens.shape[0]
+    ts = _need_strided(page_table, "page_table", torch.int32, (b, None))
+    starts = 0
+    if q_starts is not None:
+        _need_strided(q_starts, "q_starts", torch.int32, (b + 1,))
+        starts = q_starts.data_ptr()
+    if workspace is None:
+        workspace = paged_attention_workspace(q.device)
+    elif not (workspace.is_cuda and workspace.dtype == torch.uint8 and workspace.is_contiguous()):
+        raise ValueError("workspace must be a dense uint8 CUDA tensor from paged_attention_workspace()")
+    if out is None:
+        out = torch.empty((t, h, d), dtype=dtype, device=q.device)
+    os_ = _need_strided(out, "out", dtype, (t, h, d))
+    if lse is not None:
+        if _need_strided(lse, "lse", torch.float32, (t, h))[0] != h and t > 1:
+            raise ValueError("lse must be contiguous")
+    elif return_lse:
+        lse = torch.empty((t, h), dtype=torch.float32, device=q.device)
+    args = _PAGED_ARGS.pack(_PAGED_ARGS.size, code, b, t, h, kh, d, page_size, pages, page_table.shape[1],
+                            t if max_new is None else max_new, causal, window, sinks,
+                            d ** -0.5 if scale is None else scale, 0,
+                            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
+                            kv_lens.data_ptr(), starts, out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+                            workspace.data_ptr(), workspace.numel(),
+                            qs[0], qs[1], os_[0], os_[1], kc[0], kc[1], kc[2], vc[0], vc[1], vc[2], ts[0])
+    check(lib().kaio_paged_attention(args, _stream_ptr(stream)))
+    return (out, lse) if return_lse else out
