@@ -363,8 +363,8 @@ int kaio_rope_append(const kaio_rope_args* args, kaio_stream_t stream);
  *   q_starts  i32 [batch + 1]    from 0 to tokens, not decreasing; null: one
  *             token for each sequence (tokens == batch)
  *   lse       f32 [tokens, heads], dense; null: not wanted
- *   max_new   at least the largest number of new tokens of one sequence; it
- *             chooses the kernel, results do not depend on it
+ *   max_new   at least the largest number of new tokens of one sequence. It
+ *             chooses the kernel, whose results differ in rounding only
  *   workspace kaio_paged_attention_workspace() bytes of device memory,
  *             16-byte aligned, zeroed once before its first use. Every call
  *             leaves it ready for the next. Calls that share a workspace have

@@ -668,7 +668,7 @@ int float16_type(int dtype, kaio::FloatType* t) {
 }
 
 size_t paged_workspace_bytes(const DeviceInfo& info) {
-  return kaio::paged_decode_workspace_bytes(info.sms);
+  return std::max(kaio::paged_decode_workspace_bytes(info.sms), kaio::paged_chunk_workspace_bytes(info.sms));
 }
 
 int rope_impl(const kaio_rope_args* a, bool append, cudaStream_t stream) {
@@ -891,7 +891,12 @@ int kaio_paged_attention(const kaio_paged_attention_args* a, kaio_stream_t strea
   p.causal = a->causal != 0;
   p.window = std::min(a->window, kaio::kPagedMaxLen), p.sinks = std::min(a->sinks, kaio::kPagedMaxLen);
   p.scale_log2 = a->scale * 1.4426950408889634f;
-  const cudaError_t e = kaio::launch_paged_decode(t, p, a->workspace, info.sms, stream);
+  // Up to 16 rows a sequence and K/V head the warp-MMA kernel streams the keys;
+  // more rows are worth the tensor cores' 128-row tiles. (An empty cache has no
+  // tensor map; the former handles it.)
+  const bool few = static_cast<int64_t>(a->max_new) * p.group <= kaio::kPagedDecodeRows || p.max_pages == 0;
+  const cudaError_t e = few ? kaio::launch_paged_decode(t, p, a->workspace, info.sms, stream)
+                            : kaio::launch_paged_chunk(t, p, a->workspace, info.sms, stream);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention kernel launch");
   return KAIO_OK;
 }
@@ -934,9 +939,10 @@ int kaio_device_status(void) {
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
   const unsigned err_tc = kaio::read_and_clear_tc_errors();
   const unsigned err_td = kaio::read_and_clear_tc_decode_errors();
-  if (err_tc == 0xFFFFFFFFu || err_td == 0xFFFFFFFFu)
+  const unsigned err_pc = kaio::read_and_clear_chunk_errors();
+  if (err_tc == 0xFFFFFFFFu || err_td == 0xFFFFFFFFu || err_pc == 0xFFFFFFFFu)
     return fail(KAIO_ERR_CUDA, "could not read the device error word");
-  const unsigned err = err_tc | err_td;
+  const unsigned err = err_tc | err_td | err_pc;
   if (err & kaio::kDevErrTimeoutHost)
     return fail(KAIO_ERR_DEVICE_TIMEOUT, "a kernel gave up a bounded wait (device error word 0x%x)", err);
   return KAIO_OK;

@@ -129,6 +129,9 @@ constexpr int kPagedDecodeRows = 16;
 constexpr size_t kPagedCounterBytes = 4096;
 size_t paged_decode_workspace_bytes(int num_sms);
 cudaError_t launch_paged_decode(FloatType t, PagedParams p, void* workspace, int num_sms, cudaStream_t stream);
+size_t paged_chunk_workspace_bytes(int num_sms);
+cudaError_t launch_paged_chunk(FloatType t, const PagedParams& p, void* workspace, int num_sms, cudaStream_t stream);
+unsigned read_and_clear_chunk_errors();
 
 // ------------------------------------------------- tensor-core (tcgen05) paths
 struct GemmShape {
@@ -166,6 +169,10 @@ unsigned read_and_clear_tc_errors();
 cudaError_t ensure_smem_limit(const void* kernel, int bytes);
 
 // Driver entry point for tensor-map encoding (resolved once through the runtime).
+// encode_tensor_map: any rank, strides in bytes of dimensions 1 and up, nothing kept.
+CUresult encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank, const void* base,
+                           const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                           CUtensorMapSwizzle swz);
 CUresult encode_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
                               uint64_t inner, uint64_t outer, uint64_t row_bytes,
                               uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz);

@@ -464,7 +464,7 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max
     v_cache [pages, page_size, KH, D], any strides with a dense last dimension,
     page_size a power of two from 16 to 1024, H a multiple of KH; page_table
     int32 [B, P]. max_new: at least the largest number of new tokens of one
-    sequence (default: T). scale defaults to D ** -0.5. causal: a token sees
+    sequence (default: T, or 1 without q_starts). scale defaults to D ** -0.5. causal: a token sees
     positions up to its own; window: only the last `window` of them, and the
     first `sinks` positions besides. A token that sees nothing gets zeros
     and lse = -inf. workspace: from ``paged_attention_workspace``; without one
@@ -498,7 +498,7 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max
     elif return_lse:
         lse = torch.empty((t, h), dtype=torch.float32, device=q.device)
     args = _PAGED_ARGS.pack(_PAGED_ARGS.size, code, b, t, h, kh, d, page_size, pages, page_table.shape[1],
-                            t if max_new is None else max_new, causal, window, sinks,
+                            max_new if max_new is not None else t if starts else 1, causal, window, sinks,
                             d ** -0.5 if scale is None else scale, 0,
                             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
                             kv_lens.data_ptr(), starts, out.data_ptr(), 0 if lse is None else lse.data_ptr(),
