@@ -886,6 +886,7 @@ int kaio_paged_attention(const kaio_paged_attention_args* a, kaio_stream_t strea
   p.table = a->page_table, p.table_stride = a->table_stride, p.kv_lens = a->kv_lens, p.q_starts = a->q_starts;
   p.batch = a->batch, p.tokens = a->tokens, p.heads = a->heads, p.kv_heads = a->kv_heads;
   p.group = a->heads / a->kv_heads, p.dim = a->dim;
+  p.group_div = kaio::FastDiv(static_cast<uint32_t>(p.group));
   while ((1 << p.page_shift) < a->page_size) ++p.page_shift;
   p.num_pages = a->num_pages, p.max_pages = P ? a->max_pages : 0;
   p.causal = a->causal != 0;

@@ -85,6 +85,21 @@ cudaError_t launch_dequant_group_forward(FloatType t, bool q_unsigned, const voi
                                          void* out, int outer, int axis, int group, int num_sms,
                                          cudaStream_t stream);
 
+// n / d for 0 <= n < 2^31 by one multiplication (round-up reciprocal).
+struct FastDiv {
+  uint32_t mul = 1, shift = 0, d = 1;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t div) : d(div) {
+    while ((1ull << shift) < div) ++shift;
+    mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - div)) / div + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int div(int n) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
+  }
+#endif
+};
+
 // ----------------------------------------------- rotary positions, cache write
 // Strides are in elements. kv_heads == 0: q alone (no cache).
 struct RopeParams {
@@ -113,6 +128,7 @@ struct PagedParams {
   long long k_ps, k_ss, k_hs, v_ps, v_ss, v_hs, table_stride;
   const int *table, *kv_lens, *q_starts;   // q_starts may be null: one token per sequence
   int batch, tokens, heads, kv_heads, group, dim;
+  FastDiv group_div;          // group = heads / kv_heads
   int page_shift, num_pages, max_pages;
   bool causal;
   int window, sinks;          // window 0: none; both at most kPagedMaxLen

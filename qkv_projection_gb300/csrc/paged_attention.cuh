@@ -50,7 +50,7 @@ struct PagedSpan {
   int lo, hi, first;
   int sink_tiles, lo_tile, units;   // units: at least 1, so that every item is visited
   __device__ __forceinline__ PagedSpan(const PagedParams& p, const PagedSeq& s, int r0, int r1) {
-    const int t0 = r0 / p.group, t1 = (r1 - 1) / p.group;
+    const int t0 = p.group_div.div(r0), t1 = p.group_div.div(r1 - 1);
     hi = p.causal ? min(max(s.kv - s.n + t1 + 1, 0), s.kv) : s.kv;
     lo = p.window > 0 ? min(max(s.kv - s.n + t0 - p.window + 1, 0), hi) : 0;
     first = min(p.sinks, lo);
@@ -67,7 +67,7 @@ struct PagedSpan {
 struct PagedRow {
   int lo, hi;
   __device__ __forceinline__ PagedRow(const PagedParams& p, const PagedSeq& s, int r) {
-    const int pos = s.kv - s.n + r / p.group;
+    const int pos = s.kv - s.n + p.group_div.div(r);
     hi = p.causal ? min(max(pos + 1, 0), s.kv) : s.kv;
     lo = p.window > 0 ? min(max(pos - p.window + 1, 0), hi) : 0;
   }

@@ -19,12 +19,20 @@
 // results themselves (both are rare), so eight of twelve warps share nearly all
 // registers and every softmax thread keeps its whole row of S (128 values) in them.
 //
-// Warps 0-3 and 4-7: the softmax of the halves; 8: MMA (10, 11 only fill its group of
-// four, by which registers are shared out); 9: K and V tiles by TMA,
-// one box per page and 64 columns (pages of 16 to 1024 positions), pages that no
-// row sees filled with zeros by an out-of-range coordinate. Rows of V that no row
-// of the item sees are zeroed in shared memory before use: a weight of zero must
-// not meet whatever the slot holds.
+// Issuing is half the work: on the thread that issues MMAs a wait on an mbarrier
+// or a commit takes 150-300 cycles, and one thread for both halves took 5100 cycles
+// a unit for 2048 of products. So each half has an issuing warp of its own; per unit it
+// waits for the tiles while the softmax runs, then for P (in two parts, so that the
+// product starts with the first), issues PV and the next QK back to back, and makes
+// one commit. What that commit implies (the product before it is done) the softmax
+// warps pass on: they release the K and V stages with plain arrivals.
+//
+// Warps 0-3 and 4-7: the softmax of the halves; 8, 9: their MMAs; 10, 11: K and V
+// tiles by TMA, one box per page and 64 columns (pages of 16 to 1024 positions),
+// pages that no row sees filled with zeros by an out-of-range coordinate. Rows of V
+// that no row of the item sees are zeroed in shared memory before use: a weight of
+// zero must not meet whatever the slot holds. The next item's Q is fetched as soon
+// as the last QK has read this one's, and its first QK runs while O is written.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -42,10 +50,11 @@ constexpr int kRows = 256;
 constexpr int kHalf = 128;
 constexpr int kKeys = 128;
 constexpr int kSoftmaxThreads = 256;
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kMmaWarp = 8, kLoadWarp = 10;    // and the one after each
+constexpr int kWarps = 12;
 constexpr int kThreads = 384;
-// Registers a thread: 384 threads start with 168; 2 x 128 x 208 + 128 x 88 is the same total.
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+// Registers a thread: 384 threads start with 168; 2 x 128 x 224 + 128 x 56 is the same total.
+constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
 constexpr int kMinUnits = 4;
 constexpr float kLazy = 8.f;            // growth of the maximum (log2) that renews the reference
 using Walk = PagedWalk<kRows, kKeys>;
@@ -55,10 +64,25 @@ template <int kDim> struct Shape {
   static constexpr int kBoxBytes = kKeys * 128;                 // 128 rows of 64 columns
   static constexpr int kBoxes = kDim / 64;
   static constexpr int kTile = kBoxes * kBoxBytes;              // Q half, K tile or V tile
-  static constexpr int kStages = kDim == 128 ? 5 : 10;
-  static constexpr int kSmem = (2 + kStages) * kTile + 1024;
+  static constexpr int kKStages = kDim == 128 ? 3 : 5, kVStages = kDim == 128 ? 2 : 5;
   static constexpr uint32_t kS = 0, kO = 256;                   // TMEM columns: S at 0 and 128, O at 256 and 256 + kDim
 };
+
+// What the warps share besides the tiles.
+template <int kDim> struct Control {
+  uint64_t q_full[2], s_full[2], p_full[2][2], o_done[2];
+  uint64_t k_full[Shape<kDim>::kKStages], k_empty[Shape<kDim>::kKStages];
+  uint64_t v_full[Shape<kDim>::kVStages], v_empty[Shape<kDim>::kVStages], mma_done[2];
+  Walk walks[kWarps], ahead[8];      // every warp's own place in the line (in registers it would cost 20)
+  PagedShare share;
+  float row_lse[kRows];
+  uint32_t tmem_base;
+  int abort_flag, last_one;
+};
+template <int kDim>
+constexpr int kSmem = (2 + Shape<kDim>::kKStages + Shape<kDim>::kVStages) * Shape<kDim>::kTile +
+                      static_cast<int>(sizeof(Control<kDim>));
+static_assert(kSmem<128> <= 232448 && kSmem<64> <= 232448, "shared memory of one CTA");
 
 template <typename T> struct Type;
 template <> struct Type<__half> {
@@ -96,8 +120,47 @@ template <int kRegs> __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two f32 at a time.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// 32 bytes to global memory; half of them at a time where they may not be aligned.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8], bool aligned) {
+  if (aligned) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
 struct ChunkParams {
   PagedParams p;
+  bool out32;                         // rows of out are whole, aligned 32-byte pieces
   int k_heads_first, v_heads_first;   // order of a map's middle dimensions: heads before slots
 };
 
@@ -107,72 +170,83 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ ChunkParams cp) {
   using S = Shape<kDim>;
   const PagedParams& p = cp.p;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = align_smem_1024(smem_raw);
+  // (no static shared memory: the 1024-byte aligned tiles start at its beginning)
+  extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* q_smem = smem;
-  unsigned char* ring = smem + 2 * S::kTile;
-  __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_full[2], o_done[2], kv_full[S::kStages],
-      kv_empty[S::kStages], mma_done;
-  __shared__ Walk walks[kMmaWarp + 2];      // every warp's own place in the line (in registers it would cost the softmax 20)
-  __shared__ PagedShare share;
-  __shared__ uint32_t tmem_base;
-  __shared__ int abort_flag, last_one;
+  unsigned char* k_ring = smem + 2 * S::kTile;
+  unsigned char* v_ring = k_ring + S::kKStages * S::kTile;
+  Control<kDim>& ctl = *reinterpret_cast<Control<kDim>*>(v_ring + S::kVStages * S::kTile);
 
   {
     PagedShare sh;
     if (!paged_share<kRows, kKeys, kThreads>(p, blockIdx.x, gridDim.x, kMinUnits,
-                                             reinterpret_cast<long long*>(smem), &walks[0], &sh))
+                                             reinterpret_cast<long long*>(smem), &ctl.walks[0], &sh))
       return;
-    if (threadIdx.x == 0) share = sh;
-    if (threadIdx.x > 0 && threadIdx.x < kMmaWarp + 2) walks[threadIdx.x] = walks[0];
+    if (threadIdx.x == 0) ctl.share = sh;
+    if (threadIdx.x > 0 && threadIdx.x < kWarps) ctl.walks[threadIdx.x] = ctl.walks[0];
   }
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  volatile int* abort = &abort_flag;
+  volatile int* abort = &ctl.abort_flag;
   if (threadIdx.x == 0) {
     for (int h = 0; h < 2; ++h) {
-      mbar_init(&q_full[h], 4);
-      mbar_init(&s_full[h], 1);
-      mbar_init(&p_full[h], 4);
-      mbar_init(&o_done[h], 1);
+      mbar_init(&ctl.q_full[h], 4);
+      mbar_init(&ctl.s_full[h], 1);
+      mbar_init(&ctl.p_full[h][0], 4);
+      mbar_init(&ctl.p_full[h][1], 4);
+      mbar_init(&ctl.o_done[h], 1);
+      mbar_init(&ctl.mma_done[h], 1);
     }
-    for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+    for (int i = 0; i < S::kKStages; ++i) {
+      mbar_init(&ctl.k_full[i], 1);
+      mbar_init(&ctl.k_empty[i], 2);
     }
-    mbar_init(&mma_done, 1);
-    abort_flag = 0;
+    for (int i = 0; i < S::kVStages; ++i) {
+      mbar_init(&ctl.v_full[i], 1);
+      mbar_init(&ctl.v_empty[i], 2);
+    }
+    ctl.abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(&tmem_base, 512);
+    tmem_alloc(&ctl.tmem_base, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_base;
-  Walk& w = walks[min(warp, kLoadWarp)];
-  auto next_item = [&] {
+  const uint32_t tmem = ctl.tmem_base;
+  Walk& w = ctl.walks[warp];
+  auto next_item = [&](Walk& to) {
     __syncwarp();
-    if (lane == 0) w.next_item(p);
+    if (lane == 0) to.next_item(p);
     __syncwarp();
   };
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, &g_chunk_err));
+  };
+  uint32_t unit_count = 0;      // units before this item: unit n has K stage n % kKStages, V stage n % kVStages
 
-  if (warp == kLoadWarp) {
+  if (warp >= kLoadWarp) {
     fewer_registers<kOtherRegs>();
     // ------------------------------------------------------------ K, V tiles
+    const bool is_v = warp > kLoadWarp;
+    const uint32_t stages = is_v ? S::kVStages : S::kKStages;
+    uint64_t* full = is_v ? ctl.v_full : ctl.k_full;
+    uint64_t* empty = is_v ? ctl.v_empty : ctl.k_empty;
+    unsigned char* ring = is_v ? v_ring : k_ring;
+    const CUtensorMap* map = is_v ? &v_map : &k_map;
+    const bool heads_first = is_v ? cp.v_heads_first : cp.k_heads_first;
     const int shift = min(p.page_shift, 7);
     const int boxes = kKeys >> shift, box_keys = 1 << shift;
     const int page_mask = (1 << p.page_shift) - 1;
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    uint32_t used = 0;                                    // stages filled at least once
-    while (ok && w.at < share.end) {
+    uint32_t stage = 0, phase = 0;
+    while (ok && w.at < ctl.share.end) {
       const Span span(p, w.s, w.row0(), w.row1(p));
-      const int u1 = static_cast<int>(min(static_cast<long long>(w.units), w.unit + (share.end - w.at)));
+      const int u1 = static_cast<int>(min(static_cast<long long>(w.units), w.unit + (ctl.share.end - w.at)));
       const int* table = p.table + w.b * p.table_stride;
+      const int head = w.h;
       auto page_of = [&](int u) {
         int id = p.num_pages;                             // out of range: the box is filled with zeros
         if (lane < boxes && u < u1) {
@@ -184,138 +258,117 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (span.hi > 0) {
         int id = page_of(w.unit);
-        for (int u = w.unit; ok && u < u1; ++u) {
+        for (int u = w.unit; u < u1; ++u) {
           const int slot = (span.key0(u) + lane * box_keys) & page_mask;
           const int next = page_of(u + 1);
+          if (!wait(&empty[stage], phase ^ 1)) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full[stage], S::kTile);
+          __syncwarp();
+          ++unit_count;
+          if (lane < boxes) {
+            unsigned char* dst = ring + stage * S::kTile + lane * box_keys * 128;
+            const int c1 = heads_first ? head : slot, c2 = heads_first ? slot : head;
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&kv_empty[stage], phase ^ 1, abort, &g_chunk_err));
-            if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&kv_full[stage], S::kTile);
-            __syncwarp();
-            used |= 1u << stage;
-            if (lane < boxes) {
-              unsigned char* dst = ring + stage * S::kTile + lane * box_keys * 128;
-              const CUtensorMap* map = kv ? &v_map : &k_map;
-              const bool heads_first = kv ? cp.v_heads_first : cp.k_heads_first;
-              const int c1 = heads_first ? w.h : slot, c2 = heads_first ? slot : w.h;
-#pragma unroll
-              for (int b = 0; b < S::kBoxes; ++b)
-                tma_load_4d(dst + b * S::kBoxBytes, map, &kv_full[stage], 64 * b, c1, c2, id);
-            }
-            if (++stage == S::kStages) stage = 0, phase ^= 1;
+            for (int b = 0; b < S::kBoxes; ++b)
+              tma_load_4d(dst + b * S::kBoxBytes, map, &full[stage], 64 * b, c1, c2, id);
           }
+          if (++stage == stages) stage = 0, phase ^= 1;
           id = next;
         }
       }
       if (u1 < w.units) break;
-      next_item();
+      next_item(w);
     }
-    // Every copy has landed before the CTA may exit.
-    for (int i = 0; i < S::kStages; ++i)
-      if (used >> i & 1) mbar_wait_drain(&kv_full[i], i < stage ? phase : phase ^ 1, &g_chunk_err);
+    // Every copy has landed before the CTA may exit: the last fill of each stage.
+    for (uint32_t i = 0; i < stages && i < unit_count; ++i)
+      mbar_wait_drain(&full[(unit_count - 1 - i) % stages], ((unit_count - 1 - i) / stages) & 1, &g_chunk_err);
     __syncwarp();
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kMmaWarp) {
     fewer_registers<kOtherRegs>();
     // ------------------------------------------------------------------- MMA
     constexpr uint32_t kQk = idesc<T>(kKeys, false), kPv = idesc<T>(kDim, true);
-    int stage = 0;
-    uint32_t phase = 0, q_phase[2] = {}, p_phase[2] = {};
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t ph) {
-      ok = ok && mbar_wait(bar, ph, abort, &g_chunk_err);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      tc_fence_after();
-      return ok;
-    };
-    auto advance = [&](int& st, uint32_t& ph) {
-      if (++st == S::kStages) st = 0, ph ^= 1;
-    };
-    auto qk = [&](int h, int st) {
+    const int half = warp - kMmaWarp;
+    const uint32_t s_tmem = tmem + S::kS + 128 * half, o_tmem = tmem + S::kO + kDim * half;
+    const uint32_t sq = smem_u32(q_smem + half * S::kTile);
+    uint32_t q_phase = 0, p_phase = 0;
+    auto qk = [&](uint32_t n) {
       if (lane == 0) {
-        const uint32_t sq = smem_u32(q_smem + h * S::kTile), sk = smem_u32(ring + st * S::kTile);
+        const uint32_t sk = smem_u32(k_ring + (n % S::kKStages) * S::kTile);
 #pragma unroll
         for (int ks = 0; ks < kDim / 16; ++ks) {
           const uint32_t off = (ks >> 2) * S::kBoxBytes + (ks & 3) * 32;
-          umma_ss(tmem + S::kS + 128 * h, sdesc_sw128(sq + off, 16, 1024), sdesc_sw128(sk + off, 16, 1024), kQk,
-                  ks != 0);
+          umma_ss(s_tmem, sdesc_sw128(sq + off, 16, 1024), sdesc_sw128(sk + off, 16, 1024), kQk, ks != 0);
         }
-        umma_commit(&s_full[h]);
+        umma_commit(&ctl.s_full[half]);
       }
     };
-    auto pv = [&](int h, int st, bool accumulate) {
-      if (lane == 0) {
-        const uint32_t sv = smem_u32(ring + st * S::kTile);
-#pragma unroll
-        for (int ks = 0; ks < kKeys / 16; ++ks)
-          umma_ts(tmem + S::kO + kDim * h, tmem + S::kS + 128 * h + 8 * ks,
-                  sdesc_sw128(sv + ks * 2048, S::kBoxBytes, 1024), kPv, accumulate || ks != 0);
-        umma_commit(&o_done[h]);
-      }
-    };
-    while (ok && w.at < share.end) {
+    while (ok && w.at < ctl.share.end) {
       const Span span(p, w.s, w.row0(), w.row1(p));
-      const int u1 = static_cast<int>(min(static_cast<long long>(w.units), w.unit + (share.end - w.at)));
-      const int halves = w.row1(p) - w.row0() > kHalf ? 2 : 1;
-      if (span.hi > 0) {
-        int k_stage = stage;
-        if (!wait(&kv_full[k_stage], phase)) break;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h >= halves || !wait(&q_full[h], q_phase[h])) break;
-          q_phase[h] ^= 1;
-          qk(h, k_stage);
-        }
-        if (!ok) break;
-        if (lane == 0) umma_commit(&kv_empty[k_stage]);
-        advance(stage, phase);
-        for (int u = w.unit; u < u1; ++u) {
-          const int v_stage = stage;
-          if (!wait(&kv_full[v_stage], phase)) break;
-          advance(stage, phase);
+      const int u0 = w.unit;
+      const int u1 = static_cast<int>(min(static_cast<long long>(w.units), u0 + (ctl.share.end - w.at)));
+      if (span.hi > 0 && w.row1(p) - w.row0() > kHalf * half) {
+        uint32_t n = unit_count;
+        if (!wait(&ctl.k_full[n % S::kKStages], (n / S::kKStages) & 1)) break;
+        if (!wait(&ctl.q_full[half], q_phase)) break;
+        q_phase ^= 1;
+        tc_fence_after();
+        qk(n);
+        for (int u = u0; u < u1; ++u, ++n) {
+          const bool more = u + 1 < u1;
+          if (!wait(&ctl.v_full[n % S::kVStages], (n / S::kVStages) & 1)) break;
+          unsigned char* v = v_ring + (n % S::kVStages) * S::kTile;
           const int k0 = span.key0(u);
           if (k0 + kKeys > span.hi || (k0 < span.lo && k0 + kKeys > span.first)) {
-            // zero the rows of V that no row of the item sees
-            unsigned char* v = ring + v_stage * S::kTile;
+            // zero the rows of V that no row of the item sees (both halves' warps do, with the same values)
             for (int i = lane; i < kKeys * S::kBoxes * 8; i += 32) {
-              const int key = (i >> 3) & (kKeys - 1), j = k0 + key;
+              const int j = k0 + ((i >> 3) & (kKeys - 1));
               if (!(j < span.hi && (j >= span.lo || j < span.first)))
                 *reinterpret_cast<uint4*>(v + i * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
           }
-          const bool more = u + 1 < u1;
+          if (more && !wait(&ctl.k_full[(n + 1) % S::kKStages], ((n + 1) / S::kKStages) & 1)) break;
+          const uint32_t sv = smem_u32(v);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (h >= halves || !wait(&p_full[h], p_phase[h])) break;
-            p_phase[h] ^= 1;
-            pv(h, v_stage, u != w.unit);
-            if (h == halves - 1 && lane == 0) umma_commit(&kv_empty[v_stage]);
-            if (more) {
-              if (h == 0 && !wait(&kv_full[stage], phase)) break;
-              qk(h, stage);
+          for (int part = 0; part < 2; ++part) {
+            if (!wait(&ctl.p_full[half][part], p_phase)) break;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+              for (int ks = 4 * part; ks < 4 * part + 4; ++ks)
+                umma_ts(o_tmem, s_tmem + 8 * ks, sdesc_sw128(sv + ks * 2048, S::kBoxBytes, 1024), kPv,
+                        u != u0 || ks != 0);
             }
           }
           if (!ok) break;
-          if (more) {
-            if (lane == 0) umma_commit(&kv_empty[stage]);
-            advance(stage, phase);
-          }
+          p_phase ^= 1;
+          if (more) qk(n + 1);
+          else if (lane == 0) umma_commit(&ctl.o_done[half]);
+        }
+        if (!ok) break;
+      } else if (span.hi > 0) {
+        // No rows of this half: it still takes every tile in turn and releases it. A
+        // wait tells a phase from its neighbours only, so nobody may skip ahead.
+        uint32_t n = unit_count;
+        for (int u = u0; u < u1; ++u, ++n) {
+          if (!wait(&ctl.k_full[n % S::kKStages], (n / S::kKStages) & 1)) break;
+          if (lane == 0) mbar_arrive(&ctl.k_empty[n % S::kKStages]);
+          if (!wait(&ctl.v_full[n % S::kVStages], (n / S::kVStages) & 1)) break;
+          if (lane == 0) mbar_arrive(&ctl.v_empty[n % S::kVStages]);
         }
         if (!ok) break;
       }
+      if (span.hi > 0) unit_count += u1 - u0;
       if (u1 < w.units) break;
-      next_item();
+      next_item(w);
     }
     // Every MMA has completed before TMEM is released.
     if (lane == 0) {
-      umma_commit(&mma_done);
-      mbar_wait_drain(&mma_done, 0, &g_chunk_err);
+      umma_commit(&ctl.mma_done[half]);
+      mbar_wait_drain(&ctl.mma_done[half], 0, &g_chunk_err);
     }
     __syncwarp();
-  } else if (warp >= 8) {
-    fewer_registers<kOtherRegs>();
   } else {
     more_registers<kSoftmaxRegs>();
     // --------------------------------------------------------------- softmax
@@ -326,50 +379,79 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The scale is applied after the mask (-inf) and the maximum, so it has to be
     // positive: a negative one turns Q's signs, a zero makes Q zero.
     const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
-    const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-    uint32_t tile_phase = 0;                               // of s_full and o_done
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t ph) {
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar, ph, abort, &g_chunk_err));
-      tc_fence_after();
-      return ok;
+    uint32_t tile_phase = 0, o_phase = 0;
+    bool q_sent = false;                                   // this item's Q is already on its way
+    Walk& nx = ctl.ahead[warp];
+
+    // Q rows of this warp: global -> 128B-swizzled shared memory, asynchronously; rows past the item's are zero.
+    auto fetch_q = [&](const Walk& it) {
+      constexpr int kChunks = kDim / 8;
+      const int chunk = lane % kChunks, r0 = it.row0(), rows = it.row1(p) - r0;
+      const T* base = static_cast<const T*>(p.q) + it.s.q0 * p.q_ts + it.h * p.group * p.q_hs + chunk * 8;
+#pragma unroll 4
+      for (int i = 0; i < 32; i += 32 / kChunks) {
+        const int r = 32 * warp + i + lane / kChunks, rl = r & (kHalf - 1);
+        const bool real = r < rows && chunk * 8 < p.dim && p.scale_log2 != 0.f;
+        const int t = p.group_div.div(r0 + min(r, rows - 1)), g = r0 + min(r, rows - 1) - t * p.group;
+        cp_async16(q_smem + half * S::kTile + (chunk >> 3) * S::kBoxBytes + rl * 128 + (((chunk & 7) ^ (rl & 7)) << 4),
+                   real ? base + t * p.q_ts + g * p.q_hs : static_cast<const T*>(p.q), real ? 16 : 0);
+      }
     };
-    while (w.at < share.end) {
+    auto send_q = [&] {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (p.scale_log2 < 0.f) {                            // every lane turns the signs of what it fetched
+        constexpr int kChunks = kDim / 8;
+        const int chunk = lane % kChunks;
+        for (int i = 0; i < 32; i += 32 / kChunks) {
+          const int rl = (32 * warp + i + lane / kChunks) & (kHalf - 1);
+          uint4* v = reinterpret_cast<uint4*>(q_smem + half * S::kTile + (chunk >> 3) * S::kBoxBytes + rl * 128 +
+                                              (((chunk & 7) ^ (rl & 7)) << 4));
+          v->x ^= 0x80008000u, v->y ^= 0x80008000u, v->z ^= 0x80008000u, v->w ^= 0x80008000u;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.q_full[half]);
+    };
+
+    while (w.at < ctl.share.end) {
       const Span span(p, w.s, w.row0(), w.row1(p));
       const int u0 = w.unit;
-      const int u1 = static_cast<int>(min(static_cast<long long>(w.units), u0 + (share.end - w.at)));
+      const int u1 = static_cast<int>(min(static_cast<long long>(w.units), u0 + (ctl.share.end - w.at)));
       const int rows = w.row1(p) - w.row0();
-      const bool mine = half == 0 || rows > kHalf;         // this half has rows
+      const bool mine = rows > kHalf * half;               // this half has rows
       const bool keys = span.hi > 0;
+      bool looked_ahead = false, q_next = false;
       float m = kNegInf, l = 0.f;                          // reference (in units of S) and sum
       if (mine && keys && ok) {
-        {  // Q rows of this warp: global -> 128B-swizzled shared memory, rows past the item's are zero
-          constexpr int kChunks = kDim / 8;
-          const int chunk = lane % kChunks;
-#pragma unroll 4
-          for (int i = 0; i < 32; i += 32 / kChunks) {
-            const int r = 32 * warp + i + lane / kChunks;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (r < rows && chunk * 8 < p.dim && p.scale_log2 != 0.f) {
-              const int g = w.row0() + r, t = g / p.group;
-              v = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (w.s.q0 + t) * p.q_ts +
-                                                  (w.h * p.group + g - t * p.group) * p.q_hs + chunk * 8);
-              v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-            }
-            const int rl = r & (kHalf - 1);
-            *reinterpret_cast<uint4*>(q_smem + half * S::kTile + (chunk >> 3) * S::kBoxBytes + rl * 128 +
-                                      (((chunk & 7) ^ (rl & 7)) << 4)) = v;
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&q_full[half]);
+        if (!q_sent) {
+          fetch_q(w);
+          send_q();
         }
         const int h0 = w.row0() + kHalf * half, h1 = min(h0 + kHalf, w.row0() + rows) - 1;
         const int all_hi = PagedRow(p, w.s, h0).hi, all_lo = PagedRow(p, w.s, h1).lo;
         const PagedRow vis(p, w.s, min(w.row0() + my_row, h1));
+        uint32_t n = unit_count;
 #pragma unroll 1
-        for (int u = u0; u < u1; ++u) {
-          if (!wait(&s_full[half], tile_phase)) break;
+        for (int u = u0; u < u1; ++u, ++n) {
+          if (!wait(&ctl.s_full[half], tile_phase)) break;
+          tc_fence_after();
+          tile_phase ^= 1;
+          // QK of this unit is done, and so is PV of the one before
+          if ((warp & 3) == 0 && lane == 0) {
+            mbar_arrive(&ctl.k_empty[n % S::kKStages]);
+            if (u > u0) mbar_arrive(&ctl.v_empty[(n - 1) % S::kVStages]);
+          }
+          if (u + 1 == u1 && u1 == w.units) {              // Q has been read for the last time: fetch the next item's
+            looked_ahead = true;
+            if (lane == 0) nx = w;
+            next_item(nx);
+            if (nx.at < ctl.share.end && nx.row1(p) - nx.row0() > kHalf * half &&
+                Span(p, nx.s, nx.row0(), nx.row1(p)).hi > 0) {
+              q_next = true;
+              fetch_q(nx);
+            }
+          }
           uint32_t s[4][32];
 #pragma unroll
           for (int i = 0; i < 4; ++i) tmem_ld32(s_tmem + 32 * i, s[i]);
@@ -378,59 +460,77 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(k0 + kKeys <= all_hi && (k0 >= all_lo || k0 + kKeys <= p.sinks))) {
             const int hi = vis.hi - k0, lo = vis.lo - k0, first = p.sinks - k0;
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (!(i < hi && (i >= lo || i < first))) s[i >> 5][i & 31] = __float_as_uint(kNegInf);
+            for (int i = 0; i < 4; ++i) {
+              // bits below x of the 32 columns from 32 i on
+              auto below = [&](int x) {
+                x -= 32 * i;
+                return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1;
+              };
+              const uint32_t seen = below(hi) & (~below(lo) | below(first));
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(seen >> e & 1)) s[i][e] = __float_as_uint(kNegInf);
+            }
           }
           float top4[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            top4[i] = __uint_as_float(s[i][0]);
+            top4[i] = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]));
 #pragma unroll
-            for (int e = 1; e < 32; ++e) top4[i] = fmaxf(top4[i], __uint_as_float(s[i][e]));
+            for (int e = 2; e < 32; e += 2) top4[i] = max3(top4[i], __uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1]));
           }
           const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
           // (the first finite maximum after none needs no rescaling: O and l are zero)
           const bool renew = top > m && (m == kNegInf || (top - m) * scale > kLazy);
           if (__any_sync(0xFFFFFFFFu, renew && m != kNegInf)) {
-            // the product that last wrote O has to be done
-            if (!wait(&o_done[half], tile_phase ^ 1)) break;
             const float f = renew ? exp2_fast((m - top) * scale) : 1.f;
             l *= f;
 #pragma unroll 1
-            for (int c = 0; c < kDim; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(o_tmem + c, o);
+            for (int c = 0; c < kDim; c += 8) {
+              uint32_t o[8];
+              tmem_ld8(o_tmem + c, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(o_tmem + c, o);
+              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st8(o_tmem + c, o);
             }
             tmem_st_wait();
           }
           if (renew) m = top;
           const float ref = m == kNegInf ? 0.f : m * scale;
-          float sum[4] = {};
+          const uint64_t scale2 = pair(scale, scale), ref2 = pair(-ref, -ref);
+          uint64_t sum2[2] = {};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t packed[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float a = exp2_fast(fmaf(__uint_as_float(s[i][e]), scale, -ref));
-              const float b = exp2_fast(fmaf(__uint_as_float(s[i][e + 1]), scale, -ref));
-              sum[i] += a + b;
+              const float2 x = unpair(fma2(pair(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])), scale2, ref2));
+              const float a = exp2_fast(x.x), b = exp2_fast(x.y);
+              sum2[i & 1] = add2(sum2[i & 1], pair(a, b));
               packed[e >> 1] = Type<T>::pack(a, b);
             }
             tmem_st16(s_tmem + 16 * i, packed);
+            if (i & 1) {                                   // 64 keys of P are complete
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&ctl.p_full[half][i >> 1]);
+            }
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[half]);
-          tile_phase ^= 1;
+          const float2 sa = unpair(sum2[0]), sb = unpair(sum2[1]);
+          l += (sa.x + sa.y) + (sb.x + sb.y);
         }
-        if (ok) wait(&o_done[half], tile_phase ^ 1);
+        if (q_next && ok) send_q();
+        if (ok && wait(&ctl.o_done[half], o_phase)) {
+          tc_fence_after();
+          o_phase ^= 1;
+          if ((warp & 3) == 0 && lane == 0)
+            mbar_arrive(&ctl.v_empty[(unit_count + (u1 - u0) - 1) % S::kVStages]);
+        }
       }
+      if (keys) unit_count += u1 - u0;
+      q_sent = q_next;
 
       // Results of this thread's row: O / l and m + log2 l (nothing seen: zeros, -inf).
       const bool split = u0 != 0 || u1 != w.units;
@@ -438,36 +538,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = none ? 0.f : 1.f / l;
       const float lse2 = none ? kNegInf : (m == kNegInf ? 0.f : m * scale) + log2f(l);
       const bool real = mine && my_row < rows;
-      const int g = w.row0() + min(my_row, rows - 1), t = g / p.group;
+      const int g = w.row0() + min(my_row, rows - 1), t = p.group_div.div(g);
       const long long tok = w.s.q0 + t;
       const int head = w.h * p.group + g - t * p.group;
       const int slot = 2 * static_cast<int>(blockIdx.x) + (u0 == 0 ? 1 : 0);
       if (mine) {
+        float* part = p.part_o + (static_cast<long long>(slot) * kRows + my_row) * kDim;
+        T* dst = static_cast<T*>(p.out) + tok * p.o_ts + head * p.o_hs;
 #pragma unroll 1
-        for (int c = 0; c < kDim; c += 32) {
-          uint32_t o[32];
+        for (int c = 0; c < kDim; c += 64) {
+          uint32_t o[2][32];
           if (keys) {
-            tmem_ld32(o_tmem + c, o);
+            tmem_ld32(o_tmem + c, o[0]);
+            tmem_ld32(o_tmem + c + 32, o[1]);
             tmem_ld_wait();
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(none ? 0.f : __uint_as_float(o[e]) * inv);
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[i][e] = __float_as_uint(none ? 0.f : __uint_as_float(o[i][e]) * inv);
           if (real && split) {
-            float* dst = p.part_o + (static_cast<long long>(slot) * kRows + my_row) * kDim + c;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(dst + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                const uint32_t v[8] = {o[i][e], o[i][e + 1], o[i][e + 2], o[i][e + 3],
+                                       o[i][e + 4], o[i][e + 5], o[i][e + 6], o[i][e + 7]};
+                store32(part + c + 32 * i + e, v, true);
+              }
           } else if (real) {
-            T* dst = static_cast<T*>(p.out) + tok * p.o_ts + head * p.o_hs + c;
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              if (c + e < p.dim) {
-                uint4 v;
-                uint32_t* pv = &v.x;
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  pv[k] = Type<T>::pack(__uint_as_float(o[e + 2 * k]), __uint_as_float(o[e + 2 * k + 1]));
-                *reinterpret_cast<uint4*>(dst + e) = v;
+              for (int e = 0; e < 32; e += 16) {
+                const int at = c + 32 * i + e;
+                uint32_t v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  v[k] = Type<T>::pack(__uint_as_float(o[i][e + 2 * k]), __uint_as_float(o[i][e + 2 * k + 1]));
+                if (at + 16 <= p.dim) store32(dst + at, v, cp.out32);
+                else if (at < p.dim) *reinterpret_cast<uint4*>(dst + at) = make_uint4(v[0], v[1], v[2], v[3]);
               }
           }
           __syncwarp();
@@ -480,52 +590,77 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (split) {
         // All softmax threads come here for every split item, also when a wait gave up.
-        const int c0 = share.owner(w.at - u0), c1 = share.owner(w.at - u0 + w.units - 1);
-        __threadfence();
+        const int c0 = ctl.share.owner(w.at - u0), c1 = ctl.share.owner(w.at - u0 + w.units - 1);
         named_sync(1, kSoftmaxThreads);
         if (threadIdx.x == 0) {
+          __threadfence();                                 // covers what the others wrote before the barrier
           const unsigned seen = atomicAdd(p.counters + c0, 1u);
-          last_one = seen == static_cast<unsigned>(c1 - c0);
-          if (last_one) p.counters[c0] = 0;
+          ctl.last_one = seen == static_cast<unsigned>(c1 - c0);
+          if (ctl.last_one) p.counters[c0] = 0;
         }
         named_sync(1, kSoftmaxThreads);
-        if (last_one) {
+        if (ctl.last_one) {
           __threadfence();
-          constexpr int kCols = kDim / 32;                 // columns of a lane
-          for (int r = warp; r < rows; r += 8) {
-            float top = kNegInf;
-            for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(p.part_l + (2 * c + (c == c0)) * kRows + r));
-            const float ref = top == kNegInf ? 0.f : top;
-            float acc[kCols] = {}, sum = 0.f;
+          // Each row's log-sum over all parts (one thread a row); a part then
+          // weighs exp2(its own - that).
+          if (my_row < rows) {
+            float top = kNegInf, sum = 0.f;
 #pragma unroll 4
-            for (int c = c0; c <= c1; ++c) {
-              const int from = 2 * c + (c == c0);
-              const float f = exp2_fast(__ldcg(p.part_l + from * kRows + r) - ref);
-              sum += f;
-              const float* src = p.part_o + (static_cast<long long>(from) * kRows + r) * kDim + kCols * lane;
+            for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(p.part_l + (2 * c + (c == c0)) * kRows + my_row));
+            const float ref = top == kNegInf ? 0.f : top;
+#pragma unroll 4
+            for (int c = c0; c <= c1; ++c)
+              sum += exp2_fast(__ldcg(p.part_l + (2 * c + (c == c0)) * kRows + my_row) - ref);
+            ctl.row_lse[my_row] = sum == 0.f ? kNegInf : ref + log2f(sum);
+          }
+          named_sync(1, kSoftmaxThreads);
+          // Eight columns a thread, so that a part's row is read and the output's
+          // written in whole sectors; kBatch rows at once for loads in flight.
+          constexpr int kLanes = kDim / 8, kRowStep = kSoftmaxThreads / kLanes, kBatch = 4;
+          const int col = threadIdx.x % kLanes * 8;
+          for (int r0 = threadIdx.x / kLanes; r0 < rows; r0 += kBatch * kRowStep) {
+            float acc[kBatch][8] = {}, lse2r[kBatch];
 #pragma unroll
-              for (int e = 0; e < kCols; e += 2) {
-                const float2 v = __ldcg(reinterpret_cast<const float2*>(src + e));
-                acc[e] += f * v.x;
-                acc[e + 1] += f * v.y;
+            for (int k = 0; k < kBatch; ++k) lse2r[k] = r0 + k * kRowStep < rows ? ctl.row_lse[r0 + k * kRowStep] : kNegInf;
+            for (int c = c0; c <= c1; ++c) {
+              const long long from = (2 * c + (c == c0)) * kRows + r0;
+#pragma unroll
+              for (int k = 0; k < kBatch; ++k) {
+                if (lse2r[k] == kNegInf) continue;         // past the rows, or nothing seen
+                const float f = exp2_fast(__ldcg(p.part_l + from + k * kRowStep) - lse2r[k]);
+                const float4* src = reinterpret_cast<const float4*>(p.part_o + (from + k * kRowStep) * kDim + col);
+                const float4 a = __ldcg(src), b = __ldcg(src + 1);
+                acc[k][0] += f * a.x, acc[k][1] += f * a.y, acc[k][2] += f * a.z, acc[k][3] += f * a.w;
+                acc[k][4] += f * b.x, acc[k][5] += f * b.y, acc[k][6] += f * b.z, acc[k][7] += f * b.w;
               }
             }
-            const float norm = sum == 0.f ? 0.f : 1.f / sum;
-            const int gr = w.row0() + r, tr = gr / p.group, hr = w.h * p.group + gr - tr * p.group;
-            const long long at = w.s.q0 + tr;
-            if (kCols * lane < p.dim) {
-              uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + at * p.o_ts + hr * p.o_hs + kCols * lane);
 #pragma unroll
-              for (int e = 0; e < kCols; e += 2) dst[e >> 1] = Type<T>::pack(acc[e] * norm, acc[e + 1] * norm);
+            for (int k = 0; k < kBatch; ++k) {
+              const int r = r0 + k * kRowStep;
+              if (r >= rows) continue;
+              const int gr = w.row0() + r, tr = p.group_div.div(gr), hr = w.h * p.group + gr - tr * p.group;
+              const long long at = w.s.q0 + tr;
+              uint4 v;
+              v.x = Type<T>::pack(acc[k][0], acc[k][1]);
+              v.y = Type<T>::pack(acc[k][2], acc[k][3]);
+              v.z = Type<T>::pack(acc[k][4], acc[k][5]);
+              v.w = Type<T>::pack(acc[k][6], acc[k][7]);
+              if (col < p.dim)
+                *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at * p.o_ts + hr * p.o_hs + col) = v;
+              if (p.lse && col == 0) p.lse[at * p.heads + hr] = lse2r[k] * kLn2;
             }
-            if (p.lse && lane == 0)
-              p.lse[at * p.heads + hr] = sum == 0.f ? kNegInf : (ref + log2f(sum)) * kLn2;
           }
         }
-        named_sync(1, kSoftmaxThreads);                    // last_one has been read
+        named_sync(1, kSoftmaxThreads);                    // ctl.last_one has been read
       }
       if (u1 < w.units) break;
-      next_item();
+      if (looked_ahead) {
+        __syncwarp();
+        if (lane == 0) w = nx;
+        __syncwarp();
+      } else {
+        next_item(w);
+      }
     }
   }
   tc_fence_before();
@@ -562,16 +697,16 @@ cudaError_t encode_cache(CUtensorMap* map, int* heads_first, const void* base, F
 template <typename T, int kDim>
 cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const ChunkParams& cp, int ctas, cudaStream_t stream) {
   const cudaError_t e =
-      ensure_smem_limit(reinterpret_cast<const void*>(paged_chunk_kernel<T, kDim>), Shape<kDim>::kSmem);
+      ensure_smem_limit(reinterpret_cast<const void*>(paged_chunk_kernel<T, kDim>), kSmem<kDim>);
   if (e != cudaSuccess) return e;
-  paged_chunk_kernel<T, kDim><<<ctas, kThreads, Shape<kDim>::kSmem, stream>>>(km, vm, cp);
+  paged_chunk_kernel<T, kDim><<<ctas, kThreads, kSmem<kDim>, stream>>>(km, vm, cp);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t paged_chunk_workspace_bytes(int num_sms) {
-  return kPagedCounterBytes + 2 * static_cast<size_t>(num_sms) * kRows * (128 + 1) * sizeof(float);
+  return kPagedCounterBytes + 32 + 2 * static_cast<size_t>(num_sms) * kRows * (128 + 1) * sizeof(float);
 }
 
 cudaError_t launch_paged_chunk(FloatType t, const PagedParams& params, void* workspace, int num_sms,
@@ -581,7 +716,10 @@ cudaError_t launch_paged_chunk(FloatType t, const PagedParams& params, void* wor
   PagedParams& p = cp.p;
   const int ctas = std::min(num_sms, static_cast<int>(kPagedCounterBytes / sizeof(unsigned)));
   p.counters = static_cast<unsigned*>(workspace);
-  p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kPagedCounterBytes);
+  // 32-byte stores: the workspace itself is only 16-byte aligned
+  p.part_o = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(workspace) + kPagedCounterBytes + 31) & ~31ull);
+  cp.out32 = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && (p.tokens == 1 || p.o_ts % 16 == 0) &&
+             (p.heads == 1 || p.o_hs % 16 == 0);
   p.part_l = p.part_o + static_cast<size_t>(2) * ctas * kRows * (p.dim <= 64 ? 64 : 128);
   CUtensorMap km, vm;
   cudaError_t e = encode_cache(&km, &cp.k_heads_first, p.kc, t, p, p.k_ps, p.k_ss, p.k_hs);

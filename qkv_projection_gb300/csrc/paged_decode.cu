@@ -347,21 +347,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       }
       __syncthreads();
       if (last_one) {
+        // Few rows leave most threads without one: then 2, 4, 8 or 16 groups of
+        // threads take every 2nd, 4th, ... part, and are added up in shared memory.
         __threadfence();
         write = true;
-        if (row < rows) {
-          float top = kNegInf, sum = 0.f;
-          for (int c = c0; c <= c1; ++c)
-            top = fmaxf(top, __ldcg(p.part_l + (2 * c + (c == c0 ? 1 : 0)) * kRows + row));
-          const float ref = top == kNegInf ? 0.f : top;
+        int groups = kRows;
+        while (groups * rows > kRows) groups >>= 1;
+        const int group = row / (kRows / groups), r = row % (kRows / groups);
+        float top = kNegInf, sum = 0.f;
 #pragma unroll
-          for (int c = 0; c < kSeg; ++c) acc[c] = 0.f;
-#pragma unroll 2
-          for (int c = c0; c <= c1; ++c) {
+        for (int c = 0; c < kSeg; ++c) acc[c] = 0.f;
+        if (r < rows) {
+#pragma unroll 4
+          for (int c = c0; c <= c1; ++c)
+            top = fmaxf(top, __ldcg(p.part_l + (2 * c + (c == c0 ? 1 : 0)) * kRows + r));
+        }
+        const float ref = top == kNegInf ? 0.f : top;
+        if (r < rows) {
+#pragma unroll 4
+          for (int c = c0 + group; c <= c1; c += groups) {
             const int from = 2 * c + (c == c0 ? 1 : 0);
-            const float f = exp2_fast(__ldcg(p.part_l + from * kRows + row) - ref);
+            const float f = exp2_fast(__ldcg(p.part_l + from * kRows + r) - ref);
             sum += f;
-            const float* src = p.part_o + (static_cast<long long>(from) * kRows + row) * kDim + col;
+            const float* src = p.part_o + (static_cast<long long>(from) * kRows + r) * kDim + col;
 #pragma unroll
             for (int e = 0; e < kSeg; e += 4) {
               const float4 v = __ldcg(reinterpret_cast<const float4*>(src + e));
@@ -371,11 +379,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
               acc[e + 3] += f * v.w;
             }
           }
-          lse2 = sum == 0.f ? kNegInf : ref + log2f(sum);
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-          for (int c = 0; c < kSeg; ++c) acc[c] *= inv;
         }
+        if (groups > 1) {
+          float* joined = reinterpret_cast<float*>(smem);     // [kRows][kDim], and the sums after it
+#pragma unroll
+          for (int c = 0; c < kSeg; c += 4)
+            *reinterpret_cast<float4*>(joined + row * kDim + col + c) =
+                make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+          if (col == 0) joined[kRows * kDim + row] = sum;
+          __syncthreads();
+          if (row < rows) {
+            for (int g = 1; g < groups; ++g) {
+              const int other = row + g * (kRows / groups);
+              sum += joined[kRows * kDim + other];
+#pragma unroll
+              for (int c = 0; c < kSeg; c += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(joined + other * kDim + col + c);
+                acc[c] += v.x, acc[c + 1] += v.y, acc[c + 2] += v.z, acc[c + 3] += v.w;
+              }
+            }
+          }
+        }
+        lse2 = sum == 0.f ? kNegInf : ref + log2f(sum);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int c = 0; c < kSeg; ++c) acc[c] *= inv;
       }
     }
     if (write && row < rows) {

@@ -31,17 +31,6 @@ constexpr int kRopeMaxPairs = 128;
 constexpr int kRopeMaxTokens = 4;    // tokens of one CTA
 constexpr int kRopeBatch = 2;        // units whose loads one thread has in flight
 
-// n / d for 0 <= n < 2^31 by one multiplication (round-up reciprocal).
-struct FastDiv {
-  uint32_t mul, shift, d;
-  __host__ explicit FastDiv(uint32_t div) : d(div) {
-    shift = 0;
-    while ((1ull << shift) < div) ++shift;
-    mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - div)) / div + 1);
-  }
-  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
-};
-
 struct RopeKernelParams {
   RopeParams r;
   FastDiv unit_div, rot_div, copy_div;   // units per token, per rotated head, per copied head
@@ -152,11 +141,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     u.b = -1;
     u.pair = -1;
     if (i >= total) return u;
-    const uint32_t t = kp.unit_div.div(i);
+    const uint32_t t = kp.unit_div.div(static_cast<int>(i));
     uint32_t j = i - t * per_token;
     const long long tok = t0 + t;
     if (j < rot_units) {
-      const uint32_t h = kp.rot_div.div(j);
+      const uint32_t h = kp.rot_div.div(static_cast<int>(j));
       j -= h * rot;
       if (h < static_cast<uint32_t>(p.q_heads)) {
         u.src = reinterpret_cast<const char*>(static_cast<const T*>(p.q) + tok * p.q_ts + h * p.q_hs);
@@ -195,7 +184,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
       }
     } else {
       j -= rot_units;
-      const uint32_t h = kp.copy_div.div(j);
+      const uint32_t h = kp.copy_div.div(static_cast<int>(j));
       j -= h * copy;
       if (vbase[t] < 0) return u;
       u.src = reinterpret_cast<const char*>(static_cast<const T*>(p.v) + tok * p.v_ts + h * p.v_hs);

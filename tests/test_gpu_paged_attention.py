@@ -349,3 +349,10 @@ def test_a_nan_query_or_key_stays_with_those_that_use_it():
         u = 2.0 ** -11
         err = (out.double().cpu().numpy() - ref[0])[keep]
         assert np.all(np.abs(err) <= (u * np.abs(ref[0]) + (u + 1e-4) * ref[2] + 2.0 ** -25)[keep])
+
+
+@pytest.mark.parametrize("d,dtype", [(128, "bfloat16"), (64, "float16")])
+def test_tiles_of_one_half_between_tiles_of_two(d, dtype):
+    """65 tokens of 4 heads are a tile of 256 rows and one of 4, over more key tiles than
+    the shared memory holds at once, head after head and sequence after sequence."""
+    Problem([(65, 2000), (1, 1500), (70, 1700), (33, 900), (64, 800)], 8, 2, d, 32, dtype).verify()
