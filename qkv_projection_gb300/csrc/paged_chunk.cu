@@ -70,7 +70,7 @@ template <int kDim> struct Shape {
 
 // What the warps share besides the tiles.
 template <int kDim> struct Control {
-  uint64_t q_full[2], s_full[2], p_full[2][2], o_done[2];
+  uint64_t q_full[2], s_full[2], p_full[2][2], o_done[2], turn[2];
   uint64_t k_full[Shape<kDim>::kKStages], k_empty[Shape<kDim>::kKStages];
   uint64_t v_full[Shape<kDim>::kVStages], v_empty[Shape<kDim>::kVStages], mma_done[2];
   Walk walks[kWarps], ahead[8];      // every warp's own place in the line (in registers it would cost 20)
@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl.p_full[h][0], 4);
       mbar_init(&ctl.p_full[h][1], 4);
       mbar_init(&ctl.o_done[h], 1);
+      mbar_init(&ctl.turn[h], 1);
       mbar_init(&ctl.mma_done[h], 1);
     }
     for (int i = 0; i < S::kKStages; ++i) {
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = warp - kMmaWarp;
     const uint32_t s_tmem = tmem + S::kS + 128 * half, o_tmem = tmem + S::kO + kDim * half;
     const uint32_t sq = smem_u32(q_smem + half * S::kTile);
-    uint32_t q_phase = 0, p_phase = 0;
+    uint32_t q_phase = 0, p_phase = 0, turn_phase = half == 0 ? 1 : 0;   // (half 0's first turn is free)
     auto qk = [&](uint32_t n) {
       if (lane == 0) {
         const uint32_t sk = smem_u32(k_ring + (n % S::kKStages) * S::kTile);
@@ -302,17 +303,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit(&ctl.s_full[half]);
       }
     };
+    // Two halves take strict turns at the tensor cores. Left to themselves they fall
+    // into step, and then both wait for products and compute softmaxes at the same time.
+    auto take_turn = [&](bool both) {
+      if (both) {
+        wait(&ctl.turn[half], turn_phase);
+        turn_phase ^= 1;
+      }
+      return ok;
+    };
+    auto pass_turn = [&](bool both) {
+      if (both && lane == 0) mbar_arrive(&ctl.turn[half ^ 1]);
+    };
     while (ok && w.at < ctl.share.end) {
       const Span span(p, w.s, w.row0(), w.row1(p));
       const int u0 = w.unit;
       const int u1 = static_cast<int>(min(static_cast<long long>(w.units), u0 + (ctl.share.end - w.at)));
+      const bool both = w.row1(p) - w.row0() > kHalf;
       if (span.hi > 0 && w.row1(p) - w.row0() > kHalf * half) {
         uint32_t n = unit_count;
         if (!wait(&ctl.k_full[n % S::kKStages], (n / S::kKStages) & 1)) break;
         if (!wait(&ctl.q_full[half], q_phase)) break;
         q_phase ^= 1;
+        if (!take_turn(both)) break;
         tc_fence_after();
         qk(n);
+        pass_turn(both);
         for (int u = u0; u < u1; ++u, ++n) {
           const bool more = u + 1 < u1;
           if (!wait(&ctl.v_full[n % S::kVStages], (n / S::kVStages) & 1)) break;
@@ -329,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
           if (more && !wait(&ctl.k_full[(n + 1) % S::kKStages], ((n + 1) / S::kKStages) & 1)) break;
+          if (!take_turn(both)) break;
           const uint32_t sv = smem_u32(v);
 #pragma unroll
           for (int part = 0; part < 2; ++part) {
@@ -345,6 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           p_phase ^= 1;
           if (more) qk(n + 1);
           else if (lane == 0) umma_commit(&ctl.o_done[half]);
+          pass_turn(both);
         }
         if (!ok) break;
       } else if (span.hi > 0) {
@@ -438,10 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           tile_phase ^= 1;
           // QK of this unit is done, and so is PV of the one before
-          if ((warp & 3) == 0 && lane == 0) {
-            mbar_arrive(&ctl.k_empty[n % S::kKStages]);
-            if (u > u0) mbar_arrive(&ctl.v_empty[(n - 1) % S::kVStages]);
-          }
+          if ((warp & 3) == 0 && lane == 0) mbar_arrive(&ctl.k_empty[n % S::kKStages]);
+          if ((warp & 3) == 1 && lane == 0 && u > u0) mbar_arrive(&ctl.v_empty[(n - 1) % S::kVStages]);
           if (u + 1 == u1 && u1 == w.units) {              // Q has been read for the last time: fetch the next item's
             looked_ahead = true;
             if (lane == 0) nx = w;
