@@ -49,12 +49,14 @@ __device__ unsigned g_chunk_err;
 constexpr int kRows = 256;
 constexpr int kHalf = 128;
 constexpr int kKeys = 128;
-constexpr int kSoftmaxThreads = 256;
-constexpr int kMmaWarp = 8, kLoadWarp = 10;    // and the one after each
-constexpr int kWarps = 12;
-constexpr int kThreads = 384;
-// Registers a thread: 384 threads start with 168; 2 x 128 x 224 + 128 x 56 is the same total.
-constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
+constexpr int kSoftmaxWarps = 16, kSoftmaxThreads = 32 * kSoftmaxWarps;
+constexpr int kMmaWarp = 16, kLoadWarp = 18;   // and the one after each
+constexpr int kThreads = 640;
+// Registers a thread: 640 threads start with 96; 512 x 104 + 128 x 64 is the same total.
+constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
+// Named barriers (0 is __syncthreads): all softmax warps; those of a half; the
+// two warps that share 32 rows.
+constexpr int kBarAll = 1, kBarHalf = 2, kBarPair = 4;
 constexpr int kMinUnits = 4;
 constexpr float kLazy = 8.f;            // growth of the maximum (log2) that renews the reference
 using Walk = PagedWalk<kRows, kKeys>;
@@ -70,12 +72,13 @@ template <int kDim> struct Shape {
 
 // What the warps share besides the tiles.
 template <int kDim> struct Control {
-  uint64_t q_full[2], s_full[2], p_full[2][2], o_done[2], turn[2];
+  uint64_t q_full[2], s_full[2], p_full[2], o_done[2], turn[2];
   uint64_t k_full[Shape<kDim>::kKStages], k_empty[Shape<kDim>::kKStages];
   uint64_t v_full[Shape<kDim>::kVStages], v_empty[Shape<kDim>::kVStages], mma_done[2];
-  Walk walks[kWarps], ahead[8];      // every warp's own place in the line (in registers it would cost 20)
+  Walk walks[4];                     // places in the line of the MMA and load warps
+  Walk items[2][3];                  // of each half's softmax: this item, the next and the one after
   PagedShare share;
-  float row_lse[kRows];
+  float row_x[2][kRows];             // what the two threads of a row tell each other
   uint32_t tmem_base;
   int abort_flag, last_one;
 };
@@ -120,6 +123,22 @@ template <int kRegs> __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
+__device__ __forceinline__ int volatile_lane() {
+  int l;
+  asm volatile("mov.u32 %0, %%laneid;" : "=r"(l));
+  return l;
+}
+// Named barrier that ORs a flag over its `count` threads.
+__device__ __forceinline__ bool named_or(int id, int count, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.or.pred p, %2, %3, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(count)
+      : "memory");
+  return r != 0;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -183,17 +202,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              reinterpret_cast<long long*>(smem), &ctl.walks[0], &sh))
       return;
     if (threadIdx.x == 0) ctl.share = sh;
-    if (threadIdx.x > 0 && threadIdx.x < kWarps) ctl.walks[threadIdx.x] = ctl.walks[0];
+    if (threadIdx.x > 0 && threadIdx.x < 4) ctl.walks[threadIdx.x] = ctl.walks[0];
+    if (threadIdx.x >= 4 && threadIdx.x < 6) {
+      Walk first = ctl.walks[0];
+      ctl.items[threadIdx.x - 4][0] = first;
+      first.next_item(p);
+      ctl.items[threadIdx.x - 4][1] = first;
+    }
   }
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &ctl.abort_flag;
   if (threadIdx.x == 0) {
     for (int h = 0; h < 2; ++h) {
-      mbar_init(&ctl.q_full[h], 4);
+      mbar_init(&ctl.q_full[h], 8);
       mbar_init(&ctl.s_full[h], 1);
-      mbar_init(&ctl.p_full[h][0], 4);
-      mbar_init(&ctl.p_full[h][1], 4);
+      mbar_init(&ctl.p_full[h], 8);
       mbar_init(&ctl.o_done[h], 1);
       mbar_init(&ctl.turn[h], 1);
       mbar_init(&ctl.mma_done[h], 1);
@@ -217,7 +241,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
-  Walk& w = ctl.walks[warp];
   auto next_item = [&](Walk& to) {
     __syncwarp();
     if (lane == 0) to.next_item(p);
@@ -225,13 +248,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, &g_chunk_err));
+    return ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, &g_chunk_err));
   };
   uint32_t unit_count = 0;      // units before this item: unit n has K stage n % kKStages, V stage n % kVStages
 
   if (warp >= kLoadWarp) {
     fewer_registers<kOtherRegs>();
     // ------------------------------------------------------------ K, V tiles
+    Walk& w = ctl.walks[warp - kMmaWarp];
     const bool is_v = warp > kLoadWarp;
     const uint32_t stages = is_v ? S::kVStages : S::kKStages;
     uint64_t* full = is_v ? ctl.v_full : ctl.k_full;
@@ -287,18 +311,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kMmaWarp) {
     fewer_registers<kOtherRegs>();
     // ------------------------------------------------------------------- MMA
+    Walk& w = ctl.walks[warp - kMmaWarp];
     constexpr uint32_t kQk = idesc<T>(kKeys, false), kPv = idesc<T>(kDim, true);
     const int half = warp - kMmaWarp;
     const uint32_t s_tmem = tmem + S::kS + 128 * half, o_tmem = tmem + S::kO + kDim * half;
-    const uint32_t sq = smem_u32(q_smem + half * S::kTile);
+    // descriptors of the tiles' first 16 columns (K) or keys (V); addresses are in units of 16 bytes
+    const uint64_t dq = sdesc_sw128(smem_u32(q_smem + half * S::kTile), 16, 1024);
+    const uint64_t dk0 = sdesc_sw128(smem_u32(k_ring), 16, 1024);
+    const uint64_t dv0 = sdesc_sw128(smem_u32(v_ring), S::kBoxBytes, 1024);
     uint32_t q_phase = 0, p_phase = 0, turn_phase = half == 0 ? 1 : 0;   // (half 0's first turn is free)
-    auto qk = [&](uint32_t n) {
+    // QK of unit n; the turn is passed on while its last products are still queued
+    auto qk = [&](uint32_t n, bool both) {
       if (lane == 0) {
-        const uint32_t sk = smem_u32(k_ring + (n % S::kKStages) * S::kTile);
+        const uint64_t dk = dk0 + (n % S::kKStages) * (S::kTile >> 4);
 #pragma unroll
         for (int ks = 0; ks < kDim / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * S::kBoxBytes + (ks & 3) * 32;
-          umma_ss(s_tmem, sdesc_sw128(sq + off, 16, 1024), sdesc_sw128(sk + off, 16, 1024), kQk, ks != 0);
+          if (ks == kDim / 16 - 4 && both) mbar_arrive(&ctl.turn[half ^ 1]);
+          const uint32_t off = ((ks >> 2) * S::kBoxBytes + (ks & 3) * 32) >> 4;
+          umma_ss(s_tmem, dq + off, dk + off, kQk, ks != 0);
         }
         umma_commit(&ctl.s_full[half]);
       }
@@ -312,9 +342,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return ok;
     };
-    auto pass_turn = [&](bool both) {
-      if (both && lane == 0) mbar_arrive(&ctl.turn[half ^ 1]);
-    };
     while (ok && w.at < ctl.share.end) {
       const Span span(p, w.s, w.row0(), w.row1(p));
       const int u0 = w.unit;
@@ -327,8 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         q_phase ^= 1;
         if (!take_turn(both)) break;
         tc_fence_after();
-        qk(n);
-        pass_turn(both);
+        qk(n, both);
         for (int u = u0; u < u1; ++u, ++n) {
           const bool more = u + 1 < u1;
           if (!wait(&ctl.v_full[n % S::kVStages], (n / S::kVStages) & 1)) break;
@@ -345,24 +371,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
           if (more && !wait(&ctl.k_full[(n + 1) % S::kKStages], ((n + 1) / S::kKStages) & 1)) break;
+          if (!wait(&ctl.p_full[half], p_phase)) break;
+          p_phase ^= 1;
           if (!take_turn(both)) break;
-          const uint32_t sv = smem_u32(v);
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t dv = dv0 + (n % S::kVStages) * (S::kTile >> 4);
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            if (!wait(&ctl.p_full[half][part], p_phase)) break;
-            tc_fence_after();
-            if (lane == 0) {
-#pragma unroll
-              for (int ks = 4 * part; ks < 4 * part + 4; ++ks)
-                umma_ts(o_tmem, s_tmem + 8 * ks, sdesc_sw128(sv + ks * 2048, S::kBoxBytes, 1024), kPv,
-                        u != u0 || ks != 0);
+            for (int ks = 0; ks < 8; ++ks)      // P: 32 keys in the first 16 of every 32 columns of S
+              umma_ts(o_tmem, s_tmem + 32 * (ks >> 1) + 8 * (ks & 1), dv + ks * 128, kPv, u != u0 || ks != 0);
+            if (!more) {
+              if (both) mbar_arrive(&ctl.turn[half ^ 1]);
+              umma_commit(&ctl.o_done[half]);
             }
           }
-          if (!ok) break;
-          p_phase ^= 1;
-          if (more) qk(n + 1);
-          else if (lane == 0) umma_commit(&ctl.o_done[half]);
-          pass_turn(both);
+          if (more) qk(n + 1, both);
         }
         if (!ok) break;
       } else if (span.hi > 0) {
@@ -390,40 +413,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     more_registers<kSoftmaxRegs>();
     // --------------------------------------------------------------- softmax
-    const int half = warp >> 2;
+    const int half = warp >> 3, part = (warp >> 2) & 1, of_half = warp & 7;
+    const int my_row = kHalf * half + 32 * (warp & 3) + lane;      // of the item's 256
+    const int bar_pair = kBarPair + 4 * half + (warp & 3);
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t s_tmem = tmem + lanes + S::kS + 128 * half, o_tmem = tmem + lanes + S::kO + kDim * half;
-    const int my_row = 32 * warp + lane;                   // of the item's 256
+    // this thread's 64 columns of S (weights of 32 keys go over the first half of their scores) and half of O's
+    const uint32_t s_tmem = tmem + lanes + S::kS + 128 * half + 64 * part;
+    const uint32_t o_tmem = tmem + lanes + S::kO + kDim * half + kDim / 2 * part;
     // The scale is applied after the mask (-inf) and the maximum, so it has to be
     // positive: a negative one turns Q's signs, a zero makes Q zero.
     const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
     uint32_t tile_phase = 0, o_phase = 0;
     bool q_sent = false;                                   // this item's Q is already on its way
-    Walk& nx = ctl.ahead[warp];
 
-    // Q rows of this warp: global -> 128B-swizzled shared memory, asynchronously; rows past the item's are zero.
+    // Q rows, 16 a warp: global -> 128B-swizzled shared memory, asynchronously; rows past the item's are zero.
+    // (Their lane comes from a volatile read, which keeps their addresses out of the registers of the loop below.)
+    constexpr int kChunks = kDim / 8;
+    auto q_at = [&](int rl, int q_chunk) {
+      return q_smem + half * S::kTile + (q_chunk >> 3) * S::kBoxBytes + rl * 128 + (((q_chunk & 7) ^ (rl & 7)) << 4);
+    };
     auto fetch_q = [&](const Walk& it) {
-      constexpr int kChunks = kDim / 8;
-      const int chunk = lane % kChunks, r0 = it.row0(), rows = it.row1(p) - r0;
-      const T* base = static_cast<const T*>(p.q) + it.s.q0 * p.q_ts + it.h * p.group * p.q_hs + chunk * 8;
-#pragma unroll 4
-      for (int i = 0; i < 32; i += 32 / kChunks) {
-        const int r = 32 * warp + i + lane / kChunks, rl = r & (kHalf - 1);
-        const bool real = r < rows && chunk * 8 < p.dim && p.scale_log2 != 0.f;
+      const int ln = volatile_lane(), q_chunk = ln % kChunks;
+      const int r0 = it.row0(), rows = it.row1(p) - r0;
+      const T* base = static_cast<const T*>(p.q) + it.s.q0 * p.q_ts + it.h * p.group * p.q_hs + q_chunk * 8;
+#pragma unroll 2
+      for (int i = 0; i < 16; i += 32 / kChunks) {
+        const int rl = 16 * of_half + i + ln / kChunks, r = kHalf * half + rl;
+        const bool real = r < rows && q_chunk * 8 < p.dim && p.scale_log2 != 0.f;
         const int t = p.group_div.div(r0 + min(r, rows - 1)), g = r0 + min(r, rows - 1) - t * p.group;
-        cp_async16(q_smem + half * S::kTile + (chunk >> 3) * S::kBoxBytes + rl * 128 + (((chunk & 7) ^ (rl & 7)) << 4),
-                   real ? base + t * p.q_ts + g * p.q_hs : static_cast<const T*>(p.q), real ? 16 : 0);
+        cp_async16(q_at(rl, q_chunk), real ? base + t * p.q_ts + g * p.q_hs : static_cast<const T*>(p.q), real ? 16 : 0);
       }
     };
     auto send_q = [&] {
       asm volatile("cp.async.wait_all;" ::: "memory");
       if (p.scale_log2 < 0.f) {                            // every lane turns the signs of what it fetched
-        constexpr int kChunks = kDim / 8;
-        const int chunk = lane % kChunks;
-        for (int i = 0; i < 32; i += 32 / kChunks) {
-          const int rl = (32 * warp + i + lane / kChunks) & (kHalf - 1);
-          uint4* v = reinterpret_cast<uint4*>(q_smem + half * S::kTile + (chunk >> 3) * S::kBoxBytes + rl * 128 +
-                                              (((chunk & 7) ^ (rl & 7)) << 4));
+        const int ln = volatile_lane();
+        for (int i = 0; i < 16; i += 32 / kChunks) {
+          uint4* v = reinterpret_cast<uint4*>(q_at(16 * of_half + i + ln / kChunks, ln % kChunks));
           v->x ^= 0x80008000u, v->y ^= 0x80008000u, v->z ^= 0x80008000u, v->w ^= 0x80008000u;
         }
       }
@@ -432,118 +458,139 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&ctl.q_full[half]);
     };
 
-    while (w.at < ctl.share.end) {
+    // Named barriers keep the warps together, so a warp whose wait gave up (ok is
+    // false) goes through all of them too; it only no longer waits or arrives.
+    for (uint32_t item = 0;; ++item) {
+      const Walk& w = ctl.items[half][item % 3];
+      const Walk& nx = ctl.items[half][(item + 1) % 3];
+      if (w.at >= ctl.share.end) break;
       const Span span(p, w.s, w.row0(), w.row1(p));
       const int u0 = w.unit;
       const int u1 = static_cast<int>(min(static_cast<long long>(w.units), u0 + (ctl.share.end - w.at)));
       const int rows = w.row1(p) - w.row0();
       const bool mine = rows > kHalf * half;               // this half has rows
       const bool keys = span.hi > 0;
-      bool looked_ahead = false, q_next = false;
-      float m = kNegInf, l = 0.f;                          // reference (in units of S) and sum
-      if (mine && keys && ok) {
+      bool q_next = false;
+      float m = kNegInf, l = 0.f;                          // the row's reference (in units of S), this thread's sum
+      if (mine && keys) {
         if (!q_sent) {
           fetch_q(w);
           send_q();
         }
-        const int h0 = w.row0() + kHalf * half, h1 = min(h0 + kHalf, w.row0() + rows) - 1;
-        const int all_hi = PagedRow(p, w.s, h0).hi, all_lo = PagedRow(p, w.s, h1).lo;
-        const PagedRow vis(p, w.s, min(w.row0() + my_row, h1));
-        uint32_t n = unit_count;
+        // Units [plain0, plain1) are seen whole by every row of this half (tiles of
+        // sinks are left to the mask).
+        int plain0, plain1;
+        {
+          const int h0 = w.row0() + kHalf * half, h1 = min(h0 + kHalf, w.row0() + rows) - 1;
+          const int all_hi = PagedRow(p, w.s, h0).hi, all_lo = PagedRow(p, w.s, h1).lo;
+          plain1 = span.sink_tiles + max(all_hi / kKeys - span.lo_tile, 0);
+          plain0 = span.sink_tiles + (all_lo + kKeys - 1) / kKeys - span.lo_tile;
+        }
 #pragma unroll 1
-        for (int u = u0; u < u1; ++u, ++n) {
-          if (!wait(&ctl.s_full[half], tile_phase)) break;
+        for (int u = u0; u < u1; ++u) {
+          wait(&ctl.s_full[half], tile_phase);
           tc_fence_after();
           tile_phase ^= 1;
           // QK of this unit is done, and so is PV of the one before
-          if ((warp & 3) == 0 && lane == 0) mbar_arrive(&ctl.k_empty[n % S::kKStages]);
-          if ((warp & 3) == 1 && lane == 0 && u > u0) mbar_arrive(&ctl.v_empty[(n - 1) % S::kVStages]);
+          if (of_half == 0 && lane == 0 && ok) mbar_arrive(&ctl.k_empty[(unit_count + (u - u0)) % S::kKStages]);
+          if (of_half == 1 && lane == 0 && ok && u > u0)
+            mbar_arrive(&ctl.v_empty[(unit_count + (u - u0) - 1) % S::kVStages]);
           if (u + 1 == u1 && u1 == w.units) {              // Q has been read for the last time: fetch the next item's
-            looked_ahead = true;
-            if (lane == 0) nx = w;
-            next_item(nx);
-            if (nx.at < ctl.share.end && nx.row1(p) - nx.row0() > kHalf * half &&
-                Span(p, nx.s, nx.row0(), nx.row1(p)).hi > 0) {
-              q_next = true;
-              fetch_q(nx);
-            }
+            q_next = nx.at < ctl.share.end && nx.row1(p) - nx.row0() > kHalf * half &&
+                     Span(p, nx.s, nx.row0(), nx.row1(p)).hi > 0;
+            if (q_next) fetch_q(nx);
           }
-          uint32_t s[4][32];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32(s_tmem + 32 * i, s[i]);
-          tmem_ld_wait();
-          const int k0 = span.key0(u);
-          if (!(k0 + kKeys <= all_hi && (k0 >= all_lo || k0 + kKeys <= p.sinks))) {
-            const int hi = vis.hi - k0, lo = vis.lo - k0, first = p.sinks - k0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              // bits below x of the 32 columns from 32 i on
-              auto below = [&](int x) {
-                x -= 32 * i;
-                return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1;
-              };
-              const uint32_t seen = below(hi) & (~below(lo) | below(first));
+          // Scores are read 32 at a time, for the maximum and again for the weights:
+          // a row of 64 kept in registers made them spill.
+          const bool plain = u >= plain0 && u < plain1;
+          auto load = [&](int i, uint32_t (&s)[32]) {
+            tmem_ld32(s_tmem + 32 * i, s);
+            tmem_ld_wait();
+            if (!plain) {
+              const PagedRow vis(p, w.s, min(w.row0() + my_row, w.row1(p) - 1));
+              const int at = span.key0(u) + 64 * part + 32 * i;
+              // bits of the visible ones of these 32 keys
+              auto below = [&](int x) { return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1; };
+              const uint32_t seen = below(vis.hi - at) & (~below(vis.lo - at) | below(p.sinks - at));
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (!(seen >> e & 1)) s[i][e] = __float_as_uint(kNegInf);
+                if (!(seen >> e & 1)) s[e] = __float_as_uint(kNegInf);
             }
-          }
-          float top4[4];
+          };
+          float top4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            top4[i] = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]));
+          for (int i = 0; i < 2; ++i) {
+            uint32_t s[32];
+            load(i, s);
 #pragma unroll
-            for (int e = 2; e < 32; e += 2) top4[i] = max3(top4[i], __uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1]));
+            for (int e = 0; e < 32; e += 2)
+              top4[(e >> 1) & 3] = max3(top4[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
           }
-          const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+          float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
           // (the first finite maximum after none needs no rescaling: O and l are zero)
-          const bool renew = top > m && (m == kNegInf || (top - m) * scale > kLazy);
-          if (__any_sync(0xFFFFFFFFu, renew && m != kNegInf)) {
-            const float f = renew ? exp2_fast((m - top) * scale) : 1.f;
-            l *= f;
+          auto grows = [&] { return top > m && (m == kNegInf || (top - m) * scale > kLazy); };
+          if (named_or(bar_pair, 64, grows())) {           // one of the 64 threads asks for a new reference
+            ctl.row_x[part][my_row] = top;
+            named_sync(bar_pair, 64);
+            top = fmaxf(top, ctl.row_x[part ^ 1][my_row]);
+            const bool renew = grows();
+            if (__any_sync(0xFFFFFFFFu, renew && m != kNegInf)) {
+              const float f = renew ? exp2_fast((m - top) * scale) : 1.f;
+              l *= f;
 #pragma unroll 1
-            for (int c = 0; c < kDim; c += 8) {
-              uint32_t o[8];
-              tmem_ld8(o_tmem + c, o);
-              tmem_ld_wait();
+              for (int c = 0; c < kDim / 2; c += 8) {
+                uint32_t o[8];
+                tmem_ld8(o_tmem + c, o);
+                tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st8(o_tmem + c, o);
+                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st8(o_tmem + c, o);
+              }
+              tmem_st_wait();
             }
-            tmem_st_wait();
+            if (renew) m = top;
+            named_sync(bar_pair, 64);                      // row_x has been read
           }
-          if (renew) m = top;
           const float ref = m == kNegInf ? 0.f : m * scale;
           const uint64_t scale2 = pair(scale, scale), ref2 = pair(-ref, -ref);
           uint64_t sum2[2] = {};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t packed[16];
+          for (int i = 0; i < 2; ++i) {
+            uint32_t s[32], packed[16];
+            load(i, s);
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float2 x = unpair(fma2(pair(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])), scale2, ref2));
+              const float2 x = unpair(fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, ref2));
               const float a = exp2_fast(x.x), b = exp2_fast(x.y);
-              sum2[i & 1] = add2(sum2[i & 1], pair(a, b));
+              sum2[i] = add2(sum2[i], pair(a, b));
               packed[e >> 1] = Type<T>::pack(a, b);
             }
-            tmem_st16(s_tmem + 16 * i, packed);
-            if (i & 1) {                                   // 64 keys of P are complete
-              tmem_st_wait();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&ctl.p_full[half][i >> 1]);
-            }
+            tmem_st16(s_tmem + 32 * i, packed);
           }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0 && ok) mbar_arrive(&ctl.p_full[half]);
           const float2 sa = unpair(sum2[0]), sb = unpair(sum2[1]);
           l += (sa.x + sa.y) + (sb.x + sb.y);
         }
-        if (q_next && ok) send_q();
-        if (ok && wait(&ctl.o_done[half], o_phase)) {
-          tc_fence_after();
-          o_phase ^= 1;
-          if ((warp & 3) == 0 && lane == 0)
-            mbar_arrive(&ctl.v_empty[(unit_count + (u1 - u0) - 1) % S::kVStages]);
-        }
+        if (q_next) send_q();
+        ctl.row_x[part][my_row] = l;
+        named_sync(bar_pair, 64);
+        l += ctl.row_x[part ^ 1][my_row];
+      }
+      // The line's next item but one, for all warps of the half (after the barrier below).
+      if (of_half == 0 && lane == 0) {
+        Walk after = nx;
+        if (after.at < ctl.share.end) after.next_item(p);
+        ctl.items[half][(item + 2) % 3] = after;
+      }
+      if (mine && keys) {
+        wait(&ctl.o_done[half], o_phase);
+        tc_fence_after();
+        o_phase ^= 1;
+        if (of_half == 1 && lane == 0 && ok)
+          mbar_arrive(&ctl.v_empty[(unit_count + (u1 - u0) - 1) % S::kVStages]);
       }
       if (keys) unit_count += u1 - u0;
       q_sent = q_next;
@@ -552,54 +599,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool split = u0 != 0 || u1 != w.units;
       const bool none = l == 0.f;                          // (a NaN score leaves l NaN)
       const float inv = none ? 0.f : 1.f / l;
-      const float lse2 = none ? kNegInf : (m == kNegInf ? 0.f : m * scale) + log2f(l);
       const bool real = mine && my_row < rows;
       const int g = w.row0() + min(my_row, rows - 1), t = p.group_div.div(g);
       const long long tok = w.s.q0 + t;
       const int head = w.h * p.group + g - t * p.group;
       const int slot = 2 * static_cast<int>(blockIdx.x) + (u0 == 0 ? 1 : 0);
       if (mine) {
-        float* part = p.part_o + (static_cast<long long>(slot) * kRows + my_row) * kDim;
-        T* dst = static_cast<T*>(p.out) + tok * p.o_ts + head * p.o_hs;
+        float* to_part = p.part_o + (static_cast<long long>(slot) * kRows + my_row) * kDim + kDim / 2 * part;
+        T* to_out = static_cast<T*>(p.out) + tok * p.o_ts + head * p.o_hs + kDim / 2 * part;
 #pragma unroll 1
-        for (int c = 0; c < kDim; c += 64) {
-          uint32_t o[2][32];
+        for (int c = 0; c < kDim / 2; c += 32) {
+          uint32_t o[32];
           if (keys) {
-            tmem_ld32(o_tmem + c, o[0]);
-            tmem_ld32(o_tmem + c + 32, o[1]);
+            tmem_ld32(o_tmem + c, o);
             tmem_ld_wait();
           }
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[i][e] = __float_as_uint(none ? 0.f : __uint_as_float(o[i][e]) * inv);
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(none ? 0.f : __uint_as_float(o[e]) * inv);
           if (real && split) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                const uint32_t v[8] = {o[i][e], o[i][e + 1], o[i][e + 2], o[i][e + 3],
-                                       o[i][e + 4], o[i][e + 5], o[i][e + 6], o[i][e + 7]};
-                store32(part + c + 32 * i + e, v, true);
-              }
+            for (int e = 0; e < 32; e += 8) {
+              const uint32_t v[8] = {o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5], o[e + 6], o[e + 7]};
+              store32(to_part + c + e, v, true);
+            }
           } else if (real) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int e = 0; e < 32; e += 16) {
+              const int at = kDim / 2 * part + c + e;
+              uint32_t v[8];
 #pragma unroll
-              for (int e = 0; e < 32; e += 16) {
-                const int at = c + 32 * i + e;
-                uint32_t v[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  v[k] = Type<T>::pack(__uint_as_float(o[i][e + 2 * k]), __uint_as_float(o[i][e + 2 * k + 1]));
-                if (at + 16 <= p.dim) store32(dst + at, v, cp.out32);
-                else if (at < p.dim) *reinterpret_cast<uint4*>(dst + at) = make_uint4(v[0], v[1], v[2], v[3]);
-              }
+              for (int k = 0; k < 8; ++k)
+                v[k] = Type<T>::pack(__uint_as_float(o[e + 2 * k]), __uint_as_float(o[e + 2 * k + 1]));
+              if (at + 16 <= p.dim) store32(to_out + c + e, v, cp.out32);
+              else if (at < p.dim) *reinterpret_cast<uint4*>(to_out + c + e) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
           }
           __syncwarp();
         }
         tc_fence_before();
-        if (real) {
+        if (real && part == 0) {
+          const float lse2 = none ? kNegInf : (m == kNegInf ? 0.f : m * scale) + log2f(l);
           if (split) p.part_l[slot * kRows + my_row] = lse2;
           else if (p.lse) p.lse[tok * p.heads + head] = lse2 * kLn2;
         }
@@ -607,19 +646,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (split) {
         // All softmax threads come here for every split item, also when a wait gave up.
         const int c0 = ctl.share.owner(w.at - u0), c1 = ctl.share.owner(w.at - u0 + w.units - 1);
-        named_sync(1, kSoftmaxThreads);
+        named_sync(kBarAll, kSoftmaxThreads);
         if (threadIdx.x == 0) {
           __threadfence();                                 // covers what the others wrote before the barrier
           const unsigned seen = atomicAdd(p.counters + c0, 1u);
           ctl.last_one = seen == static_cast<unsigned>(c1 - c0);
           if (ctl.last_one) p.counters[c0] = 0;
         }
-        named_sync(1, kSoftmaxThreads);
+        named_sync(kBarAll, kSoftmaxThreads);
         if (ctl.last_one) {
           __threadfence();
           // Each row's log-sum over all parts (one thread a row); a part then
           // weighs exp2(its own - that).
-          if (my_row < rows) {
+          if (part == 0 && my_row < rows) {
             float top = kNegInf, sum = 0.f;
 #pragma unroll 4
             for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(p.part_l + (2 * c + (c == c0)) * kRows + my_row));
@@ -627,9 +666,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 4
             for (int c = c0; c <= c1; ++c)
               sum += exp2_fast(__ldcg(p.part_l + (2 * c + (c == c0)) * kRows + my_row) - ref);
-            ctl.row_lse[my_row] = sum == 0.f ? kNegInf : ref + log2f(sum);
+            ctl.row_x[0][my_row] = sum == 0.f ? kNegInf : ref + log2f(sum);
           }
-          named_sync(1, kSoftmaxThreads);
+          named_sync(kBarAll, kSoftmaxThreads);
           // Eight columns a thread, so that a part's row is read and the output's
           // written in whole sectors; kBatch rows at once for loads in flight.
           constexpr int kLanes = kDim / 8, kRowStep = kSoftmaxThreads / kLanes, kBatch = 4;
@@ -637,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int r0 = threadIdx.x / kLanes; r0 < rows; r0 += kBatch * kRowStep) {
             float acc[kBatch][8] = {}, lse2r[kBatch];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) lse2r[k] = r0 + k * kRowStep < rows ? ctl.row_lse[r0 + k * kRowStep] : kNegInf;
+            for (int k = 0; k < kBatch; ++k) lse2r[k] = r0 + k * kRowStep < rows ? ctl.row_x[0][r0 + k * kRowStep] : kNegInf;
             for (int c = c0; c <= c1; ++c) {
               const long long from = (2 * c + (c == c0)) * kRows + r0;
 #pragma unroll
@@ -667,16 +706,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        named_sync(1, kSoftmaxThreads);                    // ctl.last_one has been read
+        named_sync(kBarAll, kSoftmaxThreads);                    // ctl.last_one has been read
       }
       if (u1 < w.units) break;
-      if (looked_ahead) {
-        __syncwarp();
-        if (lane == 0) w = nx;
-        __syncwarp();
-      } else {
-        next_item(w);
-      }
+      named_sync(kBarHalf + half, 32 * 8);                 // all are done with this item, and the next but one is known
     }
   }
   tc_fence_before();
