@@ -49,14 +49,13 @@ __device__ unsigned g_chunk_err;
 constexpr int kRows = 256;
 constexpr int kHalf = 128;
 constexpr int kKeys = 128;
-constexpr int kSoftmaxWarps = 16, kSoftmaxThreads = 32 * kSoftmaxWarps;
-constexpr int kMmaWarp = 16, kLoadWarp = 18;   // and the one after each
-constexpr int kThreads = 640;
-// Registers a thread: 640 threads start with 96; 512 x 104 + 128 x 64 is the same total.
-constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
-// Named barriers (0 is __syncthreads): all softmax warps; those of a half; the
-// two warps that share 32 rows.
-constexpr int kBarAll = 1, kBarHalf = 2, kBarPair = 4;
+constexpr int kSoftmaxWarps = 8, kSoftmaxThreads = 32 * kSoftmaxWarps;
+constexpr int kMmaWarp = 8, kLoadWarp = 10;   // and the one after each
+constexpr int kThreads = 384;
+// Registers a thread: 384 threads start with 168; 256 x 224 + 128 x 56 is the same total.
+constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
+// Named barriers (0 is __syncthreads): all softmax warps; those of a half.
+constexpr int kBarAll = 1, kBarHalf = 2;
 constexpr int kMinUnits = 4;
 constexpr float kLazy = 8.f;            // growth of the maximum (log2) that renews the reference
 using Walk = PagedWalk<kRows, kKeys>;
@@ -72,13 +71,13 @@ template <int kDim> struct Shape {
 
 // What the warps share besides the tiles.
 template <int kDim> struct Control {
-  uint64_t q_full[2], s_full[2], p_full[2], o_done[2], turn[2];
+  uint64_t q_full[2], s_full[2], p_full[2][2], o_done[2], start;
   uint64_t k_full[Shape<kDim>::kKStages], k_empty[Shape<kDim>::kKStages];
   uint64_t v_full[Shape<kDim>::kVStages], v_empty[Shape<kDim>::kVStages], mma_done[2];
   Walk walks[4];                     // places in the line of the MMA and load warps
   Walk items[2][3];                  // of each half's softmax: this item, the next and the one after
   PagedShare share;
-  float row_x[2][kRows];             // what the two threads of a row tell each other
+  float row_lse[kRows];
   uint32_t tmem_base;
   int abort_flag, last_one;
 };
@@ -127,17 +126,6 @@ __device__ __forceinline__ int volatile_lane() {
   int l;
   asm volatile("mov.u32 %0, %%laneid;" : "=r"(l));
   return l;
-}
-// Named barrier that ORs a flag over its `count` threads.
-__device__ __forceinline__ bool named_or(int id, int count, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.or.pred p, %2, %3, q;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(count)
-      : "memory");
-  return r != 0;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -215,11 +203,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = &ctl.abort_flag;
   if (threadIdx.x == 0) {
     for (int h = 0; h < 2; ++h) {
-      mbar_init(&ctl.q_full[h], 8);
+      mbar_init(&ctl.q_full[h], 4);
       mbar_init(&ctl.s_full[h], 1);
-      mbar_init(&ctl.p_full[h], 8);
+      mbar_init(&ctl.p_full[h][0], 5);         // four softmax warps, and the other half's issuing warp
+      mbar_init(&ctl.p_full[h][1], 4);
       mbar_init(&ctl.o_done[h], 1);
-      mbar_init(&ctl.turn[h], 1);
       mbar_init(&ctl.mma_done[h], 1);
     }
     for (int i = 0; i < S::kKStages; ++i) {
@@ -230,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl.v_full[i], 1);
       mbar_init(&ctl.v_empty[i], 2);
     }
+    mbar_init(&ctl.start, 1);
     ctl.abort_flag = 0;
     fence_mbar_init();
   }
@@ -319,28 +308,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dq = sdesc_sw128(smem_u32(q_smem + half * S::kTile), 16, 1024);
     const uint64_t dk0 = sdesc_sw128(smem_u32(k_ring), 16, 1024);
     const uint64_t dv0 = sdesc_sw128(smem_u32(v_ring), S::kBoxBytes, 1024);
-    uint32_t q_phase = 0, p_phase = 0, turn_phase = half == 0 ? 1 : 0;   // (half 0's first turn is free)
-    // QK of unit n; the turn is passed on while its last products are still queued
-    auto qk = [&](uint32_t n, bool both) {
+    uint32_t q_phase = 0, p_phase = 0, start_phase = 0;
+    // Two halves take strict turns at the tensor cores. Left to themselves they fall
+    // into step, and then both wait for products and compute softmaxes at the same
+    // time. A turn is one more arrival on the barrier of P, given by the other half's
+    // warp once its batch (PV, then QK) is nearly issued; a half alone gives its own.
+    auto grant = [&](int h) { mbar_arrive(&ctl.p_full[h][0]); };
+    auto qk = [&](uint32_t n, int grant_to) {
       if (lane == 0) {
         const uint64_t dk = dk0 + (n % S::kKStages) * (S::kTile >> 4);
 #pragma unroll
         for (int ks = 0; ks < kDim / 16; ++ks) {
-          if (ks == kDim / 16 - 4 && both) mbar_arrive(&ctl.turn[half ^ 1]);
+          if (ks == kDim / 16 - 4 && grant_to >= 0) grant(grant_to);
           const uint32_t off = ((ks >> 2) * S::kBoxBytes + (ks & 3) * 32) >> 4;
           umma_ss(s_tmem, dq + off, dk + off, kQk, ks != 0);
         }
         umma_commit(&ctl.s_full[half]);
       }
-    };
-    // Two halves take strict turns at the tensor cores. Left to themselves they fall
-    // into step, and then both wait for products and compute softmaxes at the same time.
-    auto take_turn = [&](bool both) {
-      if (both) {
-        wait(&ctl.turn[half], turn_phase);
-        turn_phase ^= 1;
-      }
-      return ok;
     };
     while (ok && w.at < ctl.share.end) {
       const Span span(p, w.s, w.row0(), w.row1(p));
@@ -352,9 +336,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(&ctl.k_full[n % S::kKStages], (n / S::kKStages) & 1)) break;
         if (!wait(&ctl.q_full[half], q_phase)) break;
         q_phase ^= 1;
-        if (!take_turn(both)) break;
+        // Half 1 begins after half 0 has begun the same item: it must not grant turns of an earlier one.
+        if (half == 1) {
+          if (!wait(&ctl.start, start_phase)) break;
+          start_phase ^= 1;
+        }
         tc_fence_after();
-        qk(n, both);
+        qk(n, half == 1 || !both ? 0 : -1);
+        if (half == 0 && both && lane == 0) mbar_arrive(&ctl.start);
         for (int u = u0; u < u1; ++u, ++n) {
           const bool more = u + 1 < u1;
           if (!wait(&ctl.v_full[n % S::kVStages], (n / S::kVStages) & 1)) break;
@@ -371,21 +360,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
           if (more && !wait(&ctl.k_full[(n + 1) % S::kKStages], ((n + 1) / S::kKStages) & 1)) break;
-          if (!wait(&ctl.p_full[half], p_phase)) break;
-          p_phase ^= 1;
-          if (!take_turn(both)) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint64_t dv = dv0 + (n % S::kVStages) * (S::kTile >> 4);
+          const uint64_t dv = dv0 + (n % S::kVStages) * (S::kTile >> 4);
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)      // P: 32 keys in the first 16 of every 32 columns of S
-              umma_ts(o_tmem, s_tmem + 32 * (ks >> 1) + 8 * (ks & 1), dv + ks * 128, kPv, u != u0 || ks != 0);
-            if (!more) {
-              if (both) mbar_arrive(&ctl.turn[half ^ 1]);
-              umma_commit(&ctl.o_done[half]);
+          for (int part = 0; part < 2; ++part) {
+            if (!wait(&ctl.p_full[half][part], p_phase)) break;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+              for (int ks = 4 * part; ks < 4 * part + 4; ++ks)
+                umma_ts(o_tmem, s_tmem + 8 * ks, dv + ks * 128, kPv, u != u0 || ks != 0);
             }
           }
-          if (more) qk(n + 1, both);
+          if (!ok) break;
+          p_phase ^= 1;
+          if (more) {
+            qk(n + 1, both ? half ^ 1 : 0);
+          } else if (lane == 0) {
+            if (both && half == 0) grant(1);
+            umma_commit(&ctl.o_done[half]);
+          }
         }
         if (!ok) break;
       } else if (span.hi > 0) {
@@ -413,20 +406,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     more_registers<kSoftmaxRegs>();
     // --------------------------------------------------------------- softmax
-    const int half = warp >> 3, part = (warp >> 2) & 1, of_half = warp & 7;
-    const int my_row = kHalf * half + 32 * (warp & 3) + lane;      // of the item's 256
-    const int bar_pair = kBarPair + 4 * half + (warp & 3);
-    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    // this thread's 64 columns of S (weights of 32 keys go over the first half of their scores) and half of O's
-    const uint32_t s_tmem = tmem + lanes + S::kS + 128 * half + 64 * part;
-    const uint32_t o_tmem = tmem + lanes + S::kO + kDim * half + kDim / 2 * part;
+    const int half = warp >> 2, of_half = warp & 3;
+    const int my_row = 32 * warp + lane;                   // of the item's 256
+    const uint32_t lanes = static_cast<uint32_t>(32 * of_half) << 16;
+    const uint32_t s_tmem = tmem + lanes + S::kS + 128 * half, o_tmem = tmem + lanes + S::kO + kDim * half;
     // The scale is applied after the mask (-inf) and the maximum, so it has to be
     // positive: a negative one turns Q's signs, a zero makes Q zero.
     const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
     uint32_t tile_phase = 0, o_phase = 0;
     bool q_sent = false;                                   // this item's Q is already on its way
 
-    // Q rows, 16 a warp: global -> 128B-swizzled shared memory, asynchronously; rows past the item's are zero.
+    // Q rows of this warp: global -> 128B-swizzled shared memory, asynchronously; rows past the item's are zero.
     // (Their lane comes from a volatile read, which keeps their addresses out of the registers of the loop below.)
     constexpr int kChunks = kDim / 8;
     auto q_at = [&](int rl, int q_chunk) {
@@ -437,8 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r0 = it.row0(), rows = it.row1(p) - r0;
       const T* base = static_cast<const T*>(p.q) + it.s.q0 * p.q_ts + it.h * p.group * p.q_hs + q_chunk * 8;
 #pragma unroll 2
-      for (int i = 0; i < 16; i += 32 / kChunks) {
-        const int rl = 16 * of_half + i + ln / kChunks, r = kHalf * half + rl;
+      for (int i = 0; i < 32; i += 32 / kChunks) {
+        const int rl = 32 * of_half + i + ln / kChunks, r = kHalf * half + rl;
         const bool real = r < rows && q_chunk * 8 < p.dim && p.scale_log2 != 0.f;
         const int t = p.group_div.div(r0 + min(r, rows - 1)), g = r0 + min(r, rows - 1) - t * p.group;
         cp_async16(q_at(rl, q_chunk), real ? base + t * p.q_ts + g * p.q_hs : static_cast<const T*>(p.q), real ? 16 : 0);
@@ -448,8 +438,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("cp.async.wait_all;" ::: "memory");
       if (p.scale_log2 < 0.f) {                            // every lane turns the signs of what it fetched
         const int ln = volatile_lane();
-        for (int i = 0; i < 16; i += 32 / kChunks) {
-          uint4* v = reinterpret_cast<uint4*>(q_at(16 * of_half + i + ln / kChunks, ln % kChunks));
+        for (int i = 0; i < 32; i += 32 / kChunks) {
+          uint4* v = reinterpret_cast<uint4*>(q_at(32 * of_half + i + ln / kChunks, ln % kChunks));
           v->x ^= 0x80008000u, v->y ^= 0x80008000u, v->z ^= 0x80008000u, v->w ^= 0x80008000u;
         }
       }
@@ -500,45 +490,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                      Span(p, nx.s, nx.row0(), nx.row1(p)).hi > 0;
             if (q_next) fetch_q(nx);
           }
-          // Scores are read 32 at a time, for the maximum and again for the weights:
-          // a row of 64 kept in registers made them spill.
-          const bool plain = u >= plain0 && u < plain1;
-          auto load = [&](int i, uint32_t (&s)[32]) {
-            tmem_ld32(s_tmem + 32 * i, s);
-            tmem_ld_wait();
-            if (!plain) {
-              const PagedRow vis(p, w.s, min(w.row0() + my_row, w.row1(p) - 1));
-              const int at = span.key0(u) + 64 * part + 32 * i;
+          uint32_t s[4][32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(s_tmem + 32 * i, s[i]);
+          tmem_ld_wait();
+          if (u < plain0 || u >= plain1) {
+            const PagedRow vis(p, w.s, min(w.row0() + my_row, w.row1(p) - 1));
+            const int k0 = span.key0(u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
               // bits of the visible ones of these 32 keys
+              const int at = k0 + 32 * i;
               auto below = [&](int x) { return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1; };
               const uint32_t seen = below(vis.hi - at) & (~below(vis.lo - at) | below(p.sinks - at));
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (!(seen >> e & 1)) s[e] = __float_as_uint(kNegInf);
+                if (!(seen >> e & 1)) s[i][e] = __float_as_uint(kNegInf);
             }
-          };
-          float top4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t s[32];
-            load(i, s);
-#pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              top4[(e >> 1) & 3] = max3(top4[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
           }
-          float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+          float top8[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top8[i] = fmaxf(__uint_as_float(s[0][2 * i]), __uint_as_float(s[0][2 * i + 1]));
+#pragma unroll
+          for (int i = 8; i < 64; ++i)
+            top8[i & 7] = max3(top8[i & 7], __uint_as_float(s[i >> 4][2 * i & 31]), __uint_as_float(s[i >> 4][(2 * i & 31) + 1]));
+          const float top = fmaxf(max3(top8[0], top8[1], top8[2]), max3(max3(top8[3], top8[4], top8[5]), top8[6], top8[7]));
           // (the first finite maximum after none needs no rescaling: O and l are zero)
-          auto grows = [&] { return top > m && (m == kNegInf || (top - m) * scale > kLazy); };
-          if (named_or(bar_pair, 64, grows())) {           // one of the 64 threads asks for a new reference
-            ctl.row_x[part][my_row] = top;
-            named_sync(bar_pair, 64);
-            top = fmaxf(top, ctl.row_x[part ^ 1][my_row]);
-            const bool renew = grows();
+          const bool renew = top > m && (m == kNegInf || (top - m) * scale > kLazy);
+          if (__any_sync(0xFFFFFFFFu, renew)) {
             if (__any_sync(0xFFFFFFFFu, renew && m != kNegInf)) {
               const float f = renew ? exp2_fast((m - top) * scale) : 1.f;
               l *= f;
 #pragma unroll 1
-              for (int c = 0; c < kDim / 2; c += 8) {
+              for (int c = 0; c < kDim; c += 8) {
                 uint32_t o[8];
                 tmem_ld8(o_tmem + c, o);
                 tmem_ld_wait();
@@ -549,35 +533,32 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st_wait();
             }
             if (renew) m = top;
-            named_sync(bar_pair, 64);                      // row_x has been read
           }
           const float ref = m == kNegInf ? 0.f : m * scale;
           const uint64_t scale2 = pair(scale, scale), ref2 = pair(-ref, -ref);
           uint64_t sum2[2] = {};
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t s[32], packed[16];
-            load(i, s);
+          for (int i = 0; i < 4; ++i) {
+            uint32_t packed[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float2 x = unpair(fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, ref2));
+              const float2 x = unpair(fma2(pair(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])), scale2, ref2));
               const float a = exp2_fast(x.x), b = exp2_fast(x.y);
-              sum2[i] = add2(sum2[i], pair(a, b));
+              sum2[i & 1] = add2(sum2[i & 1], pair(a, b));
               packed[e >> 1] = Type<T>::pack(a, b);
             }
-            tmem_st16(s_tmem + 32 * i, packed);
+            tmem_st16(s_tmem + 16 * i, packed);
+            if (i & 1) {                                   // 64 keys of P are complete
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0 && ok) mbar_arrive(&ctl.p_full[half][i >> 1]);
+            }
           }
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0 && ok) mbar_arrive(&ctl.p_full[half]);
           const float2 sa = unpair(sum2[0]), sb = unpair(sum2[1]);
           l += (sa.x + sa.y) + (sb.x + sb.y);
         }
         if (q_next) send_q();
-        ctl.row_x[part][my_row] = l;
-        named_sync(bar_pair, 64);
-        l += ctl.row_x[part ^ 1][my_row];
       }
       // The line's next item but one, for all warps of the half (after the barrier below).
       if (of_half == 0 && lane == 0) {
@@ -605,10 +586,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int head = w.h * p.group + g - t * p.group;
       const int slot = 2 * static_cast<int>(blockIdx.x) + (u0 == 0 ? 1 : 0);
       if (mine) {
-        float* to_part = p.part_o + (static_cast<long long>(slot) * kRows + my_row) * kDim + kDim / 2 * part;
-        T* to_out = static_cast<T*>(p.out) + tok * p.o_ts + head * p.o_hs + kDim / 2 * part;
+        float* to_part = p.part_o + (static_cast<long long>(slot) * kRows + my_row) * kDim;
+        T* to_out = static_cast<T*>(p.out) + tok * p.o_ts + head * p.o_hs;
 #pragma unroll 1
-        for (int c = 0; c < kDim / 2; c += 32) {
+        for (int c = 0; c < kDim; c += 32) {
           uint32_t o[32];
           if (keys) {
             tmem_ld32(o_tmem + c, o);
@@ -625,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else if (real) {
 #pragma unroll
             for (int e = 0; e < 32; e += 16) {
-              const int at = kDim / 2 * part + c + e;
+              const int at = c + e;
               uint32_t v[8];
 #pragma unroll
               for (int k = 0; k < 8; ++k)
@@ -637,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         tc_fence_before();
-        if (real && part == 0) {
+        if (real) {
           const float lse2 = none ? kNegInf : (m == kNegInf ? 0.f : m * scale) + log2f(l);
           if (split) p.part_l[slot * kRows + my_row] = lse2;
           else if (p.lse) p.lse[tok * p.heads + head] = lse2 * kLn2;
@@ -658,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __threadfence();
           // Each row's log-sum over all parts (one thread a row); a part then
           // weighs exp2(its own - that).
-          if (part == 0 && my_row < rows) {
+          if (my_row < rows) {
             float top = kNegInf, sum = 0.f;
 #pragma unroll 4
             for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(p.part_l + (2 * c + (c == c0)) * kRows + my_row));
@@ -666,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 4
             for (int c = c0; c <= c1; ++c)
               sum += exp2_fast(__ldcg(p.part_l + (2 * c + (c == c0)) * kRows + my_row) - ref);
-            ctl.row_x[0][my_row] = sum == 0.f ? kNegInf : ref + log2f(sum);
+            ctl.row_lse[my_row] = sum == 0.f ? kNegInf : ref + log2f(sum);
           }
           named_sync(kBarAll, kSoftmaxThreads);
           // Eight columns a thread, so that a part's row is read and the output's
@@ -676,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int r0 = threadIdx.x / kLanes; r0 < rows; r0 += kBatch * kRowStep) {
             float acc[kBatch][8] = {}, lse2r[kBatch];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) lse2r[k] = r0 + k * kRowStep < rows ? ctl.row_x[0][r0 + k * kRowStep] : kNegInf;
+            for (int k = 0; k < kBatch; ++k) lse2r[k] = r0 + k * kRowStep < rows ? ctl.row_lse[r0 + k * kRowStep] : kNegInf;
             for (int c = c0; c <= c1; ++c) {
               const long long from = (2 * c + (c == c0)) * kRows + r0;
 #pragma unroll
@@ -709,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_sync(kBarAll, kSoftmaxThreads);                    // ctl.last_one has been read
       }
       if (u1 < w.units) break;
-      named_sync(kBarHalf + half, 32 * 8);                 // all are done with this item, and the next but one is known
+      named_sync(kBarHalf + half, 128);                 // all are done with this item, and the next but one is known
     }
   }
   tc_fence_before();
