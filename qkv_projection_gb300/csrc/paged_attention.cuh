@@ -44,22 +44,30 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
 }
 
 // Keys that the rows [r0, r1) of a sequence see: [0, first) and [lo, hi), and
-// the key tiles that hold them.
+// the key tiles that hold them. The units go through the run's tiles, the one at
+// the window's edge last (its keys are hidden from some rows, and a poor maximum to
+// begin with would have to be renewed), and then through those of the prefix.
 template <int kKeys>
 struct PagedSpan {
   int lo, hi, first;
-  int sink_tiles, lo_tile, units;   // units: at least 1, so that every item is visited
+  int lo_tile, run;    // the run's first tile, and its tiles
+  int units;           // at least 1, so that every item is visited
   __device__ __forceinline__ PagedSpan(const PagedParams& p, const PagedSeq& s, int r0, int r1) {
     const int t0 = p.group_div.div(r0), t1 = p.group_div.div(r1 - 1);
     hi = p.causal ? min(max(s.kv - s.n + t1 + 1, 0), s.kv) : s.kv;
     lo = p.window > 0 ? min(max(s.kv - s.n + t0 - p.window + 1, 0), hi) : 0;
     first = min(p.sinks, lo);
     lo_tile = lo / kKeys;
-    sink_tiles = min((first + kKeys - 1) / kKeys, lo_tile);
-    units = max(1, sink_tiles + (hi + kKeys - 1) / kKeys - lo_tile);
+    run = (hi + kKeys - 1) / kKeys - lo_tile;
+    units = max(1, run + min((first + kKeys - 1) / kKeys, lo_tile));
   }
   __device__ __forceinline__ int key0(int unit) const {
-    return (unit < sink_tiles ? unit : unit - sink_tiles + lo_tile) * kKeys;
+    int tile = unit + lo_tile;
+    if (lo > 0) {
+      if (unit >= run) tile = unit - run;
+      else tile = unit + 1 < run ? tile + 1 : lo_tile;
+    }
+    return tile * kKeys;
   }
 };
 

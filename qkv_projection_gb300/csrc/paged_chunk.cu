@@ -69,13 +69,35 @@ template <int kDim> struct Shape {
   static constexpr uint32_t kS = 0, kO = 256;                   // TMEM columns: S at 0 and 128, O at 256 and 256 + kDim
 };
 
+// A place in the line and what one half's softmax needs of it, worked out ahead.
+struct Item : Walk {
+  int plain0, plain1;    // units that every row of the half sees whole (tiles of sinks are left to the mask)
+  bool mine, keys;       // the half has rows; they see something
+  __device__ __forceinline__ void look(const PagedParams& p, int half) {
+    if (b >= p.batch) {
+      mine = keys = false;
+      return;
+    }
+    const Span span(p, s, row0(), row1(p));
+    const int rows = row1(p) - row0();
+    mine = rows > kHalf * half;
+    keys = span.hi > 0;
+    const int h0 = row0() + kHalf * half, h1 = min(h0 + kHalf, row0() + rows) - 1;
+    const int all_hi = PagedRow(p, s, h0).hi, all_lo = PagedRow(p, s, h1).lo;
+    // tiles [t0, t1) are seen whole; in units, the run's first tile comes last
+    const int t0 = (all_lo + kKeys - 1) / kKeys - span.lo_tile, t1 = min(all_hi / kKeys - span.lo_tile, span.run);
+    plain0 = span.lo > 0 ? max(t0, 1) - 1 : t0;
+    plain1 = span.lo > 0 ? t1 - 1 : t1;
+  }
+};
+
 // What the warps share besides the tiles.
 template <int kDim> struct Control {
   uint64_t q_full[2], s_full[2], p_full[2][2], o_done[2], start;
   uint64_t k_full[Shape<kDim>::kKStages], k_empty[Shape<kDim>::kKStages];
   uint64_t v_full[Shape<kDim>::kVStages], v_empty[Shape<kDim>::kVStages], mma_done[2];
   Walk walks[4];                     // places in the line of the MMA and load warps
-  Walk items[2][3];                  // of each half's softmax: this item, the next and the one after
+  Item items[2][3];                  // of each half's softmax: this item, the next and the one after
   PagedShare share;
   float row_lse[kRows];
   uint32_t tmem_base;
@@ -192,10 +214,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) ctl.share = sh;
     if (threadIdx.x > 0 && threadIdx.x < 4) ctl.walks[threadIdx.x] = ctl.walks[0];
     if (threadIdx.x >= 4 && threadIdx.x < 6) {
-      Walk first = ctl.walks[0];
-      ctl.items[threadIdx.x - 4][0] = first;
-      first.next_item(p);
-      ctl.items[threadIdx.x - 4][1] = first;
+      const int half = threadIdx.x - 4;
+      Item item;
+      static_cast<Walk&>(item) = ctl.walks[0];
+      item.look(p, half);
+      ctl.items[half][0] = item;
+      item.next_item(p);
+      item.look(p, half);
+      ctl.items[half][1] = item;
     }
   }
 
@@ -451,15 +477,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Named barriers keep the warps together, so a warp whose wait gave up (ok is
     // false) goes through all of them too; it only no longer waits or arrives.
     for (uint32_t item = 0;; ++item) {
-      const Walk& w = ctl.items[half][item % 3];
-      const Walk& nx = ctl.items[half][(item + 1) % 3];
+      const Item& w = ctl.items[half][item % 3];
+      const Item& nx = ctl.items[half][(item + 1) % 3];
       if (w.at >= ctl.share.end) break;
       const Span span(p, w.s, w.row0(), w.row1(p));
       const int u0 = w.unit;
       const int u1 = static_cast<int>(min(static_cast<long long>(w.units), u0 + (ctl.share.end - w.at)));
       const int rows = w.row1(p) - w.row0();
-      const bool mine = rows > kHalf * half;               // this half has rows
-      const bool keys = span.hi > 0;
+      const bool mine = w.mine, keys = w.keys;
       bool q_next = false;
       float m = kNegInf, l = 0.f;                          // the row's reference (in units of S), this thread's sum
       if (mine && keys) {
@@ -467,15 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fetch_q(w);
           send_q();
         }
-        // Units [plain0, plain1) are seen whole by every row of this half (tiles of
-        // sinks are left to the mask).
-        int plain0, plain1;
-        {
-          const int h0 = w.row0() + kHalf * half, h1 = min(h0 + kHalf, w.row0() + rows) - 1;
-          const int all_hi = PagedRow(p, w.s, h0).hi, all_lo = PagedRow(p, w.s, h1).lo;
-          plain1 = span.sink_tiles + max(all_hi / kKeys - span.lo_tile, 0);
-          plain0 = span.sink_tiles + (all_lo + kKeys - 1) / kKeys - span.lo_tile;
-        }
+        const int plain0 = w.plain0, plain1 = w.plain1;
 #pragma unroll 1
         for (int u = u0; u < u1; ++u) {
           wait(&ctl.s_full[half], tile_phase);
@@ -486,8 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (of_half == 1 && lane == 0 && ok && u > u0)
             mbar_arrive(&ctl.v_empty[(unit_count + (u - u0) - 1) % S::kVStages]);
           if (u + 1 == u1 && u1 == w.units) {              // Q has been read for the last time: fetch the next item's
-            q_next = nx.at < ctl.share.end && nx.row1(p) - nx.row0() > kHalf * half &&
-                     Span(p, nx.s, nx.row0(), nx.row1(p)).hi > 0;
+            q_next = nx.at < ctl.share.end && nx.mine && nx.keys;
             if (q_next) fetch_q(nx);
           }
           uint32_t s[4][32];
@@ -503,6 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int at = k0 + 32 * i;
               auto below = [&](int x) { return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1; };
               const uint32_t seen = below(vis.hi - at) & (~below(vis.lo - at) | below(p.sinks - at));
+              if (__all_sync(0xFFFFFFFFu, seen == 0xFFFFFFFFu)) continue;
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (!(seen >> e & 1)) s[i][e] = __float_as_uint(kNegInf);
@@ -522,13 +539,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float f = renew ? exp2_fast((m - top) * scale) : 1.f;
               l *= f;
 #pragma unroll 1
-              for (int c = 0; c < kDim; c += 8) {
-                uint32_t o[8];
-                tmem_ld8(o_tmem + c, o);
+              for (int c = 0; c < kDim; c += 16) {
+                uint32_t o0[8], o1[8];
+                tmem_ld8(o_tmem + c, o0);
+                tmem_ld8(o_tmem + c + 8, o1);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st8(o_tmem + c, o);
+                for (int e = 0; e < 8; ++e) {
+                  o0[e] = __float_as_uint(__uint_as_float(o0[e]) * f);
+                  o1[e] = __float_as_uint(__uint_as_float(o1[e]) * f);
+                }
+                tmem_st8(o_tmem + c, o0);
+                tmem_st8(o_tmem + c + 8, o1);
               }
               tmem_st_wait();
             }
@@ -562,8 +584,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // The line's next item but one, for all warps of the half (after the barrier below).
       if (of_half == 0 && lane == 0) {
-        Walk after = nx;
-        if (after.at < ctl.share.end) after.next_item(p);
+        Item after = nx;
+        if (after.at < ctl.share.end) {
+          after.next_item(p);
+          after.look(p, half);
+        }
         ctl.items[half][(item + 2) % 3] = after;
       }
       if (mine && keys) {

@@ -322,23 +322,27 @@ def dequantize_per_group(q, scale, group: int, out=None, stream=None):
 
 
 # ------------------------------------------- rotary positions, paged attention
-_F16_CODES = None
+# These run once per layer and step, on a few microseconds of GPU work when there
+# are few tokens, so their checks are written to be cheap: one expression for a
+# tensor that is as it should be (_fits), and _refuse to say what is wrong with
+# one that is not.
+_f16_codes = None
 
 
 def _f16_code(dtype, name):
-    global _F16_CODES
-    if _F16_CODES is None:
+    global _f16_codes
+    if _f16_codes is None:
         torch = _torch()
-        _F16_CODES = {torch.float16: KAIO_DTYPE_F16, torch.bfloat16: KAIO_DTYPE_BF16}
-    code = _F16_CODES.get(dtype)
+        _f16_codes = {torch.float16: KAIO_DTYPE_F16, torch.bfloat16: KAIO_DTYPE_BF16}
+    code = _f16_codes.get(dtype)
     if code is None:
         raise TypeError(f"{name} has dtype {dtype}, expected torch.float16 or torch.bfloat16")
     return code
 
 
-def _need_strided(t, name, dtype, shape):
-    """Checks a tensor that may have strides of its own (a dense last dimension);
-    None in ``shape`` takes any size. Returns its strides."""
+def _refuse(t, name, dtype, shape):
+    """Raises what is wrong with a tensor that may have strides of its own (a dense
+    last dimension); None in ``shape`` takes any size."""
     if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -348,30 +352,76 @@ def _need_strided(t, name, dtype, shape):
     got = t.shape
     if len(got) != len(shape):
         raise ValueError(f"{name} must be rank {len(shape)}, got shape {tuple(got)}")
-    if got != shape:
-        for g, want in zip(got, shape):
-            if want is not None and g != want:
-                raise ValueError(f"{name} has shape {tuple(got)}, expected {tuple(shape)}")
+    for g, want in zip(got, shape):
+        if want is not None and g != want:
+            raise ValueError(f"{name} has shape {tuple(got)}, expected {tuple(shape)}")
     if t.requires_grad:
         raise ValueError(f"{name} has gradient tracking enabled; these ops are forward-only: detach() it")
-    strides = t.stride()
-    if strides[-1] != 1 and got[-1] > 1:
-        raise ValueError(f"{name} must have a dense last dimension (strides {strides})")
-    return strides
+    raise ValueError(f"{name} must have a dense last dimension (strides {t.stride()})")
+
+
+def _strides(t, name, dtype, shape):
+    """Strides of a tensor of exactly this type and shape, on a GPU, without
+    gradient tracking and with a dense last dimension; anything else raises."""
+    try:
+        strides = t.stride()
+        if (t.dtype is dtype and t.shape == shape and t.is_cuda and not t.requires_grad
+                and (strides[-1] == 1 or shape[-1] <= 1)):
+            return strides
+    except (AttributeError, TypeError):
+        pass
+    _refuse(t, name, dtype, shape)
+
+
+def _size(t, name, dtype, rank, dim):
+    """One size of a tensor whose other sizes _strides checks afterwards."""
+    try:
+        return t.shape[dim]
+    except (AttributeError, IndexError, TypeError):
+        _refuse(t, name, dtype, (None,) * rank)
+
+
+def _rank3(x, name):
+    """(type code, dtype, shape) of an activation tensor [tokens, heads, columns]."""
+    try:
+        dtype, shape = x.dtype, x.shape
+        if len(shape) == 3:
+            return _f16_code(dtype, name), dtype, shape
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    raise ValueError(f"{name} must be rank 3, got shape {tuple(shape)}")
+
+
+def _raw_stream(t, stream) -> int:
+    """The stream to run on: the one given, or the current one of t's device."""
+    if stream is not None:
+        return int(stream.cuda_stream)
+    return _current_raw_stream(t.get_device())
+
+
+def _current_raw_stream(device: int) -> int:
+    global _current_raw_stream
+    torch = _torch()
+    # The same value as torch.cuda.current_stream().cuda_stream, without making a
+    # Stream object (3 of the 4 microseconds that a call may take on the host).
+    _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda d: int(torch.cuda.current_stream(d).cuda_stream))
+    return _current_raw_stream(device)
 
 
 def _rope_axes(positions, tokens, sections, pairs):
     """(axes, axis stride, sections padded to four) of a positions tensor [T] or [axes, T]."""
-    if isinstance(positions, _torch().Tensor) and positions.dim() == 1:
-        _need_strided(positions, "positions", _torch().int32, (tokens,))
+    int32 = _torch().int32
+    if getattr(positions, "ndim", None) == 1:
+        _strides(positions, "positions", int32, (tokens,))
         axes, stride = 1, 0
     else:
-        stride = _need_strided(positions, "positions", _torch().int32, (None, tokens))[0]
-        axes = positions.shape[0]
+        axes = _size(positions, "positions", int32, 2, 0)
+        stride = _strides(positions, "positions", int32, (axes, tokens))[0]
     if sections is None:
         if axes != 1:
             raise ValueError(f"positions has {axes} axes: sections has to say how many pairs each one turns")
-        sections = (pairs,)
+        return 1, stride, (pairs, 0, 0, 0)
     if len(sections) != axes or axes > 4:
         raise ValueError(f"sections {tuple(sections)} does not fit positions with {axes} axes (1 to 4)")
     return axes, stride, (*sections, 0, 0, 0)[:4]
@@ -389,19 +439,21 @@ def rope(x, positions, inv_freq, sections=None, interleaved: bool = False, inver
     result. out may be x itself.
     """
     torch = _torch()
-    code = _f16_code(x.dtype, "x")
-    xs = _need_strided(x, "x", x.dtype, (None, None, None))
-    t, h, d = x.shape
-    _need_strided(inv_freq, "inv_freq", torch.float32, (None,))
-    pairs = inv_freq.shape[0]
+    code, dtype, shape = _rank3(x, "x")
+    t, h, d = shape
+    xs = _strides(x, "x", dtype, shape)
+    pairs = _size(inv_freq, "inv_freq", torch.float32, 1, 0)
+    _strides(inv_freq, "inv_freq", torch.float32, (pairs,))
     axes, axis_stride, sec = _rope_axes(positions, t, sections, pairs)
     if out is None:
-        out = torch.empty((t, h, d), dtype=x.dtype, device=x.device)
-    os_ = _need_strided(out, "out", x.dtype, (t, h, d))
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+        os_ = (h * d, d)
+    else:
+        os_ = _strides(out, "out", dtype, shape)
     args = _ROPE_ARGS.pack(_ROPE_ARGS.size, code, t, h, 0, d, pairs, axes, *sec, interleaved, inverse, 0, 0,
                            x.data_ptr(), 0, 0, out.data_ptr(), 0, 0, positions.data_ptr(), inv_freq.data_ptr(), 0,
                            xs[0], xs[1], os_[0], os_[1], 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, axis_stride)
-    check(lib().kaio_rope(args, _stream_ptr(stream)))
+    check(lib().kaio_rope(args, _raw_stream(x, stream)))
     return out
 
 
@@ -416,29 +468,31 @@ def rope_append(q, k, v, positions, inv_freq, k_cache, v_cache, slots, sections=
     token, or -1 to store nothing. q_out may be q itself.
     """
     torch = _torch()
-    dtype = q.dtype
-    code = _f16_code(dtype, "q")
-    qs = _need_strided(q, "q", dtype, (None, None, None))
-    t, h, d = q.shape
-    ks = _need_strided(k, "k", dtype, (t, None, d))
-    kh = k.shape[1]
-    vs = _need_strided(v, "v", dtype, (t, kh, d))
-    kc = _need_strided(k_cache, "k_cache", dtype, (None, None, kh, d))
-    pages, page_size = k_cache.shape[:2]
-    vc = _need_strided(v_cache, "v_cache", dtype, (pages, page_size, kh, d))
-    _need_strided(inv_freq, "inv_freq", torch.float32, (None,))
-    _need_strided(slots, "slots", torch.int32, (t,))
-    pairs = inv_freq.shape[0]
+    code, dtype, shape = _rank3(q, "q")
+    t, h, d = shape
+    qs = _strides(q, "q", dtype, shape)
+    kh = _size(k, "k", dtype, 3, 1)
+    ks = _strides(k, "k", dtype, (t, kh, d))
+    vs = _strides(v, "v", dtype, (t, kh, d))
+    pages, page_size = _size(k_cache, "k_cache", dtype, 4, 0), _size(k_cache, "k_cache", dtype, 4, 1)
+    cache = (pages, page_size, kh, d)
+    kc = _strides(k_cache, "k_cache", dtype, cache)
+    vc = _strides(v_cache, "v_cache", dtype, cache)
+    pairs = _size(inv_freq, "inv_freq", torch.float32, 1, 0)
+    _strides(inv_freq, "inv_freq", torch.float32, (pairs,))
+    _strides(slots, "slots", torch.int32, (t,))
     axes, axis_stride, sec = _rope_axes(positions, t, sections, pairs)
     if q_out is None:
-        q_out = torch.empty((t, h, d), dtype=dtype, device=q.device)
-    os_ = _need_strided(q_out, "q_out", dtype, (t, h, d))
+        q_out = torch.empty(shape, dtype=dtype, device=q.device)
+        os_ = (h * d, d)
+    else:
+        os_ = _strides(q_out, "q_out", dtype, shape)
     args = _ROPE_ARGS.pack(_ROPE_ARGS.size, code, t, h, kh, d, pairs, axes, *sec, interleaved, 0, pages, page_size,
                            q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(),
                            v_cache.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), slots.data_ptr(),
                            qs[0], qs[1], os_[0], os_[1], ks[0], ks[1], vs[0], vs[1], kc[0], kc[1], kc[2],
                            vc[0], vc[1], vc[2], axis_stride)
-    check(lib().kaio_rope_append(args, _stream_ptr(stream)))
+    check(lib().kaio_rope_append(args, _raw_stream(q, stream)))
     return q_out
 
 
@@ -464,45 +518,55 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max
     v_cache [pages, page_size, KH, D], any strides with a dense last dimension,
     page_size a power of two from 16 to 1024, H a multiple of KH; page_table
     int32 [B, P]. max_new: at least the largest number of new tokens of one
-    sequence (default: T, or 1 without q_starts). scale defaults to D ** -0.5. causal: a token sees
-    positions up to its own; window: only the last `window` of them, and the
-    first `sinks` positions besides. A token that sees nothing gets zeros
-    and lse = -inf. workspace: from ``paged_attention_workspace``; without one
-    the call makes its own.
+    sequence (default: T, or 1 without q_starts). scale defaults to D ** -0.5.
+    causal: a token sees positions up to its own; window: only the last `window`
+    of them, and the first `sinks` positions besides. A token that sees nothing
+    gets zeros and lse = -inf. workspace: from ``paged_attention_workspace``;
+    without one the call makes its own.
     """
     torch = _torch()
-    dtype = q.dtype
-    code = _f16_code(dtype, "q")
-    qs = _need_strided(q, "q", dtype, (None, None, None))
-    t, h, d = q.shape
-    kc = _need_strided(k_cache, "k_cache", dtype, (None, None, None, d))
-    pages, page_size, kh = k_cache.shape[:3]
-    vc = _need_strided(v_cache, "v_cache", dtype, (pages, page_size, kh, d))
-    _need_strided(kv_lens, "kv_lens", torch.int32, (None,))
-    b = kv_lens.shape[0]
-    ts = _need_strided(page_table, "page_table", torch.int32, (b, None))
+    int32 = torch.int32
+    code, dtype, shape = _rank3(q, "q")
+    t, h, d = shape
+    qs = _strides(q, "q", dtype, shape)
+    cache = k_cache.shape if hasattr(k_cache, "shape") else ()
+    if len(cache) != 4:
+        _refuse(k_cache, "k_cache", dtype, (None, None, None, d))
+    pages, page_size, kh, _ = cache
+    kc = _strides(k_cache, "k_cache", dtype, (pages, page_size, kh, d))
+    vc = _strides(v_cache, "v_cache", dtype, cache)
+    b = _size(kv_lens, "kv_lens", int32, 1, 0)
+    _strides(kv_lens, "kv_lens", int32, (b,))
+    max_pages = _size(page_table, "page_table", int32, 2, 1)
+    ts = _strides(page_table, "page_table", int32, (b, max_pages))
     starts = 0
     if q_starts is not None:
-        _need_strided(q_starts, "q_starts", torch.int32, (b + 1,))
+        _strides(q_starts, "q_starts", int32, (b + 1,))
         starts = q_starts.data_ptr()
     if workspace is None:
         workspace = paged_attention_workspace(q.device)
-    elif not (workspace.is_cuda and workspace.dtype == torch.uint8 and workspace.is_contiguous()):
+    elif not (workspace.is_cuda and workspace.dtype is torch.uint8 and workspace.is_contiguous()):
         raise ValueError("workspace must be a dense uint8 CUDA tensor from paged_attention_workspace()")
     if out is None:
-        out = torch.empty((t, h, d), dtype=dtype, device=q.device)
-    os_ = _need_strided(out, "out", dtype, (t, h, d))
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+        os_ = (h * d, d)
+    else:
+        os_ = _strides(out, "out", dtype, shape)
+    lse_ptr = 0
     if lse is not None:
-        if _need_strided(lse, "lse", torch.float32, (t, h))[0] != h and t > 1:
+        if _strides(lse, "lse", torch.float32, (t, h))[0] != h and t > 1:
             raise ValueError("lse must be contiguous")
+        lse_ptr = lse.data_ptr()
     elif return_lse:
         lse = torch.empty((t, h), dtype=torch.float32, device=q.device)
-    args = _PAGED_ARGS.pack(_PAGED_ARGS.size, code, b, t, h, kh, d, page_size, pages, page_table.shape[1],
-                            max_new if max_new is not None else t if starts else 1, causal, window, sinks,
-                            d ** -0.5 if scale is None else scale, 0,
+        lse_ptr = lse.data_ptr()
+    if max_new is None:
+        max_new = t if starts else 1
+    args = _PAGED_ARGS.pack(_PAGED_ARGS.size, code, b, t, h, kh, d, page_size, pages, max_pages, max_new, causal,
+                            window, sinks, d ** -0.5 if scale is None else scale, 0,
                             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
-                            kv_lens.data_ptr(), starts, out.data_ptr(), 0 if lse is None else lse.data_ptr(),
-                            workspace.data_ptr(), workspace.numel(),
+                            kv_lens.data_ptr(), starts, out.data_ptr(), lse_ptr, workspace.data_ptr(),
+                            workspace.numel(),
                             qs[0], qs[1], os_[0], os_[1], kc[0], kc[1], kc[2], vc[0], vc[1], vc[2], ts[0])
-    check(lib().kaio_paged_attention(args, _stream_ptr(stream)))
+    check(lib().kaio_paged_attention(args, _raw_stream(q, stream)))
     return (out, lse) if return_lse else out
