@@ -376,12 +376,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           unsigned char* v = v_ring + (n % S::kVStages) * S::kTile;
           const int k0 = span.key0(u);
           if (k0 + kKeys > span.hi || (k0 < span.lo && k0 + kKeys > span.first)) {
-            // zero the rows of V that no row of the item sees (both halves' warps do, with the same values)
-            for (int i = lane; i < kKeys * S::kBoxes * 8; i += 32) {
-              const int j = k0 + ((i >> 3) & (kKeys - 1));
-              if (!(j < span.hi && (j >= span.lo || j < span.first)))
-                *reinterpret_cast<uint4*>(v + i * 16) = make_uint4(0, 0, 0, 0);
-            }
+            // Zero the rows of V that no row of the item sees: [from, to), and those past hi
+            // (both halves' warps do, with the same values).
+            const int from = max(span.first - k0, 0), to = min(max(span.lo - k0, from), kKeys);
+            auto zero = [&](int r0, int r1) {
+              for (int i = 8 * r0 + lane; i < 8 * r1; i += 32)
+#pragma unroll
+                for (int b = 0; b < S::kBoxes; ++b)
+                  *reinterpret_cast<uint4*>(v + b * S::kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
+            };
+            zero(from, to);
+            zero(max(min(span.hi - k0, kKeys), 0), kKeys);
             fence_proxy_async_smem();
             __syncwarp();
           }
@@ -451,13 +456,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto fetch_q = [&](const Walk& it) {
       const int ln = volatile_lane(), q_chunk = ln % kChunks;
       const int r0 = it.row0(), rows = it.row1(p) - r0;
-      const T* base = static_cast<const T*>(p.q) + it.s.q0 * p.q_ts + it.h * p.group * p.q_hs + q_chunk * 8;
-#pragma unroll 2
-      for (int i = 0; i < 32; i += 32 / kChunks) {
-        const int rl = 32 * of_half + i + ln / kChunks, r = kHalf * half + rl;
-        const bool real = r < rows && q_chunk * 8 < p.dim && p.scale_log2 != 0.f;
-        const int t = p.group_div.div(r0 + min(r, rows - 1)), g = r0 + min(r, rows - 1) - t * p.group;
-        cp_async16(q_at(rl, q_chunk), real ? base + t * p.q_ts + g * p.q_hs : static_cast<const T*>(p.q), real ? 16 : 0);
+      // this lane's first row as token and query head of the group, then steps of kStep rows
+      constexpr int kStep = 32 / kChunks;
+      int rl = 32 * of_half + ln / kChunks;
+      const int first = r0 + kHalf * half + rl, t0 = p.group_div.div(first);
+      int g = first - t0 * p.group;
+      const T* src = static_cast<const T*>(p.q) + (it.s.q0 + t0) * p.q_ts + (it.h * p.group + g) * p.q_hs + q_chunk * 8;
+      const long long wrap = p.q_ts - p.group * p.q_hs;
+      const int end = q_chunk * 8 < p.dim && p.scale_log2 != 0.f ? rows - kHalf * half : 0;
+#pragma unroll 4
+      for (int i = 0; i < 32; i += kStep) {
+        cp_async16(q_at(rl, q_chunk), rl < end ? src : static_cast<const T*>(p.q), rl < end ? 16 : 0);
+        rl += kStep;
+        src += kStep * p.q_hs;
+        for (g += kStep; g >= p.group; g -= p.group) src += wrap;
       }
     };
     auto send_q = [&] {
