@@ -54,8 +54,6 @@ constexpr int kMmaWarp = 8, kLoadWarp = 10;   // and the one after each
 constexpr int kThreads = 384;
 // Registers a thread: 384 threads start with 168; 256 x 224 + 128 x 56 is the same total.
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
-// Named barriers (0 is __syncthreads): all softmax warps; those of a half.
-constexpr int kBarAll = 1, kBarHalf = 2;
 constexpr int kMinUnits = 4;
 constexpr float kLazy = 8.f;            // growth of the maximum (log2) that renews the reference
 using Walk = PagedWalk<kRows, kKeys>;
@@ -69,36 +67,34 @@ template <int kDim> struct Shape {
   static constexpr uint32_t kS = 0, kO = 256;                   // TMEM columns: S at 0 and 128, O at 256 and 256 + kDim
 };
 
-// A place in the line and what one half's softmax needs of it, worked out ahead.
-struct Item : Walk {
-  int plain0, plain1;    // units that every row of the half sees whole (tiles of sinks are left to the mask)
-  bool mine, keys;       // the half has rows; they see something
-  __device__ __forceinline__ void look(const PagedParams& p, int half) {
-    if (b >= p.batch) {
-      mine = keys = false;
-      return;
-    }
-    const Span span(p, s, row0(), row1(p));
-    const int rows = row1(p) - row0();
-    mine = rows > kHalf * half;
-    keys = span.hi > 0;
-    const int h0 = row0() + kHalf * half, h1 = min(h0 + kHalf, row0() + rows) - 1;
-    const int all_hi = PagedRow(p, s, h0).hi, all_lo = PagedRow(p, s, h1).lo;
-    // tiles [t0, t1) are seen whole; in units, the run's first tile comes last
-    const int t0 = (all_lo + kKeys - 1) / kKeys - span.lo_tile, t1 = min(all_hi / kKeys - span.lo_tile, span.run);
-    plain0 = span.lo > 0 ? max(t0, 1) - 1 : t0;
-    plain1 = span.lo > 0 ? t1 - 1 : t1;
-  }
+// How the halves share an item: one has up to 128 rows and works alone; both have
+// rows; or up to 128 rows and at least two units are worked on by both, who take
+// every other unit and join their results at the end (few rows against many keys are
+// bound by one half's chain of product, softmax and product).
+enum class Mode : int { kEnd, kNoKeys, kAlone, kBoth, kPair };
+
+// An item, or this CTA's part of one, as the load warp works it out for all others.
+struct Job {
+  Mode mode;
+  int q0, row0, rows, h, b;           // first token of the sequence; rows of the item; K/V head, sequence
+  PagedSeq s;
+  int u0, u1;                         // units of this part
+  int plain0[2], plain1[2];           // units that every row of a half sees whole (tiles of sinks are left to the mask)
+  int c0, c1;                         // the CTAs that share the item, if more than one do
+  bool split, whole_end;              // only a part of the item; ends where the item ends
+  Span span;
 };
+constexpr int kJobs = 4;
 
 // What the warps share besides the tiles.
 template <int kDim> struct Control {
-  uint64_t q_full[2], s_full[2], p_full[2][2], o_done[2], start;
+  uint64_t q_full[2], s_full[2], p_full[2][2], o_done[2], start, meet;
   uint64_t k_full[Shape<kDim>::kKStages], k_empty[Shape<kDim>::kKStages];
   uint64_t v_full[Shape<kDim>::kVStages], v_empty[Shape<kDim>::kVStages], mma_done[2];
-  Walk walks[4];                     // places in the line of the MMA and load warps
-  Item items[2][3];                  // of each half's softmax: this item, the next and the one after
+  uint64_t job_full[kJobs], job_empty[kJobs];
+  Walk place;
   PagedShare share;
+  Job jobs[kJobs];
   float row_lse[kRows];
   uint32_t tmem_base;
   int abort_flag, last_one;
@@ -209,20 +205,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   {
     PagedShare sh;
     if (!paged_share<kRows, kKeys, kThreads>(p, blockIdx.x, gridDim.x, kMinUnits,
-                                             reinterpret_cast<long long*>(smem), &ctl.walks[0], &sh))
+                                             reinterpret_cast<long long*>(smem), &ctl.place, &sh))
       return;
     if (threadIdx.x == 0) ctl.share = sh;
-    if (threadIdx.x > 0 && threadIdx.x < 4) ctl.walks[threadIdx.x] = ctl.walks[0];
-    if (threadIdx.x >= 4 && threadIdx.x < 6) {
-      const int half = threadIdx.x - 4;
-      Item item;
-      static_cast<Walk&>(item) = ctl.walks[0];
-      item.look(p, half);
-      ctl.items[half][0] = item;
-      item.next_item(p);
-      item.look(p, half);
-      ctl.items[half][1] = item;
-    }
   }
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -245,6 +230,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl.v_empty[i], 2);
     }
     mbar_init(&ctl.start, 1);
+    mbar_init(&ctl.meet, kSoftmaxWarps);
+    for (int i = 0; i < kJobs; ++i) {
+      mbar_init(&ctl.job_full[i], 1);
+      mbar_init(&ctl.job_empty[i], kSoftmaxWarps + 3);      // the softmax, MMA and V warps
+    }
     ctl.abort_flag = 0;
     fence_mbar_init();
   }
@@ -256,21 +246,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
-  auto next_item = [&](Walk& to) {
-    __syncwarp();
-    if (lane == 0) to.next_item(p);
-    __syncwarp();
-  };
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, &g_chunk_err));
   };
-  uint32_t unit_count = 0;      // units before this item: unit n has K stage n % kKStages, V stage n % kVStages
+  uint32_t unit_count = 0;      // units before this job: unit n has K stage n % kKStages, V stage n % kVStages
+  auto job_ready = [&](uint32_t k) -> const Job& {
+    wait(&ctl.job_full[k % kJobs], (k / kJobs) & 1);
+    return ctl.jobs[k % kJobs];
+  };
+  auto job_done = [&](uint32_t k) {
+    __syncwarp();
+    if (lane == 0 && ok) mbar_arrive(&ctl.job_empty[k % kJobs]);
+  };
 
   if (warp >= kLoadWarp) {
     fewer_registers<kOtherRegs>();
-    // ------------------------------------------------------------ K, V tiles
-    Walk& w = ctl.walks[warp - kMmaWarp];
+    // ---------------------------------------------------- jobs, K and V tiles
     const bool is_v = warp > kLoadWarp;
     const uint32_t stages = is_v ? S::kVStages : S::kKStages;
     uint64_t* full = is_v ? ctl.v_full : ctl.k_full;
@@ -282,23 +274,66 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int boxes = kKeys >> shift, box_keys = 1 << shift;
     const int page_mask = (1 << p.page_shift) - 1;
     uint32_t stage = 0, phase = 0;
-    while (ok && w.at < ctl.share.end) {
-      const Span span(p, w.s, w.row0(), w.row1(p));
-      const int u1 = static_cast<int>(min(static_cast<long long>(w.units), w.unit + (ctl.share.end - w.at)));
-      const int* table = p.table + w.b * p.table_stride;
-      const int head = w.h;
-      auto page_of = [&](int u) {
-        int id = p.num_pages;                             // out of range: the box is filled with zeros
-        if (lane < boxes && u < u1) {
-          const int k0 = span.key0(u) + lane * box_keys;
-          if (k0 < span.hi && (k0 + box_keys > span.lo || k0 < span.first)) id = table[k0 >> p.page_shift];
-          if (id < 0 || id > p.num_pages) id = p.num_pages;
+    for (uint32_t k = 0;; ++k) {
+      if (!is_v) {
+        // work out the next job, while the others are still busy with earlier ones
+        if (!wait(&ctl.job_empty[k % kJobs], ((k / kJobs) & 1) ^ 1)) break;
+        if (lane == 0) {
+          Walk& w = ctl.place;
+          Job& job = ctl.jobs[k % kJobs];
+          if (w.at >= ctl.share.end) {
+            job.mode = Mode::kEnd;
+          } else {
+            const int row0 = w.row0(), rows = w.row1(p) - row0;
+            const Span span(p, w.s, row0, row0 + rows);
+            const int u0 = w.unit;
+            const int u1 = static_cast<int>(min(static_cast<long long>(w.units), u0 + (ctl.share.end - w.at)));
+            job.mode = span.hi == 0 ? Mode::kNoKeys : rows > kHalf ? Mode::kBoth : u1 - u0 > 1 ? Mode::kPair : Mode::kAlone;
+            job.q0 = w.s.q0, job.row0 = row0, job.rows = rows, job.h = w.h, job.b = w.b, job.s = w.s;
+            job.u0 = u0, job.u1 = u1, job.span = span;
+            job.split = u0 != 0 || u1 != w.units;
+            job.whole_end = u1 == w.units;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              const int h0 = row0 + (rows > kHalf ? kHalf * half : 0), h1 = min(h0 + kHalf, row0 + rows) - 1;
+              const int all_hi = PagedRow(p, w.s, h0).hi, all_lo = PagedRow(p, w.s, h1).lo;
+              // tiles [t0, t1) are seen whole; in units, the run's first tile comes last
+              const int t0 = (all_lo + kKeys - 1) / kKeys - span.lo_tile, t1 = min(all_hi / kKeys - span.lo_tile, span.run);
+              job.plain0[half] = span.lo > 0 ? max(t0, 1) - 1 : t0;
+              job.plain1[half] = span.lo > 0 ? t1 - 1 : t1;
+            }
+            if (job.split) {
+              job.c0 = ctl.share.owner(w.at - u0);
+              job.c1 = ctl.share.owner(w.at - u0 + w.units - 1);
+            }
+            if (job.whole_end) w.next_item(p);
+            else w.at = ctl.share.end;
+          }
+          mbar_arrive(&ctl.job_full[k % kJobs]);
         }
-        return id;
-      };
-      if (span.hi > 0) {
-        int id = page_of(w.unit);
-        for (int u = w.unit; u < u1; ++u) {
+        __syncwarp();
+      } else {
+        job_ready(k);
+        if (!ok) break;
+      }
+      const Job& job = ctl.jobs[k % kJobs];
+      const Mode mode = job.mode;
+      if (mode == Mode::kEnd) break;
+      if (mode != Mode::kNoKeys) {
+        const int* table = p.table + job.b * p.table_stride;
+        const int head = job.h, u1 = job.u1;
+        const Span span = job.span;
+        auto page_of = [&](int u) {
+          int id = p.num_pages;                             // out of range: the box is filled with zeros
+          if (lane < boxes && u < u1) {
+            const int k0 = span.key0(u) + lane * box_keys;
+            if (k0 < span.hi && (k0 + box_keys > span.lo || k0 < span.first)) id = table[k0 >> p.page_shift];
+            if (id < 0 || id > p.num_pages) id = p.num_pages;
+          }
+          return id;
+        };
+        int id = page_of(job.u0);
+        for (int u = job.u0; u < u1; ++u) {
           const int slot = (span.key0(u) + lane * box_keys) & page_mask;
           const int next = page_of(u + 1);
           if (!wait(&empty[stage], phase ^ 1)) break;
@@ -316,8 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           id = next;
         }
       }
-      if (u1 < w.units) break;
-      next_item(w);
+      if (!ok) break;
+      if (is_v) job_done(k);
     }
     // Every copy has landed before the CTA may exit: the last fill of each stage.
     for (uint32_t i = 0; i < stages && i < unit_count; ++i)
@@ -326,7 +361,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kMmaWarp) {
     fewer_registers<kOtherRegs>();
     // ------------------------------------------------------------------- MMA
-    Walk& w = ctl.walks[warp - kMmaWarp];
     constexpr uint32_t kQk = idesc<T>(kKeys, false), kPv = idesc<T>(kDim, true);
     const int half = warp - kMmaWarp;
     const uint32_t s_tmem = tmem + S::kS + 128 * half, o_tmem = tmem + S::kO + kDim * half;
@@ -352,81 +386,102 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit(&ctl.s_full[half]);
       }
     };
-    while (ok && w.at < ctl.share.end) {
-      const Span span(p, w.s, w.row0(), w.row1(p));
-      const int u0 = w.unit;
-      const int u1 = static_cast<int>(min(static_cast<long long>(w.units), u0 + (ctl.share.end - w.at)));
-      const bool both = w.row1(p) - w.row0() > kHalf;
-      if (span.hi > 0 && w.row1(p) - w.row0() > kHalf * half) {
-        uint32_t n = unit_count;
-        if (!wait(&ctl.k_full[n % S::kKStages], (n / S::kKStages) & 1)) break;
-        if (!wait(&ctl.q_full[half], q_phase)) break;
-        q_phase ^= 1;
-        // Half 1 begins after half 0 has begun the same item: it must not grant turns of an earlier one.
-        if (half == 1) {
-          if (!wait(&ctl.start, start_phase)) break;
-          start_phase ^= 1;
-        }
-        tc_fence_after();
-        qk(n, half == 1 || !both ? 0 : -1);
-        if (half == 0 && both && lane == 0) mbar_arrive(&ctl.start);
-        for (int u = u0; u < u1; ++u, ++n) {
-          const bool more = u + 1 < u1;
-          if (!wait(&ctl.v_full[n % S::kVStages], (n / S::kVStages) & 1)) break;
-          unsigned char* v = v_ring + (n % S::kVStages) * S::kTile;
-          const int k0 = span.key0(u);
-          if (k0 + kKeys > span.hi || (k0 < span.lo && k0 + kKeys > span.first)) {
-            // Zero the rows of V that no row of the item sees: [from, to), and those past hi
-            // (both halves' warps do, with the same values).
-            const int from = max(span.first - k0, 0), to = min(max(span.lo - k0, from), kKeys);
-            auto zero = [&](int r0, int r1) {
-              for (int i = 8 * r0 + lane; i < 8 * r1; i += 32)
-#pragma unroll
-                for (int b = 0; b < S::kBoxes; ++b)
-                  *reinterpret_cast<uint4*>(v + b * S::kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
-            };
-            zero(from, to);
-            zero(max(min(span.hi - k0, kKeys), 0), kKeys);
-            fence_proxy_async_smem();
-            __syncwarp();
+    // The tiles that this half does not use it still takes in turn and releases (kn,
+    // vn: the next of each): a wait tells a phase from its neighbours only, so nobody may skip ahead.
+    uint32_t kn = 0, vn = 0;
+    auto pass_k = [&](uint32_t upto) {
+      for (; ok && kn < upto; ++kn)
+        if (wait(&ctl.k_full[kn % S::kKStages], (kn / S::kKStages) & 1) && lane == 0)
+          mbar_arrive(&ctl.k_empty[kn % S::kKStages]);
+    };
+    auto pass_v = [&](uint32_t upto) {
+      for (; ok && vn < upto; ++vn)
+        if (wait(&ctl.v_full[vn % S::kVStages], (vn / S::kVStages) & 1) && lane == 0)
+          mbar_arrive(&ctl.v_empty[vn % S::kVStages]);
+    };
+    auto take_k = [&](uint32_t n) {
+      pass_k(n);
+      ++kn;
+      return wait(&ctl.k_full[n % S::kKStages], (n / S::kKStages) & 1);
+    };
+    auto take_v = [&](uint32_t n) {
+      pass_v(n);
+      ++vn;
+      return wait(&ctl.v_full[n % S::kVStages], (n / S::kVStages) & 1);
+    };
+    for (uint32_t k = 0;; ++k) {
+      const Job& job = job_ready(k);
+      if (!ok || job.mode == Mode::kEnd) break;
+      const Mode mode = job.mode;
+      if (mode != Mode::kNoKeys) {
+        const uint32_t end = unit_count + (job.u1 - job.u0);
+        if (half == 0 || mode != Mode::kAlone) {
+          const bool both = mode == Mode::kBoth;
+          const uint32_t step = mode == Mode::kPair ? 2 : 1;
+          const uint32_t n0 = unit_count + (mode == Mode::kPair ? half : 0);
+          if (!take_k(n0) || !wait(&ctl.q_full[half], q_phase)) break;
+          q_phase ^= 1;
+          // Half 1 begins after half 0 has begun the same item: it must not grant turns of an earlier one.
+          if (both && half == 1) {
+            if (!wait(&ctl.start, start_phase)) break;
+            start_phase ^= 1;
           }
-          if (more && !wait(&ctl.k_full[(n + 1) % S::kKStages], ((n + 1) / S::kKStages) & 1)) break;
-          const uint64_t dv = dv0 + (n % S::kVStages) * (S::kTile >> 4);
+          tc_fence_after();
+          qk(n0, !both ? half : half == 1 ? 0 : -1);
+          if (both && half == 0 && lane == 0) mbar_arrive(&ctl.start);
+#pragma unroll 1
+          for (uint32_t n = n0; n < end; n += step) {
+            const bool more = n + step < end;
+            if (!take_v(n)) break;
+            const int k0 = job.span.key0(job.u0 + static_cast<int>(n - unit_count));
+            const int lo = job.span.lo, hi = job.span.hi, first = job.span.first;
+            if (k0 + kKeys > hi || (k0 < lo && k0 + kKeys > first)) {
+              // Zero the rows of V that no row of the item sees: [from, to), and those past hi
+              // (where both halves use the tile, both do, with the same values).
+              unsigned char* v = v_ring + (n % S::kVStages) * S::kTile;
+              const int from = max(first - k0, 0), to = min(max(lo - k0, from), kKeys);
+              const int from2 = max(min(hi - k0, kKeys), to);
+              for (int i = lane; i < 8 * kKeys; i += 32)
+                if ((i >= 8 * from && i < 8 * to) || i >= 8 * from2) {
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            if (!wait(&ctl.p_full[half][part], p_phase)) break;
-            tc_fence_after();
-            if (lane == 0) {
+                  for (int b = 0; b < S::kBoxes; ++b)
+                    *reinterpret_cast<uint4*>(v + b * S::kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
+                }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            if (more && !take_k(n + step)) break;
+            const uint64_t dv = dv0 + (n % S::kVStages) * (S::kTile >> 4);
 #pragma unroll
-              for (int ks = 4 * part; ks < 4 * part + 4; ++ks)
-                umma_ts(o_tmem, s_tmem + 8 * ks, dv + ks * 128, kPv, u != u0 || ks != 0);
+            for (int part = 0; part < 2; ++part) {
+              if (!wait(&ctl.p_full[half][part], p_phase)) break;
+              tc_fence_after();
+              if (lane == 0) {
+#pragma unroll
+                for (int ks = 4 * part; ks < 4 * part + 4; ++ks)
+                  umma_ts(o_tmem, s_tmem + 8 * ks, dv + ks * 128, kPv, n != n0 || ks != 0);
+              }
+            }
+            if (!ok) break;
+            p_phase ^= 1;
+            if (more) {
+              qk(n + step, both ? half ^ 1 : half);
+            } else if (lane == 0) {
+              if (both && half == 0) grant(1);
+              umma_commit(&ctl.o_done[half]);
             }
           }
           if (!ok) break;
-          p_phase ^= 1;
-          if (more) {
-            qk(n + 1, both ? half ^ 1 : 0);
-          } else if (lane == 0) {
-            if (both && half == 0) grant(1);
-            umma_commit(&ctl.o_done[half]);
-          }
         }
-        if (!ok) break;
-      } else if (span.hi > 0) {
-        // No rows of this half: it still takes every tile in turn and releases it. A
-        // wait tells a phase from its neighbours only, so nobody may skip ahead.
-        uint32_t n = unit_count;
-        for (int u = u0; u < u1; ++u, ++n) {
-          if (!wait(&ctl.k_full[n % S::kKStages], (n / S::kKStages) & 1)) break;
-          if (lane == 0) mbar_arrive(&ctl.k_empty[n % S::kKStages]);
-          if (!wait(&ctl.v_full[n % S::kVStages], (n / S::kVStages) & 1)) break;
-          if (lane == 0) mbar_arrive(&ctl.v_empty[n % S::kVStages]);
+        while (ok && vn < end) {
+          pass_k(min(vn + 1, end));
+          pass_v(vn + 1);
         }
+        pass_k(end);
         if (!ok) break;
+        unit_count = end;
       }
-      if (span.hi > 0) unit_count += u1 - u0;
-      if (u1 < w.units) break;
-      next_item(w);
+      job_done(k);
     }
     // Every MMA has completed before TMEM is released.
     if (lane == 0) {
@@ -438,7 +493,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     more_registers<kSoftmaxRegs>();
     // --------------------------------------------------------------- softmax
     const int half = warp >> 2, of_half = warp & 3;
-    const int my_row = 32 * warp + lane;                   // of the item's 256
     const uint32_t lanes = static_cast<uint32_t>(32 * of_half) << 16;
     const uint32_t s_tmem = tmem + lanes + S::kS + 128 * half, o_tmem = tmem + lanes + S::kO + kDim * half;
     // The scale is applied after the mask (-inf) and the maximum, so it has to be
@@ -453,17 +507,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto q_at = [&](int rl, int q_chunk) {
       return q_smem + half * S::kTile + (q_chunk >> 3) * S::kBoxBytes + rl * 128 + (((q_chunk & 7) ^ (rl & 7)) << 4);
     };
-    auto fetch_q = [&](const Walk& it) {
+    auto fetch_q = [&](const Job& it) {
       const int ln = volatile_lane(), q_chunk = ln % kChunks;
-      const int r0 = it.row0(), rows = it.row1(p) - r0;
+      const int base = it.mode == Mode::kBoth ? kHalf * half : 0;
       // this lane's first row as token and query head of the group, then steps of kStep rows
       constexpr int kStep = 32 / kChunks;
       int rl = 32 * of_half + ln / kChunks;
-      const int first = r0 + kHalf * half + rl, t0 = p.group_div.div(first);
+      const int first = it.row0 + base + rl, t0 = p.group_div.div(first);
       int g = first - t0 * p.group;
-      const T* src = static_cast<const T*>(p.q) + (it.s.q0 + t0) * p.q_ts + (it.h * p.group + g) * p.q_hs + q_chunk * 8;
+      const T* src = static_cast<const T*>(p.q) + (it.q0 + t0) * p.q_ts + (it.h * p.group + g) * p.q_hs + q_chunk * 8;
       const long long wrap = p.q_ts - p.group * p.q_hs;
-      const int end = q_chunk * 8 < p.dim && p.scale_log2 != 0.f ? rows - kHalf * half : 0;
+      const int end = q_chunk * 8 < p.dim && p.scale_log2 != 0.f ? it.rows - base : 0;
 #pragma unroll 4
       for (int i = 0; i < 32; i += kStep) {
         cp_async16(q_at(rl, q_chunk), rl < end ? src : static_cast<const T*>(p.q), rl < end ? 16 : 0);
@@ -486,36 +540,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&ctl.q_full[half]);
     };
 
-    // Named barriers keep the warps together, so a warp whose wait gave up (ok is
-    // false) goes through all of them too; it only no longer waits or arrives.
-    for (uint32_t item = 0;; ++item) {
-      const Item& w = ctl.items[half][item % 3];
-      const Item& nx = ctl.items[half][(item + 1) % 3];
-      if (w.at >= ctl.share.end) break;
-      const Span span(p, w.s, w.row0(), w.row1(p));
-      const int u0 = w.unit;
-      const int u1 = static_cast<int>(min(static_cast<long long>(w.units), u0 + (ctl.share.end - w.at)));
-      const int rows = w.row1(p) - w.row0();
-      const bool mine = w.mine, keys = w.keys;
+    auto works = [&](Mode mode) { return mode >= Mode::kBoth || (mode == Mode::kAlone && half == 0); };
+
+    // All softmax warps meet where halves or parts are joined (on an mbarrier, whose wait is bounded).
+    uint32_t meet_phase = 0;
+    auto meet = [&] {
+      __syncwarp();
+      if (lane == 0 && ok) mbar_arrive(&ctl.meet);
+      wait(&ctl.meet, meet_phase);
+      meet_phase ^= 1;
+    };
+    // A warp whose wait gave up (ok is false) runs on to the end of its job without
+    // waiting or arriving anywhere, and leaves.
+    for (uint32_t k = 0;; ++k) {
+      const Job& w = job_ready(k);
+      if (!ok || w.mode == Mode::kEnd) break;
+      const Mode mode = w.mode;
+      const int rows = w.rows, n_units = w.u1 - w.u0;
+      const int my_row = (rows > kHalf ? kHalf * half : 0) + 32 * of_half + lane;   // of the item's 256
+      const bool mine = works(mode) || (mode == Mode::kNoKeys && rows > kHalf * half);
+      const bool keys = mode != Mode::kNoKeys;
       bool q_next = false;
-      float m = kNegInf, l = 0.f;                          // the row's reference (in units of S), this thread's sum
-      if (mine && keys) {
+      float m = kNegInf, l = 0.f;                          // the row's reference (in units of S) and sum
+      if (works(mode)) {
         if (!q_sent) {
           fetch_q(w);
           send_q();
         }
-        const int plain0 = w.plain0, plain1 = w.plain1;
+        const int plain0 = w.plain0[half], plain1 = w.plain1[half], u1 = w.u1;
+        const int step = mode == Mode::kPair ? 2 : 1, first_unit = w.u0 + (mode == Mode::kPair ? half : 0);
+        uint32_t n = unit_count + (mode == Mode::kPair ? half : 0);
 #pragma unroll 1
-        for (int u = u0; u < u1; ++u) {
+        for (int u = first_unit; u < u1; u += step, n += step) {
           wait(&ctl.s_full[half], tile_phase);
           tc_fence_after();
           tile_phase ^= 1;
           // QK of this unit is done, and so is PV of the one before
-          if (of_half == 0 && lane == 0 && ok) mbar_arrive(&ctl.k_empty[(unit_count + (u - u0)) % S::kKStages]);
-          if (of_half == 1 && lane == 0 && ok && u > u0)
-            mbar_arrive(&ctl.v_empty[(unit_count + (u - u0) - 1) % S::kVStages]);
-          if (u + 1 == u1 && u1 == w.units) {              // Q has been read for the last time: fetch the next item's
-            q_next = nx.at < ctl.share.end && nx.mine && nx.keys;
+          if (of_half == 0 && lane == 0 && ok) mbar_arrive(&ctl.k_empty[n % S::kKStages]);
+          if (of_half == 1 && lane == 0 && ok && u > first_unit) mbar_arrive(&ctl.v_empty[(n - step) % S::kVStages]);
+          if (u + step >= u1) {                            // Q has been read for the last time: fetch the next job's
+            const Job& nx = job_ready(k + 1);
+            q_next = ok && works(nx.mode);
             if (q_next) fetch_q(nx);
           }
           uint32_t s[4][32];
@@ -523,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 4; ++i) tmem_ld32(s_tmem + 32 * i, s[i]);
           tmem_ld_wait();
           if (u < plain0 || u >= plain1) {
-            const PagedRow vis(p, w.s, min(w.row0() + my_row, w.row1(p) - 1));
-            const int k0 = span.key0(u);
+            const PagedRow vis(p, w.s, w.row0 + min(my_row, rows - 1));
+            const int k0 = w.span.key0(u);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               // bits of the visible ones of these 32 keys
@@ -593,37 +658,40 @@ __global__ void __launch_bounds__(kThreads, 1)
           l += (sa.x + sa.y) + (sb.x + sb.y);
         }
         if (q_next) send_q();
-      }
-      // The line's next item but one, for all warps of the half (after the barrier below).
-      if (of_half == 0 && lane == 0) {
-        Item after = nx;
-        if (after.at < ctl.share.end) {
-          after.next_item(p);
-          after.look(p, half);
-        }
-        ctl.items[half][(item + 2) % 3] = after;
-      }
-      if (mine && keys) {
         wait(&ctl.o_done[half], o_phase);
         tc_fence_after();
         o_phase ^= 1;
-        if (of_half == 1 && lane == 0 && ok)
-          mbar_arrive(&ctl.v_empty[(unit_count + (u1 - u0) - 1) % S::kVStages]);
+        if (of_half == 1 && lane == 0 && ok) mbar_arrive(&ctl.v_empty[(n - step) % S::kVStages]);
       }
-      if (keys) unit_count += u1 - u0;
+      if (keys) unit_count += n_units;
       q_sent = q_next;
 
       // Results of this thread's row: O / l and m + log2 l (nothing seen: zeros, -inf).
-      const bool split = u0 != 0 || u1 != w.units;
       const bool none = l == 0.f;                          // (a NaN score leaves l NaN)
-      const float inv = none ? 0.f : 1.f / l;
-      const bool real = mine && my_row < rows;
-      const int g = w.row0() + min(my_row, rows - 1), t = p.group_div.div(g);
-      const long long tok = w.s.q0 + t;
-      const int head = w.h * p.group + g - t * p.group;
-      const int slot = 2 * static_cast<int>(blockIdx.x) + (u0 == 0 ? 1 : 0);
+      float lse2 = none ? kNegInf : (m == kNegInf ? 0.f : m * scale) + log2f(l);
+      float mul = none ? 0.f : 1.f / l, mul_other = 0.f;
+      bool real = mine && my_row < rows;
+      const bool pair = mode == Mode::kPair, split = w.split;
+      // Half 1 of a pair leaves its results in the CTA's scratch, in the form of a part; half 0 adds them up.
+      float* pair_o = p.pair_o + (static_cast<long long>(blockIdx.x) * kHalf + my_row) * kDim;
+      float* pair_l = p.pair_l + blockIdx.x * kHalf + my_row;
+      const bool gives = pair && half == 1;
+      if (pair && half == 0) {
+        meet();              // half 1 has written
+        if (real) {
+          const float other = __ldcg(pair_l), top = fmaxf(lse2, other), ref = top == kNegInf ? 0.f : top;
+          const float a = exp2_fast(lse2 - ref), b = exp2_fast(other - ref), sum = a + b;
+          lse2 = sum == 0.f ? kNegInf : ref + log2f(sum);
+          mul = sum == 0.f ? 0.f : mul * a / sum;
+          mul_other = sum == 0.f ? 0.f : b / sum;
+        }
+      }
       if (mine) {
-        float* to_part = p.part_o + (static_cast<long long>(slot) * kRows + my_row) * kDim;
+        const int g = w.row0 + min(my_row, rows - 1), t = p.group_div.div(g);
+        const long long tok = w.q0 + t;
+        const int head = w.h * p.group + g - t * p.group;
+        const int slot = 2 * static_cast<int>(blockIdx.x) + (w.u0 == 0 ? 1 : 0);
+        float* to_part = gives ? pair_o : p.part_o + (static_cast<long long>(slot) * kRows + my_row) * kDim;
         T* to_out = static_cast<T*>(p.out) + tok * p.o_ts + head * p.o_hs;
 #pragma unroll 1
         for (int c = 0; c < kDim; c += 32) {
@@ -633,8 +701,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_wait();
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(none ? 0.f : __uint_as_float(o[e]) * inv);
-          if (real && split) {
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(mul == 0.f ? 0.f : __uint_as_float(o[e]) * mul);
+          if (mul_other != 0.f) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(pair_o + c + e));
+              o[e] = __float_as_uint(fmaf(x.x, mul_other, __uint_as_float(o[e])));
+              o[e + 1] = __float_as_uint(fmaf(x.y, mul_other, __uint_as_float(o[e + 1])));
+              o[e + 2] = __float_as_uint(fmaf(x.z, mul_other, __uint_as_float(o[e + 2])));
+              o[e + 3] = __float_as_uint(fmaf(x.w, mul_other, __uint_as_float(o[e + 3])));
+            }
+          }
+          if (real && (split || gives)) {
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
               const uint32_t v[8] = {o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5], o[e + 6], o[e + 7]};
@@ -656,37 +734,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         if (real) {
-          const float lse2 = none ? kNegInf : (m == kNegInf ? 0.f : m * scale) + log2f(l);
-          if (split) p.part_l[slot * kRows + my_row] = lse2;
+          if (gives) *pair_l = lse2;
+          else if (split) p.part_l[slot * kRows + my_row] = lse2;
           else if (p.lse) p.lse[tok * p.heads + head] = lse2 * kLn2;
         }
       }
+      if (gives) meet();
+      if (pair) meet();      // the scratch has been read
       if (split) {
-        // All softmax threads come here for every split item, also when a wait gave up.
-        const int c0 = ctl.share.owner(w.at - u0), c1 = ctl.share.owner(w.at - u0 + w.units - 1);
-        named_sync(kBarAll, kSoftmaxThreads);
+        // All softmax threads come here for every split item.
+        const int c0 = w.c0, c1 = w.c1;
+        meet();
         if (threadIdx.x == 0) {
           __threadfence();                                 // covers what the others wrote before the barrier
           const unsigned seen = atomicAdd(p.counters + c0, 1u);
           ctl.last_one = seen == static_cast<unsigned>(c1 - c0);
           if (ctl.last_one) p.counters[c0] = 0;
         }
-        named_sync(kBarAll, kSoftmaxThreads);
+        meet();
         if (ctl.last_one) {
           __threadfence();
           // Each row's log-sum over all parts (one thread a row); a part then
           // weighs exp2(its own - that).
-          if (my_row < rows) {
+          if (threadIdx.x < rows) {
+            const int row = threadIdx.x;
             float top = kNegInf, sum = 0.f;
 #pragma unroll 4
-            for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(p.part_l + (2 * c + (c == c0)) * kRows + my_row));
+            for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(p.part_l + (2 * c + (c == c0)) * kRows + row));
             const float ref = top == kNegInf ? 0.f : top;
 #pragma unroll 4
             for (int c = c0; c <= c1; ++c)
-              sum += exp2_fast(__ldcg(p.part_l + (2 * c + (c == c0)) * kRows + my_row) - ref);
-            ctl.row_lse[my_row] = sum == 0.f ? kNegInf : ref + log2f(sum);
+              sum += exp2_fast(__ldcg(p.part_l + (2 * c + (c == c0)) * kRows + row) - ref);
+            ctl.row_lse[row] = sum == 0.f ? kNegInf : ref + log2f(sum);
           }
-          named_sync(kBarAll, kSoftmaxThreads);
+          meet();
           // Eight columns a thread, so that a part's row is read and the output's
           // written in whole sectors; kBatch rows at once for loads in flight.
           constexpr int kLanes = kDim / 8, kRowStep = kSoftmaxThreads / kLanes, kBatch = 4;
@@ -711,8 +792,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < kBatch; ++k) {
               const int r = r0 + k * kRowStep;
               if (r >= rows) continue;
-              const int gr = w.row0() + r, tr = p.group_div.div(gr), hr = w.h * p.group + gr - tr * p.group;
-              const long long at = w.s.q0 + tr;
+              const int gr = w.row0 + r, tr = p.group_div.div(gr), hr = w.h * p.group + gr - tr * p.group;
+              const long long at = w.q0 + tr;
               uint4 v;
               v.x = Type<T>::pack(acc[k][0], acc[k][1]);
               v.y = Type<T>::pack(acc[k][2], acc[k][3]);
@@ -724,10 +805,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        named_sync(kBarAll, kSoftmaxThreads);                    // ctl.last_one has been read
+        meet();                    // ctl.last_one has been read
       }
-      if (u1 < w.units) break;
-      named_sync(kBarHalf + half, 128);                 // all are done with this item, and the next but one is known
+      job_done(k);
     }
   }
   tc_fence_before();
@@ -773,7 +853,7 @@ cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const ChunkPara
 }  // namespace
 
 size_t paged_chunk_workspace_bytes(int num_sms) {
-  return kPagedCounterBytes + 32 + 2 * static_cast<size_t>(num_sms) * kRows * (128 + 1) * sizeof(float);
+  return kPagedCounterBytes + 32 + static_cast<size_t>(num_sms) * (2 * kRows + kHalf) * (128 + 1) * sizeof(float);
 }
 
 cudaError_t launch_paged_chunk(FloatType t, const PagedParams& params, void* workspace, int num_sms,
@@ -787,7 +867,10 @@ cudaError_t launch_paged_chunk(FloatType t, const PagedParams& params, void* wor
   p.part_o = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(workspace) + kPagedCounterBytes + 31) & ~31ull);
   cp.out32 = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && (p.tokens == 1 || p.o_ts % 16 == 0) &&
              (p.heads == 1 || p.o_hs % 16 == 0);
-  p.part_l = p.part_o + static_cast<size_t>(2) * ctas * kRows * (p.dim <= 64 ? 64 : 128);
+  const size_t dim = p.dim <= 64 ? 64 : 128;
+  p.pair_o = p.part_o + 2 * ctas * kRows * dim;
+  p.part_l = p.pair_o + ctas * kHalf * dim;
+  p.pair_l = p.part_l + 2 * ctas * kRows;
   CUtensorMap km, vm;
   cudaError_t e = encode_cache(&km, &cp.k_heads_first, p.kc, t, p, p.k_ps, p.k_ss, p.k_hs);
   if (e == cudaSuccess) e = encode_cache(&vm, &cp.v_heads_first, p.vc, t, p, p.v_ps, p.v_ss, p.v_hs);

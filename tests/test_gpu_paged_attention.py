@@ -356,3 +356,10 @@ def test_tiles_of_one_half_between_tiles_of_two(d, dtype):
     """65 tokens of 4 heads are a tile of 256 rows and one of 4, over more key tiles than
     the shared memory holds at once, head after head and sequence after sequence."""
     Problem([(65, 2000), (1, 1500), (70, 1700), (33, 900), (64, 800)], 8, 2, d, 32, dtype).verify()
+
+
+@pytest.mark.parametrize("n,kv", [(5, 129), (5, 256), (5, 257), (5, 384), (20, 1000), (32, 4000), (30, 40)])
+def test_few_rows_of_a_chunk_share_the_keys_between_two_halves(n, kv):
+    for mask in ({}, dict(window=100, sinks=3)):
+        Problem([(n, kv), (n, kv - 3)], 8, 2, 128, 16, "bfloat16", seed=kv).verify(**mask)
+        Problem([(n, kv), (0, 3), (n + 1, kv)], 4, 1, 64, 32, seed=n).verify(**mask)
