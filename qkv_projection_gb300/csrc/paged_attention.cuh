@@ -81,31 +81,53 @@ struct PagedRow {
   }
 };
 
-// A position in the line of units, and the item that it lies in.
-template <int kRows, int kKeys>
+// A place in the line of units: an item, and a unit in it. In the line a unit of an
+// item with more than kHeavyRows rows counts twice (it takes about twice as long). An
+// item of at most kWhole places is not split: it belongs to the share that holds its
+// last place. (Writing and joining parts costs more than such an item's imbalance.)
+template <int kRows, int kKeys, int kHeavyRows, int kWhole>
 struct PagedWalk {
+  static constexpr int kWholeLength = kWhole;
   int b, h, tile, tiles;      // item: sequence, K/V head, row tile of `tiles`
   int unit, units;            // unit within the item
-  long long at;               // index in the whole line
+  long long at;               // where in the line the item begins
   PagedSeq s;
 
   __device__ __forceinline__ static int row_tiles(const PagedParams& p, const PagedSeq& s) {
-    return static_cast<int>((static_cast<long long>(s.n) * p.group + kRows - 1) / kRows);
+    return (s.n * p.group + kRows - 1) / kRows;
   }
   __device__ __forceinline__ int row0() const { return tile * kRows; }
   __device__ __forceinline__ int row1(const PagedParams& p) const { return min(tile * kRows + kRows, s.n * p.group); }
   __device__ __forceinline__ static int item_units(const PagedParams& p, const PagedSeq& s, int tile) {
     return PagedSpan<kKeys>(p, s, tile * kRows, min(tile * kRows + kRows, s.n * p.group)).units;
   }
-  __device__ __forceinline__ static long long head_units(const PagedParams& p, const PagedSeq& s) {
+  __device__ __forceinline__ static int item_weight(const PagedParams& p, const PagedSeq& s, int tile) {
+    return s.n * p.group - tile * kRows > kHeavyRows ? 2 : 1;
+  }
+  __device__ __forceinline__ bool heavy(const PagedParams& p) const { return item_weight(p, s, tile) == 2; }
+  __device__ __forceinline__ long long length(const PagedParams& p) const {
+    return static_cast<long long>(units) << (heavy(p) ? 1 : 0);
+  }
+  __device__ __forceinline__ static long long head_length(const PagedParams& p, const PagedSeq& s) {
     long long u = 0;
     const int tiles = row_tiles(p, s);
-    for (int i = 0; i < tiles; ++i) u += item_units(p, s, i);
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i) u += item_units(p, s, i) * item_weight(p, s, i);
     return u;
+  }
+  // The first unit past a CTA's share that ends at `end`. (A unit belongs to the
+  // share that holds the last of its places.)
+  __device__ __forceinline__ int unit_at(const PagedParams& p, long long end) const {
+    const long long to = max(end - at, 0ll);
+    if (to >= length(p)) return units;
+    return length(p) <= kWhole ? 0 : static_cast<int>(to >> (heavy(p) ? 1 : 0));
+  }
+  __device__ __forceinline__ long long place_of(const PagedParams& p, int u) const {
+    return at + ((static_cast<long long>(u) + 1) << (heavy(p) ? 1 : 0)) - 1;
   }
   // To the first unit of the next item (past the line's end: b == batch).
   __device__ __forceinline__ void next_item(const PagedParams& p) {
-    at += units - unit;
+    at += length(p);
     unit = 0;
     if (++tile == tiles) {
       tile = 0;
@@ -122,30 +144,51 @@ struct PagedWalk {
   }
 };
 
-// One CTA's share [begin, end) of a line of `total` units among `ctas` CTAs.
+// a / b for 0 <= a < 2^53, 0 < b < 2^31, by a rounded estimate and its correction
+// (the compiler's 64-bit division is some hundred instructions, and code is fetched
+// slowly at a kernel's start).
+__device__ __forceinline__ long long paged_div(long long a, int b) {
+  const float inv = 1.0f / static_cast<float>(b);
+  long long q = static_cast<long long>(static_cast<float>(a) * inv);
+  long long r = a - q * b;
+#pragma unroll 1
+  while (r < 0 || r >= b) {
+    long long step = static_cast<long long>(static_cast<float>(r) * inv);
+    if (step == 0) step = r < 0 ? -1 : 1;
+    q += step;
+    r -= step * b;
+  }
+  return q;
+}
+
+// One CTA's share [begin, end) of a line of `total` places among `ctas` CTAs: the
+// first total % ctas shares have one place more than the others.
 struct PagedShare {
-  long long begin, end, total;
-  int ctas;
-  __device__ __forceinline__ int owner(long long u) const {
-    return static_cast<int>(((u + 1) * ctas + total - 1) / total) - 1;
+  long long begin, end, each;    // each = total / ctas
+  int ctas, more;                // more = total % ctas
+  __device__ __forceinline__ int owner(long long place) const {
+    const long long first = (each + 1) * more;
+    if (place < first) return static_cast<int>(paged_div(place, static_cast<int>(each + 1)));
+    return more + static_cast<int>(paged_div(place - first, static_cast<int>(each)));
   }
 };
 
-// Found by all threads of the CTA together: the share of CTA `cta`, and the
-// place of its first unit. Every thread sums a run of sequences; a scan gives
-// the total and the run in which the share begins. `sums` holds kThreads values
-// in shared memory. Returns false if the share is empty.
-template <int kRows, int kKeys, int kThreads>
-__device__ bool paged_share(const PagedParams& p, int cta, int grid, int min_units, long long* sums,
-                            PagedWalk<kRows, kKeys>* place, PagedShare* share) {
-  using Walk = PagedWalk<kRows, kKeys>;
+// Found by all threads of the CTA together: the share of CTA `cta`, and the place of
+// its first unit. Every thread sums a run of sequences; a scan gives the total and
+// the run in which the share begins. `sums` holds kThreads values in shared memory.
+// Returns false if the share is empty.
+template <int kThreads, typename Walk>
+__device__ bool paged_share(const PagedParams& p, int cta, int grid, int min_units, long long* sums, Walk* place,
+                            PagedShare* share) {
   const int tid = threadIdx.x;
   const int per = (p.batch + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += p.kv_heads * Walk::head_units(p, paged_seq(p, b));
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) mine += p.kv_heads * Walk::head_length(p, paged_seq(p, b));
   sums[tid] = mine;
   __syncthreads();
+#pragma unroll 1
   for (int d = 1; d < kThreads; d <<= 1) {
     const long long add = tid >= d ? sums[tid - d] : 0;
     __syncthreads();
@@ -154,34 +197,36 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, int min_uni
   }
   const long long total = sums[kThreads - 1];
   if (total == 0) return false;
-  share->total = total;
-  share->ctas = static_cast<int>(max(1ll, min(static_cast<long long>(grid), total / min_units)));
+  share->ctas = static_cast<int>(min(static_cast<long long>(grid), max(1ll, paged_div(total, min_units))));
   if (cta >= share->ctas) return false;
-  share->begin = cta * total / share->ctas;
-  share->end = (cta + 1) * total / share->ctas;
+  share->each = paged_div(total, share->ctas);
+  share->more = static_cast<int>(total - share->each * share->ctas);
+  share->begin = cta * share->each + min(cta, share->more);
+  share->end = share->begin + share->each + (cta < share->more ? 1 : 0);
   const long long upto = sums[tid], from = upto - mine;
   if (share->begin >= from && share->begin < upto) {
     long long left = share->begin - from;
     Walk w;
-    w.b = b0;
-    for (;; ++w.b) {
+#pragma unroll 1
+    for (w.b = b0;; ++w.b) {
       w.s = paged_seq(p, w.b);
-      const long long head = Walk::head_units(p, w.s);
+      const long long head = Walk::head_length(p, w.s);
       if (left < head * p.kv_heads) {
         w.tiles = Walk::row_tiles(p, w.s);
-        w.h = static_cast<int>(left / head);
+        w.h = static_cast<int>(paged_div(left, static_cast<int>(head)));
         left -= w.h * head;
         break;
       }
       left -= head * p.kv_heads;
     }
+#pragma unroll 1
     for (w.tile = 0;; ++w.tile) {
       w.units = Walk::item_units(p, w.s, w.tile);
-      if (left < w.units) break;
-      left -= w.units;
+      if (left < w.length(p)) break;
+      left -= w.length(p);
     }
-    w.unit = static_cast<int>(left);
-    w.at = share->begin;
+    w.unit = w.length(p) <= Walk::kWholeLength ? 0 : static_cast<int>(left >> (w.heavy(p) ? 1 : 0));
+    w.at = share->begin - left;
     *place = w;
   }
   __syncthreads();

@@ -49,14 +49,15 @@ __device__ unsigned g_chunk_err;
 constexpr int kRows = 256;
 constexpr int kHalf = 128;
 constexpr int kKeys = 128;
-constexpr int kSoftmaxWarps = 8, kSoftmaxThreads = 32 * kSoftmaxWarps;
+constexpr int kSoftmaxWarps = 8;
 constexpr int kMmaWarp = 8, kLoadWarp = 10;   // and the one after each
 constexpr int kThreads = 384;
 // Registers a thread: 384 threads start with 168; 256 x 224 + 128 x 56 is the same total.
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
-constexpr int kMinUnits = 4;
+constexpr int kMinUnits = 4;            // places of the line worth a CTA of their own
+constexpr int kWhole = 16;              // places of an item that is not split
 constexpr float kLazy = 8.f;            // growth of the maximum (log2) that renews the reference
-using Walk = PagedWalk<kRows, kKeys>;
+using Walk = PagedWalk<kRows, kKeys, kHalf, kWhole>;
 using Span = PagedSpan<kKeys>;
 
 template <int kDim> struct Shape {
@@ -81,7 +82,7 @@ struct Job {
   int u0, u1;                         // units of this part
   int plain0[2], plain1[2];           // units that every row of a half sees whole (tiles of sinks are left to the mask)
   int c0, c1;                         // the CTAs that share the item, if more than one do
-  bool split, whole_end;              // only a part of the item; ends where the item ends
+  bool split;                         // only a part of the item
   Span span;
 };
 constexpr int kJobs = 4;
@@ -95,7 +96,6 @@ template <int kDim> struct Control {
   Walk place;
   PagedShare share;
   Job jobs[kJobs];
-  float row_lse[kRows];
   uint32_t tmem_base;
   int abort_flag, last_one;
 };
@@ -202,14 +202,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* v_ring = k_ring + S::kKStages * S::kTile;
   Control<kDim>& ctl = *reinterpret_cast<Control<kDim>*>(v_ring + S::kVStages * S::kTile);
 
-  {
-    PagedShare sh;
-    if (!paged_share<kRows, kKeys, kThreads>(p, blockIdx.x, gridDim.x, kMinUnits,
-                                             reinterpret_cast<long long*>(smem), &ctl.place, &sh))
-      return;
-    if (threadIdx.x == 0) ctl.share = sh;
-  }
-
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &ctl.abort_flag;
   if (threadIdx.x == 0) {
@@ -246,6 +238,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
+  allow_dependents_launch();
+  grid_dependency_wait();
+  // An empty share goes on with a plan of no jobs.
+  bool any;
+  {
+    PagedShare sh;
+    any = paged_share<kThreads>(p, blockIdx.x, gridDim.x, kMinUnits, reinterpret_cast<long long*>(smem), &ctl.place, &sh);
+    if (any && threadIdx.x == 0) ctl.share = sh;
+    __syncthreads();
+  }
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, &g_chunk_err));
@@ -281,18 +283,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           Walk& w = ctl.place;
           Job& job = ctl.jobs[k % kJobs];
-          if (w.at >= ctl.share.end) {
+          const int u0 = any ? w.unit : 0, u1 = any && w.b < p.batch ? w.unit_at(p, ctl.share.end) : 0;
+          if (u1 <= u0) {
             job.mode = Mode::kEnd;
           } else {
             const int row0 = w.row0(), rows = w.row1(p) - row0;
             const Span span(p, w.s, row0, row0 + rows);
-            const int u0 = w.unit;
-            const int u1 = static_cast<int>(min(static_cast<long long>(w.units), u0 + (ctl.share.end - w.at)));
             job.mode = span.hi == 0 ? Mode::kNoKeys : rows > kHalf ? Mode::kBoth : u1 - u0 > 1 ? Mode::kPair : Mode::kAlone;
             job.q0 = w.s.q0, job.row0 = row0, job.rows = rows, job.h = w.h, job.b = w.b, job.s = w.s;
             job.u0 = u0, job.u1 = u1, job.span = span;
             job.split = u0 != 0 || u1 != w.units;
-            job.whole_end = u1 == w.units;
+            const bool last = u1 == w.units;
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
               const int h0 = row0 + (rows > kHalf ? kHalf * half : 0), h1 = min(h0 + kHalf, row0 + rows) - 1;
@@ -303,11 +304,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               job.plain1[half] = span.lo > 0 ? t1 - 1 : t1;
             }
             if (job.split) {
-              job.c0 = ctl.share.owner(w.at - u0);
-              job.c1 = ctl.share.owner(w.at - u0 + w.units - 1);
+              job.c0 = ctl.share.owner(w.place_of(p, 0));
+              job.c1 = ctl.share.owner(w.place_of(p, w.units - 1));
             }
-            if (job.whole_end) w.next_item(p);
-            else w.at = ctl.share.end;
+            if (last) w.next_item(p);
+            else w.unit = w.units;                         // the share ends here
           }
           mbar_arrive(&ctl.job_full[k % kJobs]);
         }
@@ -666,6 +667,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (keys) unit_count += n_units;
       q_sent = q_next;
 
+      // Of a split item the CTA that finds all other parts written is the last.
+      if (w.split) {
+        if (threadIdx.x == 0) {
+          unsigned seen;
+          asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(p.counters + w.c0) : "memory");
+          ctl.last_one = seen == static_cast<unsigned>(w.c1 - w.c0);
+        }
+        meet();
+      }
+
       // Results of this thread's row: O / l and m + log2 l (nothing seen: zeros, -inf).
       const bool none = l == 0.f;                          // (a NaN score leaves l NaN)
       float lse2 = none ? kNegInf : (m == kNegInf ? 0.f : m * scale) + log2f(l);
@@ -673,7 +684,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool real = mine && my_row < rows;
       const bool pair = mode == Mode::kPair, split = w.split;
       // Half 1 of a pair leaves its results in the CTA's scratch, in the form of a part; half 0 adds them up.
-      float* pair_o = p.pair_o + (static_cast<long long>(blockIdx.x) * kHalf + my_row) * kDim;
+      // (Both are laid out [dim / 8][rows][8], so that a warp's 32 rows are contiguous.)
+      float* pair_o = p.pair_o + (static_cast<long long>(blockIdx.x) * kHalf * kDim) + my_row * 8;
       float* pair_l = p.pair_l + blockIdx.x * kHalf + my_row;
       const bool gives = pair && half == 1;
       if (pair && half == 0) {
@@ -686,127 +698,123 @@ __global__ void __launch_bounds__(kThreads, 1)
           mul_other = sum == 0.f ? 0.f : b / sum;
         }
       }
-      if (mine) {
-        const int g = w.row0 + min(my_row, rows - 1), t = p.group_div.div(g);
-        const long long tok = w.q0 + t;
-        const int head = w.h * p.group + g - t * p.group;
-        const int slot = 2 * static_cast<int>(blockIdx.x) + (w.u0 == 0 ? 1 : 0);
-        float* to_part = gives ? pair_o : p.part_o + (static_cast<long long>(slot) * kRows + my_row) * kDim;
-        T* to_out = static_cast<T*>(p.out) + tok * p.o_ts + head * p.o_hs;
+      const int g = w.row0 + min(my_row, rows - 1), t = p.group_div.div(g);
+      const long long tok = w.q0 + t;
+      const int head = w.h * p.group + g - t * p.group;
+      const int own = static_cast<int>(blockIdx.x), c0 = w.c0, c1 = w.c1;
+      auto part_at = [&](int c) { return 2 * c + (c == c0 ? 1 : 0); };     // a CTA's part of an item is its first but where the item begins
+      // The last CTA of a split item does not write its part: it joins the others' with
+      // its own. A CTA that is the last only once it has written goes round once more.
+      bool last = split && ctl.last_one;
+      float row_lse = lse2, base = 0.f;                    // of the whole item
+      float* to_part = gives ? pair_o : p.part_o + static_cast<long long>(part_at(own)) * kRows * kDim + my_row * 8;
+      const int part_step = gives ? kHalf : kRows;         // from eight columns to the next eight
+      T* to_out = static_cast<T*>(p.out) + tok * p.o_ts + head * p.o_hs;
 #pragma unroll 1
-        for (int c = 0; c < kDim; c += 32) {
-          uint32_t o[32];
-          if (keys) {
-            tmem_ld32(o_tmem + c, o);
-            tmem_ld_wait();
-          }
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(mul == 0.f ? 0.f : __uint_as_float(o[e]) * mul);
-          if (mul_other != 0.f) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(pair_o + c + e));
-              o[e] = __float_as_uint(fmaf(x.x, mul_other, __uint_as_float(o[e])));
-              o[e + 1] = __float_as_uint(fmaf(x.y, mul_other, __uint_as_float(o[e + 1])));
-              o[e + 2] = __float_as_uint(fmaf(x.z, mul_other, __uint_as_float(o[e + 2])));
-              o[e + 3] = __float_as_uint(fmaf(x.w, mul_other, __uint_as_float(o[e + 3])));
-            }
-          }
-          if (real && (split || gives)) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              const uint32_t v[8] = {o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5], o[e + 6], o[e + 7]};
-              store32(to_part + c + e, v, true);
-            }
-          } else if (real) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 16) {
-              const int at = c + e;
-              uint32_t v[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                v[k] = Type<T>::pack(__uint_as_float(o[e + 2 * k]), __uint_as_float(o[e + 2 * k + 1]));
-              if (at + 16 <= p.dim) store32(to_out + c + e, v, cp.out32);
-              else if (at < p.dim) *reinterpret_cast<uint4*>(to_out + c + e) = make_uint4(v[0], v[1], v[2], v[3]);
-            }
-          }
-          __syncwarp();
-        }
-        tc_fence_before();
-        if (real) {
-          if (gives) *pair_l = lse2;
-          else if (split) p.part_l[slot * kRows + my_row] = lse2;
-          else if (p.lse) p.lse[tok * p.heads + head] = lse2 * kLn2;
-        }
-      }
-      if (gives) meet();
-      if (pair) meet();      // the scratch has been read
-      if (split) {
-        // All softmax threads come here for every split item.
-        const int c0 = w.c0, c1 = w.c1;
-        meet();
-        if (threadIdx.x == 0) {
-          __threadfence();                                 // covers what the others wrote before the barrier
-          const unsigned seen = atomicAdd(p.counters + c0, 1u);
-          ctl.last_one = seen == static_cast<unsigned>(c1 - c0);
-          if (ctl.last_one) p.counters[c0] = 0;
-        }
-        meet();
-        if (ctl.last_one) {
+      for (bool first = true;; first = false) {
+        const bool joins = last && !gives;
+        if (joins) {
           __threadfence();
-          // Each row's log-sum over all parts (one thread a row); a part then
-          // weighs exp2(its own - that).
-          if (threadIdx.x < rows) {
-            const int row = threadIdx.x;
-            float top = kNegInf, sum = 0.f;
-#pragma unroll 4
-            for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(p.part_l + (2 * c + (c == c0)) * kRows + row));
-            const float ref = top == kNegInf ? 0.f : top;
-#pragma unroll 4
-            for (int c = c0; c <= c1; ++c)
-              sum += exp2_fast(__ldcg(p.part_l + (2 * c + (c == c0)) * kRows + row) - ref);
-            ctl.row_lse[row] = sum == 0.f ? kNegInf : ref + log2f(sum);
-          }
-          meet();
-          // Eight columns a thread, so that a part's row is read and the output's
-          // written in whole sectors; kBatch rows at once for loads in flight.
-          constexpr int kLanes = kDim / 8, kRowStep = kSoftmaxThreads / kLanes, kBatch = 4;
-          const int col = threadIdx.x % kLanes * 8;
-          for (int r0 = threadIdx.x / kLanes; r0 < rows; r0 += kBatch * kRowStep) {
-            float acc[kBatch][8] = {}, lse2r[kBatch];
+          if (threadIdx.x == 0) p.counters[c0] = 0;
+          // the log-sum over all parts, in their order; a part then weighs exp2(its own - that)
+          float top = lse2, sum = 0.f;
+#pragma unroll 1
+          for (int c = c0; c <= c1; ++c)
+            if (c != own) top = fmaxf(top, __ldcg(p.part_l + part_at(c) * kRows + my_row));
+          const float ref = top == kNegInf ? 0.f : top;
+#pragma unroll 1
+          for (int c = c0; c <= c1; ++c)
+            sum += exp2_fast((c == own ? lse2 : __ldcg(p.part_l + part_at(c) * kRows + my_row)) - ref);
+          row_lse = sum == 0.f ? kNegInf : ref + log2f(sum);
+          base = sum == 0.f ? 0.f : row_lse;
+        }
+        const bool writes_part = gives || (split && !last);
+        if (mine && (first || !gives)) {
+#pragma unroll 1
+          for (int c = 0; c < kDim; c += 32) {
+            // 32 columns of this thread's row, joined with the other half's
+            uint32_t o[32];
+            if (keys) {
+              __syncwarp();
+              tmem_ld32(o_tmem + c, o);
+              tmem_ld_wait();
+            }
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) lse2r[k] = r0 + k * kRowStep < rows ? ctl.row_lse[r0 + k * kRowStep] : kNegInf;
-            for (int c = c0; c <= c1; ++c) {
-              const long long from = (2 * c + (c == c0)) * kRows + r0;
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(mul == 0.f ? 0.f : __uint_as_float(o[e]) * mul);
+            if (mul_other != 0.f) {
 #pragma unroll
-              for (int k = 0; k < kBatch; ++k) {
-                if (lse2r[k] == kNegInf) continue;         // past the rows, or nothing seen
-                const float f = exp2_fast(__ldcg(p.part_l + from + k * kRowStep) - lse2r[k]);
-                const float4* src = reinterpret_cast<const float4*>(p.part_o + (from + k * kRowStep) * kDim + col);
-                const float4 a = __ldcg(src), b = __ldcg(src + 1);
-                acc[k][0] += f * a.x, acc[k][1] += f * a.y, acc[k][2] += f * a.z, acc[k][3] += f * a.w;
-                acc[k][4] += f * b.x, acc[k][5] += f * b.y, acc[k][6] += f * b.z, acc[k][7] += f * b.w;
+              for (int e = 0; e < 32; e += 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(pair_o + (c + (e & ~7)) * kHalf + (e & 4)));
+                o[e] = __float_as_uint(fmaf(x.x, mul_other, __uint_as_float(o[e])));
+                o[e + 1] = __float_as_uint(fmaf(x.y, mul_other, __uint_as_float(o[e + 1])));
+                o[e + 2] = __float_as_uint(fmaf(x.z, mul_other, __uint_as_float(o[e + 2])));
+                o[e + 3] = __float_as_uint(fmaf(x.w, mul_other, __uint_as_float(o[e + 3])));
               }
             }
+            if (joins) {
+              float acc[32];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-              const int r = r0 + k * kRowStep;
-              if (r >= rows) continue;
-              const int gr = w.row0 + r, tr = p.group_div.div(gr), hr = w.h * p.group + gr - tr * p.group;
-              const long long at = w.q0 + tr;
-              uint4 v;
-              v.x = Type<T>::pack(acc[k][0], acc[k][1]);
-              v.y = Type<T>::pack(acc[k][2], acc[k][3]);
-              v.z = Type<T>::pack(acc[k][4], acc[k][5]);
-              v.w = Type<T>::pack(acc[k][6], acc[k][7]);
-              if (col < p.dim)
-                *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at * p.o_ts + hr * p.o_hs + col) = v;
-              if (p.lse && col == 0) p.lse[at * p.heads + hr] = lse2r[k] * kLn2;
+              for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+#pragma unroll 1
+              for (int i = c0; i <= c1; ++i) {
+                if (i == own) {
+                  const float f = exp2_fast(lse2 - base);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) acc[e] = fmaf(f, __uint_as_float(o[e]), acc[e]);
+                } else {
+                  const float f = exp2_fast(__ldcg(p.part_l + part_at(i) * kRows + my_row) - base);
+                  const float* src = p.part_o + (static_cast<long long>(part_at(i)) * kDim + c) * kRows + my_row * 8;
+#pragma unroll
+                  for (int e = 0; e < 32; e += 4) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4*>(src + (e & ~7) * kRows + (e & 4)));
+                    acc[e] = fmaf(f, x.x, acc[e]);
+                    acc[e + 1] = fmaf(f, x.y, acc[e + 1]);
+                    acc[e + 2] = fmaf(f, x.z, acc[e + 2]);
+                    acc[e + 3] = fmaf(f, x.w, acc[e + 3]);
+                  }
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(acc[e]);
+            }
+            if (real && writes_part) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                const uint32_t v[8] = {o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5], o[e + 6], o[e + 7]};
+                store32(to_part + (c + e) * part_step, v, true);
+              }
+            } else if (real) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 16) {
+                const int at = c + e;
+                uint32_t v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  v[i] = Type<T>::pack(__uint_as_float(o[e + 2 * i]), __uint_as_float(o[e + 2 * i + 1]));
+                if (at + 16 <= p.dim) store32(to_out + at, v, cp.out32);
+                else if (at < p.dim) *reinterpret_cast<uint4*>(to_out + at) = make_uint4(v[0], v[1], v[2], v[3]);
+              }
             }
           }
+          if (real) {
+            if (gives) *pair_l = lse2;
+            else if (writes_part) p.part_l[part_at(own) * kRows + my_row] = lse2;
+            else if (p.lse) p.lse[tok * p.heads + head] = row_lse * kLn2;
+          }
         }
-        meet();                    // ctl.last_one has been read
+        if (gives && first) meet();                        // (half 0 of the pair is waiting)
+        if (!split || last) break;
+        meet();
+        if (threadIdx.x == 0) {
+          __threadfence();                                 // covers what the others wrote before they met
+          ctl.last_one = atomicAdd(p.counters + c0, 1u) == static_cast<unsigned>(c1 - c0);
+        }
+        meet();
+        last = ctl.last_one;
+        if (!last) break;
       }
+      tc_fence_before();
+      if (pair || split) meet();                           // scratch and last_one have been read
       job_done(k);
     }
   }
@@ -846,8 +854,7 @@ cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const ChunkPara
   const cudaError_t e =
       ensure_smem_limit(reinterpret_cast<const void*>(paged_chunk_kernel<T, kDim>), kSmem<kDim>);
   if (e != cudaSuccess) return e;
-  paged_chunk_kernel<T, kDim><<<ctas, kThreads, kSmem<kDim>, stream>>>(km, vm, cp);
-  return cudaGetLastError();
+  return launch_dependent(paged_chunk_kernel<T, kDim>, ctas, kThreads, kSmem<kDim>, stream, km, vm, cp);
 }
 
 }  // namespace

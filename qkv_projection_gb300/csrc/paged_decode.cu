@@ -33,7 +33,8 @@ constexpr int kUnitKeys = kWarps * kStepKeys;    // 64
 constexpr int kRows = kPagedDecodeRows;
 constexpr int kCtasPerSm = 2;
 constexpr int kMinUnits = 2;                     // units worth a CTA of their own
-using Walk = PagedWalk<kRows, kUnitKeys>;
+constexpr int kWhole = 0;                        // units of an item that is not split
+using Walk = PagedWalk<kRows, kUnitKeys, kPagedMaxLen, kWhole>;    // (no heavy items)
 using Span = PagedSpan<kUnitKeys>;
 
 template <int kDim> struct Shape {
@@ -104,8 +105,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   __shared__ float warp_m[kWarps][kRows], warp_l[kWarps][kRows];
   __shared__ int last_one;
 
+  allow_dependents_launch();
+  grid_dependency_wait();
   PagedShare share;
-  if (!paged_share<kRows, kUnitKeys, kThreads>(p, blockIdx.x, gridDim.x, kMinUnits, sums, &place, &share)) return;
+  if (!paged_share<kThreads>(p, blockIdx.x, gridDim.x, kMinUnits, sums, &place, &share)) return;
   Walk w = place;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -120,11 +123,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   // this lane's rows of the score tile
   const int row_a = lane >> 2, row_b = row_a + 8;
 
-  while (w.at < share.end) {
+  for (;;) {
     const Span span(p, w.s, w.row0(), w.row1(p));
     const int rows = w.row1(p) - w.row0();
-    const int u0 = w.unit;
-    const int u1 = static_cast<int>(min(static_cast<long long>(w.units), u0 + (share.end - w.at)));
+    const int u0 = w.unit, u1 = w.unit_at(p, share.end);
+    if (u1 <= u0) break;
     const int steps = span.hi > 0 ? u1 - u0 : 0;
     const T* kbase = static_cast<const T*>(p.kc) + w.h * p.k_hs + chunk * 8;
     const T* vbase = static_cast<const T*>(p.vc) + w.h * p.v_hs + chunk * 8;
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
           *reinterpret_cast<float4*>(dst + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
         if (col == 0) p.part_l[slot * kRows + row] = lse2;
       }
-      const int c0 = share.owner(w.at - u0), c1 = share.owner(w.at - u0 + w.units - 1);
+      const int c0 = share.owner(w.place_of(p, 0)), c1 = share.owner(w.place_of(p, w.units - 1));
       __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
@@ -424,6 +427,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     __syncthreads();       // shared memory is free for the next item
     if (u1 < w.units) break;
     w.next_item(p);
+    if (w.b >= p.batch) break;
   }
 }
 
@@ -432,8 +436,7 @@ cudaError_t launch(const PagedParams& p, int ctas, cudaStream_t stream) {
   const void* kernel = reinterpret_cast<const void*>(paged_decode_kernel<T, kDim>);
   const cudaError_t e = ensure_smem_limit(kernel, Shape<kDim>::kSmem);
   if (e != cudaSuccess) return e;
-  paged_decode_kernel<T, kDim><<<ctas, kThreads, Shape<kDim>::kSmem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(paged_decode_kernel<T, kDim>, ctas, kThreads, Shape<kDim>::kSmem, stream, p);
 }
 
 }  // namespace

@@ -21,6 +21,7 @@
 
 #include <cstdint>
 
+#include "kaio_device.cuh"
 #include "kaio_internal.h"
 
 namespace kaio {
@@ -104,6 +105,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const int t0 = static_cast<int>(blockIdx.x) * kp.tokens_per_cta;
   const int nt = min(kp.tokens_per_cta, p.tokens - t0);
   const int R = p.pairs;
+  allow_dependents_launch();
+  grid_dependency_wait();
 
   for (int i = threadIdx.x; i < nt * R; i += kRopeThreads) {
     const int t = i / R, pair = i - t * R;
@@ -255,10 +258,8 @@ cudaError_t launch(const RopeParams& r, int num_sms, cudaStream_t stream) {
   const int per_token = (r.q_heads + r.kv_heads) * rot + r.kv_heads * copy;
   const int tokens = r.tokens >= 8 * num_sms * kRopeMaxTokens ? kRopeMaxTokens : 1;
   const RopeKernelParams kp{r, FastDiv(per_token), FastDiv(rot), FastDiv(copy), tokens};
-  const unsigned grid = static_cast<unsigned>((r.tokens + tokens - 1) / tokens);
-  if (vec) rope_kernel<T, true><<<grid, kRopeThreads, 0, stream>>>(kp);
-  else rope_kernel<T, false><<<grid, kRopeThreads, 0, stream>>>(kp);
-  return cudaGetLastError();
+  const int grid = (r.tokens + tokens - 1) / tokens;
+  return launch_dependent(vec ? rope_kernel<T, true> : rope_kernel<T, false>, grid, kRopeThreads, 0, stream, kp);
 }
 
 }  // namespace

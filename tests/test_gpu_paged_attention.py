@@ -363,3 +363,15 @@ def test_few_rows_of_a_chunk_share_the_keys_between_two_halves(n, kv):
     for mask in ({}, dict(window=100, sinks=3)):
         Problem([(n, kv), (n, kv - 3)], 8, 2, 128, 16, "bfloat16", seed=kv).verify(**mask)
         Problem([(n, kv), (0, 3), (n + 1, kv)], 4, 1, 64, 32, seed=n).verify(**mask)
+
+
+def test_split_items_joined_by_whichever_part_comes_last():
+    """The parts of an item that several CTAs share finish in any order; repeated calls
+    go through all of the ways to join them."""
+    import torch
+    for args, lens in (((40, 2, 64, 16), [(1, 1000), (1, 2311)]), ((8, 1, 128, 32, "bfloat16"), [(64, 5000), (3, 900)])):
+        p = Problem(lens, *args, seed=40)
+        ws = kaio.paged_attention_workspace()
+        first = p.verify()
+        for _ in range(50):
+            assert all(torch.equal(a, b) for a, b in zip(first, p.run(workspace=ws)))
