@@ -175,7 +175,7 @@ struct PagedShare {
 
 // Found by all threads of the CTA together: the share of CTA `cta`, and the place of
 // its first unit. Every thread sums a run of sequences; a scan gives the total and
-// the run in which the share begins. `sums` holds kThreads values in shared memory.
+// the run in which the share begins. `sums` holds a value for each warp in shared memory.
 // Returns false if the share is empty.
 template <int kThreads, typename Walk>
 __device__ bool paged_share(const PagedParams& p, int cta, int grid, int min_units, long long* sums, Walk* place,
@@ -186,16 +186,20 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, int min_uni
   long long mine = 0;
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) mine += p.kv_heads * Walk::head_length(p, paged_seq(p, b));
-  sums[tid] = mine;
-  __syncthreads();
-#pragma unroll 1
-  for (int d = 1; d < kThreads; d <<= 1) {
-    const long long add = tid >= d ? sums[tid - d] : 0;
-    __syncthreads();
-    sums[tid] += add;
-    __syncthreads();
+  long long upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long add = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+    if ((tid & 31) >= d) upto += add;
   }
-  const long long total = sums[kThreads - 1];
+  if ((tid & 31) == 31) sums[tid >> 5] = upto;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i == (tid >> 5)) upto += total;
+    total += sums[i];
+  }
   if (total == 0) return false;
   share->ctas = static_cast<int>(min(static_cast<long long>(grid), max(1ll, paged_div(total, min_units))));
   if (cta >= share->ctas) return false;
@@ -203,7 +207,7 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, int min_uni
   share->more = static_cast<int>(total - share->each * share->ctas);
   share->begin = cta * share->each + min(cta, share->more);
   share->end = share->begin + share->each + (cta < share->more ? 1 : 0);
-  const long long upto = sums[tid], from = upto - mine;
+  const long long from = upto - mine;
   if (share->begin >= from && share->begin < upto) {
     long long left = share->begin - from;
     Walk w;

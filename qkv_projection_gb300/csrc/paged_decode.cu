@@ -96,13 +96,16 @@ __device__ __forceinline__ float quad_sum(float v) {
   return v + __shfl_xor_sync(0xFFFFFFFFu, v, 2);
 }
 
+// Shared memory of a CTA: a ring for each warp. Between items the first stage
+// already takes the next item's first keys; the others hold what the warps and CTAs
+// tell each other (kScratch floats of each warp's are used as one array).
 template <typename T, int kDim>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(const __grid_constant__ PagedParams p) {
   using S = Shape<kDim>;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long sums[kThreads];
+  __shared__ long long sums[kWarps];
   __shared__ Walk place;
-  __shared__ float warp_m[kWarps][kRows], warp_l[kWarps][kRows];
+  __shared__ float warp_m[kWarps][kRows], warp_l[kWarps][kRows], own_lse[kRows];
   __shared__ int last_one;
 
   allow_dependents_launch();
@@ -112,9 +115,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   Walk w = place;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  unsigned char* ring = smem + warp * S::kStages * S::kStage;
+  constexpr int kRing = S::kStages * S::kStage;
+  unsigned char* ring = smem + warp * kRing;
   const uint32_t ring_addr = smem_u32(ring);
   const int page_mask = (1 << p.page_shift) - 1;
+  // rows of the warps' outputs are padded by eight floats: four rows' stores then fall on different banks
+  constexpr int kPad = kDim + 8;
+  auto scratch = [&](int of_warp) { return reinterpret_cast<float*>(smem + of_warp * kRing + S::kStage); };
+  constexpr int kScratch = 4096;
+  static_assert(kScratch * 4 <= kRing - S::kStage && kRows * kPad <= kScratch, "scratch");
+  auto weight_at = [&](int i) { return scratch(i / kScratch) + i % kScratch; };
 
   // this lane's place in a step's copies: one chunk of every (32 / kChunks)-th key
   const int chunk = lane % S::kChunks, key_in_step = lane / S::kChunks;
@@ -123,23 +133,79 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   // this lane's rows of the score tile
   const int row_a = lane >> 2, row_b = row_a + 8;
 
+  // What the copies of the item at `w` go by.
+  int lo, hi, first, u0, u1, steps, ids, ids_next;
+  Span span(p, w.s, w.row0(), w.row1(p));
+  const T *kbase, *vbase;
+  const int* table;
+  // Page ids of 32 steps at a time, one a lane; the next 32 are fetched while these are used.
+  auto page_of = [&](int step) {
+    int id = -1;
+    if (step < steps) {
+      const int k0 = span.key0(u0 + step) + warp * kStepKeys;
+      const bool seen = k0 < hi && (k0 + kStepKeys > lo || k0 < first);
+      if (seen) id = table[k0 >> p.page_shift];
+      if (id >= p.num_pages) id = -1;
+    }
+    return id;
+  };
+  auto issue = [&](int step) {
+    if (step < steps) {
+      if (step > 0 && (step & 31) == 0) {
+        ids = ids_next;
+        ids_next = page_of(step + 32 + lane);
+      }
+      const int id = __shfl_sync(0xFFFFFFFFu, ids, step & 31);
+      const int k0 = span.key0(u0 + step) + warp * kStepKeys;
+      const long long slot0 = k0 & page_mask;
+      const T* kp = kbase + (id < 0 ? 0 : id * p.k_ps + slot0 * p.k_ss);
+      const T* vp = vbase + (id < 0 ? 0 : id * p.v_ps + slot0 * p.v_ss);
+      unsigned char* st = ring + (step % S::kStages) * S::kStage;
+#pragma unroll
+      for (int i = 0; i < kStepKeys / kKeyStep; ++i) {
+        const int key = key_in_step + i * kKeyStep;
+        const int j = k0 + key;
+        const bool real = id >= 0 && chunk_real && j < hi && (j >= lo || j < first);
+        const int at = key * S::kRowBytes + ((chunk ^ (key & 7)) << 4);
+        cp_async16(st + at, real ? kp + key * p.k_ss : static_cast<const T*>(p.kc), real ? 16 : 0);
+        cp_async16(st + S::kTile + at, real ? vp + key * p.v_ss : static_cast<const T*>(p.vc), real ? 16 : 0);
+      }
+    }
+    cp_async_commit();
+  };
+  // Begins the item at `w` (its page ids and first step); false if the share ends before it.
+  auto begin = [&] {
+    if (w.b >= p.batch) return false;
+    u0 = w.unit;
+    u1 = w.unit_at(p, share.end);
+    if (u1 <= u0) return false;
+    span = Span(p, w.s, w.row0(), w.row1(p));
+    lo = span.lo, hi = span.hi, first = span.first;
+    steps = hi > 0 ? u1 - u0 : 0;
+    kbase = static_cast<const T*>(p.kc) + w.h * p.k_hs + chunk * 8;
+    vbase = static_cast<const T*>(p.vc) + w.h * p.v_hs + chunk * 8;
+    table = p.table + w.b * p.table_stride;
+    ids = page_of(lane);
+    ids_next = page_of(32 + lane);
+    issue(0);
+    return true;
+  };
+  if (!begin()) return;
+
+#pragma unroll 1
   for (;;) {
-    const Span span(p, w.s, w.row0(), w.row1(p));
-    const int rows = w.row1(p) - w.row0();
-    const int u0 = w.unit, u1 = w.unit_at(p, share.end);
-    if (u1 <= u0) break;
-    const int steps = span.hi > 0 ? u1 - u0 : 0;
-    const T* kbase = static_cast<const T*>(p.kc) + w.h * p.k_hs + chunk * 8;
-    const T* vbase = static_cast<const T*>(p.vc) + w.h * p.v_hs + chunk * 8;
+    const PagedSeq seq = w.s;
+    const int rows = w.row1(p) - w.row0(), row0 = w.row0(), head0 = w.h * p.group;
+    const bool split = u0 != 0 || u1 != w.units;
+    const int c0 = split ? share.owner(w.place_of(p, 0)) : 0, c1 = split ? share.owner(w.place_of(p, w.units - 1)) : 0;
 
     // Q fragments (A operand): rows past the item's are zero
     uint32_t qf[kDim / 16][4];
     {
-      const int ra = min(row_a, rows - 1), rb = min(row_b, rows - 1);
-      const int ta = (w.row0() + ra) / p.group, tb = (w.row0() + rb) / p.group;
-      const int ha = w.h * p.group + (w.row0() + ra) % p.group, hb = w.h * p.group + (w.row0() + rb) % p.group;
-      const T* qa = static_cast<const T*>(p.q) + (w.s.q0 + ta) * p.q_ts + ha * p.q_hs;
-      const T* qb = static_cast<const T*>(p.q) + (w.s.q0 + tb) * p.q_ts + hb * p.q_hs;
+      const int ra = row0 + min(row_a, rows - 1), rb = row0 + min(row_b, rows - 1);
+      const int ta = p.group_div.div(ra), tb = p.group_div.div(rb);
+      const T* qa = static_cast<const T*>(p.q) + (seq.q0 + ta) * p.q_ts + (head0 + ra - ta * p.group) * p.q_hs;
+      const T* qb = static_cast<const T*>(p.q) + (seq.q0 + tb) * p.q_ts + (head0 + rb - tb * p.group) * p.q_hs;
 #pragma unroll
       for (int ks = 0; ks < kDim / 16; ++ks) {
 #pragma unroll
@@ -151,56 +217,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
         }
       }
     }
-    const PagedRow vis_a(p, w.s, w.row0() + min(row_a, rows - 1)), vis_b(p, w.s, w.row0() + min(row_b, rows - 1));
+    const PagedRow vis_a(p, seq, row0 + min(row_a, rows - 1)), vis_b(p, seq, row0 + min(row_b, rows - 1));
     // keys in [all_lo, all_hi) are seen by every row
-    const int all_hi = PagedRow(p, w.s, w.row0()).hi, all_lo = PagedRow(p, w.s, w.row1(p) - 1).lo;
+    const int all_hi = PagedRow(p, seq, row0).hi, all_lo = PagedRow(p, seq, row0 + rows - 1).lo;
 
     float o[kDim / 8][4];
 #pragma unroll
     for (int n = 0; n < kDim / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     float m_a = kNegInf, m_b = kNegInf, l_a = 0.f, l_b = 0.f;
 
-    // Page ids of 32 steps at a time, one a lane; the next 32 are fetched while these are used.
-    const int* table = p.table + w.b * p.table_stride;
-    auto page_of = [&](int step) {
-      int id = -1;
-      if (step < steps) {
-        const int k0 = span.key0(u0 + step) + warp * kStepKeys;
-        const bool seen = k0 < span.hi && (k0 + kStepKeys > span.lo || k0 < span.first);
-        if (seen) id = table[k0 >> p.page_shift];
-        if (id >= p.num_pages) id = -1;
-      }
-      return id;
-    };
-    int ids = page_of(lane), ids_next = page_of(32 + lane);
-
-    auto issue = [&](int step) {
-      if (step < steps) {
-        if (step > 0 && (step & 31) == 0) {
-          ids = ids_next;
-          ids_next = page_of(step + 32 + lane);
-        }
-        const int id = __shfl_sync(0xFFFFFFFFu, ids, step & 31);
-        const int k0 = span.key0(u0 + step) + warp * kStepKeys;
-        const long long slot0 = k0 & page_mask;
-        const T* kp = kbase + (id < 0 ? 0 : id * p.k_ps + slot0 * p.k_ss);
-        const T* vp = vbase + (id < 0 ? 0 : id * p.v_ps + slot0 * p.v_ss);
-        unsigned char* st = ring + (step % S::kStages) * S::kStage;
-#pragma unroll
-        for (int i = 0; i < kStepKeys / kKeyStep; ++i) {
-          const int key = key_in_step + i * kKeyStep;
-          const int j = k0 + key;
-          const bool real = id >= 0 && chunk_real && j < span.hi && (j >= span.lo || j < span.first);
-          const int at = key * S::kRowBytes + ((chunk ^ (key & 7)) << 4);
-          cp_async16(st + at, real ? kp + key * p.k_ss : static_cast<const T*>(p.kc), real ? 16 : 0);
-          cp_async16(st + S::kTile + at, real ? vp + key * p.v_ss : static_cast<const T*>(p.vc), real ? 16 : 0);
-        }
-      }
-      cp_async_commit();
-    };
-
 #pragma unroll 1
-    for (int i = 0; i < S::kStages - 1; ++i) issue(i);
+    for (int i = 1; i < S::kStages - 1; ++i) issue(i);
 #pragma unroll 1
     for (int step = 0; step < steps; ++step) {
       cp_async_wait<S::kStages - 2>();
@@ -208,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       issue(step + S::kStages - 1);
       const uint32_t st = ring_addr + (step % S::kStages) * S::kStage;
       const int k0 = span.key0(u0 + step) + warp * kStepKeys;
-      if (k0 >= span.hi) continue;      // this warp's keys of the last unit lie past the end
+      if (k0 >= hi) continue;      // this warp's keys of the last unit lie past the end
 
       // scores of 16 keys: two column tiles of eight
       float s[2][4] = {};
@@ -272,162 +299,147 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     }
     cp_async_wait<0>();
     __syncwarp();
+    // Of a split item the CTA that finds all other parts written is the last.
+    unsigned seen = 0;
+    if (split && threadIdx.x == 0)
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(p.counters + c0) : "memory");
 
-    // The four warps' results are joined through shared memory (the ring's first stages).
+    // The next item's first keys are on their way while this one is finished.
+    const bool ends = u1 == w.units;
+    bool more = false;
+    if (ends) {
+      w.next_item(p);
+      more = begin();
+    }
+
+    // The four warps' results: maxima, sums and outputs of the real rows.
     l_a = quad_sum(l_a);
     l_b = quad_sum(l_b);
-    float* mine = reinterpret_cast<float*>(ring);
     if ((lane & 3) == 0) {
       warp_m[warp][row_a] = m_a;
       warp_m[warp][row_b] = m_b;
       warp_l[warp][row_a] = l_a;
       warp_l[warp][row_b] = l_b;
     }
+    float* mine = scratch(warp);
 #pragma unroll
     for (int n = 0; n < kDim / 8; ++n) {
       const int c = 8 * n + 2 * (lane & 3);
-      *reinterpret_cast<float2*>(mine + row_a * kDim + c) = make_float2(o[n][0], o[n][1]);
-      *reinterpret_cast<float2*>(mine + row_b * kDim + c) = make_float2(o[n][2], o[n][3]);
+      if (row_a < rows) *reinterpret_cast<float2*>(mine + row_a * kPad + c) = make_float2(o[n][0], o[n][1]);
+      if (row_b < rows) *reinterpret_cast<float2*>(mine + row_b * kPad + c) = make_float2(o[n][2], o[n][3]);
     }
+    if (threadIdx.x == 0) last_one = split && seen == static_cast<unsigned>(c1 - c0);
     __syncthreads();
 
-    // thread: one row, kSeg columns
-    constexpr int kSeg = kRows * kDim / kThreads;
-    const int row = threadIdx.x / (kThreads / kRows), col = threadIdx.x % (kThreads / kRows) * kSeg;
-    const bool whole_item = u0 == 0 && u1 == w.units;
-    const int tok = w.s.q0 + (w.row0() + row) / p.group, head = w.h * p.group + (w.row0() + row) % p.group;
-    float acc[kSeg];
-    float lse2 = kNegInf;
-    if (row < rows) {
+    // A thread takes four columns of a row at a time; up to kMine of them.
+    constexpr int kQuads = kDim / 4, kMine = kRows * kQuads / kThreads;
+    const int quads = rows * kQuads;
+    float4 acc[kMine];
+    float lse2[kMine];
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+      const int i = threadIdx.x + k * kThreads, row = i / kQuads, col = i % kQuads * 4;
+      acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      lse2[k] = kNegInf;
+      if (i >= quads) continue;
       float top = kNegInf, sum = 0.f, f[kWarps];
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) top = fmaxf(top, warp_m[i][row]);
+      for (int j = 0; j < kWarps; ++j) top = fmaxf(top, warp_m[j][row]);
       const float ref = top == kNegInf ? 0.f : top;
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        f[i] = exp2_fast(warp_m[i][row] - ref);
-        sum += f[i] * warp_l[i][row];
+      for (int j = 0; j < kWarps; ++j) {
+        f[j] = exp2_fast(warp_m[j][row] - ref);
+        sum += f[j] * warp_l[j][row];
       }
       // the sum is zero exactly when nothing was seen: zeros, and a log-sum of -inf
       // (a NaN score leaves a NaN sum)
-      lse2 = sum == 0.f ? kNegInf : ref + log2f(sum);
+      lse2[k] = sum == 0.f ? kNegInf : ref + log2f(sum);
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-      for (int c = 0; c < kSeg; ++c) acc[c] = 0.f;
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        const float* src = reinterpret_cast<const float*>(smem + i * S::kStages * S::kStage) + row * kDim + col;
-#pragma unroll
-        for (int c = 0; c < kSeg; c += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src + c);
-          acc[c] += f[i] * v.x;
-          acc[c + 1] += f[i] * v.y;
-          acc[c + 2] += f[i] * v.z;
-          acc[c + 3] += f[i] * v.w;
-        }
+      for (int j = 0; j < kWarps; ++j) {
+        const float4 v = *reinterpret_cast<const float4*>(scratch(j) + row * kPad + col);
+        acc[k].x += f[j] * v.x, acc[k].y += f[j] * v.y, acc[k].z += f[j] * v.z, acc[k].w += f[j] * v.w;
       }
-#pragma unroll
-      for (int c = 0; c < kSeg; ++c) acc[c] *= inv;
+      acc[k].x *= inv, acc[k].y *= inv, acc[k].z *= inv, acc[k].w *= inv;
+      if (col == 0) own_lse[row] = lse2[k];
     }
 
-    bool write = whole_item;
-    if (!whole_item) {
-      const int slot = 2 * static_cast<int>(blockIdx.x) + (u0 == 0 ? 1 : 0);
-      if (row < rows) {
-        float* dst = p.part_o + (static_cast<long long>(slot) * kRows + row) * kDim + col;
+    auto part_at = [&](int c) { return 2 * c + (c == c0 ? 1 : 0); };   // a CTA's part of an item is its first but where the item begins
+    bool last = split && last_one;
+    if (split && !last) {
 #pragma unroll
-        for (int c = 0; c < kSeg; c += 4)
-          *reinterpret_cast<float4*>(dst + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
-        if (col == 0) p.part_l[slot * kRows + row] = lse2;
+      for (int k = 0; k < kMine; ++k) {
+        const int i = threadIdx.x + k * kThreads;
+        if (i >= quads) continue;
+        *reinterpret_cast<float4*>(p.part_o + static_cast<long long>(part_at(blockIdx.x)) * kRows * kDim + i * 4) = acc[k];
+        if (i % kQuads == 0) p.part_l[part_at(blockIdx.x) * kRows + i / kQuads] = lse2[k];
       }
-      const int c0 = share.owner(w.place_of(p, 0)), c1 = share.owner(w.place_of(p, w.units - 1));
-      __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
-        const unsigned seen = atomicAdd(p.counters + c0, 1u);
-        last_one = seen == static_cast<unsigned>(c1 - c0);
-        if (last_one) p.counters[c0] = 0;
+        __threadfence();                                   // covers what the others wrote before they met
+        last_one = atomicAdd(p.counters + c0, 1u) == static_cast<unsigned>(c1 - c0);
       }
       __syncthreads();
-      if (last_one) {
-        // Few rows leave most threads without one: then 2, 4, 8 or 16 groups of
-        // threads take every 2nd, 4th, ... part, and are added up in shared memory.
-        __threadfence();
-        write = true;
-        int groups = kRows;
-        while (groups * rows > kRows) groups >>= 1;
-        const int group = row / (kRows / groups), r = row % (kRows / groups);
+      last = last_one;
+    }
+    if (last) {
+      // All parts' log-sums first, then each part weighs exp2(its own - the row's); always in
+      // the parts' order. This CTA's own part comes from its registers.
+      const int own = static_cast<int>(blockIdx.x), parts = c1 - c0 + 1;
+      __threadfence();
+      if (threadIdx.x == 0) p.counters[c0] = 0;
+      __syncthreads();                                     // the warps' outputs have been read, own_lse is written
+#pragma unroll 4
+      for (int i = threadIdx.x; i < parts * rows; i += kThreads) {
+        const int part = c0 + i / rows, row = i % rows;
+        *weight_at(i) = part == own ? own_lse[row] : __ldcg(p.part_l + part_at(part) * kRows + row);
+      }
+      __syncthreads();
+#pragma unroll 1
+      for (int i = threadIdx.x; i < rows; i += kThreads) {
         float top = kNegInf, sum = 0.f;
-#pragma unroll
-        for (int c = 0; c < kSeg; ++c) acc[c] = 0.f;
-        if (r < rows) {
-#pragma unroll 4
-          for (int c = c0; c <= c1; ++c)
-            top = fmaxf(top, __ldcg(p.part_l + (2 * c + (c == c0 ? 1 : 0)) * kRows + r));
-        }
+#pragma unroll 8
+        for (int c = 0; c < parts; ++c) top = fmaxf(top, *weight_at(c * rows + i));
         const float ref = top == kNegInf ? 0.f : top;
-        if (r < rows) {
-#pragma unroll 4
-          for (int c = c0 + group; c <= c1; c += groups) {
-            const int from = 2 * c + (c == c0 ? 1 : 0);
-            const float f = exp2_fast(__ldcg(p.part_l + from * kRows + r) - ref);
-            sum += f;
-            const float* src = p.part_o + (static_cast<long long>(from) * kRows + r) * kDim + col;
+#pragma unroll 8
+        for (int c = 0; c < parts; ++c) sum += exp2_fast(*weight_at(c * rows + i) - ref);
+        own_lse[i] = sum == 0.f ? kNegInf : ref + log2f(sum);
+      }
+      __syncthreads();
 #pragma unroll
-            for (int e = 0; e < kSeg; e += 4) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(src + e));
-              acc[e] += f * v.x;
-              acc[e + 1] += f * v.y;
-              acc[e + 2] += f * v.z;
-              acc[e + 3] += f * v.w;
-            }
-          }
+      for (int k = 0; k < kMine; ++k) {
+        const int i = threadIdx.x + k * kThreads, row = i / kQuads;
+        if (i >= quads) continue;
+        const float4 mine4 = acc[k];
+        lse2[k] = own_lse[row];
+        const float base = lse2[k] == kNegInf ? 0.f : lse2[k];
+        acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int c = 0; c < parts; ++c) {
+          const float f = exp2_fast(*weight_at(c * rows + row) - base);
+          const float4 v = c0 + c == own ? mine4
+                                         : __ldcg(reinterpret_cast<const float4*>(
+                                               p.part_o + static_cast<long long>(part_at(c0 + c)) * kRows * kDim + i * 4));
+          acc[k].x += f * v.x, acc[k].y += f * v.y, acc[k].z += f * v.z, acc[k].w += f * v.w;
         }
-        if (groups > 1) {
-          float* joined = reinterpret_cast<float*>(smem);     // [kRows][kDim], and the sums after it
-#pragma unroll
-          for (int c = 0; c < kSeg; c += 4)
-            *reinterpret_cast<float4*>(joined + row * kDim + col + c) =
-                make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
-          if (col == 0) joined[kRows * kDim + row] = sum;
-          __syncthreads();
-          if (row < rows) {
-            for (int g = 1; g < groups; ++g) {
-              const int other = row + g * (kRows / groups);
-              sum += joined[kRows * kDim + other];
-#pragma unroll
-              for (int c = 0; c < kSeg; c += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(joined + other * kDim + col + c);
-                acc[c] += v.x, acc[c + 1] += v.y, acc[c + 2] += v.z, acc[c + 3] += v.w;
-              }
-            }
-          }
-        }
-        lse2 = sum == 0.f ? kNegInf : ref + log2f(sum);
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-        for (int c = 0; c < kSeg; ++c) acc[c] *= inv;
       }
     }
-    if (write && row < rows) {
-      T* dst = static_cast<T*>(p.out) + tok * p.o_ts + head * p.o_hs + col;
+    if (!split || last) {
 #pragma unroll
-      for (int c = 0; c < kSeg; c += 8) {
-        if (col + c < p.dim) {
-          uint4 v;
-          v.x = Mma<T>::pack(acc[c], acc[c + 1]);
-          v.y = Mma<T>::pack(acc[c + 2], acc[c + 3]);
-          v.z = Mma<T>::pack(acc[c + 4], acc[c + 5]);
-          v.w = Mma<T>::pack(acc[c + 6], acc[c + 7]);
-          *reinterpret_cast<uint4*>(dst + c) = v;
-        }
+      for (int k = 0; k < kMine; ++k) {
+        const int i = threadIdx.x + k * kThreads, row = row0 + i / kQuads, col = i % kQuads * 4;
+        if (i >= quads) continue;
+        const int t = p.group_div.div(row);
+        const long long tok = seq.q0 + t;
+        const int head = head0 + row - t * p.group;
+        if (col < p.dim)
+          *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + tok * p.o_ts + head * p.o_hs + col) =
+              make_uint2(Mma<T>::pack(acc[k].x, acc[k].y), Mma<T>::pack(acc[k].z, acc[k].w));
+        if (p.lse && col == 0) p.lse[tok * p.heads + head] = lse2[k] * kLn2;
       }
-      if (p.lse && col == 0) p.lse[static_cast<long long>(tok) * p.heads + head] = lse2 * kLn2;
     }
-    __syncthreads();       // shared memory is free for the next item
-    if (u1 < w.units) break;
-    w.next_item(p);
-    if (w.b >= p.batch) break;
+    if (!more) break;
+    __syncthreads();       // the scratch is free for the next item's keys
   }
 }
 
