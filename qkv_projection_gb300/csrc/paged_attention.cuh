@@ -81,69 +81,6 @@ struct PagedRow {
   }
 };
 
-// A place in the line of units: an item, and a unit in it. In the line a unit of an
-// item with more than kHeavyRows rows counts twice (it takes about twice as long). An
-// item of at most kWhole places is not split: it belongs to the share that holds its
-// last place. (Writing and joining parts costs more than such an item's imbalance.)
-template <int kRows, int kKeys, int kHeavyRows, int kWhole>
-struct PagedWalk {
-  static constexpr int kWholeLength = kWhole;
-  int b, h, tile, tiles;      // item: sequence, K/V head, row tile of `tiles`
-  int unit, units;            // unit within the item
-  long long at;               // where in the line the item begins
-  PagedSeq s;
-
-  __device__ __forceinline__ static int row_tiles(const PagedParams& p, const PagedSeq& s) {
-    return (s.n * p.group + kRows - 1) / kRows;
-  }
-  __device__ __forceinline__ int row0() const { return tile * kRows; }
-  __device__ __forceinline__ int row1(const PagedParams& p) const { return min(tile * kRows + kRows, s.n * p.group); }
-  __device__ __forceinline__ static int item_units(const PagedParams& p, const PagedSeq& s, int tile) {
-    return PagedSpan<kKeys>(p, s, tile * kRows, min(tile * kRows + kRows, s.n * p.group)).units;
-  }
-  __device__ __forceinline__ static int item_weight(const PagedParams& p, const PagedSeq& s, int tile) {
-    return s.n * p.group - tile * kRows > kHeavyRows ? 2 : 1;
-  }
-  __device__ __forceinline__ bool heavy(const PagedParams& p) const { return item_weight(p, s, tile) == 2; }
-  __device__ __forceinline__ long long length(const PagedParams& p) const {
-    return static_cast<long long>(units) << (heavy(p) ? 1 : 0);
-  }
-  __device__ __forceinline__ static long long head_length(const PagedParams& p, const PagedSeq& s) {
-    long long u = 0;
-    const int tiles = row_tiles(p, s);
-#pragma unroll 1
-    for (int i = 0; i < tiles; ++i) u += item_units(p, s, i) * item_weight(p, s, i);
-    return u;
-  }
-  // The first unit past a CTA's share that ends at `end`. (A unit belongs to the
-  // share that holds the last of its places.)
-  __device__ __forceinline__ int unit_at(const PagedParams& p, long long end) const {
-    const long long to = max(end - at, 0ll);
-    if (to >= length(p)) return units;
-    return length(p) <= kWhole ? 0 : static_cast<int>(to >> (heavy(p) ? 1 : 0));
-  }
-  __device__ __forceinline__ long long place_of(const PagedParams& p, int u) const {
-    return at + ((static_cast<long long>(u) + 1) << (heavy(p) ? 1 : 0)) - 1;
-  }
-  // To the first unit of the next item (past the line's end: b == batch).
-  __device__ __forceinline__ void next_item(const PagedParams& p) {
-    at += length(p);
-    unit = 0;
-    if (++tile == tiles) {
-      tile = 0;
-      if (++h == p.kv_heads) {
-        h = 0;
-        do {
-          if (++b >= p.batch) return;
-          s = paged_seq(p, b);
-          tiles = row_tiles(p, s);
-        } while (tiles == 0);
-      }
-    }
-    units = item_units(p, s, tile);
-  }
-};
-
 // a / b for 0 <= a < 2^53, 0 < b < 2^31, by a rounded estimate and its correction
 // (the compiler's 64-bit division is some hundred instructions, and code is fetched
 // slowly at a kernel's start).
@@ -161,15 +98,65 @@ __device__ __forceinline__ long long paged_div(long long a, int b) {
   return q;
 }
 
-// One CTA's share [begin, end) of a line of `total` places among `ctas` CTAs: the
-// first total % ctas shares have one place more than the others.
+// A place in the line of units: an item, and a unit in it. An item of at most kWhole
+// units is not split: it belongs to the share that holds its last unit. (Writing and
+// joining parts costs more than such an item's imbalance.)
+template <int kRows, int kKeys, int kWhole>
+struct PagedWalk {
+  static constexpr int kWholeUnits = kWhole;
+  int b, h, tile, tiles;      // item: sequence, K/V head, row tile of `tiles`
+  int unit, units;            // unit within the item
+  long long at;               // where in the line the item begins
+  PagedSeq s;
+
+  __device__ __forceinline__ static int row_tiles(const PagedParams& p, const PagedSeq& s) {
+    return (s.n * p.group + kRows - 1) / kRows;
+  }
+  __device__ __forceinline__ int row0() const { return tile * kRows; }
+  __device__ __forceinline__ int row1(const PagedParams& p) const { return min(tile * kRows + kRows, s.n * p.group); }
+  __device__ __forceinline__ static int item_units(const PagedParams& p, const PagedSeq& s, int tile) {
+    return PagedSpan<kKeys>(p, s, tile * kRows, min(tile * kRows + kRows, s.n * p.group)).units;
+  }
+  __device__ __forceinline__ static long long head_length(const PagedParams& p, const PagedSeq& s) {
+    long long u = 0;
+    const int tiles = row_tiles(p, s);
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i) u += item_units(p, s, i);
+    return u;
+  }
+  // The first unit past a CTA's share that ends at `end`.
+  __device__ __forceinline__ int unit_at(long long end) const {
+    const long long to = max(end - at, 0ll);
+    return to >= units ? units : units <= kWhole ? 0 : static_cast<int>(to);
+  }
+  // To the first unit of the next item (past the line's end: b == batch).
+  __device__ __forceinline__ void next_item(const PagedParams& p) {
+    at += units;
+    unit = 0;
+    if (++tile == tiles) {
+      tile = 0;
+      if (++h == p.kv_heads) {
+        h = 0;
+        do {
+          if (++b >= p.batch) return;
+          s = paged_seq(p, b);
+          tiles = row_tiles(p, s);
+        } while (tiles == 0);
+      }
+    }
+    units = item_units(p, s, tile);
+  }
+};
+
+// One CTA's share [begin, end) of a line of `total` units among `ctas` CTAs: the
+// first total % ctas shares have one unit more than the others.
 struct PagedShare {
   long long begin, end, each;    // each = total / ctas
   int ctas, more;                // more = total % ctas
-  __device__ __forceinline__ int owner(long long place) const {
+  __device__ __forceinline__ int owner(long long unit) const {
     const long long first = (each + 1) * more;
-    if (place < first) return static_cast<int>(paged_div(place, static_cast<int>(each + 1)));
-    return more + static_cast<int>(paged_div(place - first, static_cast<int>(each)));
+    if (unit < first) return static_cast<int>(paged_div(unit, static_cast<int>(each + 1)));
+    return more + static_cast<int>(paged_div(unit - first, static_cast<int>(each)));
   }
 };
 
@@ -226,10 +213,10 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, int min_uni
 #pragma unroll 1
     for (w.tile = 0;; ++w.tile) {
       w.units = Walk::item_units(p, w.s, w.tile);
-      if (left < w.length(p)) break;
-      left -= w.length(p);
+      if (left < w.units) break;
+      left -= w.units;
     }
-    w.unit = w.length(p) <= Walk::kWholeLength ? 0 : static_cast<int>(left >> (w.heavy(p) ? 1 : 0));
+    w.unit = w.units <= Walk::kWholeUnits ? 0 : static_cast<int>(left);
     w.at = share->begin - left;
     *place = w;
   }

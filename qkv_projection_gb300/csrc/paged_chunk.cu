@@ -54,10 +54,10 @@ constexpr int kMmaWarp = 8, kLoadWarp = 10;   // and the one after each
 constexpr int kThreads = 384;
 // Registers a thread: 384 threads start with 168; 256 x 224 + 128 x 56 is the same total.
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
-constexpr int kMinUnits = 4;            // places of the line worth a CTA of their own
-constexpr int kWhole = 16;              // places of an item that is not split
+constexpr int kMinUnits = 4;            // units worth a CTA of their own
+constexpr int kWhole = 16;              // units of an item that is not split
 constexpr float kLazy = 8.f;            // growth of the maximum (log2) that renews the reference
-using Walk = PagedWalk<kRows, kKeys, kHalf, kWhole>;
+using Walk = PagedWalk<kRows, kKeys, kWhole>;
 using Span = PagedSpan<kKeys>;
 
 template <int kDim> struct Shape {
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           Walk& w = ctl.place;
           Job& job = ctl.jobs[k % kJobs];
-          const int u0 = any ? w.unit : 0, u1 = any && w.b < p.batch ? w.unit_at(p, ctl.share.end) : 0;
+          const int u0 = any ? w.unit : 0, u1 = any && w.b < p.batch ? w.unit_at(ctl.share.end) : 0;
           if (u1 <= u0) {
             job.mode = Mode::kEnd;
           } else {
@@ -304,8 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               job.plain1[half] = span.lo > 0 ? t1 - 1 : t1;
             }
             if (job.split) {
-              job.c0 = ctl.share.owner(w.place_of(p, 0));
-              job.c1 = ctl.share.owner(w.place_of(p, w.units - 1));
+              job.c0 = ctl.share.owner(w.at);
+              job.c1 = ctl.share.owner(w.at + w.units - 1);
             }
             if (last) w.next_item(p);
             else w.unit = w.units;                         // the share ends here
@@ -562,6 +562,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool mine = works(mode) || (mode == Mode::kNoKeys && rows > kHalf * half);
       const bool keys = mode != Mode::kNoKeys;
       bool q_next = false;
+      // Of a split item the CTA that finds all other parts written is the last.
+      auto look_for_others = [&] {
+        if (w.split && threadIdx.x == 0) {
+          unsigned seen;
+          asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(p.counters + w.c0) : "memory");
+          ctl.last_one = seen == static_cast<unsigned>(w.c1 - w.c0);
+        }
+      };
       float m = kNegInf, l = 0.f;                          // the row's reference (in units of S) and sum
       if (works(mode)) {
         if (!q_sent) {
@@ -659,6 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l += (sa.x + sa.y) + (sb.x + sb.y);
         }
         if (q_next) send_q();
+        look_for_others();
         wait(&ctl.o_done[half], o_phase);
         tc_fence_after();
         o_phase ^= 1;
@@ -667,15 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (keys) unit_count += n_units;
       q_sent = q_next;
 
-      // Of a split item the CTA that finds all other parts written is the last.
-      if (w.split) {
-        if (threadIdx.x == 0) {
-          unsigned seen;
-          asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(p.counters + w.c0) : "memory");
-          ctl.last_one = seen == static_cast<unsigned>(w.c1 - w.c0);
-        }
-        meet();
-      }
+      if (w.split) meet();                                 // last_one is known
 
       // Results of this thread's row: O / l and m + log2 l (nothing seen: zeros, -inf).
       const bool none = l == 0.f;                          // (a NaN score leaves l NaN)
@@ -719,12 +720,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the log-sum over all parts, in their order; a part then weighs exp2(its own - that)
           float top = lse2, sum = 0.f;
 #pragma unroll 1
-          for (int c = c0; c <= c1; ++c)
-            if (c != own) top = fmaxf(top, __ldcg(p.part_l + part_at(c) * kRows + my_row));
-          const float ref = top == kNegInf ? 0.f : top;
+          for (int pass = 0; pass < 2; ++pass) {
+            const float ref = top == kNegInf ? 0.f : top;
 #pragma unroll 1
-          for (int c = c0; c <= c1; ++c)
-            sum += exp2_fast((c == own ? lse2 : __ldcg(p.part_l + part_at(c) * kRows + my_row)) - ref);
+            for (int i = c0; i <= c1; i += 4) {
+              float x[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                x[k] = i + k > c1 ? kNegInf
+                       : i + k == own ? lse2
+                                      : __ldcg(p.part_l + part_at(i + k) * kRows + my_row);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if (pass == 0) top = fmaxf(top, x[k]);
+                else sum += exp2_fast(x[k] - ref);
+              }
+            }
+          }
+          const float ref = top == kNegInf ? 0.f : top;
           row_lse = sum == 0.f ? kNegInf : ref + log2f(sum);
           base = sum == 0.f ? 0.f : row_lse;
         }

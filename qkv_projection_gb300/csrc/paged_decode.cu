@@ -33,8 +33,7 @@ constexpr int kUnitKeys = kWarps * kStepKeys;    // 64
 constexpr int kRows = kPagedDecodeRows;
 constexpr int kCtasPerSm = 2;
 constexpr int kMinUnits = 2;                     // units worth a CTA of their own
-constexpr int kWhole = 0;                        // units of an item that is not split
-using Walk = PagedWalk<kRows, kUnitKeys, kPagedMaxLen, kWhole>;    // (no heavy items)
+using Walk = PagedWalk<kRows, kUnitKeys, 0>;
 using Span = PagedSpan<kUnitKeys>;
 
 template <int kDim> struct Shape {
@@ -177,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   auto begin = [&] {
     if (w.b >= p.batch) return false;
     u0 = w.unit;
-    u1 = w.unit_at(p, share.end);
+    u1 = w.unit_at(share.end);
     if (u1 <= u0) return false;
     span = Span(p, w.s, w.row0(), w.row1(p));
     lo = span.lo, hi = span.hi, first = span.first;
@@ -197,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     const PagedSeq seq = w.s;
     const int rows = w.row1(p) - w.row0(), row0 = w.row0(), head0 = w.h * p.group;
     const bool split = u0 != 0 || u1 != w.units;
-    const int c0 = split ? share.owner(w.place_of(p, 0)) : 0, c1 = split ? share.owner(w.place_of(p, w.units - 1)) : 0;
+    const int c0 = split ? share.owner(w.at) : 0, c1 = split ? share.owner(w.at + w.units - 1) : 0;
 
     // Q fragments (A operand): rows past the item's are zero
     uint32_t qf[kDim / 16][4];

@@ -59,8 +59,6 @@ template <> struct Pack<__nv_bfloat16> {
 };
 __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void from_f(float v, __half* o) { *o = __float2half_rn(v); }
-__device__ __forceinline__ void from_f(float v, __nv_bfloat16* o) { *o = __float2bfloat16_rn(v); }
 
 // Two vectors of eight values, rotated: `half` pairs a[e] with b[e]; otherwise
 // neighbours within each vector are pairs (a's first).
