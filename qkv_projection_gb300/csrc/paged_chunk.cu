@@ -52,8 +52,8 @@ constexpr int kKeys = 128;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kMmaWarp = 8, kLoadWarp = 10;   // and the one after each
 constexpr int kThreads = 384;
-// Registers a thread: 384 threads start with 168; 256 x 224 + 128 x 56 is the same total.
-constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
+// Registers a thread: 384 threads start with 168; 256 x 216 + 128 x 72 is the same total.
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr int kMinUnits = 4;            // units worth a CTA of their own
 constexpr int kWhole = 16;              // units of an item that is not split
 constexpr float kLazy = 8.f;            // growth of the maximum (log2) that renews the reference
