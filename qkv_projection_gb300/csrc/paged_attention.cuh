@@ -101,9 +101,10 @@ __device__ __forceinline__ long long paged_div(long long a, int b) {
 // A place in the line of units: an item, and a unit in it. An item of at most kWhole
 // units is not split: it belongs to the share that holds its last unit. (Writing and
 // joining parts costs more than such an item's imbalance.)
-template <int kRows, int kKeys, int kWhole>
+template <int kRows, int kKeys, int kWhole, int kPartWorthPercent>
 struct PagedWalk {
   static constexpr int kWholeUnits = kWhole;
+  static constexpr float kPartWorth = 0.01f * kPartWorthPercent;   // joining a part, in units
   int b, h, tile, tiles;      // item: sequence, K/V head, row tile of `tiles`
   int unit, units;            // unit within the item
   long long at;               // where in the line the item begins
@@ -117,11 +118,15 @@ struct PagedWalk {
   __device__ __forceinline__ static int item_units(const PagedParams& p, const PagedSeq& s, int tile) {
     return PagedSpan<kKeys>(p, s, tile * kRows, min(tile * kRows + kRows, s.n * p.group)).units;
   }
-  __device__ __forceinline__ static long long head_length(const PagedParams& p, const PagedSeq& s) {
+  __device__ __forceinline__ static long long head_length(const PagedParams& p, const PagedSeq& s, int* longest) {
     long long u = 0;
     const int tiles = row_tiles(p, s);
 #pragma unroll 1
-    for (int i = 0; i < tiles; ++i) u += item_units(p, s, i);
+    for (int i = 0; i < tiles; ++i) {
+      const int units = item_units(p, s, i);
+      u += units;
+      *longest = max(*longest, units);
+    }
     return u;
   }
   // The first unit past a CTA's share that ends at `end`.
@@ -165,30 +170,42 @@ struct PagedShare {
 // the run in which the share begins. `sums` holds a value for each warp in shared memory.
 // Returns false if the share is empty.
 template <int kThreads, typename Walk>
-__device__ bool paged_share(const PagedParams& p, int cta, int grid, int min_units, long long* sums, Walk* place,
+__device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* sums, Walk* place,
                             PagedShare* share) {
   const int tid = threadIdx.x;
   const int per = (p.batch + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
   long long mine = 0;
+  int longest = 0;
 #pragma unroll 1
-  for (int b = b0; b < b1; ++b) mine += p.kv_heads * Walk::head_length(p, paged_seq(p, b));
+  for (int b = b0; b < b1; ++b) mine += p.kv_heads * Walk::head_length(p, paged_seq(p, b), &longest);
   long long upto = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const long long add = __shfl_up_sync(0xFFFFFFFFu, upto, d);
     if ((tid & 31) >= d) upto += add;
   }
-  if ((tid & 31) == 31) sums[tid >> 5] = upto;
+  longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+  if ((tid & 31) == 31) {
+    sums[tid >> 5] = upto;
+    sums[kThreads / 32 + (tid >> 5)] = longest;
+  }
   __syncthreads();
   long long total = 0;
 #pragma unroll
   for (int i = 0; i < kThreads / 32; ++i) {
     if (i == (tid >> 5)) upto += total;
     total += sums[i];
+    longest = max(longest, static_cast<int>(sums[kThreads / 32 + i]));
   }
   if (total == 0) return false;
-  share->ctas = static_cast<int>(min(static_cast<long long>(grid), max(1ll, paged_div(total, min_units))));
+  // The share has to be worth its CTA: one unit where no item is split. An item of U units
+  // in shares of u takes about u units' time, and then U / u parts to join one after another;
+  // with a part at about kWorth units the sum is least for u = sqrt(kWorth U).
+  const int least = longest <= Walk::kWholeUnits
+                        ? 1
+                        : max(1, static_cast<int>(sqrtf(Walk::kPartWorth * static_cast<float>(longest))));
+  share->ctas = static_cast<int>(min(static_cast<long long>(grid), max(1ll, paged_div(total, least))));
   if (cta >= share->ctas) return false;
   share->each = paged_div(total, share->ctas);
   share->more = static_cast<int>(total - share->each * share->ctas);
@@ -201,7 +218,7 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, int min_uni
 #pragma unroll 1
     for (w.b = b0;; ++w.b) {
       w.s = paged_seq(p, w.b);
-      const long long head = Walk::head_length(p, w.s);
+      const long long head = Walk::head_length(p, w.s, &longest);
       if (left < head * p.kv_heads) {
         w.tiles = Walk::row_tiles(p, w.s);
         w.h = static_cast<int>(paged_div(left, static_cast<int>(head)));

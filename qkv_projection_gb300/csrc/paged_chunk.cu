@@ -54,10 +54,10 @@ constexpr int kMmaWarp = 8, kLoadWarp = 10;   // and the one after each
 constexpr int kThreads = 384;
 // Registers a thread: 384 threads start with 168; 256 x 216 + 128 x 72 is the same total.
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
-constexpr int kMinUnits = 4;            // units worth a CTA of their own
 constexpr int kWhole = 16;              // units of an item that is not split
+constexpr int kFewParts = 3;            // parts - 1 up to which the last CTA joins the others' with its own from tensor memory
 constexpr float kLazy = 8.f;            // growth of the maximum (log2) that renews the reference
-using Walk = PagedWalk<kRows, kKeys, kWhole>;
+using Walk = PagedWalk<kRows, kKeys, kWhole, 100>;
 using Span = PagedSpan<kKeys>;
 
 template <int kDim> struct Shape {
@@ -96,6 +96,7 @@ template <int kDim> struct Control {
   Walk place;
   PagedShare share;
   Job jobs[kJobs];
+  float row_lse[kRows];
   uint32_t tmem_base;
   int abort_flag, last_one;
 };
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool any;
   {
     PagedShare sh;
-    any = paged_share<kThreads>(p, blockIdx.x, gridDim.x, kMinUnits, reinterpret_cast<long long*>(smem), &ctl.place, &sh);
+    any = paged_share<kThreads>(p, blockIdx.x, gridDim.x, reinterpret_cast<long long*>(smem), &ctl.place, &sh);
     if (any && threadIdx.x == 0) ctl.share = sh;
     __syncthreads();
   }
@@ -562,12 +563,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool mine = works(mode) || (mode == Mode::kNoKeys && rows > kHalf * half);
       const bool keys = mode != Mode::kNoKeys;
       bool q_next = false;
-      // Of a split item the CTA that finds all other parts written is the last.
+      // Of an item in few parts the CTA that finds all others written is the last.
       auto look_for_others = [&] {
         if (w.split && threadIdx.x == 0) {
           unsigned seen;
           asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(p.counters + w.c0) : "memory");
-          ctl.last_one = seen == static_cast<unsigned>(w.c1 - w.c0);
+          ctl.last_one = w.c1 - w.c0 < kFewParts && seen == static_cast<unsigned>(w.c1 - w.c0);
         }
       };
       float m = kNegInf, l = 0.f;                          // the row's reference (in units of S) and sum
@@ -713,6 +714,82 @@ __global__ void __launch_bounds__(kThreads, 1)
       T* to_out = static_cast<T*>(p.out) + tok * p.o_ts + head * p.o_hs;
 #pragma unroll 1
       for (bool first = true;; first = false) {
+        if (last && c1 - c0 >= kFewParts) {
+          // Many parts, all in memory: a round trip takes 1500 cycles or more, so a thread has the
+          // loads of five parts and two pieces of eight columns in flight at a time;
+          // neighbouring lanes take neighbouring rows.
+          __threadfence();
+          if (threadIdx.x == 0) p.counters[c0] = 0;
+          const int r = threadIdx.x;
+          if (r < rows) {
+            float top = kNegInf, sum = 0.f;
+#pragma unroll 8
+            for (int i = c0; i <= c1; ++i) top = fmaxf(top, __ldcg(p.part_l + part_at(i) * kRows + r));
+            const float ref = top == kNegInf ? 0.f : top;
+#pragma unroll 8
+            for (int i = c0; i <= c1; ++i) sum += exp2_fast(__ldcg(p.part_l + part_at(i) * kRows + r) - ref);
+            ctl.row_lse[r] = sum == 0.f ? kNegInf : ref + log2f(sum);
+          }
+          meet();
+          constexpr int kThreads8 = 32 * kSoftmaxWarps, kBatch = 2, kGroup = 5;
+          const int work = rows * (kDim / 8);
+#pragma unroll 1
+          for (int i0 = threadIdx.x; i0 < work; i0 += kBatch * kThreads8) {
+            float x[kBatch][8], from0[kBatch];
+            int row[kBatch], col[kBatch];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+              const int at = min(i0 + b * kThreads8, work - 1);
+              col[b] = at / rows;
+              row[b] = at - col[b] * rows;
+              from0[b] = ctl.row_lse[row[b]] == kNegInf ? 0.f : ctl.row_lse[row[b]];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[b][e] = 0.f;
+            }
+#pragma unroll 1
+            for (int i = c0; i <= c1; i += kGroup) {
+              float4 v[kGroup][kBatch][2];
+              float f[kGroup][kBatch];
+#pragma unroll
+              for (int k = 0; k < kGroup; ++k) {
+                const long long from = part_at(min(i + k, c1));
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                  f[k][b] = __ldcg(p.part_l + from * kRows + row[b]);
+                  const float4* at =
+                      reinterpret_cast<const float4*>(p.part_o + (from * kDim + col[b] * 8) * kRows + row[b] * 8);
+                  v[k][b][0] = __ldcg(at);
+                  v[k][b][1] = __ldcg(at + 1);
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < kGroup; ++k) {
+                if (i + k > c1) break;
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                  const float g = exp2_fast(f[k][b] - from0[b]);
+                  const float4 a = v[k][b][0], c = v[k][b][1];
+                  x[b][0] = fmaf(g, a.x, x[b][0]), x[b][1] = fmaf(g, a.y, x[b][1]);
+                  x[b][2] = fmaf(g, a.z, x[b][2]), x[b][3] = fmaf(g, a.w, x[b][3]);
+                  x[b][4] = fmaf(g, c.x, x[b][4]), x[b][5] = fmaf(g, c.y, x[b][5]);
+                  x[b][6] = fmaf(g, c.z, x[b][6]), x[b][7] = fmaf(g, c.w, x[b][7]);
+                }
+              }
+            }
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+              if (i0 + b * kThreads8 >= work) continue;
+              const int gr = w.row0 + row[b], tr = p.group_div.div(gr), hr = w.h * p.group + gr - tr * p.group;
+              const long long at = w.q0 + tr;
+              if (col[b] * 8 < p.dim)
+                *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at * p.o_ts + hr * p.o_hs + col[b] * 8) =
+                    make_uint4(Type<T>::pack(x[b][0], x[b][1]), Type<T>::pack(x[b][2], x[b][3]),
+                               Type<T>::pack(x[b][4], x[b][5]), Type<T>::pack(x[b][6], x[b][7]));
+              if (p.lse && col[b] == 0) p.lse[at * p.heads + hr] = ctl.row_lse[row[b]] * kLn2;
+            }
+          }
+          break;
+        }
         const bool joins = last && !gives;
         if (joins) {
           __threadfence();

@@ -32,8 +32,10 @@ constexpr int kStepKeys = 16;                    // keys of one warp and step
 constexpr int kUnitKeys = kWarps * kStepKeys;    // 64
 constexpr int kRows = kPagedDecodeRows;
 constexpr int kCtasPerSm = 2;
-constexpr int kMinUnits = 2;                     // units worth a CTA of their own
-using Walk = PagedWalk<kRows, kUnitKeys, 0>;
+// Units of an item that is not split: joining parts takes 4-6 us, a unit 0.6 us (32
+// sequences of 300 positions: 10.0 us whole, 16.5 us split; 16 units and more are better split).
+constexpr int kWhole = 8;
+using Walk = PagedWalk<kRows, kUnitKeys, kWhole, 20>;
 using Span = PagedSpan<kUnitKeys>;
 
 template <int kDim> struct Shape {
@@ -102,7 +104,7 @@ template <typename T, int kDim>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(const __grid_constant__ PagedParams p) {
   using S = Shape<kDim>;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long sums[kWarps];
+  __shared__ long long sums[2 * kWarps];
   __shared__ Walk place;
   __shared__ float warp_m[kWarps][kRows], warp_l[kWarps][kRows], own_lse[kRows];
   __shared__ int last_one;
@@ -110,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   allow_dependents_launch();
   grid_dependency_wait();
   PagedShare share;
-  if (!paged_share<kThreads>(p, blockIdx.x, gridDim.x, kMinUnits, sums, &place, &share)) return;
+  if (!paged_share<kThreads>(p, blockIdx.x, gridDim.x, sums, &place, &share)) return;
   Walk w = place;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -458,12 +460,12 @@ size_t paged_decode_workspace_bytes(int num_sms) {
 }
 
 cudaError_t launch_paged_decode(FloatType t, PagedParams p, void* workspace, int num_sms, cudaStream_t stream) {
-  // No more CTAs than counters, and than there can be shares of kMinUnits units.
+  // No more CTAs than counters, and than there can be units.
   const long long most = static_cast<long long>(p.max_pages) << p.page_shift;
   const long long units = (most + kUnitKeys - 1) / kUnitKeys + 1;
   const long long tiles = (static_cast<long long>(p.tokens) * p.group + kRows - 1) / kRows + p.batch;
   int ctas = std::min(num_sms * kCtasPerSm, static_cast<int>(kPagedCounterBytes / sizeof(unsigned)));
-  ctas = static_cast<int>(std::max(1ll, std::min<long long>(ctas, units * tiles * p.kv_heads / kMinUnits)));
+  ctas = static_cast<int>(std::max(1ll, std::min<long long>(ctas, units * tiles * p.kv_heads)));
   p.counters = static_cast<unsigned*>(workspace);
   p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kPagedCounterBytes);
   p.part_l = p.part_o + static_cast<size_t>(2) * ctas * kRows * (p.dim <= 64 ? 64 : 128);
