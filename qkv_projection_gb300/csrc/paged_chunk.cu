@@ -686,8 +686,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool real = mine && my_row < rows;
       const bool pair = mode == Mode::kPair, split = w.split;
       // Half 1 of a pair leaves its results in the CTA's scratch, in the form of a part; half 0 adds them up.
-      // (Both are laid out [dim / 8][rows][8], so that a warp's 32 rows are contiguous.)
-      float* pair_o = p.pair_o + (static_cast<long long>(blockIdx.x) * kHalf * kDim) + my_row * 8;
+      // (Both are laid out [dim / 4][rows][4], so that a warp's 32 rows are contiguous.)
+      float* pair_o = p.pair_o + static_cast<long long>(blockIdx.x) * kHalf * kDim + my_row * 4;
       float* pair_l = p.pair_l + blockIdx.x * kHalf + my_row;
       const bool gives = pair && half == 1;
       if (pair && half == 0) {
@@ -709,8 +709,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // its own. A CTA that is the last only once it has written goes round once more.
       bool last = split && ctl.last_one;
       float row_lse = lse2, base = 0.f;                    // of the whole item
-      float* to_part = gives ? pair_o : p.part_o + static_cast<long long>(part_at(own)) * kRows * kDim + my_row * 8;
-      const int part_step = gives ? kHalf : kRows;         // from eight columns to the next eight
+      float* to_part = gives ? pair_o : p.part_o + static_cast<long long>(part_at(own)) * kRows * kDim + my_row * 4;
+      const int part_step = gives ? kHalf : kRows;
       T* to_out = static_cast<T*>(p.out) + tok * p.o_ts + head * p.o_hs;
 #pragma unroll 1
       for (bool first = true;; first = false) {
@@ -757,9 +757,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int b = 0; b < kBatch; ++b) {
                   f[k][b] = __ldcg(p.part_l + from * kRows + row[b]);
                   const float4* at =
-                      reinterpret_cast<const float4*>(p.part_o + (from * kDim + col[b] * 8) * kRows + row[b] * 8);
+                      reinterpret_cast<const float4*>(p.part_o + (from * kDim + col[b] * 8) * kRows) + row[b];
                   v[k][b][0] = __ldcg(at);
-                  v[k][b][1] = __ldcg(at + 1);
+                  v[k][b][1] = __ldcg(at + kRows);
                 }
               }
 #pragma unroll
@@ -834,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (mul_other != 0.f) {
 #pragma unroll
               for (int e = 0; e < 32; e += 4) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(pair_o + (c + (e & ~7)) * kHalf + (e & 4)));
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(pair_o + (c + e) * kHalf));
                 o[e] = __float_as_uint(fmaf(x.x, mul_other, __uint_as_float(o[e])));
                 o[e + 1] = __float_as_uint(fmaf(x.y, mul_other, __uint_as_float(o[e + 1])));
                 o[e + 2] = __float_as_uint(fmaf(x.z, mul_other, __uint_as_float(o[e + 2])));
@@ -853,10 +853,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                   for (int e = 0; e < 32; ++e) acc[e] = fmaf(f, __uint_as_float(o[e]), acc[e]);
                 } else {
                   const float f = exp2_fast(__ldcg(p.part_l + part_at(i) * kRows + my_row) - base);
-                  const float* src = p.part_o + (static_cast<long long>(part_at(i)) * kDim + c) * kRows + my_row * 8;
+                  const float* src = p.part_o + (static_cast<long long>(part_at(i)) * kDim + c) * kRows + my_row * 4;
 #pragma unroll
                   for (int e = 0; e < 32; e += 4) {
-                    const float4 x = __ldcg(reinterpret_cast<const float4*>(src + (e & ~7) * kRows + (e & 4)));
+                    const float4 x = __ldcg(reinterpret_cast<const float4*>(src + e * kRows));
                     acc[e] = fmaf(f, x.x, acc[e]);
                     acc[e + 1] = fmaf(f, x.y, acc[e + 1]);
                     acc[e + 2] = fmaf(f, x.z, acc[e + 2]);
@@ -869,10 +869,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (real && writes_part) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                const uint32_t v[8] = {o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5], o[e + 6], o[e + 7]};
-                store32(to_part + (c + e) * part_step, v, true);
-              }
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<uint4*>(to_part + (c + e) * part_step) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             } else if (real) {
 #pragma unroll
               for (int e = 0; e < 32; e += 16) {
