@@ -669,28 +669,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (q_next) send_q();
         look_for_others();
-        wait(&ctl.o_done[half], o_phase);
-        tc_fence_after();
-        o_phase ^= 1;
-        if (of_half == 1 && lane == 0 && ok) mbar_arrive(&ctl.v_empty[(n - step) % S::kVStages]);
       }
-      if (keys) unit_count += n_units;
-      q_sent = q_next;
-
-      if (w.split) meet();                                 // last_one is known
 
       // Results of this thread's row: O / l and m + log2 l (nothing seen: zeros, -inf).
       const bool none = l == 0.f;                          // (a NaN score leaves l NaN)
       float lse2 = none ? kNegInf : (m == kNegInf ? 0.f : m * scale) + log2f(l);
       float mul = none ? 0.f : 1.f / l, mul_other = 0.f;
       bool real = mine && my_row < rows;
-      const bool pair = mode == Mode::kPair, split = w.split;
+      const bool paired = mode == Mode::kPair, split = w.split;
       // Half 1 of a pair leaves its results in the CTA's scratch, in the form of a part; half 0 adds them up.
       // (Both are laid out [dim / 4][rows][4], so that a warp's 32 rows are contiguous.)
       float* pair_o = p.pair_o + static_cast<long long>(blockIdx.x) * kHalf * kDim + my_row * 4;
       float* pair_l = p.pair_l + blockIdx.x * kHalf + my_row;
-      const bool gives = pair && half == 1;
-      if (pair && half == 0) {
+      const bool gives = paired && half == 1;
+      const int g = w.row0 + min(my_row, rows - 1), t = p.group_div.div(g);
+      const long long tok = w.q0 + t;
+      const int head = w.h * p.group + g - t * p.group;
+      T* to_out = static_cast<T*>(p.out) + tok * p.o_ts + head * p.o_hs;
+      // The common case, a whole item with a half to each row. Little is left for after
+      // the last product: what runs once an item is bound by the fetching of its code.
+      const bool plain = keys && !split && !paired;
+      if (plain && real && p.lse) p.lse[tok * p.heads + head] = lse2 * kLn2;
+      if (works(mode)) {
+        wait(&ctl.o_done[half], o_phase);
+        tc_fence_after();
+        o_phase ^= 1;
+        if (of_half == 1 && lane == 0 && ok) {             // the last unit of this half
+          const uint32_t n = unit_count + n_units - 1;
+          mbar_arrive(&ctl.v_empty[(paired && ((n_units - 1) & 1) != half ? n - 1 : n) % S::kVStages]);
+        }
+      }
+      if (keys) unit_count += n_units;
+      q_sent = q_next;
+      if (split) meet();                                   // last_one is known
+      if (plain && mine) {
+        const uint64_t mul2 = pair(mul, mul);
+        __syncwarp();
+#pragma unroll 1
+        for (int c = 0; c < kDim; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(o_tmem + c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; e += 16) {
+            uint32_t v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 x =
+                  unpair(fma2(pair(__uint_as_float(o[e + 2 * i]), __uint_as_float(o[e + 2 * i + 1])), mul2, 0));
+              v[i] = Type<T>::pack(x.x, x.y);
+            }
+            if (mul == 0.f) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = 0;
+            }
+            if (real && c + e + 16 <= p.dim) store32(to_out + c + e, v, cp.out32);
+            else if (real && c + e < p.dim) *reinterpret_cast<uint4*>(to_out + c + e) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+      }
+      if (paired && half == 0) {
         meet();              // half 1 has written
         if (real) {
           const float other = __ldcg(pair_l), top = fmaxf(lse2, other), ref = top == kNegInf ? 0.f : top;
@@ -700,9 +738,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           mul_other = sum == 0.f ? 0.f : b / sum;
         }
       }
-      const int g = w.row0 + min(my_row, rows - 1), t = p.group_div.div(g);
-      const long long tok = w.q0 + t;
-      const int head = w.h * p.group + g - t * p.group;
       const int own = static_cast<int>(blockIdx.x), c0 = w.c0, c1 = w.c1;
       auto part_at = [&](int c) { return 2 * c + (c == c0 ? 1 : 0); };     // a CTA's part of an item is its first but where the item begins
       // The last CTA of a split item does not write its part: it joins the others' with
@@ -711,9 +746,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float row_lse = lse2, base = 0.f;                    // of the whole item
       float* to_part = gives ? pair_o : p.part_o + static_cast<long long>(part_at(own)) * kRows * kDim + my_row * 4;
       const int part_step = gives ? kHalf : kRows;
-      T* to_out = static_cast<T*>(p.out) + tok * p.o_ts + head * p.o_hs;
 #pragma unroll 1
-      for (bool first = true;; first = false) {
+      for (bool first = true; !plain; first = false) {
         if (last && c1 - c0 >= kFewParts) {
           // Many parts, all in memory: a round trip takes 1500 cycles or more, so a thread has the
           // loads of five parts and two pieces of eight columns in flight at a time;
@@ -902,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!last) break;
       }
       tc_fence_before();
-      if (pair || split) meet();                           // scratch and last_one have been read
+      if (paired || split) meet();                           // scratch and last_one have been read
       job_done(k);
     }
   }
