@@ -135,7 +135,6 @@ struct PagedParams {
   float scale_log2;           // softmax scale * log2(e)
   float* part_o;              // [2 * ctas][rows][dim] partial outputs of split work
   float* part_l;              // [2 * ctas][rows] their log2-sum-exp2
-  float *pair_o, *pair_l;     // [ctas][128][dim], [ctas][128]: what the halves of one CTA tell each other
   unsigned* counters;         // [ctas], zero between launches
 };
 constexpr int kPagedMaxLen = 1 << 30;

@@ -98,15 +98,30 @@ __device__ __forceinline__ long long paged_div(long long a, int b) {
   return q;
 }
 
-// A place in the line of units: an item, and a unit in it. An item of at most kWhole
-// units is not split: it belongs to the share that holds its last unit. (Writing and
-// joining parts costs more than such an item's imbalance.)
-template <int kRows, int kKeys, int kWhole, int kPartWorthPercent>
+// One CTA's share [begin, end) of a line of `total` cost among `ctas` CTAs: the
+// first total % ctas shares have one more than the others.
+struct PagedShare {
+  long long begin, end, each;    // each = total / ctas
+  int ctas, more;                // more = total % ctas
+  __device__ __forceinline__ int owner(long long at) const {
+    const long long first = (each + 1) * more;
+    if (at < first) return static_cast<int>(paged_div(at, static_cast<int>(each + 1)));
+    return more + static_cast<int>(paged_div(at - first, static_cast<int>(each)));
+  }
+};
+
+// A place in the line of work: an item, and a unit in it. A unit of an item of at most
+// kSmallRows rows costs kSmallCost, any other kCost. An item of at most kWhole units is
+// not split: it belongs to the share that holds its beginning. (Writing and joining parts
+// costs more than such an item's imbalance. By their ends, the last tile of a causal head,
+// its longest, would share a CTA with the first ones of the next.)
+template <int kRows, int kKeys, int kWhole, int kPartWorthPercent, int kSmallRows, int kSmallCost, int kCost>
 struct PagedWalk {
+  static_assert(kSmallCost <= kCost && kCost < 8);
   static constexpr int kWholeUnits = kWhole;
   static constexpr float kPartWorth = 0.01f * kPartWorthPercent;   // joining a part, in units
   int b, h, tile, tiles;      // item: sequence, K/V head, row tile of `tiles`
-  int unit, units;            // unit within the item
+  int unit, units, cost;      // unit within the item; cost of one
   long long at;               // where in the line the item begins
   PagedSeq s;
 
@@ -118,25 +133,31 @@ struct PagedWalk {
   __device__ __forceinline__ static int item_units(const PagedParams& p, const PagedSeq& s, int tile) {
     return PagedSpan<kKeys>(p, s, tile * kRows, min(tile * kRows + kRows, s.n * p.group)).units;
   }
-  __device__ __forceinline__ static long long head_length(const PagedParams& p, const PagedSeq& s, int* longest) {
+  __device__ __forceinline__ static int item_cost(const PagedParams& p, const PagedSeq& s, int tile) {
+    return s.n * p.group - tile * kRows <= kSmallRows ? kSmallCost : kCost;
+  }
+  __device__ __forceinline__ static long long head_length(const PagedParams& p, const PagedSeq& s, int* longest) {   // (8 units + cost)
     long long u = 0;
     const int tiles = row_tiles(p, s);
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i) {
-      const int units = item_units(p, s, i);
-      u += units;
-      *longest = max(*longest, units);
+      const int units = item_units(p, s, i), cost = item_cost(p, s, i);
+      u += units * cost;
+      *longest = max(*longest, 8 * units + cost);
     }
     return u;
   }
   // The first unit past a CTA's share that ends at `end`.
   __device__ __forceinline__ int unit_at(long long end) const {
     const long long to = max(end - at, 0ll);
-    return to >= units ? units : units <= kWhole ? 0 : static_cast<int>(to);
+    return to >= units * cost ? units : units > kWhole ? static_cast<int>(to) / cost : to > 0 ? units : 0;
   }
+  // The CTAs that hold its first and its last unit.
+  __device__ __forceinline__ int first_owner(const PagedShare& share) const { return share.owner(at + cost - 1); }
+  __device__ __forceinline__ int last_owner(const PagedShare& share) const { return share.owner(at + units * cost - 1); }
   // To the first unit of the next item (past the line's end: b == batch).
   __device__ __forceinline__ void next_item(const PagedParams& p) {
-    at += units;
+    at += units * cost;
     unit = 0;
     if (++tile == tiles) {
       tile = 0;
@@ -150,18 +171,7 @@ struct PagedWalk {
       }
     }
     units = item_units(p, s, tile);
-  }
-};
-
-// One CTA's share [begin, end) of a line of `total` units among `ctas` CTAs: the
-// first total % ctas shares have one unit more than the others.
-struct PagedShare {
-  long long begin, end, each;    // each = total / ctas
-  int ctas, more;                // more = total % ctas
-  __device__ __forceinline__ int owner(long long unit) const {
-    const long long first = (each + 1) * more;
-    if (unit < first) return static_cast<int>(paged_div(unit, static_cast<int>(each + 1)));
-    return more + static_cast<int>(paged_div(unit - first, static_cast<int>(each)));
+    cost = item_cost(p, s, tile);
   }
 };
 
@@ -202,10 +212,9 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
   // The share has to be worth its CTA: one unit where no item is split. An item of U units
   // in shares of u takes about u units' time, and then U / u parts to join one after another;
   // with a part at about kWorth units the sum is least for u = sqrt(kWorth U).
-  const int least = longest <= Walk::kWholeUnits
-                        ? 1
-                        : max(1, static_cast<int>(sqrtf(Walk::kPartWorth * static_cast<float>(longest))));
-  share->ctas = static_cast<int>(min(static_cast<long long>(grid), max(1ll, paged_div(total, least))));
+  const int units = longest >> 3, cost = longest & 7;
+  const int least = units <= Walk::kWholeUnits ? 1 : max(1, static_cast<int>(sqrtf(Walk::kPartWorth * static_cast<float>(units))));
+  share->ctas = static_cast<int>(min(static_cast<long long>(grid), max(1ll, paged_div(total, least * cost))));
   if (cta >= share->ctas) return false;
   share->each = paged_div(total, share->ctas);
   share->more = static_cast<int>(total - share->each * share->ctas);
@@ -230,11 +239,13 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
 #pragma unroll 1
     for (w.tile = 0;; ++w.tile) {
       w.units = Walk::item_units(p, w.s, w.tile);
-      if (left < w.units) break;
-      left -= w.units;
+      w.cost = Walk::item_cost(p, w.s, w.tile);
+      if (left < w.units * w.cost) break;
+      left -= w.units * w.cost;
     }
-    w.unit = w.units <= Walk::kWholeUnits ? 0 : static_cast<int>(left);
+    w.unit = w.units <= Walk::kWholeUnits ? 0 : static_cast<int>(left) / w.cost;
     w.at = share->begin - left;
+    if (w.units <= Walk::kWholeUnits && left > 0) w.next_item(p);
     *place = w;
   }
   __syncthreads();

@@ -57,7 +57,7 @@ constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr int kWhole = 16;              // units of an item that is not split
 constexpr int kFewParts = 3;            // parts - 1 up to which the last CTA joins the others' with its own from tensor memory
 constexpr float kLazy = 8.f;            // growth of the maximum (log2) that renews the reference
-using Walk = PagedWalk<kRows, kKeys, kWhole, 100>;
+using Walk = PagedWalk<kRows, kKeys, kWhole, 100, kHalf, 3, 4>;
 using Span = PagedSpan<kKeys>;
 
 template <int kDim> struct Shape {
@@ -96,7 +96,7 @@ template <int kDim> struct Control {
   Walk place;
   PagedShare share;
   Job jobs[kJobs];
-  float row_lse[kRows];
+  float row_lse[kRows], row_mul[kRows];
   uint32_t tmem_base;
   int abort_flag, last_one;
 };
@@ -305,8 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               job.plain1[half] = span.lo > 0 ? t1 - 1 : t1;
             }
             if (job.split) {
-              job.c0 = ctl.share.owner(w.at);
-              job.c1 = ctl.share.owner(w.at + w.units - 1);
+              job.c0 = w.first_owner(ctl.share);
+              job.c1 = w.last_owner(ctl.share);
             }
             if (last) w.next_item(p);
             else w.unit = w.units;                         // the share ends here
@@ -675,21 +675,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool none = l == 0.f;                          // (a NaN score leaves l NaN)
       float lse2 = none ? kNegInf : (m == kNegInf ? 0.f : m * scale) + log2f(l);
       float mul = none ? 0.f : 1.f / l, mul_other = 0.f;
-      bool real = mine && my_row < rows;
       const bool paired = mode == Mode::kPair, split = w.split;
-      // Half 1 of a pair leaves its results in the CTA's scratch, in the form of a part; half 0 adds them up.
-      // (Both are laid out [dim / 4][rows][4], so that a warp's 32 rows are contiguous.)
-      float* pair_o = p.pair_o + static_cast<long long>(blockIdx.x) * kHalf * kDim + my_row * 4;
-      float* pair_l = p.pair_l + blockIdx.x * kHalf + my_row;
-      const bool gives = paired && half == 1;
+      const bool real = mine && my_row < rows;
+      const bool tells = real && !(paired && half == 1);   // writes the row's log-sum
+      const int col0 = paired ? kDim / 2 * half : 0, col1 = paired ? col0 + kDim / 2 : kDim;
       const int g = w.row0 + min(my_row, rows - 1), t = p.group_div.div(g);
       const long long tok = w.q0 + t;
       const int head = w.h * p.group + g - t * p.group;
       T* to_out = static_cast<T*>(p.out) + tok * p.o_ts + head * p.o_hs;
-      // The common case, a whole item with a half to each row. Little is left for after
-      // the last product: what runs once an item is bound by the fetching of its code.
-      const bool plain = keys && !split && !paired;
-      if (plain && real && p.lse) p.lse[tok * p.heads + head] = lse2 * kLn2;
+      // The common case, a whole item. Little is left for after the last product: what
+      // runs once an item is bound by the fetching of its code.
+      const bool plain = keys && !split;
+      if (plain && !paired && real && p.lse) p.lse[tok * p.heads + head] = lse2 * kLn2;
       if (works(mode)) {
         wait(&ctl.o_done[half], o_phase);
         tc_fence_after();
@@ -701,41 +698,67 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (keys) unit_count += n_units;
       q_sent = q_next;
-      if (split) meet();                                   // last_one is known
-      if (plain && mine) {
-        const uint64_t mul2 = pair(mul, mul);
+      // The halves of a pair hold the same rows in the same lanes of tensor memory: they tell
+      // each other log-sums and factors, and each joins half the columns of both.
+      if (paired) {
+        ctl.row_lse[kHalf * half + my_row] = lse2;
+        ctl.row_mul[kHalf * half + my_row] = mul;
+        tc_fence_before();
+      }
+      if (split || paired) meet();                         // (and last_one is known)
+      if (paired) {
+        tc_fence_after();
+        const int at = kHalf * (half ^ 1) + my_row;
+        const float other = ctl.row_lse[at], top = fmaxf(lse2, other), ref = top == kNegInf ? 0.f : top;
+        const float a = exp2_fast(lse2 - ref), b = exp2_fast(other - ref), sum = a + b;
+        lse2 = sum == 0.f ? kNegInf : ref + log2f(sum);
+        mul = sum == 0.f ? 0.f : mul * a / sum;
+        mul_other = sum == 0.f ? 0.f : ctl.row_mul[at] * b / sum;
+        if (plain && tells && p.lse) p.lse[tok * p.heads + head] = lse2 * kLn2;
+      }
+      // 32 columns of this thread's row, normalised
+      auto load_o = [&](int c, uint32_t (&o)[32]) {
         __syncwarp();
-#pragma unroll 1
-        for (int c = 0; c < kDim; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(o_tmem + c, o);
+        tmem_ld32(o_tmem + c, o);
+        tmem_ld_wait();
+        const uint64_t mul2 = pair(mul, mul);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float2 x = unpair(fma2(pair(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), mul2, 0));
+          o[e] = __float_as_uint(x.x), o[e + 1] = __float_as_uint(x.y);
+        }
+        if (mul == 0.f) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+        if (paired) {
+          uint32_t x[32];
+          tmem_ld32((half ? o_tmem - kDim : o_tmem + kDim) + c, x);
           tmem_ld_wait();
+          if (mul_other != 0.f) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 16) {
-            uint32_t v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 x =
-                  unpair(fma2(pair(__uint_as_float(o[e + 2 * i]), __uint_as_float(o[e + 2 * i + 1])), mul2, 0));
-              v[i] = Type<T>::pack(x.x, x.y);
-            }
-            if (mul == 0.f) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = 0;
-            }
-            if (real && c + e + 16 <= p.dim) store32(to_out + c + e, v, cp.out32);
-            else if (real && c + e < p.dim) *reinterpret_cast<uint4*>(to_out + c + e) = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(fmaf(__uint_as_float(x[e]), mul_other, __uint_as_float(o[e])));
           }
         }
-      }
-      if (paired && half == 0) {
-        meet();              // half 1 has written
-        if (real) {
-          const float other = __ldcg(pair_l), top = fmaxf(lse2, other), ref = top == kNegInf ? 0.f : top;
-          const float a = exp2_fast(lse2 - ref), b = exp2_fast(other - ref), sum = a + b;
-          lse2 = sum == 0.f ? kNegInf : ref + log2f(sum);
-          mul = sum == 0.f ? 0.f : mul * a / sum;
-          mul_other = sum == 0.f ? 0.f : b / sum;
+      };
+      auto store_o = [&](int c, const uint32_t (&o)[32]) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 16) {
+          uint32_t v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            v[i] = Type<T>::pack(__uint_as_float(o[e + 2 * i]), __uint_as_float(o[e + 2 * i + 1]));
+          if (c + e + 16 <= p.dim) store32(to_out + c + e, v, cp.out32);
+          else if (c + e < p.dim) *reinterpret_cast<uint4*>(to_out + c + e) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+      };
+      if (plain && mine) {
+#pragma unroll 1
+        for (int c = col0; c < col1; c += 32) {
+          uint32_t o[32];
+          load_o(c, o);
+          if (real) store_o(c, o);
         }
       }
       const int own = static_cast<int>(blockIdx.x), c0 = w.c0, c1 = w.c1;
@@ -744,10 +767,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // its own. A CTA that is the last only once it has written goes round once more.
       bool last = split && ctl.last_one;
       float row_lse = lse2, base = 0.f;                    // of the whole item
-      float* to_part = gives ? pair_o : p.part_o + static_cast<long long>(part_at(own)) * kRows * kDim + my_row * 4;
-      const int part_step = gives ? kHalf : kRows;
+      float* to_part = p.part_o + static_cast<long long>(part_at(own)) * kRows * kDim + my_row * 4;
 #pragma unroll 1
-      for (bool first = true; !plain; first = false) {
+      while (!plain) {
         if (last && c1 - c0 >= kFewParts) {
           // Many parts, all in memory: a round trip takes 1500 cycles or more, so a thread has the
           // loads of five parts and two pieces of eight columns in flight at a time;
@@ -824,8 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           break;
         }
-        const bool joins = last && !gives;
-        if (joins) {
+        if (last) {
           __threadfence();
           if (threadIdx.x == 0) p.counters[c0] = 0;
           // the log-sum over all parts, in their order; a part then weighs exp2(its own - that)
@@ -852,30 +873,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           row_lse = sum == 0.f ? kNegInf : ref + log2f(sum);
           base = sum == 0.f ? 0.f : row_lse;
         }
-        const bool writes_part = gives || (split && !last);
-        if (mine && (first || !gives)) {
+        if (mine) {
 #pragma unroll 1
-          for (int c = 0; c < kDim; c += 32) {
-            // 32 columns of this thread's row, joined with the other half's
+          for (int c = col0; c < col1; c += 32) {
             uint32_t o[32];
             if (keys) {
-              __syncwarp();
-              tmem_ld32(o_tmem + c, o);
-              tmem_ld_wait();
-            }
+              load_o(c, o);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(mul == 0.f ? 0.f : __uint_as_float(o[e]) * mul);
-            if (mul_other != 0.f) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(pair_o + (c + e) * kHalf));
-                o[e] = __float_as_uint(fmaf(x.x, mul_other, __uint_as_float(o[e])));
-                o[e + 1] = __float_as_uint(fmaf(x.y, mul_other, __uint_as_float(o[e + 1])));
-                o[e + 2] = __float_as_uint(fmaf(x.z, mul_other, __uint_as_float(o[e + 2])));
-                o[e + 3] = __float_as_uint(fmaf(x.w, mul_other, __uint_as_float(o[e + 3])));
-              }
+              for (int e = 0; e < 32; ++e) o[e] = 0;
             }
-            if (joins) {
+            if (last) {
               float acc[32];
 #pragma unroll
               for (int e = 0; e < 32; ++e) acc[e] = 0.f;
@@ -901,30 +909,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(acc[e]);
             }
-            if (real && writes_part) {
+            if (real && split && !last) {
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<uint4*>(to_part + (c + e) * part_step) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                *reinterpret_cast<uint4*>(to_part + (c + e) * kRows) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             } else if (real) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 16) {
-                const int at = c + e;
-                uint32_t v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  v[i] = Type<T>::pack(__uint_as_float(o[e + 2 * i]), __uint_as_float(o[e + 2 * i + 1]));
-                if (at + 16 <= p.dim) store32(to_out + at, v, cp.out32);
-                else if (at < p.dim) *reinterpret_cast<uint4*>(to_out + at) = make_uint4(v[0], v[1], v[2], v[3]);
-              }
+              store_o(c, o);
             }
           }
-          if (real) {
-            if (gives) *pair_l = lse2;
-            else if (writes_part) p.part_l[part_at(own) * kRows + my_row] = lse2;
-            else if (p.lse) p.lse[tok * p.heads + head] = row_lse * kLn2;
-          }
+          if (tells && split && !last) p.part_l[part_at(own) * kRows + my_row] = lse2;
+          else if (tells && p.lse) p.lse[tok * p.heads + head] = row_lse * kLn2;
         }
-        if (gives && first) meet();                        // (half 0 of the pair is waiting)
         if (!split || last) break;
         meet();
         if (threadIdx.x == 0) {
@@ -936,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!last) break;
       }
       tc_fence_before();
-      if (paired || split) meet();                           // scratch and last_one have been read
+      if (paired || split) meet();                         // all of it has been read
       job_done(k);
     }
   }
@@ -982,7 +977,7 @@ cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const ChunkPara
 }  // namespace
 
 size_t paged_chunk_workspace_bytes(int num_sms) {
-  return kPagedCounterBytes + 32 + static_cast<size_t>(num_sms) * (2 * kRows + kHalf) * (128 + 1) * sizeof(float);
+  return kPagedCounterBytes + 32 + static_cast<size_t>(num_sms) * 2 * kRows * (128 + 1) * sizeof(float);
 }
 
 cudaError_t launch_paged_chunk(FloatType t, const PagedParams& params, void* workspace, int num_sms,
@@ -997,9 +992,7 @@ cudaError_t launch_paged_chunk(FloatType t, const PagedParams& params, void* wor
   cp.out32 = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && (p.tokens == 1 || p.o_ts % 16 == 0) &&
              (p.heads == 1 || p.o_hs % 16 == 0);
   const size_t dim = p.dim <= 64 ? 64 : 128;
-  p.pair_o = p.part_o + 2 * ctas * kRows * dim;
-  p.part_l = p.pair_o + ctas * kHalf * dim;
-  p.pair_l = p.part_l + 2 * ctas * kRows;
+  p.part_l = p.part_o + 2 * ctas * kRows * dim;
   CUtensorMap km, vm;
   cudaError_t e = encode_cache(&km, &cp.k_heads_first, p.kc, t, p, p.k_ps, p.k_ss, p.k_hs);
   if (e == cudaSuccess) e = encode_cache(&vm, &cp.v_heads_first, p.vc, t, p, p.v_ps, p.v_ss, p.v_hs);

@@ -35,7 +35,7 @@ constexpr int kCtasPerSm = 2;
 // Units of an item that is not split: joining parts takes 4-6 us, a unit 0.6 us (32
 // sequences of 300 positions: 10.0 us whole, 16.5 us split; 16 units and more are better split).
 constexpr int kWhole = 8;
-using Walk = PagedWalk<kRows, kUnitKeys, kWhole, 20>;
+using Walk = PagedWalk<kRows, kUnitKeys, kWhole, 20, 0, 1, 1>;
 using Span = PagedSpan<kUnitKeys>;
 
 template <int kDim> struct Shape {
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     const PagedSeq seq = w.s;
     const int rows = w.row1(p) - w.row0(), row0 = w.row0(), head0 = w.h * p.group;
     const bool split = u0 != 0 || u1 != w.units;
-    const int c0 = split ? share.owner(w.at) : 0, c1 = split ? share.owner(w.at + w.units - 1) : 0;
+    const int c0 = split ? w.first_owner(share) : 0, c1 = split ? w.last_owner(share) : 0;
 
     // Q fragments (A operand): rows past the item's are zero
     uint32_t qf[kDim / 16][4];
