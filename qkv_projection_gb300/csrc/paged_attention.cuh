@@ -136,6 +136,10 @@ struct PagedWalk {
   __device__ __forceinline__ static int item_cost(const PagedParams& p, const PagedSeq& s, int tile) {
     return s.n * p.group - tile * kRows <= kSmallRows ? kSmallCost : kCost;
   }
+  // (divisions by constants)
+  __device__ __forceinline__ int whole_units(int length) const {
+    return kSmallCost != kCost && cost == kSmallCost ? length / kSmallCost : length / kCost;
+  }
   __device__ __forceinline__ static long long head_length(const PagedParams& p, const PagedSeq& s, int* longest) {   // (8 units + cost)
     long long u = 0;
     const int tiles = row_tiles(p, s);
@@ -150,7 +154,7 @@ struct PagedWalk {
   // The first unit past a CTA's share that ends at `end`.
   __device__ __forceinline__ int unit_at(long long end) const {
     const long long to = max(end - at, 0ll);
-    return to >= units * cost ? units : units > kWhole ? static_cast<int>(to) / cost : to > 0 ? units : 0;
+    return to >= units * cost ? units : units > kWhole ? whole_units(static_cast<int>(to)) : to > 0 ? units : 0;
   }
   // The CTAs that hold its first and its last unit.
   __device__ __forceinline__ int first_owner(const PagedShare& share) const { return share.owner(at + cost - 1); }
@@ -243,7 +247,7 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
       if (left < w.units * w.cost) break;
       left -= w.units * w.cost;
     }
-    w.unit = w.units <= Walk::kWholeUnits ? 0 : static_cast<int>(left) / w.cost;
+    w.unit = w.units <= Walk::kWholeUnits ? 0 : w.whole_units(static_cast<int>(left));
     w.at = share->begin - left;
     if (w.units <= Walk::kWholeUnits && left > 0) w.next_item(p);
     *place = w;
