@@ -3,6 +3,10 @@
 Each .cu file is compiled to an object in parallel, then linked into one shared
 library next to this file. The CUDA runtime is linked statically, so loading
 the library needs no GPU; the driver is reached only at the first CUDA call.
+
+_host.so, the Python module of host_calls.cpp, is compiled beside them against the
+installed Python and torch. Without their headers it is left out, and the calls
+that it shortens go through Python.
 """
 from __future__ import annotations
 
@@ -19,6 +23,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libkaio_qkv.so")
 SOURCES = ["api.cu", "decode_w4a16.cu", "tc_decode.cu", "tc_kernels.cu", "dequant_group.cu",
            "rope.cu", "paged_decode.cu", "paged_chunk.cu"]
+HOST_SOURCE = os.path.join(CSRC, "host_calls.cpp")
+HOST_LIB = os.path.join(HERE, "_host.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-I", os.path.join(ROOT, "include")]
@@ -44,10 +50,37 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _compile_host() -> None:
+    import sysconfig
+
+    import torch
+    include = sysconfig.get_paths()["include"]
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    if not (os.path.exists(os.path.join(include, "Python.h")) and os.path.isdir(os.path.join(base, "include", "ATen"))):
+        if os.path.exists(HOST_LIB):
+            os.remove(HOST_LIB)
+        return
+    tmp = HOST_LIB + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", os.path.join(ROOT, "include"), "-isystem", include, "-isystem", cuda,
+           "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           HOST_SOURCE, "-o", tmp, "-L", os.path.join(base, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on {HOST_SOURCE}:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, HOST_LIB)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        host = ex.submit(_compile_host)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        host.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)

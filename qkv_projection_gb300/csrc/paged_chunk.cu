@@ -12,27 +12,47 @@
 // by more than 2^8, so weights stay below 256 (an f16 holds 65504) and a renewal
 // is rare; sums are of the unrounded f32 weights.
 //
-// What bounds it: the tensor cores. 256 rows make each K and V tile that the TMA
-// brings serve two products of 128 rows, and the two halves take turns: while the
-// softmax of one half runs, the tensor cores work for the other. TMEM is full:
-// two S and two O of 128 columns. The softmax warps rescale O and write the
-// results themselves (both are rare), so eight of twelve warps share nearly all
-// registers and every softmax thread keeps its whole row of S (128 values) in them.
+// What bounds it: many rows, the chain of each half (below); few rows, the bytes of K
+// and V. 256 rows make each K and V tile that the TMA brings serve two products of
+// 128 rows. The two halves take strict turns at the tensor cores: while the softmax
+// of one runs, they work for the other. A unit of 256 rows takes 3100-3250 cycles for
+// 2016 of products; the rest is the way from product to softmax to product, with one
+// wait and one commit of 150-300 cycles each. TMEM is full (two S and two O of 128
+// columns), so there is no third half to fill the gap. 4096 tokens over 16384 keys,
+// 32 heads on 8 of 128: 1.40-1.43 PFLOP/s, 0.73 of what the measured library product
+// reaches in a burst, 0.82 of it sustained.
+//
+// Registers: the softmax warps rescale O and write the results themselves (both are
+// rare), so eight of twelve warps share nearly all registers (216 a thread, 72 for the
+// others) and every softmax thread keeps its whole row of S, 128 values, in them. The
+// loop is sensitive to that: some hundred bytes of spills cost 8-20 %.
 //
 // Issuing is half the work: on the thread that issues MMAs a wait on an mbarrier
 // or a commit takes 150-300 cycles, and one thread for both halves took 5100 cycles
-// a unit for 2048 of products. So each half has an issuing warp of its own; per unit it
+// a unit for 2016 of products. So each half has an issuing warp of its own; per unit it
 // waits for the tiles while the softmax runs, then for P (in two parts, so that the
 // product starts with the first), issues PV and the next QK back to back, and makes
 // one commit. What that commit implies (the product before it is done) the softmax
-// warps pass on: they release the K and V stages with plain arrivals.
+// warps pass on: they release the K and V stages with plain arrivals. A turn rides on
+// the barrier of P as one more arrival.
 //
-// Warps 0-3 and 4-7: the softmax of the halves; 8, 9: their MMAs; 10, 11: K and V
-// tiles by TMA, one box per page and 64 columns (pages of 16 to 1024 positions),
-// pages that no row sees filled with zeros by an out-of-range coordinate. Rows of V
-// that no row of the item sees are zeroed in shared memory before use: a weight of
-// zero must not meet whatever the slot holds. The next item's Q is fetched as soon
-// as the last QK has read this one's, and its first QK runs while O is written.
+// Few rows (single tokens among chunks, short chunks): up to 128 rows and at least two
+// units make the halves a pair, which takes every other unit each on the same rows and
+// joins in tensor memory at the end: 2600 cycles a unit, 43 GB/s for each SM, which is
+// the memory's rate. Such a unit counts 3 in the line of work, one of 256 rows 4 (a mixed
+// step of 31 single tokens and 512 new ones: 136 us with equal counts, 121 us so).
+//
+// Warps 0-3 and 4-7: the softmax of the halves; 8, 9: their MMAs; 10: works out the
+// jobs (items, or this CTA's part of one) a few ahead and loads K; 11: loads V. Tiles
+// come by TMA, one box per page and 64 columns (pages of 16 to 1024 positions), pages
+// that no row sees filled with zeros by an out-of-range coordinate. Rows of V that no
+// row of the item sees are zeroed in shared memory before use: a weight of zero must not
+// meet whatever the slot holds. The next item's Q is fetched as soon as the last QK has
+// read this one's, and its first QK runs while O is written.
+//
+// Split items: the CTA that is last joins the parts in their order. Up to three parts it
+// joins from its own tensor memory and the workspace; more only from the workspace, with
+// ten loads of a thread in flight (one after another a part took 6000 cycles).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -54,9 +74,11 @@ constexpr int kMmaWarp = 8, kLoadWarp = 10;   // and the one after each
 constexpr int kThreads = 384;
 // Registers a thread: 384 threads start with 168; 256 x 216 + 128 x 72 is the same total.
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
-constexpr int kWhole = 16;              // units of an item that is not split
+constexpr int kWhole = 16;              // units of an item that is not split (a part and its join cost 5 to 7 units)
 constexpr int kFewParts = 3;            // parts - 1 up to which the last CTA joins the others' with its own from tensor memory
 constexpr float kLazy = 8.f;            // growth of the maximum (log2) that renews the reference
+// A part is worth a unit in the size of shares: 100 tokens over 9000 keys with 32/8 heads take 75 us, and 62 us
+// with two units, but 20 over 60000 with 8/1 76 and 82, 100 over 14000 with 8/1 42 and 50.
 using Walk = PagedWalk<kRows, kKeys, kWhole, 100, kHalf, 3, 4>;
 using Span = PagedSpan<kKeys>;
 

@@ -427,6 +427,28 @@ def _rope_axes(positions, tokens, sections, pairs):
     return axes, stride, (*sections, 0, 0, 0)[:4]
 
 
+_host_module = None
+
+
+def _host():
+    """The module that makes an ordinary call in one step (csrc/host_calls.cpp): its
+    functions return the result, or None to leave a call to the code here. False
+    where it was not built."""
+    global _host_module
+    if _host_module is None:
+        L = lib()
+        _torch()                                           # its libraries have to be loaded first
+        try:
+            from . import _host as module
+        except ImportError:
+            _host_module = False
+        else:
+            module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                          for f in (L.kaio_rope, L.kaio_rope_append, L.kaio_paged_attention)))
+            _host_module = module
+    return _host_module
+
+
 def rope(x, positions, inv_freq, sections=None, interleaved: bool = False, inverse: bool = False, out=None,
          stream=None):
     """Rotary positions: returns x [T, H, D] (f16 or bf16) with its first 2 * R
@@ -438,6 +460,11 @@ def rope(x, positions, inv_freq, sections=None, interleaved: bool = False, inver
     way: the gradient of the rotation with respect to x, given that of its
     result. out may be x itself.
     """
+    host = _host_module or _host()
+    if host:
+        done = host.rope(x, positions, inv_freq, sections, interleaved, inverse, out, stream)
+        if done is not None:
+            return done
     torch = _torch()
     code, dtype, shape = _rank3(x, "x")
     t, h, d = shape
@@ -467,6 +494,12 @@ def rope_append(q, k, v, positions, inv_freq, k_cache, v_cache, slots, sections=
     page_size, D]); slots int32 [T]: page * page_size + place in the page for each
     token, or -1 to store nothing. q_out may be q itself.
     """
+    host = _host_module or _host()
+    if host:
+        done = host.rope_append(q, k, v, positions, inv_freq, k_cache, v_cache, slots, sections, interleaved, q_out,
+                                stream)
+        if done is not None:
+            return done
     torch = _torch()
     code, dtype, shape = _rank3(q, "q")
     t, h, d = shape
@@ -524,6 +557,12 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max
     gets zeros and lse = -inf. workspace: from ``paged_attention_workspace``;
     without one the call makes its own.
     """
+    host = _host_module or _host()
+    if host:
+        done = host.paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts, max_new, scale, causal, window,
+                                    sinks, workspace, out, return_lse, lse, stream)
+        if done is not None:
+            return done
     torch = _torch()
     int32 = torch.int32
     code, dtype, shape = _rank3(q, "q")
