@@ -103,6 +103,7 @@ __device__ __forceinline__ long long paged_div(long long a, int b) {
 struct PagedShare {
   long long begin, end, each;    // each = total / ctas
   int ctas, more;                // more = total % ctas
+  int snap;                      // a boundary this near to an item's moves there
   __device__ __forceinline__ int owner(long long at) const {
     const long long first = (each + 1) * more;
     if (at < first) return static_cast<int>(paged_div(at, static_cast<int>(each + 1)));
@@ -115,10 +116,15 @@ struct PagedShare {
 // not split: it belongs to the share that holds its beginning. (Writing and joining parts
 // costs more than such an item's imbalance. By their ends, the last tile of a causal head,
 // its longest, would share a CTA with the first ones of the next.)
-template <int kRows, int kKeys, int kWhole, int kPartWorthPercent, int kSmallRows, int kSmallCost, int kCost>
+//
+// A boundary inside a longer item moves to the item's begin or end if that is nearer
+// than half a share and than kSnap: a CTA with parts of two items does everything that
+// precedes and follows their units twice.
+template <int kRows, int kKeys, int kWhole, int kPartWorthPercent, int kSmallRows, int kSmallCost, int kCost, int kSnapCost>
 struct PagedWalk {
   static_assert(kSmallCost <= kCost && kCost < 8);
-  static constexpr int kWholeUnits = kWhole;
+  static_assert(2 * kSnapCost < kWhole * kSmallCost, "a boundary may not be near both ends of an item that is split");
+  static constexpr int kWholeUnits = kWhole, kSnap = kSnapCost;
   static constexpr float kPartWorth = 0.01f * kPartWorthPercent;   // joining a part, in units
   int b, h, tile, tiles;      // item: sequence, K/V head, row tile of `tiles`
   int unit, units, cost;      // unit within the item; cost of one
@@ -151,14 +157,22 @@ struct PagedWalk {
     }
     return u;
   }
-  // The first unit past a CTA's share that ends at `end`.
-  __device__ __forceinline__ int unit_at(long long end) const {
-    const long long to = max(end - at, 0ll);
-    return to >= units * cost ? units : units > kWhole ? whole_units(static_cast<int>(to)) : to > 0 ? units : 0;
+  // The unit at which a boundary of shares cuts this item: 0 and `units` for those before and past it.
+  __device__ __forceinline__ int cut(long long boundary, int snap) const {
+    const int length = units * cost;
+    const long long to = boundary - at;
+    if (to <= 0 || to >= length) return to <= 0 ? 0 : units;
+    if (units <= kWhole) return units;
+    const int into = static_cast<int>(to);
+    return into <= snap ? 0 : length - into <= snap ? units : whole_units(into);
   }
   // The CTAs that hold its first and its last unit.
-  __device__ __forceinline__ int first_owner(const PagedShare& share) const { return share.owner(at + cost - 1); }
-  __device__ __forceinline__ int last_owner(const PagedShare& share) const { return share.owner(at + units * cost - 1); }
+  __device__ __forceinline__ int first_owner(const PagedShare& share) const {
+    return share.owner(at + max(cost - 1, share.snap));
+  }
+  __device__ __forceinline__ int last_owner(const PagedShare& share) const {
+    return share.owner(at + units * cost - share.snap - 1);
+  }
   // To the first unit of the next item (past the line's end: b == batch).
   __device__ __forceinline__ void next_item(const PagedParams& p) {
     at += units * cost;
@@ -222,6 +236,7 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
   if (cta >= share->ctas) return false;
   share->each = paged_div(total, share->ctas);
   share->more = static_cast<int>(total - share->each * share->ctas);
+  share->snap = min(Walk::kSnap, static_cast<int>(min(share->each, 1ll << 30) + 1) / 2);
   share->begin = cta * share->each + min(cta, share->more);
   share->end = share->begin + share->each + (cta < share->more ? 1 : 0);
   const long long from = upto - mine;
@@ -247,9 +262,9 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
       if (left < w.units * w.cost) break;
       left -= w.units * w.cost;
     }
-    w.unit = w.units <= Walk::kWholeUnits ? 0 : w.whole_units(static_cast<int>(left));
     w.at = share->begin - left;
-    if (w.units <= Walk::kWholeUnits && left > 0) w.next_item(p);
+    w.unit = w.cut(share->begin, share->snap);
+    if (w.unit == w.units) w.next_item(p);
     *place = w;
   }
   __syncthreads();

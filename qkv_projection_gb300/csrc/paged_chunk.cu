@@ -79,7 +79,7 @@ constexpr int kFewParts = 3;            // parts - 1 up to which the last CTA jo
 constexpr float kLazy = 8.f;            // growth of the maximum (log2) that renews the reference
 // A part is worth a unit in the size of shares: 100 tokens over 9000 keys with 32/8 heads take 75 us, and 62 us
 // with two units, but 20 over 60000 with 8/1 76 and 82, 100 over 14000 with 8/1 42 and 50.
-using Walk = PagedWalk<kRows, kKeys, kWhole, 100, kHalf, 3, 4>;
+using Walk = PagedWalk<kRows, kKeys, kWhole, 100, kHalf, 3, 4, 16>;
 using Span = PagedSpan<kKeys>;
 
 template <int kDim> struct Shape {
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           Walk& w = ctl.place;
           Job& job = ctl.jobs[k % kJobs];
-          const int u0 = any ? w.unit : 0, u1 = any && w.b < p.batch ? w.unit_at(ctl.share.end) : 0;
+          const int u0 = any ? w.unit : 0, u1 = any && w.b < p.batch ? w.cut(ctl.share.end, ctl.share.snap) : 0;
           if (u1 <= u0) {
             job.mode = Mode::kEnd;
           } else {

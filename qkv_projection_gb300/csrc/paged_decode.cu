@@ -35,7 +35,7 @@ constexpr int kCtasPerSm = 2;
 // Units of an item that is not split: joining parts takes 4-6 us, a unit 0.6 us (32
 // sequences of 300 positions: 10.0 us whole, 16.5 us split; 16 units and more are better split).
 constexpr int kWhole = 8;
-using Walk = PagedWalk<kRows, kUnitKeys, kWhole, 20, 0, 1, 1>;
+using Walk = PagedWalk<kRows, kUnitKeys, kWhole, 20, 0, 4, 4, 12>;
 using Span = PagedSpan<kUnitKeys>;
 
 template <int kDim> struct Shape {
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   auto begin = [&] {
     if (w.b >= p.batch) return false;
     u0 = w.unit;
-    u1 = w.unit_at(share.end);
+    u1 = w.cut(share.end, share.snap);
     if (u1 <= u0) return false;
     span = Span(p, w.s, w.row0(), w.row1(p));
     lo = span.lo, hi = span.hi, first = span.first;
