@@ -79,7 +79,7 @@ constexpr int kFewParts = 3;            // parts - 1 up to which the last CTA jo
 constexpr float kLazy = 8.f;            // growth of the maximum (log2) that renews the reference
 // A part is worth a unit in the size of shares: 100 tokens over 9000 keys with 32/8 heads take 75 us, and 62 us
 // with two units, but 20 over 60000 with 8/1 76 and 82, 100 over 14000 with 8/1 42 and 50.
-using Walk = PagedWalk<kRows, kKeys, kWhole, 100, kHalf, 3, 4, 16>;
+using Walk = PagedWalk<kRows, kHalf, kKeys, kWhole, 100, kHalf, 3, 4, 16>;
 using Span = PagedSpan<kKeys>;
 
 template <int kDim> struct Shape {

@@ -35,7 +35,7 @@ constexpr int kCtasPerSm = 2;
 // Units of an item that is not split: joining parts takes 4-6 us, a unit 0.6 us (32
 // sequences of 300 positions: 10.0 us whole, 16.5 us split; 16 units and more are better split).
 constexpr int kWhole = 8;
-using Walk = PagedWalk<kRows, kUnitKeys, kWhole, 20, 0, 4, 4, 12>;
+using Walk = PagedWalk<kRows, kRows, kUnitKeys, kWhole, 20, 0, 4, 4, 12>;
 using Span = PagedSpan<kUnitKeys>;
 
 template <int kDim> struct Shape {
