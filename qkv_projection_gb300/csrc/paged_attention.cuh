@@ -8,9 +8,9 @@
 // tokens) and a run that ends at its last token.
 //
 // All units of all items stand in one line (sequence, K/V head, row tile, key
-// tile), and CTA c takes the c-th equal share of it. So a batch of unlike
-// lengths, one long sequence and many short ones all load the GPU evenly, and
-// the lengths are read where they are, on the device. An item that a boundary
+// tile), each as long as it costs, and CTA c takes the c-th equal share of it. So a
+// batch of unlike lengths, one long sequence and many short ones all load the GPU
+// evenly, and the lengths are read where they are, on the device. An item that a boundary
 // cuts is finished from partial results: each CTA writes its output (normalised,
 // f32) and log-sum-exp to the workspace, and the CTA that arrives last joins
 // them, always in the order of the keys, so results do not depend on timing.
@@ -104,6 +104,7 @@ struct PagedShare {
   long long begin, end, each;    // each = total / ctas
   int ctas, more;                // more = total % ctas
   int snap;                      // a boundary this near to an item's moves there
+  int whole;                     // items of so many units are not cut at all
   __device__ __forceinline__ int owner(long long at) const {
     const long long first = (each + 1) * more;
     if (at < first) return static_cast<int>(paged_div(at, static_cast<int>(each + 1)));
@@ -111,27 +112,33 @@ struct PagedShare {
   }
 };
 
-// A place in the line of work: an item, and a unit in it. A unit of an item of at most
-// kSmallRows rows costs kSmallCost, any other kCost. An item of at most kWhole units is
-// not split: it belongs to the share that holds its beginning. (Writing and joining parts
-// costs more than such an item's imbalance. By their ends, the last tile of a causal head,
-// its longest, would share a CTA with the first ones of the next.)
-//
-// A boundary inside a longer item moves to the item's begin or end if that is nearer
-// than half a share and than kSnap: a CTA with parts of two items does everything that
-// precedes and follows their units twice.
-//
-// Where no item is split and there are at most half as many as CTAs, tiles of kFewRows
-// rows take the place of those of kRows (three chunks of 77 tokens over 613 keys, 15/3
-// heads: 15.5 us in 18 tiles, 13.1 us in 36; four of 60 over 1000, 16/4 heads: 19.9 and 15.0).
-template <int kRows, int kFewRows, int kKeys, int kWhole, int kPartWorthPercent, int kSmallRows, int kSmallCost, int kCost,
-          int kSnapCost>
-struct PagedWalk {
+// A place in the line of work: an item, and a unit in it. The constants of `Work`:
+//   kRows, kKeys          rows of a tile, keys of a unit
+//   kCost, kSmallCost     length of a unit in the line; the second for items of at most
+//                         kSmallRows rows
+//   kItemCost             what an item costs besides its units
+//   kPartWorth            what joining a part costs, in units, in the size of shares
+//   kWhole, kJoin         An item that is not split waits for one CTA, a split one for its
+//                         parts to be written and joined. With at most as many items as
+//                         CTAs one of kWhole units, or of kJoin more than a share, stays
+//                         whole and belongs to the share that holds its beginning. (By
+//                         their ends, the last tile of a causal head, its longest, would
+//                         share a CTA with the first ones of the next.) Of more items
+//                         those of kWholeOfMany units do.
+//   kSnap                 A boundary inside another item moves to its begin or end if that
+//                         is nearer than half a share and than kSnap: a CTA with parts of
+//                         two items does all that precedes and follows their units twice.
+//                         (One token over 1037 keys of 32 heads, 9 shares to an item: 15.5
+//                         us with boundaries where they fall, 11.6 us so; 100 tokens over
+//                         9000, 32/8 heads: 73 and 59.)
+//   kFewRows              Where no item is split and there are at most half as many as
+//                         CTAs, the rows of a tile instead (three chunks of 77 tokens over
+//                         613 keys, 15/3 heads: 15.5 us in 18 tiles, 13.1 us in 36; four
+//                         of 60 over 1000, 16/4 heads: 19.9 and 15.0).
+template <typename Work>
+struct PagedWalk : Work {
+  using Work::kRows, Work::kFewRows, Work::kKeys, Work::kCost, Work::kSmallCost, Work::kSmallRows, Work::kItemCost;
   static_assert(kSmallCost <= kCost && kCost < 8);
-  static_assert(2 * kSnapCost < kWhole * kSmallCost, "a boundary may not be near both ends of an item that is split");
-  static constexpr int kWholeUnits = kWhole, kSnap = kSnapCost;
-  static constexpr int kMostRows = kRows, kLeastRows = kFewRows;
-  static constexpr float kPartWorth = 0.01f * kPartWorthPercent;   // joining a part, in units
   int tile_rows;              // kRows or kFewRows
   int b, h, tile, tiles;      // item: sequence, K/V head, row tile of `tiles`
   int unit, units, cost;      // unit within the item; cost of one
@@ -150,6 +157,7 @@ struct PagedWalk {
   __device__ __forceinline__ int item_cost(const PagedParams& p, const PagedSeq& s, int tile) const {
     return s.n * p.group - tile * step() <= kSmallRows || (kFewRows <= kSmallRows && step() == kFewRows) ? kSmallCost : kCost;
   }
+  __device__ __forceinline__ int length() const { return kItemCost + units * cost; }
   // (divisions by constants)
   __device__ __forceinline__ int whole_units(int length) const {
     return kSmallCost != kCost && cost == kSmallCost ? length / kSmallCost : length / kCost;
@@ -160,30 +168,29 @@ struct PagedWalk {
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i) {
       const int units = item_units(p, s, i), cost = item_cost(p, s, i);
-      u += units * cost;
+      u += kItemCost + units * cost;
       *longest = max(*longest, 8 * units + cost);
     }
     return u;
   }
   // The unit at which a boundary of shares cuts this item: 0 and `units` for those before and past it.
-  __device__ __forceinline__ int cut(long long boundary, int snap) const {
-    const int length = units * cost;
+  __device__ __forceinline__ int cut(long long boundary, const PagedShare& share) const {
     const long long to = boundary - at;
-    if (to <= 0 || to >= length) return to <= 0 ? 0 : units;
-    if (units <= kWhole) return units;
+    if (to <= 0 || to >= length()) return to <= 0 ? 0 : units;
+    if (units <= share.whole) return units;
     const int into = static_cast<int>(to);
-    return into <= snap ? 0 : length - into <= snap ? units : whole_units(into);
+    return into <= share.snap ? 0 : length() - into <= share.snap ? units : whole_units(max(into - kItemCost, 0));
   }
   // The CTAs that hold its first and its last unit.
   __device__ __forceinline__ int first_owner(const PagedShare& share) const {
-    return share.owner(at + max(cost - 1, share.snap));
+    return share.owner(at + max(kItemCost + cost - 1, share.snap));
   }
   __device__ __forceinline__ int last_owner(const PagedShare& share) const {
-    return share.owner(at + units * cost - share.snap - 1);
+    return share.owner(at + max(length() - share.snap - 1, share.snap));
   }
   // To the first unit of the next item (past the line's end: b == batch).
   __device__ __forceinline__ void next_item(const PagedParams& p) {
-    at += units * cost;
+    at += length();
     unit = 0;
     if (++tile == tiles) {
       tile = 0;
@@ -212,19 +219,18 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
   const int per = (p.batch + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
   constexpr int kWarps = kThreads / 32;
-  constexpr bool kTwoSizes = Walk::kLeastRows < Walk::kMostRows;
+  constexpr bool kTwoSizes = Walk::kFewRows < Walk::kRows;
   Walk w;
   long long mine, upto, total;
-  int longest;
+  int longest, items;
 #pragma unroll 1
-  for (w.tile_rows = Walk::kMostRows;; w.tile_rows = Walk::kLeastRows) {
-    mine = 0, total = 0, longest = 0;
-    int items = 0;
+  for (w.tile_rows = Walk::kRows;; w.tile_rows = Walk::kFewRows) {
+    mine = 0, total = 0, longest = 0, items = 0;
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       const PagedSeq s = paged_seq(p, b);
       mine += p.kv_heads * w.head_length(p, s, &longest);
-      if (kTwoSizes) items = min(items + p.kv_heads * w.row_tiles(p, s), 1 << 20);
+      items = min(items + p.kv_heads * w.row_tiles(p, s), 1 << 20);
     }
     upto = mine;
 #pragma unroll
@@ -233,7 +239,7 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
       if ((tid & 31) >= d) upto += add;
     }
     longest = __reduce_max_sync(0xFFFFFFFFu, longest);
-    if (kTwoSizes) items = __reduce_add_sync(0xFFFFFFFFu, items);
+    items = __reduce_add_sync(0xFFFFFFFFu, items);
     if ((tid & 31) == 31) {
       sums[tid >> 5] = upto;
       sums[kWarps + (tid >> 5)] = longest | static_cast<long long>(items) << 32;
@@ -247,7 +253,7 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
       longest = max(longest, static_cast<int>(sums[kWarps + i]));
       items += static_cast<int>(sums[kWarps + i] >> 32);
     }
-    if (!kTwoSizes || w.tile_rows == Walk::kLeastRows || (longest >> 3) > Walk::kWholeUnits || 2 * items > grid) break;
+    if (!kTwoSizes || w.tile_rows == Walk::kFewRows || (longest >> 3) > Walk::kWhole || 2 * items > grid) break;
     __syncthreads();                                       // sums have been read
   }
   if (total == 0) return false;
@@ -255,12 +261,17 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
   // in shares of u takes about u units' time, and then U / u parts to join one after another;
   // with a part at about kWorth units the sum is least for u = sqrt(kWorth U).
   const int units = longest >> 3, cost = longest & 7;
-  const int least = units <= Walk::kWholeUnits ? 1 : max(1, static_cast<int>(sqrtf(Walk::kPartWorth * static_cast<float>(units))));
-  share->ctas = static_cast<int>(min(static_cast<long long>(grid), max(1ll, paged_div(total, least * cost))));
+  const int least = units <= Walk::kWhole ? 1 : max(1, static_cast<int>(sqrtf(Walk::kPartWorth * static_cast<float>(units))));
+  // (a share that cuts an item holds a unit at least)
+  const bool few = items <= grid;
+  const int worth = max(least * cost, units <= (few ? Walk::kWhole : Walk::kWholeOfMany) ? 1 : Walk::kCost);
+  share->ctas = static_cast<int>(min(static_cast<long long>(grid), max(1ll, paged_div(total, worth))));
   if (cta >= share->ctas) return false;
   share->each = paged_div(total, share->ctas);
   share->more = static_cast<int>(total - share->each * share->ctas);
-  share->snap = min(Walk::kSnap, static_cast<int>(min(share->each, 1ll << 30) + 1) / 2);
+  const int each = static_cast<int>(min(share->each, 1ll << 30));
+  share->whole = few ? max(Walk::kWhole, Walk::kJoin + each / Walk::kCost) : Walk::kWholeOfMany;
+  share->snap = min(Walk::kSnap, (each + 1) / 2);
   share->begin = cta * share->each + min(cta, share->more);
   share->end = share->begin + share->each + (cta < share->more ? 1 : 0);
   const long long from = upto - mine;
@@ -282,11 +293,11 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
     for (w.tile = 0;; ++w.tile) {
       w.units = w.item_units(p, w.s, w.tile);
       w.cost = w.item_cost(p, w.s, w.tile);
-      if (left < w.units * w.cost) break;
-      left -= w.units * w.cost;
+      if (left < w.length()) break;
+      left -= w.length();
     }
     w.at = share->begin - left;
-    w.unit = w.cut(share->begin, share->snap);
+    w.unit = w.cut(share->begin, *share);
     if (w.unit == w.units) w.next_item(p);
     *place = w;
   }

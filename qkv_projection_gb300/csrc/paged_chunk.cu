@@ -74,12 +74,19 @@ constexpr int kMmaWarp = 8, kLoadWarp = 10;   // and the one after each
 constexpr int kThreads = 384;
 // Registers a thread: 384 threads start with 168; 256 x 216 + 128 x 72 is the same total.
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
-constexpr int kWhole = 16;              // units of an item that is not split (a part and its join cost 5 to 7 units)
 constexpr int kFewParts = 3;            // parts - 1 up to which the last CTA joins the others' with its own from tensor memory
 constexpr float kLazy = 8.f;            // growth of the maximum (log2) that renews the reference
-// A part is worth a unit in the size of shares: 100 tokens over 9000 keys with 32/8 heads take 75 us, and 62 us
-// with two units, but 20 over 60000 with 8/1 76 and 82, 100 over 14000 with 8/1 42 and 50.
-using Walk = PagedWalk<kRows, kHalf, kKeys, kWhole, 100, kHalf, 3, 4, 16>;
+// An item besides its units takes 7500 cycles, two units' time, whatever its length (2574
+// new tokens, 32/8 heads, tiles of 1 to 21 units: 85 us with items of up to 16 whole and free
+// of cost, 71 us so). A part is worth a unit: 100 tokens over 9000 keys with 32/8 heads take
+// 59 us, and 61 us with 0.6 units, 20 over 60000 with 8/1 79 and 81, with two units 84.
+struct Work {
+  static constexpr int kRows = 256, kFewRows = 128, kKeys = 128;
+  static constexpr int kCost = 4, kSmallRows = 128, kSmallCost = 3, kItemCost = 8, kSnap = 16;
+  static constexpr int kWhole = 16, kJoin = 6, kWholeOfMany = 0;
+  static constexpr float kPartWorth = 1.f;
+};
+using Walk = PagedWalk<Work>;
 using Span = PagedSpan<kKeys>;
 
 template <int kDim> struct Shape {
@@ -306,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           Walk& w = ctl.place;
           Job& job = ctl.jobs[k % kJobs];
-          const int u0 = any ? w.unit : 0, u1 = any && w.b < p.batch ? w.cut(ctl.share.end, ctl.share.snap) : 0;
+          const int u0 = any ? w.unit : 0, u1 = any && w.b < p.batch ? w.cut(ctl.share.end, ctl.share) : 0;
           if (u1 <= u0) {
             job.mode = Mode::kEnd;
           } else {

@@ -14,7 +14,16 @@
 // 16-byte asynchronous copies and computes with warp-level m16n8k16 products
 // (up to 16 rows; the rate does not matter here, the rows are few), so the main
 // loop has no barrier between warps. Keys that no row of the item sees are
-// filled with zeros and their pages are not read.
+// filled with zeros and their pages are not read. Two CTAs of four warps on an SM
+// with three or six stages of 8 or 4 KB each keep 150 to 190 KB in flight on it.
+// 64 tokens over contexts of up to 8192, 32 heads on 8 of 128: 205-210 us, 6.4-6.6 TB/s
+// (0.95-0.97 of a measured copy); one token over 131072: 91 us (0.86); 16 tokens of 64
+// heads with a window of 4096: 52-53 us (0.75; 5 us of it before the first keys arrive).
+//
+// Short calls are bound by what surrounds the units. One token over 1037 keys, 32 heads
+// (11.6 us): 4 us from the launch to the first copies (the shares, then page ids, then
+// keys: three round trips, in code that is fetched for the first time), 2 us for two
+// units, 4 us to write a part, to find out who is last and to join nine of them.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -32,10 +41,17 @@ constexpr int kStepKeys = 16;                    // keys of one warp and step
 constexpr int kUnitKeys = kWarps * kStepKeys;    // 64
 constexpr int kRows = kPagedDecodeRows;
 constexpr int kCtasPerSm = 2;
-// Units of an item that is not split: joining parts takes 4-6 us, a unit 0.6 us (32
-// sequences of 300 positions: 10.0 us whole, 16.5 us split; 16 units and more are better split).
-constexpr int kWhole = 8;
-using Walk = PagedWalk<kRows, kRows, kUnitKeys, kWhole, 20, 0, 4, 4, 12>;
+// Joining parts takes 4-6 us, a unit 0.6 us (32 sequences of 300 positions, 5 units: 10.0 us
+// whole, 16.5 us split; 64 of 900, 15 units to shares of 13: 20.6 whole, 25.3 split). A part is
+// worth 0.2 units in the size of shares (one token over 9000 keys, 32/8 heads: 17.1 us, with 0.4
+// 18.4, 0.8 22.6; 4 over 2000: 13.6, 13.3, 15.0).
+struct Work {
+  static constexpr int kRows = kPagedDecodeRows, kFewRows = kRows, kKeys = kUnitKeys;
+  static constexpr int kCost = 4, kSmallRows = 0, kSmallCost = 4, kItemCost = 8, kSnap = 12;
+  static constexpr int kWhole = 8, kJoin = 8, kWholeOfMany = 8;
+  static constexpr float kPartWorth = 0.2f;
+};
+using Walk = PagedWalk<Work>;
 using Span = PagedSpan<kUnitKeys>;
 
 template <int kDim> struct Shape {
@@ -178,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   auto begin = [&] {
     if (w.b >= p.batch) return false;
     u0 = w.unit;
-    u1 = w.cut(share.end, share.snap);
+    u1 = w.cut(share.end, share);
     if (u1 <= u0) return false;
     span = Span(p, w.s, w.row0(), w.row1(p));
     lo = span.lo, hi = span.hi, first = span.first;
