@@ -24,6 +24,7 @@
 #include <utility>
 
 #include "../../include/kaio_qkv.h"
+#include "attention_internal.h"
 #include "kaio_internal.h"
 
 namespace {

@@ -85,70 +85,6 @@ cudaError_t launch_dequant_group_forward(FloatType t, bool q_unsigned, const voi
                                          void* out, int outer, int axis, int group, int num_sms,
                                          cudaStream_t stream);
 
-// n / d for 0 <= n < 2^31 by one multiplication (round-up reciprocal).
-struct FastDiv {
-  uint32_t mul = 1, shift = 0, d = 1;
-  FastDiv() = default;
-  explicit FastDiv(uint32_t div) : d(div) {
-    while ((1ull << shift) < div) ++shift;
-    mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - div)) / div + 1);
-  }
-#ifdef __CUDACC__
-  __device__ __forceinline__ int div(int n) const {
-    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
-  }
-#endif
-};
-
-// ----------------------------------------------- rotary positions, cache write
-// Strides are in elements. kv_heads == 0: q alone (no cache).
-struct RopeParams {
-  const void *q, *k, *v;
-  void *qo, *kc, *vc;
-  long long q_ts, q_hs, qo_ts, qo_hs, k_ts, k_hs, v_ts, v_hs;   // token and head strides
-  long long kc_ps, kc_ss, kc_hs, vc_ps, vc_ss, vc_hs;           // page, slot and head strides
-  const int* slots;           // [tokens] page * page_size + slot; outside the cache: not stored
-  const int* positions;       // [axes][tokens], axis stride pos_stride
-  long long pos_stride;
-  const float* inv_freq;      // [pairs]
-  int tokens, q_heads, kv_heads, dim, pairs, axes;
-  int section_end[4];         // first pair past each axis's section
-  int num_pages, page_size;
-  bool interleaved, inverse;
-};
-cudaError_t launch_rope(FloatType t, const RopeParams& r, int num_sms, cudaStream_t stream);
-
-// ------------------------------------------------------------- paged attention
-// Strides are in elements.
-struct PagedParams {
-  const void *q, *kc, *vc;
-  void* out;
-  float* lse;                 // [tokens][heads], natural logarithm; may be null
-  long long q_ts, q_hs, o_ts, o_hs;
-  long long k_ps, k_ss, k_hs, v_ps, v_ss, v_hs, table_stride;
-  const int *table, *kv_lens, *q_starts;   // q_starts may be null: one token per sequence
-  int batch, tokens, heads, kv_heads, group, dim;
-  FastDiv group_div;          // group = heads / kv_heads
-  int page_shift, num_pages, max_pages;
-  bool causal;
-  int window, sinks;          // window 0: none; both at most kPagedMaxLen
-  float scale_log2;           // softmax scale * log2(e)
-  float* part_o;              // [2 * ctas][rows][dim] partial outputs of split work
-  float* part_l;              // [2 * ctas][rows] their log2-sum-exp2
-  unsigned* counters;         // [ctas], zero between launches
-};
-constexpr int kPagedMaxLen = 1 << 30;
-// Rows (tokens x query heads of one K/V head) that one CTA of the warp-MMA
-// kernel takes at a time.
-constexpr int kPagedDecodeRows = 16;
-// Workspace layout: counters first, then the partial sums.
-constexpr size_t kPagedCounterBytes = 4096;
-size_t paged_decode_workspace_bytes(int num_sms);
-cudaError_t launch_paged_decode(FloatType t, PagedParams p, void* workspace, int num_sms, cudaStream_t stream);
-size_t paged_chunk_workspace_bytes(int num_sms);
-cudaError_t launch_paged_chunk(FloatType t, const PagedParams& p, void* workspace, int num_sms, cudaStream_t stream);
-unsigned read_and_clear_chunk_errors();
-
 // ------------------------------------------------- tensor-core (tcgen05) paths
 struct GemmShape {
   int M, N, K;              // C[M, N] = sum_k Aop[M, k] * Bop[k, N]
@@ -185,31 +121,8 @@ unsigned read_and_clear_tc_errors();
 cudaError_t ensure_smem_limit(const void* kernel, int bytes);
 
 // Driver entry point for tensor-map encoding (resolved once through the runtime).
-// encode_tensor_map: any rank, strides in bytes of dimensions 1 and up, nothing kept.
-CUresult encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank, const void* base,
-                           const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
-                           CUtensorMapSwizzle swz);
 CUresult encode_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
                               uint64_t inner, uint64_t outer, uint64_t row_bytes,
                               uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz);
-
-// A launch that may begin while the kernel before it in the stream still runs
-// (programmatic dependent launch): the kernel waits for it (grid_dependency_wait)
-// before it touches memory.
-template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), int grid, int threads, int smem, cudaStream_t stream,
-                             const Args&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
 
 }  // namespace kaio

@@ -16,8 +16,8 @@
 // them, always in the order of the keys, so results do not depend on timing.
 #pragma once
 
+#include "attention_internal.h"
 #include "kaio_device.cuh"
-#include "kaio_internal.h"
 
 namespace kaio {
 
@@ -120,11 +120,11 @@ struct PagedShare {
 //   kPartWorth            what joining a part costs, in units, in the size of shares
 //   kWhole, kJoin         An item that is not split waits for one CTA, a split one for its
 //                         parts to be written and joined. With at most as many items as
-//                         CTAs one of kWhole units, or of kJoin more than a share, stays
-//                         whole and belongs to the share that holds its beginning. (By
-//                         their ends, the last tile of a causal head, its longest, would
-//                         share a CTA with the first ones of the next.) Of more items
-//                         those of kWholeOfMany units do.
+//                         CTAs, none longer than kWhole units or than a share and kJoin,
+//                         all stay whole and belong to the share that holds their
+//                         beginning. (By their ends, the last tile of a causal head, its
+//                         longest, would share a CTA with the first ones of the next.)
+//                         Otherwise those of kWholeOfMany units do.
 //   kSnap                 A boundary inside another item moves to its begin or end if that
 //                         is nearer than half a share and than kSnap: a CTA with parts of
 //                         two items does all that precedes and follows their units twice.
@@ -230,7 +230,7 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
     for (int b = b0; b < b1; ++b) {
       const PagedSeq s = paged_seq(p, b);
       mine += p.kv_heads * w.head_length(p, s, &longest);
-      items = min(items + p.kv_heads * w.row_tiles(p, s), 1 << 20);
+      if (kTwoSizes) items = min(items + p.kv_heads * w.row_tiles(p, s), 1 << 20);
     }
     upto = mine;
 #pragma unroll
@@ -239,7 +239,7 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
       if ((tid & 31) >= d) upto += add;
     }
     longest = __reduce_max_sync(0xFFFFFFFFu, longest);
-    items = __reduce_add_sync(0xFFFFFFFFu, items);
+    if (kTwoSizes) items = __reduce_add_sync(0xFFFFFFFFu, items);
     if ((tid & 31) == 31) {
       sums[tid >> 5] = upto;
       sums[kWarps + (tid >> 5)] = longest | static_cast<long long>(items) << 32;
@@ -251,7 +251,7 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
       if (i == (tid >> 5)) upto += total;
       total += sums[i];
       longest = max(longest, static_cast<int>(sums[kWarps + i]));
-      items += static_cast<int>(sums[kWarps + i] >> 32);
+      if (kTwoSizes) items += static_cast<int>(sums[kWarps + i] >> 32);
     }
     if (!kTwoSizes || w.tile_rows == Walk::kFewRows || (longest >> 3) > Walk::kWhole || 2 * items > grid) break;
     __syncthreads();                                       // sums have been read
@@ -263,14 +263,20 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
   const int units = longest >> 3, cost = longest & 7;
   const int least = units <= Walk::kWhole ? 1 : max(1, static_cast<int>(sqrtf(Walk::kPartWorth * static_cast<float>(units))));
   // (a share that cuts an item holds a unit at least)
-  const bool few = items <= grid;
-  const int worth = max(least * cost, units <= (few ? Walk::kWhole : Walk::kWholeOfMany) ? 1 : Walk::kCost);
-  share->ctas = static_cast<int>(min(static_cast<long long>(grid), max(1ll, paged_div(total, worth))));
+  // (tiles of one size take a sequence's few rows: one item for each K/V head, not counted)
+  const bool few = kTwoSizes ? items <= grid : static_cast<long long>(p.batch) * p.kv_heads <= grid;
+  // (Where nothing is cut: enough shares that no item meets another, and no more, since idle
+  // CTAs slow the others' start: 10 sequences of 4 keys, 4 K/V heads: 6.4 us on 120, 6.2 on 40.)
+  const bool uncut = units <= (few ? Walk::kWhole : Walk::kWholeOfMany);
+  const long long length = uncut && kTwoSizes ? total - items * Walk::kItemCost : total;
+  const int worth = !uncut ? max(least * cost, Walk::kCost) : kTwoSizes ? cost : Walk::kItemCost + cost;
+  share->ctas = static_cast<int>(min(static_cast<long long>(grid), max(1ll, paged_div(length, worth))));
   if (cta >= share->ctas) return false;
   share->each = paged_div(total, share->ctas);
   share->more = static_cast<int>(total - share->each * share->ctas);
   const int each = static_cast<int>(min(share->each, 1ll << 30));
-  share->whole = few ? max(Walk::kWhole, Walk::kJoin + each / Walk::kCost) : Walk::kWholeOfMany;
+  const int limit = max(Walk::kWhole, Walk::kJoin + each / Walk::kCost);
+  share->whole = few && units <= limit ? limit : Walk::kWholeOfMany;
   share->snap = min(Walk::kSnap, (each + 1) / 2);
   share->begin = cta * share->each + min(cta, share->more);
   share->end = share->begin + share->each + (cta < share->more ? 1 : 0);

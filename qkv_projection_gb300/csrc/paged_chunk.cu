@@ -19,8 +19,8 @@
 // 2016 of products; the rest is the way from product to softmax to product, with one
 // wait and one commit of 150-300 cycles each. TMEM is full (two S and two O of 128
 // columns), so there is no third half to fill the gap. 4096 tokens over 16384 keys,
-// 32 heads on 8 of 128: 1.40-1.43 PFLOP/s, 0.73 of what the measured library product
-// reaches in a burst, 0.82 of it sustained.
+// 32 heads on 8 of 128: 680-730 us with the power limit, 1.32-1.42 PFLOP/s, 0.68-0.73 of
+// what the measured library product reaches in a burst, 0.76-0.82 of it sustained.
 //
 // Registers: the softmax warps rescale O and write the results themselves (both are
 // rare), so eight of twelve warps share nearly all registers (216 a thread, 72 for the
@@ -40,7 +40,8 @@
 // units make the halves a pair, which takes every other unit each on the same rows and
 // joins in tensor memory at the end: 2600 cycles a unit, 43 GB/s for each SM, which is
 // the memory's rate. Such a unit counts 3 in the line of work, one of 256 rows 4 (a mixed
-// step of 31 single tokens and 512 new ones: 136 us with equal counts, 121 us so).
+// step of 31 single tokens and 512 new ones: 136 us with equal counts, 121 us so, 114 with
+// the cost of an item).
 //
 // Warps 0-3 and 4-7: the softmax of the halves; 8, 9: their MMAs; 10: works out the
 // jobs (items, or this CTA's part of one) a few ahead and loads K; 11: loads V. Tiles
@@ -53,6 +54,8 @@
 // Split items: the CTA that is last joins the parts in their order. Up to three parts it
 // joins from its own tensor memory and the workspace; more only from the workspace, with
 // ten loads of a thread in flight (one after another a part took 6000 cycles).
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -74,7 +77,7 @@ constexpr int kMmaWarp = 8, kLoadWarp = 10;   // and the one after each
 constexpr int kThreads = 384;
 // Registers a thread: 384 threads start with 168; 256 x 216 + 128 x 72 is the same total.
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
-constexpr int kFewParts = 3;            // parts - 1 up to which the last CTA joins the others' with its own from tensor memory
+constexpr int kFewParts = 3;            // parts up to which the last CTA joins the others' with its own still in tensor memory
 constexpr float kLazy = 8.f;            // growth of the maximum (log2) that renews the reference
 // An item besides its units takes 7500 cycles, two units' time, whatever its length (2574
 // new tokens, 32/8 heads, tiles of 1 to 21 units: 85 us with items of up to 16 whole and free
@@ -970,6 +973,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
+// The driver's tensor-map encoder, resolved once through the runtime.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) ==
+                        cudaSuccess && found == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f) : nullptr;
+  }();
+  return fn;
+}
+
 // [pages][slots][heads][dim] (strides in elements) as a 4-D map of boxes of 64
 // columns x up to 128 slots of one head of one page, the middle dimensions in
 // the order of their strides.
@@ -988,10 +1003,13 @@ cudaError_t encode_cache(CUtensorMap* map, int* heads_first, const void* base, F
     std::swap(strides[0], strides[1]);
     std::swap(box[1], box[2]);
   }
-  const CUresult r = encode_tensor_map(map,
-                                       t == FloatType::BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                                       4, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (!encode) return cudaErrorNotSupported;
+  const uint32_t steps[4] = {1, 1, 1, 1};
+  const CUresult r = encode(map, t == FloatType::BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                            4, const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 

@@ -24,8 +24,8 @@
 
 #include <cstdint>
 
+#include "attention_internal.h"
 #include "kaio_device.cuh"
-#include "kaio_internal.h"
 
 namespace kaio {
 namespace {

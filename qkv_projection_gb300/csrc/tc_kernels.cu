@@ -721,7 +721,9 @@ struct TmKeyHash {
 constexpr size_t kTmCacheMax = 512;   // entries per host thread before the cache is emptied
 }  // namespace
 
-static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+CUresult encode_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
+                              uint64_t inner, uint64_t outer, uint64_t row_bytes,
+                              uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -732,26 +734,6 @@ static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
         q == cudaDriverEntryPointSuccess)
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
   });
-  return fn;
-}
-
-CUresult encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank, const void* base,
-                           const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
-                           CUtensorMapSwizzle swz) {
-  const PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
-  if (!fn) return CUDA_ERROR_NOT_FOUND;
-  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  cuuint64_t d[5], st[4];
-  for (uint32_t i = 0; i < rank; ++i) d[i] = dims[i];
-  for (uint32_t i = 0; i + 1 < rank; ++i) st[i] = strides[i];
-  return fn(map, dtype, rank, const_cast<void*>(base), d, st, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-}
-
-CUresult encode_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
-                              uint64_t inner, uint64_t outer, uint64_t row_bytes,
-                              uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz) {
-  const PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
   if (!fn) return CUDA_ERROR_NOT_FOUND;
   thread_local std::unordered_map<TmKey, CUtensorMap, TmKeyHash> cache;
   const TmKey key{reinterpret_cast<uint64_t>(base), inner, outer, row_bytes, box_inner, box_outer,
