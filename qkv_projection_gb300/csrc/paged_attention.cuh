@@ -259,13 +259,12 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
   if (total == 0) return false;
   // The share has to be worth its CTA: one unit where no item is split. An item of U units
   // in shares of u takes about u units' time, and then U / u parts to join one after another;
-  // with a part at about kWorth units the sum is least for u = sqrt(kWorth U).
+  // with a part at kPartWorth units the sum is least for u = sqrt(kPartWorth U).
   const int units = longest >> 3, cost = longest & 7;
   const int least = units <= Walk::kWhole ? 1 : max(1, static_cast<int>(sqrtf(Walk::kPartWorth * static_cast<float>(units))));
-  // (a share that cuts an item holds a unit at least)
   // (tiles of one size take a sequence's few rows: one item for each K/V head, not counted)
   const bool few = kTwoSizes ? items <= grid : static_cast<long long>(p.batch) * p.kv_heads <= grid;
-  // (Where nothing is cut: enough shares that no item meets another, and no more, since idle
+  // (A share that cuts an item holds a unit at least. Where nothing is cut: enough shares that no item meets another, and no more, since idle
   // CTAs slow the others' start: 10 sequences of 4 keys, 4 K/V heads: 6.4 us on 120, 6.2 on 40.)
   const bool uncut = units <= (few ? Walk::kWhole : Walk::kWholeOfMany);
   const long long length = uncut && kTwoSizes ? total - items * Walk::kItemCost : total;
@@ -289,8 +288,8 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
       const long long head = w.head_length(p, w.s, &longest);
       if (left < head * p.kv_heads) {
         w.tiles = w.row_tiles(p, w.s);
-        w.h = static_cast<int>(paged_div(left, static_cast<int>(head)));
-        left -= w.h * head;
+#pragma unroll 1
+        for (w.h = 0; left >= head; ++w.h) left -= head;
         break;
       }
       left -= head * p.kv_heads;
