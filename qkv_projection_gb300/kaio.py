@@ -529,12 +529,15 @@ def rope_append(q, k, v, positions, inv_freq, k_cache, v_cache, slots, sections=
     return q_out
 
 
-def paged_attention_workspace(device=None):
+def paged_attention_workspace(device=None, stream=None):
     """A workspace for ``paged_attention`` on a device: allocate it once and keep
-    it. Calls that use the same one must be ordered (one stream, or events)."""
+    it. It is zeroed on ``stream`` (default: the current one). Its zeroing and the
+    calls that use it must be ordered (one stream, or events)."""
     torch = _torch()
     n = ctypes.c_uint64()
-    with torch.cuda.device(device):
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream), device=device)
+    with torch.cuda.device(device), torch.cuda.stream(stream):
         check(lib().kaio_paged_attention_workspace(ctypes.byref(n)))
         return torch.zeros(n.value, dtype=torch.uint8, device="cuda")
 
@@ -583,7 +586,8 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max
         _strides(q_starts, "q_starts", int32, (b + 1,))
         starts = q_starts.data_ptr()
     if workspace is None:
-        workspace = paged_attention_workspace(q.device)
+        # on the call's own stream: zeroed before the kernel, and freed to that stream's later work
+        workspace = paged_attention_workspace(q.device, stream)
     elif not (workspace.is_cuda and workspace.dtype is torch.uint8 and workspace.is_contiguous()):
         raise ValueError("workspace must be a dense uint8 CUDA tensor from paged_attention_workspace()")
     if out is None:
