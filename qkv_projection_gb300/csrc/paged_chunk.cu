@@ -9,8 +9,10 @@
 //   O += P V           tcgen05.mma, P from TMEM, V in shared memory, O (f32) in TMEM
 // with the online softmax of paged_decode.cu in its lazy form: the reference m of
 // a row is renewed, and O and the sum rescaled, only when the maximum has grown
-// by more than 2^8, so weights stay below 256 (an f16 holds 65504) and a renewal
-// is rare; sums are of the unrounded f32 weights.
+// by more than 2^8, so a renewal is rare; sums are of the unrounded f32 weights. In f16
+// the exponents are raised by 7 (for the reason in paged_decode.cu): the largest weight
+// of a row lies between 2^7 and 2^15, of the 65504 that fit, and what is lost 2^-32 or
+// more below it.
 //
 // What bounds it: many rows, the chain of each half (below); few rows, the bytes of K
 // and V. 256 rows make each K and V tile that the TMA brings serve two products of
@@ -140,6 +142,7 @@ static_assert(kSmem<128> <= 232448 && kSmem<64> <= 232448, "shared memory of one
 template <typename T> struct Type;
 template <> struct Type<__half> {
   static constexpr uint32_t kFormat = 0;
+  static constexpr int kShift = 7;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -147,6 +150,7 @@ template <> struct Type<__half> {
 };
 template <> struct Type<__nv_bfloat16> {
   static constexpr uint32_t kFormat = 1;
+  static constexpr int kShift = 0;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -532,6 +536,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The scale is applied after the mask (-inf) and the maximum, so it has to be
     // positive: a negative one turns Q's signs, a zero makes Q zero.
     const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
+    // What a row's scores, times the scale, get added as exponents of its weights. Rounded
+    // down, so that no weight is above 2^(kLazy + kShift) at any size of the reference.
+    constexpr int kShift = Type<T>::kShift;
+    auto addend = [&](float m) { return m == kNegInf ? kShift : __fmaf_rd(-m, scale, kShift); };
     uint32_t tile_phase = 0, o_phase = 0;
     bool q_sent = false;                                   // this item's Q is already on its way
 
@@ -655,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool renew = top > m && (m == kNegInf || (top - m) * scale > kLazy);
           if (__any_sync(0xFFFFFFFFu, renew)) {
             if (__any_sync(0xFFFFFFFFu, renew && m != kNegInf)) {
-              const float f = renew ? exp2_fast((m - top) * scale) : 1.f;
+              const float f = !renew ? 1.f : m == kNegInf ? 0.f : exp2_fast(addend(top) - addend(m));
               l *= f;
 #pragma unroll 1
               for (int c = 0; c < kDim; c += 16) {
@@ -675,15 +683,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (renew) m = top;
           }
-          const float ref = m == kNegInf ? 0.f : m * scale;
-          const uint64_t scale2 = pair(scale, scale), ref2 = pair(-ref, -ref);
+          const float add = addend(m);
+          const uint64_t scale2 = pair(scale, scale), addend2 = pair(add, add);
           uint64_t sum2[2] = {};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t packed[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float2 x = unpair(fma2(pair(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])), scale2, ref2));
+              const float2 x = unpair(fma2(pair(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])), scale2, addend2));
               const float a = exp2_fast(x.x), b = exp2_fast(x.y);
               sum2[i & 1] = add2(sum2[i & 1], pair(a, b));
               packed[e >> 1] = Type<T>::pack(a, b);
@@ -703,9 +711,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         look_for_others();
       }
 
-      // Results of this thread's row: O / l and m + log2 l (nothing seen: zeros, -inf).
+      // Results of this thread's row: O / l and reference + log2 l (nothing seen: zeros, -inf).
       const bool none = l == 0.f;                          // (a NaN score leaves l NaN)
-      float lse2 = none ? kNegInf : (m == kNegInf ? 0.f : m * scale) + log2f(l);
+      float lse2 = none ? kNegInf : (kShift - addend(m)) + log2f(l * (1.f / (1 << kShift)));
       float mul = none ? 0.f : 1.f / l, mul_other = 0.f;
       const bool paired = mode == Mode::kPair, split = w.split;
       const bool real = mine && my_row < rows;

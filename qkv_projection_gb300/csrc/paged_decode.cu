@@ -6,8 +6,11 @@
 // Online softmax: for each row a running maximum m and sum l over the keys seen
 // so far, and the output scaled by exp2(-m); a new maximum rescales l and the
 // output. Scores, statistics and outputs are f32; the weights are rounded to the
-// tensors' 16-bit type as the operand of the second product (relative error
-// 2^-11 or 2^-8 each, the same as the rounding of the result).
+// tensors' 16-bit type as the operand of the second product. That is a relative error of
+// 2^-8 each in bf16, the same as the rounding of the result. An f16 holds 2^-11 only down
+// to 2^-14 and nothing below 2^-25, and many keys far below one may weigh as much
+// together as they are many, so its weights are exp2(s - m + 14): the largest is 2^14 of
+// the 65504 that fit, and what is lost lies 2^-39 below it.
 //
 // What bounds it: the bytes of K and V, each read once. Every warp streams its
 // own 16 keys of a 64-key unit through its own ring of shared-memory stages with
@@ -65,6 +68,7 @@ template <int kDim> struct Shape {
 
 template <typename T> struct Mma;
 template <> struct Mma<__half> {
+  static constexpr int kShift = 14;      // log2 of the largest weight
   static __device__ __forceinline__ void run(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     mma_16816(d, a, b0, b1);
   }
@@ -74,6 +78,7 @@ template <> struct Mma<__half> {
   }
 };
 template <> struct Mma<__nv_bfloat16> {
+  static constexpr int kShift = 0;       // (f32's range)
   static __device__ __forceinline__ void run(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
@@ -113,16 +118,23 @@ __device__ __forceinline__ float quad_sum(float v) {
   return v + __shfl_xor_sync(0xFFFFFFFFu, v, 2);
 }
 
+// What the exponents of a row with maximum m are relative to. Rounded up, so that at any
+// size of m the largest weight is between 1 and 2^kShift.
+template <int kShift> __device__ __forceinline__ float reference(float m) {
+  return kShift ? __fadd_ru(m, -static_cast<float>(kShift)) : m;
+}
+
 // Shared memory of a CTA: a ring for each warp. Between items the first stage
 // already takes the next item's first keys; the others hold what the warps and CTAs
 // tell each other (kScratch floats of each warp's are used as one array).
 template <typename T, int kDim>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(const __grid_constant__ PagedParams p) {
   using S = Shape<kDim>;
+  constexpr int kShift = Mma<T>::kShift;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long sums[2 * kWarps];
   __shared__ Walk place;
-  __shared__ float warp_m[kWarps][kRows], warp_l[kWarps][kRows], own_lse[kRows];
+  __shared__ float warp_ref[kWarps][kRows], warp_l[kWarps][kRows], own_lse[kRows];
   __shared__ int last_one;
 
   allow_dependents_launch();
@@ -279,9 +291,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       const float top_a = fmaxf(m_a, quad_max(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]))));
       const float top_b = fmaxf(m_b, quad_max(fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]))));
       // a row that has seen nothing yet keeps weights and sums of zero
-      const float ref_a = top_a == kNegInf ? 0.f : top_a, ref_b = top_b == kNegInf ? 0.f : top_b;
+      const float ref_a = top_a == kNegInf ? 0.f : reference<kShift>(top_a);
+      const float ref_b = top_b == kNegInf ? 0.f : reference<kShift>(top_b);
       if (__any_sync(0xFFFFFFFFu, top_a != m_a || top_b != m_b)) {
-        const float fa = exp2_fast(m_a - ref_a), fb = exp2_fast(m_b - ref_b);
+        const float fa = exp2_fast(reference<kShift>(m_a) - ref_a), fb = exp2_fast(reference<kShift>(m_b) - ref_b);
         l_a *= fa;
         l_b *= fb;
 #pragma unroll
@@ -329,12 +342,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       more = begin();
     }
 
-    // The four warps' results: maxima, sums and outputs of the real rows.
+    // The four warps' results: references, sums and outputs of the real rows.
     l_a = quad_sum(l_a);
     l_b = quad_sum(l_b);
     if ((lane & 3) == 0) {
-      warp_m[warp][row_a] = m_a;
-      warp_m[warp][row_b] = m_b;
+      warp_ref[warp][row_a] = reference<kShift>(m_a);
+      warp_ref[warp][row_b] = reference<kShift>(m_b);
       warp_l[warp][row_a] = l_a;
       warp_l[warp][row_b] = l_b;
     }
@@ -361,16 +374,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       if (i >= quads) continue;
       float top = kNegInf, sum = 0.f, f[kWarps];
 #pragma unroll
-      for (int j = 0; j < kWarps; ++j) top = fmaxf(top, warp_m[j][row]);
+      for (int j = 0; j < kWarps; ++j) top = fmaxf(top, warp_ref[j][row]);
       const float ref = top == kNegInf ? 0.f : top;
 #pragma unroll
       for (int j = 0; j < kWarps; ++j) {
-        f[j] = exp2_fast(warp_m[j][row] - ref);
+        f[j] = exp2_fast(warp_ref[j][row] - ref);
         sum += f[j] * warp_l[j][row];
       }
       // the sum is zero exactly when nothing was seen: zeros, and a log-sum of -inf
       // (a NaN score leaves a NaN sum)
-      lse2[k] = sum == 0.f ? kNegInf : ref + log2f(sum);
+      lse2[k] = sum == 0.f ? kNegInf : (ref + kShift) + log2f(sum * (1.f / (1 << kShift)));
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
       for (int j = 0; j < kWarps; ++j) {
