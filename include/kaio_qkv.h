@@ -367,7 +367,9 @@ int kaio_rope_append(const kaio_rope_args* args, kaio_stream_t stream);
  *             chooses the kernel, whose results differ in rounding only
  *   workspace kaio_paged_attention_workspace() bytes of device memory,
  *             16-byte aligned, zeroed once before its first use. Every call
- *             leaves it ready for the next. Calls that share a workspace have
+ *             leaves it ready for the next, also one that gave up a wait
+ *             (KAIO_ERR_DEVICE_TIMEOUT from kaio_device_status(); its outputs
+ *             are undefined). Calls that share a workspace have
  *             to be ordered (one stream, or events); concurrent calls need one
  *             each.
  *
@@ -414,6 +416,17 @@ typedef struct {
 } kaio_paged_attention_args;
 
 int kaio_paged_attention(const kaio_paged_attention_args* args, kaio_stream_t stream);
+
+/*
+ * Test entry for the bounded waits of the kernel that kaio_paged_attention runs
+ * for chunks: the same call with every wait of its pipeline limited to
+ * wait_limit_ns instead of 2 s. What a wait that gives up leaves behind is as
+ * for kaio_debug_decode_wait_limit, and the workspace stays usable. Arguments
+ * and errors as kaio_paged_attention, with dtype F16, dim above 64 and
+ * max_new * heads / kv_heads above 16.
+ */
+int kaio_debug_paged_attention_wait_limit(const kaio_paged_attention_args* args, uint64_t wait_limit_ns,
+                                          kaio_stream_t stream);
 
 /* Bytes of workspace that kaio_paged_attention needs on the current device, for
  * any sizes. Returns KAIO_OK and writes *bytes, or an error status. */

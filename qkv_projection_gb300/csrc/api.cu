@@ -804,9 +804,10 @@ int kaio_paged_attention_workspace(uint64_t* bytes) {
   return KAIO_OK;
 }
 
-int kaio_paged_attention(const kaio_paged_attention_args* a, kaio_stream_t stream_) {
-  g_last_error.clear();
-  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+namespace {
+
+// wait_ns: kOwnWaitLimit, or a limit to test the tensor-core kernel with.
+int paged_attention_impl(const kaio_paged_attention_args* a, uint64_t wait_ns, cudaStream_t stream) {
   if (a == nullptr) return fail(KAIO_ERR_INVALID_VALUE, "args is a null pointer");
   if (a->struct_size != sizeof(*a))
     return fail(KAIO_ERR_INVALID_VALUE, "struct_size %u is not sizeof(kaio_paged_attention_args) (%zu)",
@@ -827,6 +828,11 @@ int kaio_paged_attention(const kaio_paged_attention_args* a, kaio_stream_t strea
   if (a->window < 0 || a->sinks < 0)
     return fail(KAIO_ERR_INVALID_VALUE, "window (%d) and sinks (%d) must not be negative", a->window, a->sinks);
   if (!(a->scale > -3.0e38f && a->scale < 3.0e38f)) return fail(KAIO_ERR_INVALID_VALUE, "scale must be finite");
+  const int64_t rows = a->max_new * (H / KH);
+  if (wait_ns != kaio::kOwnWaitLimit &&
+      (rows <= kaio::kPagedDecodeRows || P == 0 || W == 0 || !kaio::paged_chunk_limit_ok(t, a->dim)))
+    return fail(KAIO_ERR_INVALID_VALUE, "a wait limit is for F16, dim above 64 and max_new * heads / kv_heads above %d",
+                kaio::kPagedDecodeRows);
   if (a->q_starts == nullptr && T != B)
     return fail(KAIO_ERR_INVALID_VALUE, "without q_starts there is one token for each sequence: tokens (%d) != batch (%d)",
                 a->tokens, a->batch);
@@ -896,11 +902,24 @@ int kaio_paged_attention(const kaio_paged_attention_args* a, kaio_stream_t strea
   // Up to 16 rows a sequence and K/V head the warp-MMA kernel streams the keys;
   // more rows are worth the tensor cores' 128-row tiles. (An empty cache has no
   // tensor map; the former handles it.)
-  const bool few = static_cast<int64_t>(a->max_new) * p.group <= kaio::kPagedDecodeRows || p.max_pages == 0;
+  const bool few = rows <= kaio::kPagedDecodeRows || p.max_pages == 0;
   const cudaError_t e = few ? kaio::launch_paged_decode(t, p, a->workspace, info.sms, stream)
-                            : kaio::launch_paged_chunk(t, p, a->workspace, info.sms, stream);
+                            : kaio::launch_paged_chunk(t, p, a->workspace, info.sms, stream, wait_ns);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention kernel launch");
   return KAIO_OK;
+}
+
+}  // namespace
+
+int kaio_paged_attention(const kaio_paged_attention_args* args, kaio_stream_t stream) {
+  g_last_error.clear();
+  return paged_attention_impl(args, kaio::kOwnWaitLimit, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kaio_debug_paged_attention_wait_limit(const kaio_paged_attention_args* args, uint64_t wait_limit_ns,
+                                          kaio_stream_t stream) {
+  g_last_error.clear();
+  return paged_attention_impl(args, wait_limit_ns, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int kaio_dequant_int4_debug(const uint32_t* w, const void* s, void* out, uint32_t K, uint32_t N,

@@ -71,7 +71,12 @@ constexpr size_t kPagedCounterBytes = 4096;
 size_t paged_decode_workspace_bytes(int num_sms);
 cudaError_t launch_paged_decode(FloatType t, PagedParams p, void* workspace, int num_sms, cudaStream_t stream);
 size_t paged_chunk_workspace_bytes(int num_sms);
-cudaError_t launch_paged_chunk(FloatType t, const PagedParams& p, void* workspace, int num_sms, cudaStream_t stream);
+// wait_ns: limit of the pipeline's waits, kOwnWaitLimit but in a test of the path that gives
+// up, which is built for one type and width.
+constexpr unsigned long long kOwnWaitLimit = ~0ull;
+constexpr bool paged_chunk_limit_ok(FloatType t, int dim) { return t == FloatType::F16 && dim > 64; }
+cudaError_t launch_paged_chunk(FloatType t, const PagedParams& p, void* workspace, int num_sms, cudaStream_t stream,
+                               unsigned long long wait_ns);
 unsigned read_and_clear_chunk_errors();
 
 // A launch that may begin while the kernel before it in the stream still runs

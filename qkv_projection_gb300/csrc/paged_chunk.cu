@@ -56,6 +56,10 @@
 // Split items: the CTA that is last joins the parts in their order. Up to three parts it
 // joins from its own tensor memory and the workspace; more only from the workspace, with
 // ten loads of a thread in flight (one after another a part took 6000 cycles).
+//
+// A CTA whose wait gave up still counts itself in at every split item of its share, so
+// that the last one to come clears the counter, as always: the outputs are lost, the
+// workspace is not.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -131,7 +135,7 @@ template <int kDim> struct Control {
   PagedShare share;
   Job jobs[kJobs];
   float row_lse[kRows], row_mul[kRows];
-  uint32_t tmem_base;
+  uint32_t tmem_base, planned, entered;   // jobs worked out, and begun by thread 0
   int abort_flag, last_one;
 };
 template <int kDim>
@@ -224,9 +228,11 @@ struct ChunkParams {
   PagedParams p;
   bool out32;                         // rows of out are whole, aligned 32-byte pieces
   int k_heads_first, v_heads_first;   // order of a map's middle dimensions: heads before slots
+  unsigned long long wait_ns;         // limit of a wait; used where kLimited
 };
 
-template <typename T, int kDim>
+// kLimited: waits are limited to wait_ns (a test of the path that gives up).
+template <typename T, int kDim, bool kLimited>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                        const __grid_constant__ ChunkParams cp) {
@@ -265,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl.job_empty[i], kSoftmaxWarps + 3);      // the softmax, MMA and V warps
     }
     ctl.abort_flag = 0;
+    ctl.planned = ctl.entered = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -287,8 +294,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, &g_chunk_err));
+    auto done = [&] {
+      if constexpr (kLimited) return mbar_wait_lim(bar, parity, abort, &g_chunk_err, cp.wait_ns);
+      else return mbar_wait(bar, parity, abort, &g_chunk_err);
+    };
+    return ok = ok && __all_sync(0xFFFFFFFFu, done());
   };
+  // All warps are out of their jobs.
+  auto all_out = [&] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
   uint32_t unit_count = 0;      // units before this job: unit n has K stage n % kKStages, V stage n % kVStages
   auto job_ready = [&](uint32_t k) -> const Job& {
     wait(&ctl.job_full[k % kJobs], (k / kJobs) & 1);
@@ -347,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (last) w.next_item(p);
             else w.unit = w.units;                         // the share ends here
           }
+          if (job.mode != Mode::kEnd) ctl.planned = k + 1;
           mbar_arrive(&ctl.job_full[k % kJobs]);
         }
         __syncwarp();
@@ -396,6 +410,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t i = 0; i < stages && i < unit_count; ++i)
       mbar_wait_drain(&full[(unit_count - 1 - i) % stages], ((unit_count - 1 - i) / stages) & 1, &g_chunk_err);
     __syncwarp();
+    all_out();
+    if (!is_v && lane == 0 && *abort) {
+      // The split items that thread 0 did not come to: those of planned jobs, and the last
+      // one of the share. (The first job is planned before any wait that can give up, so no
+      // other is left that begins before the share.)
+      auto count_in = [&](int c0, int c1) {
+        if (atomicAdd(p.counters + c0, 1u) == static_cast<unsigned>(c1 - c0)) p.counters[c0] = 0;
+      };
+      for (uint32_t k = ctl.entered; k < ctl.planned; ++k) {
+        const Job& job = ctl.jobs[k % kJobs];
+        if (job.split) count_in(job.c0, job.c1);
+      }
+      Walk& w = ctl.place;
+      while (any && w.b < p.batch && w.unit == 0) {
+        const int u1 = w.cut(ctl.share.end, ctl.share);
+        if (u1 < w.units) {
+          if (u1 > 0) count_in(blockIdx.x, w.last_owner(ctl.share));
+          break;
+        }
+        w.next_item(p);
+      }
+    }
   } else if (warp >= kMmaWarp) {
     fewer_registers<kOtherRegs>();
     // ------------------------------------------------------------------- MMA
@@ -527,6 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_drain(&ctl.mma_done[half], 0, &g_chunk_err);
     }
     __syncwarp();
+    all_out();
   } else {
     more_registers<kSoftmaxRegs>();
     // --------------------------------------------------------------- softmax
@@ -597,6 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t k = 0;; ++k) {
       const Job& w = job_ready(k);
       if (!ok || w.mode == Mode::kEnd) break;
+      if (threadIdx.x == 0) ctl.entered = k + 1;
       const Mode mode = w.mode;
       const int rows = w.rows, n_units = w.u1 - w.u0;
       const int my_row = (rows > kHalf ? kHalf * half : 0) + 32 * of_half + lane;   // of the item's 256
@@ -974,6 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (paired || split) meet();                         // all of it has been read
       job_done(k);
     }
+    all_out();
   }
   tc_fence_before();
   __syncthreads();
@@ -1021,12 +1060,12 @@ cudaError_t encode_cache(CUtensorMap* map, int* heads_first, const void* base, F
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <typename T, int kDim>
+template <typename T, int kDim, bool kLimited = false>
 cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const ChunkParams& cp, int ctas, cudaStream_t stream) {
   const cudaError_t e =
-      ensure_smem_limit(reinterpret_cast<const void*>(paged_chunk_kernel<T, kDim>), kSmem<kDim>);
+      ensure_smem_limit(reinterpret_cast<const void*>(paged_chunk_kernel<T, kDim, kLimited>), kSmem<kDim>);
   if (e != cudaSuccess) return e;
-  return launch_dependent(paged_chunk_kernel<T, kDim>, ctas, kThreads, kSmem<kDim>, stream, km, vm, cp);
+  return launch_dependent(paged_chunk_kernel<T, kDim, kLimited>, ctas, kThreads, kSmem<kDim>, stream, km, vm, cp);
 }
 
 }  // namespace
@@ -1036,9 +1075,10 @@ size_t paged_chunk_workspace_bytes(int num_sms) {
 }
 
 cudaError_t launch_paged_chunk(FloatType t, const PagedParams& params, void* workspace, int num_sms,
-                               cudaStream_t stream) {
+                               cudaStream_t stream, unsigned long long wait_ns) {
   ChunkParams cp{};
   cp.p = params;
+  cp.wait_ns = wait_ns;
   PagedParams& p = cp.p;
   const int ctas = std::min(num_sms, static_cast<int>(kPagedCounterBytes / sizeof(unsigned)));
   p.counters = static_cast<unsigned*>(workspace);
@@ -1052,6 +1092,8 @@ cudaError_t launch_paged_chunk(FloatType t, const PagedParams& params, void* wor
   cudaError_t e = encode_cache(&km, &cp.k_heads_first, p.kc, t, p, p.k_ps, p.k_ss, p.k_hs);
   if (e == cudaSuccess) e = encode_cache(&vm, &cp.v_heads_first, p.vc, t, p, p.v_ps, p.v_ss, p.v_hs);
   if (e != cudaSuccess) return e;
+  if (wait_ns != kOwnWaitLimit)
+    return paged_chunk_limit_ok(t, p.dim) ? launch<__half, 128, true>(km, vm, cp, ctas, stream) : cudaErrorNotSupported;
   if (t == FloatType::BF16)
     return p.dim <= 64 ? launch<__nv_bfloat16, 64>(km, vm, cp, ctas, stream)
                        : launch<__nv_bfloat16, 128>(km, vm, cp, ctas, stream);

@@ -44,6 +44,7 @@ _SIGNATURES = {
     "kaio_rope": ([_vp, _vp], _i32),
     "kaio_rope_append": ([_vp, _vp], _i32),
     "kaio_paged_attention": ([_vp, _vp], _i32),
+    "kaio_debug_paged_attention_wait_limit": ([_vp, ctypes.c_uint64, _vp], _i32),
     "kaio_paged_attention_workspace": ([_vp], _i32),
     "kaio_qkv_path": ([_u32], _i32),
     "kaio_last_error": ([], ctypes.c_char_p),
