@@ -5,8 +5,9 @@ library next to this file. The CUDA runtime is linked statically, so loading
 the library needs no GPU; the driver is reached only at the first CUDA call.
 
 _host.so, the Python module of host_calls.cpp, is compiled beside them against the
-installed Python and torch. Without their headers it is left out, and the calls
-that it shortens go through Python.
+installed Python and torch. Where that cannot be done (no torch, no headers, no host
+compiler) it is left out with a warning, and the calls that it shortens go through
+Python; the library itself needs nvcc alone.
 """
 from __future__ import annotations
 
@@ -50,29 +51,45 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def _compile_host() -> None:
+def _host_command(out: str):
+    """The compiler's command for _host.so, or why there is none."""
     import sysconfig
-
-    import torch
+    try:
+        import torch
+    except ImportError as e:
+        return None, f"torch cannot be imported ({e})"
     include = sysconfig.get_paths()["include"]
     base = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
-    if not (os.path.exists(os.path.join(include, "Python.h")) and os.path.isdir(os.path.join(base, "include", "ATen"))):
-        if os.path.exists(HOST_LIB):
-            os.remove(HOST_LIB)
-        return
+    for needed in (os.path.join(include, "Python.h"), os.path.join(base, "include", "ATen", "ATen.h"),
+                   os.path.join(base, "lib", "libc10_cuda.so")):
+        if not os.path.exists(needed):
+            return None, f"{needed} is missing"
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            "-I", os.path.join(ROOT, "include"), "-isystem", include, "-isystem", cuda,
+            "-isystem", os.path.join(base, "include"),
+            "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+            HOST_SOURCE, "-o", out, "-L", os.path.join(base, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], ""
+
+
+def _compile_host() -> None:
+    """Builds _host.so, or says on stderr why it is left out; one of an earlier build goes."""
     tmp = HOST_LIB + ".tmp"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
-           "-I", os.path.join(ROOT, "include"), "-isystem", include, "-isystem", cuda,
-           "-isystem", os.path.join(base, "include"),
-           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
-           HOST_SOURCE, "-o", tmp, "-L", os.path.join(base, "lib"),
-           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"g++ failed on {HOST_SOURCE}:\n{res.stdout}\n{res.stderr}")
-    os.replace(tmp, HOST_LIB)
+    cmd, why = _host_command(tmp)
+    if cmd:
+        try:
+            res = subprocess.run(cmd, capture_output=True, text=True)
+            if res.returncode == 0:
+                os.replace(tmp, HOST_LIB)
+                return
+            why = f"g++ failed on {HOST_SOURCE}:\n{res.stdout}\n{res.stderr}"
+        except OSError as e:
+            why = f"g++ cannot be run ({e})"
+    if os.path.exists(HOST_LIB):
+        os.remove(HOST_LIB)
+    sys.stderr.write(f"warning: built without {os.path.basename(HOST_LIB)}: {why}\n")
 
 
 def build(verbose: bool = False) -> str:
