@@ -285,7 +285,8 @@ int kaio_dequantize_per_group(int q_dtype, int dtype, int32_t outer, int32_t axi
  * products and sums, the angle reduced exactly at any int32 position, one
  * rounding to the tensors' type.
  *
- *   q, q_out  [tokens, heads, dim]      out may be q itself (same strides)
+ *   q, q_out  [tokens, heads, dim]      out may be q itself (same strides); k and
+ *             v may then be other columns of the same rows (one packed buffer)
  *   k, v      [tokens, kv_heads, dim]   (append only)
  *   k_cache, v_cache [num_pages, page_size, kv_heads, dim]  (append only): the
  *             rotated k and the unchanged v of token t go to slot slots[t] =

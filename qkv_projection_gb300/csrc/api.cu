@@ -646,6 +646,20 @@ int check_strides(const char* name, std::initializer_list<std::pair<int64_t, int
   return KAIO_OK;
 }
 
+// Whether two 16-bit tensors [tokens, heads, dim] of the same tokens share memory: their
+// extents overlap, and they are not different columns of one buffer's rows (equal token
+// strides, and one's rows in what the other's leave between them).
+bool rows_overlap(const Span& a, int64_t heads_a, int64_t hs_a, const Span& b, int64_t heads_b, int64_t hs_b,
+                  int64_t ts_a, int64_t ts_b, int64_t dim) {
+  if (!overlaps(a, b)) return false;
+  if (ts_a != ts_b || ts_a <= 0) return true;
+  const int64_t row_a = ((heads_a - 1) * hs_a + dim) * 2, row_b = ((heads_b - 1) * hs_b + dim) * 2, step = ts_a * 2;
+  int64_t from = (static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.p)) -
+                  static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.p))) % step;
+  if (from < 0) from += step;
+  return from < row_a || from + row_b > step;
+}
+
 int check_sizes(std::initializer_list<std::pair<const char*, int64_t>> sizes) {
   for (const auto& v : sizes)
     if (v.second < 0 || v.second >= kMaxSize)
@@ -750,6 +764,13 @@ int rope_impl(const kaio_rope_args* a, bool append, cudaStream_t stream) {
                         (H == 1 || a->q_head_stride == a->q_out_head_stride);
   if (!in_place) KAIO_TRY(check_overlap(&q, 1, out, 1));
   KAIO_TRY(check_overlap(in, in_place ? n_small : n_in, out, 1));
+  // in place, k and v may lie beside q in one packed buffer
+  for (int i = n_small; in_place && i < n_in; ++i) {
+    const bool is_k = i == n_small;
+    if (rows_overlap(qo, H, a->q_out_head_stride, in[i], KH, is_k ? a->k_head_stride : a->v_head_stride,
+                     a->q_out_token_stride, is_k ? a->k_token_stride : a->v_token_stride, D))
+      return fail(KAIO_ERR_INVALID_VALUE, "output q_out overlaps input %s", in[i].name);
+  }
   for (int i = 1; i < n_out; ++i) {
     KAIO_TRY(check_overlap(&q, 1, out + i, 1));
     KAIO_TRY(check_overlap(in, n_in, out + i, 1));
