@@ -282,8 +282,8 @@ int kaio_dequantize_per_group(int q_dtype, int dtype, int32_t outer, int32_t axi
  * where (x0, x1) are elements (i, i + pairs), or (2i, 2i + 1) if interleaved.
  * inverse negates the angle: the inverse rotation, which is also the gradient
  * (dx = inverse rotation of dy). Elements from 2 * pairs on are copied. f32
- * products and sums, the angle reduced exactly at any int32 position, one
- * rounding to the tensors' type.
+ * products and sums, the angle good to 2^-24 turns at any int32 position (for
+ * |inv_freq| up to 2^64), one rounding to the tensors' type.
  *
  *   q, q_out  [tokens, heads, dim]      out may be q itself (same strides); k and
  *             v may then be other columns of the same rows (one packed buffer)

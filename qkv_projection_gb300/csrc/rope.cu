@@ -7,18 +7,20 @@
 // which is also the gradient, the rotation being orthogonal). Elements past 2R
 // are copied. Products and sums in f32, one rounding to the tensors' type.
 //
-// The angle is reduced exactly in fixed point: inv_freq / 2 pi is held as a
-// fraction of a turn in 64 bits, its product with the integer position wraps
-// modulo one turn by itself, and the top 32 bits of the product are the angle
-// in turns. The error is about 2^-24 turns at every position (an f32 product of
+// The angle is reduced in fixed point (the idea of Payne and Hanek, Radian reduction for
+// trigonometric functions, 1983): the turns of one position, inv_freq / 2 pi, are held
+// modulo one turn in 64 bits, from as many bits of 1 / 2 pi as inv_freq's exponent asks
+// for; their product with the integer position wraps modulo one turn by itself, and its
+// top 32 bits are the angle in turns. What is dropped before that is 2^-32 turns at any
+// position, so the error is that of the angle's f32, 2^-25 turns (an f32 product of
 // position and frequency is off by 0.004 radians at position 100000).
 //
 // What bounds it: bytes. Every value is read once and written once; the sines
 // are computed once per token and pair and shared by all heads through shared
 // memory. A thread moves 32 bytes (both halves of eight pairs) at a time, in few
 // registers: eight CTAs of 256 threads on an SM hide the latency better than
-// several units in flight per thread (two: 38 us, four: 46 us, one: 36.4 us for the
-// fused write of 8192 tokens of 32 + 8 heads of 128, 5.5 TB/s read and written).
+// several units in flight per thread (two: 38 us, four: 46 us, one: 37 us for the
+// fused write of 8192 tokens of 32 + 8 heads of 128, 5.4 TB/s read and written).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -39,6 +41,20 @@ struct RopeKernelParams {
   FastDiv unit_div, rot_div, copy_div;   // units per token, per rotated head, per copied head
   int tokens_per_cta;
 };
+
+// inv_freq / 2 pi modulo one, in units of 2^-64: with inv_freq = m 2^(e - 150), m of 24 bits,
+// it is m times 2^(e - 86) / 2 pi, of which the lowest 64 bits before the point count and 32
+// behind it for rounding. (In integers: the same in f64 was a tenth of the gradient's time.)
+__device__ __forceinline__ unsigned long long turns_of(float inv_freq) {
+  constexpr unsigned __int128 kInv2Pi =      // floor(2^128 / 2 pi)
+      static_cast<unsigned __int128>(0x28BE60DB9391054Aull) << 64 | 0x7F09D5F47D4D3770ull;
+  const uint32_t bits = __float_as_uint(inv_freq), m = (bits & 0x7FFFFFu) | 0x800000u;
+  const int right = 182 - static_cast<int>(bits >> 23 & 255u);      // 150 or more: all of it lies below 2^-64 (zero among them)
+  const unsigned __int128 window = right >= 128 ? 0 : right >= 0 ? kInv2Pi >> right : kInv2Pi << -right;
+  const unsigned long long low = static_cast<uint32_t>(window), high = static_cast<unsigned long long>(window >> 32);
+  const unsigned long long turns = m * high + (m * low >> 32);
+  return bits >> 31 ? 0 - turns : turns;
+}
 
 template <typename T> struct Pack;
 template <> struct Pack<__half> {
@@ -111,10 +127,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const int t = i / R, pair = i - t * R;
     int axis = 0;
     while (axis + 1 < p.axes && pair >= p.section_end[axis]) ++axis;
-    // turns per position, modulo one turn, in units of 2^-64
-    double turns = static_cast<double>(p.inv_freq[pair]) * 0.15915494309189533577;
-    turns -= floor(turns);
-    const unsigned long long frac = static_cast<unsigned long long>(turns * 18446744073709551616.0);
+    const unsigned long long frac = turns_of(p.inv_freq[pair]);
     const long long pos = p.positions[axis * p.pos_stride + t0 + t];
     const unsigned long long angle = frac * static_cast<unsigned long long>(pos);
     const float half_turns = static_cast<float>(static_cast<int32_t>(angle >> 32)) * 0x1p-31f;
@@ -257,7 +270,7 @@ cudaError_t launch(const RopeParams& r, int num_sms, cudaStream_t stream) {
   const int copy = !vec ? 1 : (D + 15) / 16;
   const int per_token = (r.q_heads + r.kv_heads) * rot + r.kv_heads * copy;
   // Tokens of a CTA: 4 or 2 where that still leaves every SM its eight CTAs (8192 tokens of
-  // 48 heads: 36 us with 4, 43 with 1; 4099 of 32 heads: 14.3 with 2, 15.1 with 1, 15.9 with 4).
+  // 48 heads: 37.3 us with 4 or 2, 42.2 with 1; 4099 of 32 heads: 15.3 with 2, 16.2 with 1, 16.8 with 4).
   int tokens = kRopeMaxTokens;
   while (tokens > 1 && r.tokens < 8 * num_sms * tokens) tokens >>= 1;
   const RopeKernelParams kp{r, FastDiv(per_token), FastDiv(rot), FastDiv(copy), tokens};
