@@ -301,8 +301,8 @@ int kaio_dequantize_per_group(int q_dtype, int dtype, int32_t outer, int32_t axi
  * Errors (KAIO_ERR_INVALID_VALUE unless noted): struct_size other than
  * sizeof(kaio_rope_args); another dtype; dim not a multiple of 8 in 8..256;
  * pairs < 1 or 2 * pairs > dim; axes not 1..4, a negative section, or sections
- * that do not sum to pairs; a bad stride; sizes of 2^30 or more; a null
- * pointer; an output overlapping an input (other than out == q) or k_cache
+ * that do not sum to pairs; a bad stride; sizes of 2^30 or more (tokens *
+ * heads, and the pieces of 16 values of one token's heads, too); a null pointer; an output overlapping an input (other than out == q) or k_cache
  * starting where v_cache does; memory of another device; KAIO_ERR_MISALIGNED
  * (16 bytes; positions, slots and inv_freq: 4). tokens == 0 returns KAIO_OK.
  */

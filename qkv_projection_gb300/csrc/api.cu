@@ -725,6 +725,25 @@ int rope_impl(const kaio_rope_args* a, bool append, cudaStream_t stream) {
     KAIO_TRY(check_strides("v_cache", {{P, a->v_page_stride}, {ps, a->v_slot_stride}, {KH, a->v_cache_head_stride}},
                            D, true));
   }
+  kaio::RopeParams r{};
+  r.q = a->q, r.qo = a->q_out;
+  r.q_ts = a->q_token_stride, r.q_hs = a->q_head_stride;
+  r.qo_ts = a->q_out_token_stride, r.qo_hs = a->q_out_head_stride;
+  r.positions = a->positions, r.pos_stride = a->positions_axis_stride, r.inv_freq = a->inv_freq;
+  r.tokens = a->tokens, r.q_heads = a->heads, r.dim = a->dim, r.pairs = a->pairs, r.axes = a->axes;
+  r.interleaved = a->interleaved != 0, r.inverse = a->inverse != 0;
+  for (int i = 0, end = 0; i < 4; ++i) r.section_end[i] = end += i < a->axes ? a->sections[i] : 0;
+  if (append) {
+    r.k = a->k, r.v = a->v, r.kc = a->k_cache, r.vc = a->v_cache, r.slots = a->slots;
+    r.k_ts = a->k_token_stride, r.k_hs = a->k_head_stride;
+    r.v_ts = a->v_token_stride, r.v_hs = a->v_head_stride;
+    r.kc_ps = a->k_page_stride, r.kc_ss = a->k_slot_stride, r.kc_hs = a->k_cache_head_stride;
+    r.vc_ps = a->v_page_stride, r.vc_ss = a->v_slot_stride, r.vc_hs = a->v_cache_head_stride;
+    r.kv_heads = a->kv_heads, r.num_pages = a->num_pages, r.page_size = a->page_size;
+  }
+  if (kaio::RopeUnits(r).per_token(r) >= kMaxSize)
+    return fail(KAIO_ERR_INVALID_VALUE, "heads of one token (%lld of %d values) must be below 2^30 pieces of 16 values",
+                static_cast<long long>(H + 2 * KH), a->dim);
   int dev;
   DeviceInfo info;
   if (T == 0) return current_device(&dev, &info);
@@ -782,22 +801,6 @@ int rope_impl(const kaio_rope_args* a, bool append, cudaStream_t stream) {
   KAIO_TRY(check_on_device(in, n_in, dev));
   KAIO_TRY(check_on_device(out, n_out, dev));
 
-  kaio::RopeParams r{};
-  r.q = a->q, r.qo = a->q_out;
-  r.q_ts = a->q_token_stride, r.q_hs = a->q_head_stride;
-  r.qo_ts = a->q_out_token_stride, r.qo_hs = a->q_out_head_stride;
-  r.positions = a->positions, r.pos_stride = a->positions_axis_stride, r.inv_freq = a->inv_freq;
-  r.tokens = a->tokens, r.q_heads = a->heads, r.dim = a->dim, r.pairs = a->pairs, r.axes = a->axes;
-  r.interleaved = a->interleaved != 0, r.inverse = a->inverse != 0;
-  for (int i = 0, end = 0; i < 4; ++i) r.section_end[i] = end += i < a->axes ? a->sections[i] : 0;
-  if (append) {
-    r.k = a->k, r.v = a->v, r.kc = a->k_cache, r.vc = a->v_cache, r.slots = a->slots;
-    r.k_ts = a->k_token_stride, r.k_hs = a->k_head_stride;
-    r.v_ts = a->v_token_stride, r.v_hs = a->v_head_stride;
-    r.kc_ps = a->k_page_stride, r.kc_ss = a->k_slot_stride, r.kc_hs = a->k_cache_head_stride;
-    r.vc_ps = a->v_page_stride, r.vc_ss = a->v_slot_stride, r.vc_hs = a->v_cache_head_stride;
-    r.kv_heads = a->kv_heads, r.num_pages = a->num_pages, r.page_size = a->page_size;
-  }
   const cudaError_t e = kaio::launch_rope(t, r, info.sms, stream);
   if (e != cudaSuccess) return cuda_fail(e, "rotary kernel launch");
   return KAIO_OK;

@@ -41,6 +41,20 @@ struct RopeParams {
   int num_pages, page_size;
   bool interleaved, inverse;
 };
+// A thread's units of work: up to two 16-byte vectors of one head (pairs that are whole
+// vectors), or a head's row.
+struct RopeUnits {
+  bool vec;
+  int rot, copy;                 // of a rotated and of a copied head
+  explicit RopeUnits(const RopeParams& r)
+      : vec(r.interleaved ? r.pairs % 4 == 0 : r.pairs % 8 == 0),
+        rot(!vec ? 1 : r.interleaved ? (r.dim + 15) / 16 : r.pairs / 8 + (r.dim - 2 * r.pairs + 15) / 16),
+        copy(!vec ? 1 : (r.dim + 15) / 16) {}
+  // Of one token; the kernel counts them in 32 bits.
+  int64_t per_token(const RopeParams& r) const {
+    return (static_cast<int64_t>(r.q_heads) + r.kv_heads) * rot + static_cast<int64_t>(r.kv_heads) * copy;
+  }
+};
 cudaError_t launch_rope(FloatType t, const RopeParams& r, int num_sms, cudaStream_t stream);
 
 // ------------------------------------------------------------- paged attention

@@ -264,18 +264,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 
 template <typename T>
 cudaError_t launch(const RopeParams& r, int num_sms, cudaStream_t stream) {
-  const int R = r.pairs, D = r.dim;
-  const bool vec = r.interleaved ? R % 4 == 0 : R % 8 == 0;
-  const int rot = !vec ? 1 : r.interleaved ? (D + 15) / 16 : R / 8 + (D - 2 * R + 15) / 16;
-  const int copy = !vec ? 1 : (D + 15) / 16;
-  const int per_token = (r.q_heads + r.kv_heads) * rot + r.kv_heads * copy;
+  const RopeUnits u(r);
+  const int per_token = static_cast<int>(u.per_token(r));
   // Tokens of a CTA: 4 or 2 where that still leaves every SM its eight CTAs (8192 tokens of
   // 48 heads: 37.3 us with 4 or 2, 42.2 with 1; 4099 of 32 heads: 15.3 with 2, 16.2 with 1, 16.8 with 4).
   int tokens = kRopeMaxTokens;
   while (tokens > 1 && r.tokens < 8 * num_sms * tokens) tokens >>= 1;
-  const RopeKernelParams kp{r, FastDiv(per_token), FastDiv(rot), FastDiv(copy), tokens};
+  const RopeKernelParams kp{r, FastDiv(per_token), FastDiv(u.rot), FastDiv(u.copy), tokens};
   const int grid = (r.tokens + tokens - 1) / tokens;
-  return launch_dependent(vec ? rope_kernel<T, true> : rope_kernel<T, false>, grid, kRopeThreads, 0, stream, kp);
+  return launch_dependent(u.vec ? rope_kernel<T, true> : rope_kernel<T, false>, grid, kRopeThreads, 0, stream, kp);
 }
 
 }  // namespace
