@@ -367,7 +367,8 @@ int kaio_rope_append(const kaio_rope_args* args, kaio_stream_t stream);
  *   max_new   at least the largest number of new tokens of one sequence. It
  *             chooses the kernel, whose results differ in rounding only
  *   workspace kaio_paged_attention_workspace() bytes of device memory,
- *             16-byte aligned, zeroed once before its first use. Every call
+ *             16-byte aligned, its first KAIO_PAGED_ATTENTION_COUNTERS
+ *             bytes zeroed once before its first use. Every call
  *             leaves it ready for the next, also one that gave up a wait
  *             (KAIO_ERR_DEVICE_TIMEOUT from kaio_device_status(); its outputs
  *             are undefined). Calls that share a workspace have
@@ -390,6 +391,8 @@ int kaio_rope_append(const kaio_rope_args* args, kaio_stream_t stream);
  * KAIO_ERR_MISALIGNED (16 bytes; tables and lse: 4). tokens == 0 or batch == 0
  * returns KAIO_OK without a launch.
  */
+#define KAIO_PAGED_ATTENTION_COUNTERS 4096
+
 typedef struct {
   uint32_t struct_size; /* sizeof(kaio_paged_attention_args) */
   int32_t dtype;        /* KAIO_DTYPE_F16 or KAIO_DTYPE_BF16 */

@@ -6,6 +6,7 @@
 
 #include <cstdint>
 
+#include "../../include/kaio_qkv.h"
 #include "kaio_internal.h"
 
 namespace kaio {
@@ -81,7 +82,7 @@ constexpr int kPagedMaxLen = 1 << 30;
 // kernel takes at a time.
 constexpr int kPagedDecodeRows = 16;
 // Workspace layout: counters first, then the partial sums.
-constexpr size_t kPagedCounterBytes = 4096;
+constexpr size_t kPagedCounterBytes = KAIO_PAGED_ATTENTION_COUNTERS;
 size_t paged_decode_workspace_bytes(int num_sms);
 cudaError_t launch_paged_decode(FloatType t, PagedParams p, void* workspace, int num_sms, cudaStream_t stream);
 size_t paged_chunk_workspace_bytes(int num_sms);

@@ -24,6 +24,8 @@ KAIO_ERR_UNSUPPORTED_DEVICE = 3
 KAIO_ERR_CUDA = 4
 KAIO_ERR_DEVICE_TIMEOUT = 5
 
+KAIO_PAGED_ATTENTION_COUNTERS = 4096
+
 KAIO_DTYPE_F32, KAIO_DTYPE_F64, KAIO_DTYPE_F16, KAIO_DTYPE_BF16, KAIO_DTYPE_S8, KAIO_DTYPE_U8 = range(6)
 
 _lib = None
@@ -532,15 +534,17 @@ def rope_append(q, k, v, positions, inv_freq, k_cache, v_cache, slots, sections=
 
 def paged_attention_workspace(device=None, stream=None):
     """A workspace for ``paged_attention`` on a device: allocate it once and keep
-    it. It is zeroed on ``stream`` (default: the current one). Its zeroing and the
-    calls that use it must be ordered (one stream, or events)."""
+    it. What has to be zero in it is zeroed on ``stream`` (default: the current one).
+    That and the calls that use it must be ordered (one stream, or events)."""
     torch = _torch()
     n = ctypes.c_uint64()
     if stream is not None and not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream.cuda_stream), device=device)
     with torch.cuda.device(device), torch.cuda.stream(stream):
         check(lib().kaio_paged_attention_workspace(ctypes.byref(n)))
-        return torch.zeros(n.value, dtype=torch.uint8, device="cuda")
+        workspace = torch.empty(n.value, dtype=torch.uint8, device="cuda")
+        workspace[:KAIO_PAGED_ATTENTION_COUNTERS].zero_()
+        return workspace
 
 
 def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max_new: Optional[int] = None,
