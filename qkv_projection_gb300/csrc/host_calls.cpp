@@ -14,12 +14,14 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
 #include <cstdint>
 #include <limits>
+#include <optional>
 
 #include "kaio_qkv.h"
 
@@ -117,11 +119,20 @@ bool rope_angles(kaio_rope_args* a, PyObject* positions, PyObject* inv_freq, PyO
   return true;
 }
 
+// A new result, which belongs to the stream that the kernel runs on (see kaio._empty).
+at::Tensor new_tensor(at::IntArrayRef sizes, const at::TensorOptions& options, PyObject* given_stream, void* stream) {
+  std::optional<c10::cuda::CUDAStreamGuard> on;
+  if (given_stream != Py_None)
+    on.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), options.device().index()));
+  return at::empty(sizes, options);
+}
+
 // The result: the tensor given, or a new dense one like x.
-const at::Tensor* result_like(PyObject* given, const at::Tensor& x, at::Tensor* made, int64_t* ts, int64_t* hs) {
+const at::Tensor* result_like(PyObject* given, const at::Tensor& x, PyObject* given_stream, void* stream,
+                              at::Tensor* made, int64_t* ts, int64_t* hs) {
   const at::Tensor* out;
   if (given == Py_None) {
-    *made = at::empty(x.sizes(), x.options());
+    *made = new_tensor(x.sizes(), x.options(), given_stream, stream);
     *ts = x.size(1) * x.size(2);
     *hs = x.size(2);
     return made;
@@ -151,7 +162,7 @@ PyObject* rope(PyObject* const* v) {
       !stream_of(v[7], *x, &stream))
     return nullptr;
   at::Tensor made;
-  const at::Tensor* out = result_like(v[6], *x, &made, &a.q_out_token_stride, &a.q_out_head_stride);
+  const at::Tensor* out = result_like(v[6], *x, v[7], stream, &made, &a.q_out_token_stride, &a.q_out_head_stride);
   if (!out) return nullptr;
   a.q_out = out->data_ptr();
   return call(g_rope, a, stream) ? hand_back(v[6], made) : nullptr;
@@ -185,7 +196,7 @@ PyObject* rope_append(PyObject* const* v) {
   void* stream;
   if (!rope_angles(&a, v[3], v[4], v[8], t) || !to_flag(v[9], &a.interleaved) || !stream_of(v[11], *q, &stream)) return nullptr;
   at::Tensor made;
-  const at::Tensor* out = result_like(v[10], *q, &made, &a.q_out_token_stride, &a.q_out_head_stride);
+  const at::Tensor* out = result_like(v[10], *q, v[11], stream, &made, &a.q_out_token_stride, &a.q_out_head_stride);
   if (!out) return nullptr;
   a.q_out = out->data_ptr();
   return call(g_rope_append, a, stream) ? hand_back(v[10], made) : nullptr;
@@ -236,7 +247,7 @@ PyObject* paged_attention(PyObject* const* v) {
       !stream_of(v[15], *q, &stream))
     return nullptr;
   at::Tensor made, made_lse;
-  const at::Tensor* out = result_like(v[12], *q, &made, &a.out_token_stride, &a.out_head_stride);
+  const at::Tensor* out = result_like(v[12], *q, v[15], stream, &made, &a.out_token_stride, &a.out_head_stride);
   if (!out) return nullptr;
   a.out = out->data_ptr();
   const bool wants_lse = v[13] == Py_True;
@@ -245,7 +256,7 @@ PyObject* paged_attention(PyObject* const* v) {
     if (!lse || (t > 1 && lse->stride(0) != h)) return nullptr;
     a.lse = static_cast<float*>(lse->data_ptr());
   } else if (wants_lse) {
-    made_lse = at::empty(lse_size, q->options().dtype(at::kFloat));
+    made_lse = new_tensor(lse_size, q->options().dtype(at::kFloat), v[15], stream);
     a.lse = static_cast<float*>(made_lse.data_ptr());
   }
   if (!call(g_paged_attention, a, stream)) return nullptr;

@@ -402,6 +402,25 @@ def _raw_stream(t, stream) -> int:
     return _current_raw_stream(t.get_device())
 
 
+def _torch_stream(stream, device):
+    """The stream given as torch's own (None: the current one, for torch.cuda.stream)."""
+    torch = _torch()
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream.cuda_stream), device=device)
+
+
+def _empty(shape, dtype, device, stream):
+    """A new result. It belongs to the stream that the kernel runs on: on another one's
+    memory that stream's earlier work might not be done, and its later work would get the
+    memory back while the kernel still writes."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _current_raw_stream(device: int) -> int:
     global _current_raw_stream
     torch = _torch()
@@ -476,7 +495,7 @@ def rope(x, positions, inv_freq, sections=None, interleaved: bool = False, inver
     _strides(inv_freq, "inv_freq", torch.float32, (pairs,))
     axes, axis_stride, sec = _rope_axes(positions, t, sections, pairs)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=x.device)
+        out = _empty(shape, dtype, x.device, stream)
         os_ = (h * d, d)
     else:
         os_ = _strides(out, "out", dtype, shape)
@@ -519,7 +538,7 @@ def rope_append(q, k, v, positions, inv_freq, k_cache, v_cache, slots, sections=
     _strides(slots, "slots", torch.int32, (t,))
     axes, axis_stride, sec = _rope_axes(positions, t, sections, pairs)
     if q_out is None:
-        q_out = torch.empty(shape, dtype=dtype, device=q.device)
+        q_out = _empty(shape, dtype, q.device, stream)
         os_ = (h * d, d)
     else:
         os_ = _strides(q_out, "q_out", dtype, shape)
@@ -538,9 +557,7 @@ def paged_attention_workspace(device=None, stream=None):
     That and the calls that use it must be ordered (one stream, or events)."""
     torch = _torch()
     n = ctypes.c_uint64()
-    if stream is not None and not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream.cuda_stream), device=device)
-    with torch.cuda.device(device), torch.cuda.stream(stream):
+    with torch.cuda.device(device), torch.cuda.stream(_torch_stream(stream, device)):
         check(lib().kaio_paged_attention_workspace(ctypes.byref(n)))
         workspace = torch.empty(n.value, dtype=torch.uint8, device="cuda")
         workspace[:KAIO_PAGED_ATTENTION_COUNTERS].zero_()
@@ -596,7 +613,7 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max
     elif not (workspace.is_cuda and workspace.dtype is torch.uint8 and workspace.is_contiguous()):
         raise ValueError("workspace must be a dense uint8 CUDA tensor from paged_attention_workspace()")
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=q.device)
+        out = _empty(shape, dtype, q.device, stream)
         os_ = (h * d, d)
     else:
         os_ = _strides(out, "out", dtype, shape)
@@ -606,7 +623,7 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max
             raise ValueError("lse must be contiguous")
         lse_ptr = lse.data_ptr()
     elif return_lse:
-        lse = torch.empty((t, h), dtype=torch.float32, device=q.device)
+        lse = _empty((t, h), torch.float32, q.device, stream)
         lse_ptr = lse.data_ptr()
     if max_new is None:
         max_new = t if starts else 1
