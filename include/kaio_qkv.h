@@ -297,7 +297,8 @@ int kaio_dequantize_per_group(int q_dtype, int dtype, int32_t outer, int32_t axi
  *
  * dtype F16 or BF16 for every tensor of the rotation. Strides are in elements;
  * the last dimension is dense; strides of q, k, v, caches and output are
- * multiples of 8 (16 bytes), those of a written tensor at least dim.
+ * multiples of 8 (16 bytes), those of a written tensor at least dim and such that
+ * its rows share no element (each steps over what the smaller ones reach).
  * Errors (KAIO_ERR_INVALID_VALUE unless noted): struct_size other than
  * sizeof(kaio_rope_args); another dtype; dim not a multiple of 8 in 8..256;
  * pairs < 1 or 2 * pairs > dim; axes not 1..4, a negative section, or sections
@@ -381,7 +382,8 @@ int kaio_rope_append(const kaio_rope_args* args, kaio_stream_t stream);
  * Lengths and table stay on the device: the call does not synchronise, and work
  * is divided by the actual lengths.
  *
- * Strides are in elements, multiples of 8; the last dimension is dense.
+ * Strides are in elements, multiples of 8; the last dimension is dense. Rows of
+ * out share no element, as for kaio_rope.
  * Errors (KAIO_ERR_INVALID_VALUE unless noted): struct_size; another dtype; dim
  * not a multiple of 8 in 8..128; heads not a multiple of kv_heads; page_size
  * not a power of two in 16..1024; q_starts null with tokens != batch; negative

@@ -631,7 +631,8 @@ size_t extent16(std::initializer_list<std::pair<int64_t, int64_t>> size_stride, 
 }
 
 // Strides of a 16-bit tensor whose rows are `dim` dense elements: multiples of
-// 16 bytes, not negative; a written tensor's rows must not share elements.
+// 16 bytes, not negative; a written tensor's rows must not share elements: from the
+// smallest stride up, each steps over all that the ones before reach.
 int check_strides(const char* name, std::initializer_list<std::pair<int64_t, int64_t>> size_stride, int64_t dim,
                   bool written) {
   for (const auto& d : size_stride) {
@@ -642,6 +643,22 @@ int check_strides(const char* name, std::initializer_list<std::pair<int64_t, int
     if (written && d.second < dim)
       return fail(KAIO_ERR_INVALID_VALUE, "%s: stride %lld of a written tensor is below dim (%lld)", name,
                   static_cast<long long>(d.second), static_cast<long long>(dim));
+  }
+  __int128 reach = dim;
+  int64_t above = 0;
+  for (size_t i = 0; written && i < size_stride.size(); ++i) {
+    const std::pair<int64_t, int64_t>* next = nullptr;
+    int same = 0;
+    for (const auto& d : size_stride) {
+      if (d.first <= 1) continue;
+      same += d.second == above;
+      if (d.second > above && (next == nullptr || d.second < next->second)) next = &d;
+    }
+    if (same > 1 || (next != nullptr && next->second < reach))
+      return fail(KAIO_ERR_INVALID_VALUE, "%s: rows of a written tensor share elements", name);
+    if (next == nullptr) break;
+    above = next->second;
+    reach += static_cast<__int128>(next->first - 1) * above;
   }
   return KAIO_OK;
 }
