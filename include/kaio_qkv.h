@@ -387,11 +387,11 @@ int kaio_rope_append(const kaio_rope_args* args, kaio_stream_t stream);
  * Errors (KAIO_ERR_INVALID_VALUE unless noted): struct_size; another dtype; dim
  * not a multiple of 8 in 8..128; heads not a multiple of kv_heads; page_size
  * not a power of two in 16..1024; q_starts null with tokens != batch; negative
- * sizes, window or sinks; scale not finite; a bad stride; sizes of 2^30 or more
- * (tokens * heads too); a null pointer; out or lse overlapping an input or each
- * other; workspace_bytes too small; memory of another device;
- * KAIO_ERR_MISALIGNED (16 bytes; tables and lse: 4). tokens == 0 or batch == 0
- * returns KAIO_OK without a launch.
+ * sizes, window or sinks; scale not finite (times log2(e) too); a bad stride;
+ * sizes of 2^30 or more (tokens * heads too); a null pointer; out or lse
+ * overlapping an input or each other; workspace_bytes too small; memory of
+ * another device; KAIO_ERR_MISALIGNED (16 bytes; tables and lse: 4). tokens == 0
+ * or batch == 0 returns KAIO_OK without a launch.
  */
 #define KAIO_PAGED_ATTENTION_COUNTERS 4096
 

@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdarg>
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -868,7 +869,8 @@ int paged_attention_impl(const kaio_paged_attention_args* a, uint64_t wait_ns, c
     return fail(KAIO_ERR_INVALID_VALUE, "page_size (%d) must be a power of two in 16..1024", a->page_size);
   if (a->window < 0 || a->sinks < 0)
     return fail(KAIO_ERR_INVALID_VALUE, "window (%d) and sinks (%d) must not be negative", a->window, a->sinks);
-  if (!(a->scale > -3.0e38f && a->scale < 3.0e38f)) return fail(KAIO_ERR_INVALID_VALUE, "scale must be finite");
+  const float scale_log2 = a->scale * 1.4426950408889634f;
+  if (!std::isfinite(scale_log2)) return fail(KAIO_ERR_INVALID_VALUE, "scale (%g) must be finite, times log2(e) too", a->scale);
   const int64_t rows = a->max_new * (H / KH);
   if (wait_ns != kaio::kOwnWaitLimit &&
       (rows <= kaio::kPagedDecodeRows || P == 0 || W == 0 || !kaio::paged_chunk_limit_ok(t, a->dim)))
@@ -939,7 +941,7 @@ int paged_attention_impl(const kaio_paged_attention_args* a, uint64_t wait_ns, c
   p.num_pages = a->num_pages, p.max_pages = P ? a->max_pages : 0;
   p.causal = a->causal != 0;
   p.window = std::min(a->window, kaio::kPagedMaxLen), p.sinks = std::min(a->sinks, kaio::kPagedMaxLen);
-  p.scale_log2 = a->scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   // Up to 16 rows a sequence and K/V head the warp-MMA kernel streams the keys;
   // more rows are worth the tensor cores' 128-row tiles. (An empty cache has no
   // tensor map; the former handles it.)
