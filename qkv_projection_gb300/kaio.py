@@ -8,6 +8,7 @@ library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import re
 import struct
@@ -402,6 +403,24 @@ def _raw_stream(t, stream) -> int:
     return _current_raw_stream(t.get_device())
 
 
+def _int32(v, name):
+    try:
+        i = operator.index(v)
+    except TypeError:
+        raise TypeError(f"{name} must be an integer, got {type(v).__name__}") from None
+    if not -2 ** 31 <= i < 2 ** 31:
+        raise ValueError(f"{name} ({i}) is out of range")
+    return i
+
+
+def _pack(fields, *values):
+    """An argument block; sizes of tensors that its fields do not hold raise."""
+    try:
+        return fields.pack(*values)
+    except struct.error as e:
+        raise ValueError(f"a tensor's size is out of range ({e})") from None
+
+
 def _torch_stream(stream, device):
     """The stream given as torch's own (None: the current one, for torch.cuda.stream)."""
     torch = _torch()
@@ -446,7 +465,7 @@ def _rope_axes(positions, tokens, sections, pairs):
         return 1, stride, (pairs, 0, 0, 0)
     if len(sections) != axes or axes > 4:
         raise ValueError(f"sections {tuple(sections)} does not fit positions with {axes} axes (1 to 4)")
-    return axes, stride, (*sections, 0, 0, 0)[:4]
+    return axes, stride, (*(_int32(s, "sections") for s in sections), 0, 0, 0)[:4]
 
 
 _host_module = None
@@ -499,9 +518,10 @@ def rope(x, positions, inv_freq, sections=None, interleaved: bool = False, inver
         os_ = (h * d, d)
     else:
         os_ = _strides(out, "out", dtype, shape)
-    args = _ROPE_ARGS.pack(_ROPE_ARGS.size, code, t, h, 0, d, pairs, axes, *sec, interleaved, inverse, 0, 0,
-                           x.data_ptr(), 0, 0, out.data_ptr(), 0, 0, positions.data_ptr(), inv_freq.data_ptr(), 0,
-                           xs[0], xs[1], os_[0], os_[1], 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, axis_stride)
+    args = _pack(_ROPE_ARGS, _ROPE_ARGS.size, code, t, h, 0, d, pairs, axes, *sec,
+                 bool(interleaved), bool(inverse), 0, 0,
+                 x.data_ptr(), 0, 0, out.data_ptr(), 0, 0, positions.data_ptr(), inv_freq.data_ptr(), 0,
+                 xs[0], xs[1], os_[0], os_[1], 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, axis_stride)
     check(lib().kaio_rope(args, _raw_stream(x, stream)))
     return out
 
@@ -542,11 +562,12 @@ def rope_append(q, k, v, positions, inv_freq, k_cache, v_cache, slots, sections=
         os_ = (h * d, d)
     else:
         os_ = _strides(q_out, "q_out", dtype, shape)
-    args = _ROPE_ARGS.pack(_ROPE_ARGS.size, code, t, h, kh, d, pairs, axes, *sec, interleaved, 0, pages, page_size,
-                           q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(),
-                           v_cache.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), slots.data_ptr(),
-                           qs[0], qs[1], os_[0], os_[1], ks[0], ks[1], vs[0], vs[1], kc[0], kc[1], kc[2],
-                           vc[0], vc[1], vc[2], axis_stride)
+    args = _pack(_ROPE_ARGS, _ROPE_ARGS.size, code, t, h, kh, d, pairs, axes, *sec,
+                 bool(interleaved), 0, pages, page_size,
+                 q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(),
+                 v_cache.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), slots.data_ptr(),
+                 qs[0], qs[1], os_[0], os_[1], ks[0], ks[1], vs[0], vs[1], kc[0], kc[1], kc[2],
+                 vc[0], vc[1], vc[2], axis_stride)
     check(lib().kaio_rope_append(args, _raw_stream(q, stream)))
     return q_out
 
@@ -610,7 +631,7 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max
     if workspace is None:
         # on the call's own stream: zeroed before the kernel, and freed to that stream's later work
         workspace = paged_attention_workspace(q.device, stream)
-    elif not (workspace.is_cuda and workspace.dtype is torch.uint8 and workspace.is_contiguous()):
+    elif not (getattr(workspace, "is_cuda", False) and workspace.dtype is torch.uint8 and workspace.is_contiguous()):
         raise ValueError("workspace must be a dense uint8 CUDA tensor from paged_attention_workspace()")
     if out is None:
         out = _empty(shape, dtype, q.device, stream)
@@ -627,11 +648,14 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max
         lse_ptr = lse.data_ptr()
     if max_new is None:
         max_new = t if starts else 1
-    args = _PAGED_ARGS.pack(_PAGED_ARGS.size, code, b, t, h, kh, d, page_size, pages, max_pages, max_new, causal,
-                            window, sinks, d ** -0.5 if scale is None else scale, 0,
-                            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
-                            kv_lens.data_ptr(), starts, out.data_ptr(), lse_ptr, workspace.data_ptr(),
-                            workspace.numel(),
-                            qs[0], qs[1], os_[0], os_[1], kc[0], kc[1], kc[2], vc[0], vc[1], vc[2], ts[0])
+    if scale is None:
+        scale = max(d, 1) ** -0.5
+    args = _pack(_PAGED_ARGS, _PAGED_ARGS.size, code, b, t, h, kh, d, page_size, pages, max_pages,
+                 _int32(max_new, "max_new"), bool(causal), _int32(window, "window"), _int32(sinks, "sinks"),
+                 ctypes.c_float(scale).value, 0,
+                 q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
+                 kv_lens.data_ptr(), starts, out.data_ptr(), lse_ptr, workspace.data_ptr(),
+                 workspace.numel(),
+                 qs[0], qs[1], os_[0], os_[1], kc[0], kc[1], kc[2], vc[0], vc[1], vc[2], ts[0])
     check(lib().kaio_paged_attention(args, _raw_stream(q, stream)))
     return (out, lse) if return_lse else out
