@@ -21,8 +21,8 @@
 // 2016 of products; the rest is the way from product to softmax to product, with one
 // wait and one commit of 150-300 cycles each. TMEM is full (two S and two O of 128
 // columns), so there is no third half to fill the gap. 4096 tokens over 16384 keys,
-// 32 heads on 8 of 128: 680-730 us with the power limit, 1.32-1.42 PFLOP/s, 0.68-0.73 of
-// what the measured library product reaches in a burst, 0.76-0.82 of it sustained.
+// 32 heads on 8 of 128: 726-750 us with the power limit, 1.28-1.33 PFLOP/s, 0.66-0.68 of
+// what the measured library product reaches in a burst, 0.74-0.77 of it sustained.
 //
 // Registers: the softmax warps rescale O and write the results themselves (both are
 // rare), so eight of twelve warps share nearly all registers (216 a thread, 72 for the

@@ -19,12 +19,12 @@
 // loop has no barrier between warps. Keys that no row of the item sees are
 // filled with zeros and their pages are not read. Two CTAs of four warps on an SM
 // with three or six stages of 8 or 4 KB each keep 150 to 190 KB in flight on it.
-// 64 tokens over contexts of up to 8192, 32 heads on 8 of 128: 205-210 us, 6.4-6.6 TB/s
-// (0.95-0.97 of a measured copy); one token over 131072: 91 us (0.86); 16 tokens of 64
-// heads with a window of 4096: 52-53 us (0.75; 5 us of it before the first keys arrive).
+// 64 tokens over contexts of up to 8192, 32 heads on 8 of 128: 203-210 us, 6.4-6.7 TB/s
+// (0.95-0.98 of a measured copy); one token over 131071: 90-91 us (0.87); 16 tokens of 64
+// heads with a window of 4096: 52-54 us (0.75; 5 us of it before the first keys arrive).
 //
 // Short calls are bound by what surrounds the units. One token over 1037 keys, 32 heads
-// (11.6 us): 4 us from the launch to the first copies (the shares, then page ids, then
+// (12.0 us): 4 us from the launch to the first copies (the shares, then page ids, then
 // keys: three round trips, in code that is fetched for the first time), 2 us for two
 // units, 4 us to write a part, to find out who is last and to join nine of them.
 #include <cuda_bf16.h>

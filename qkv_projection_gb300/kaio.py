@@ -499,7 +499,8 @@ def rope(x, positions, inv_freq, sections=None, interleaved: bool = False, inver
     consecutive pairs each axis turns (default: all by the one axis). Pairs are
     columns (i, i + R), or (2i, 2i + 1) if interleaved. inverse turns the other
     way: the gradient of the rotation with respect to x, given that of its
-    result. out may be x itself.
+    result. out may be x itself. A new result belongs to ``stream`` (default: the
+    current one).
     """
     host = _host_module or _host()
     if host:
@@ -534,7 +535,8 @@ def rope_append(q, k, v, positions, inv_freq, k_cache, v_cache, slots, sections=
     q [T, H, D], k and v [T, KH, D]; k_cache and v_cache [pages, page_size, KH, D]
     (any strides with a dense last dimension, such as a transposed [pages, KH,
     page_size, D]); slots int32 [T]: page * page_size + place in the page for each
-    token, or -1 to store nothing. q_out may be q itself.
+    token, or -1 to store nothing. q_out may be q itself; k and v may then lie beside
+    it in one packed buffer. A new result belongs to ``stream``, as for ``rope``.
     """
     host = _host_module or _host()
     if host:
@@ -597,11 +599,13 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max
     v_cache [pages, page_size, KH, D], any strides with a dense last dimension,
     page_size a power of two from 16 to 1024, H a multiple of KH; page_table
     int32 [B, P]. max_new: at least the largest number of new tokens of one
-    sequence (default: T, or 1 without q_starts). scale defaults to D ** -0.5.
+    sequence (default: T, or 1 without q_starts); it chooses the kernel, so give 1 for
+    a batch of single tokens with q_starts. scale defaults to D ** -0.5.
     causal: a token sees positions up to its own; window: only the last `window`
     of them, and the first `sinks` positions besides. A token that sees nothing
     gets zeros and lse = -inf. workspace: from ``paged_attention_workspace``;
-    without one the call makes its own.
+    without one the call makes its own. New results and that workspace belong to
+    ``stream`` (default: the current one).
     """
     host = _host_module or _host()
     if host:
