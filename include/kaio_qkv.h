@@ -424,6 +424,41 @@ typedef struct {
 int kaio_paged_attention(const kaio_paged_attention_args* args, kaio_stream_t stream);
 
 /*
+ * The same attention with scores that are capped or lose with distance, and with
+ * documents and prefixes. Token t at position p of sequence b sees position j if
+ *   doc_starts[t] <= j < kv_lens[b]  and  (j < prefix_lens[b]  or
+ *     ((not causal or j <= p) and (window == 0 or j > p - window or j < sinks)))
+ * and its score there is, for query head h,
+ *   s = scale * sum_d q[d] k_j[d];  s = softcap * tanh(s / softcap) if softcap;
+ *   s = s - slopes[h] * |p - j| if slopes.
+ * Output, lse, types, layouts, workspace and errors as above; struct_size is that of
+ * the whole block.
+ *
+ *   softcap     0: none; else in (0, 256], with 2 log2(e) |scale| / softcap in 2^-100..2^100
+ *               (or scale 0). Scores are then good to 24 * 2^-24 softcap.
+ *   slopes      f32 [heads], finite, of either sign; null: none
+ *   prefix_lens i32 [batch]; null: none. The first prefix_lens[b] positions (cut to 0..kv_lens[b])
+ *               are seen by all new tokens, also by those before them.
+ *   doc_starts  i32 [tokens]; null: 0. The position where the document of each token begins (below 0: 0),
+ *               not decreasing within a sequence. Keys before it are hidden, of the prefix and the sinks too.
+ *
+ * A NaN or infinity in v can then reach the tokens of a sequence from any position
+ * between the first and the last that they see. Further errors (KAIO_ERR_INVALID_VALUE): softcap
+ * out of range; slopes, prefix_lens or doc_starts overlapping an output or of
+ * another device; KAIO_ERR_MISALIGNED (4 bytes).
+ */
+typedef struct {
+  kaio_paged_attention_args base;
+  float softcap;
+  int32_t reserved; /* 0 */
+  const float* slopes;
+  const int32_t* prefix_lens;
+  const int32_t* doc_starts;
+} kaio_paged_attention_scored_args;
+
+int kaio_paged_attention_scored(const kaio_paged_attention_scored_args* args, kaio_stream_t stream);
+
+/*
  * Test entry for the bounded waits of the kernel that kaio_paged_attention runs
  * for chunks: the same call with every wait of its pipeline limited to
  * wait_limit_ns instead of 2 s. What a wait that gives up leaves behind is as
@@ -437,6 +472,98 @@ int kaio_debug_paged_attention_wait_limit(const kaio_paged_attention_args* args,
 /* Bytes of workspace that kaio_paged_attention needs on the current device, for
  * any sizes. Returns KAIO_OK and writes *bytes, or an error status. */
 int kaio_paged_attention_workspace(uint64_t* bytes);
+
+/*
+ * Upkeep of the paged cache that kaio_rope_append writes and kaio_paged_attention
+ * reads: copies of pages, and the books of who holds which.
+ *
+ * kaio_cache_copy_pages copies page src[i] to page dst[i] of every cache, K and V of
+ * all layers in one call, i in 0..pairs - 1. Pairs with a src or dst outside the
+ * cache (such as -1) are left out. No dst may be another pair's src or dst.
+ *
+ *   cache     host array [caches] of device pointers, each [num_pages, page_size,
+ *             kv_heads, dim] of 16-bit values
+ *   strides   host array [caches][3]: page, slot and head stride of each, in elements,
+ *             multiples of 8, such that its rows share no element
+ *   src, dst  i32 [pairs] on the device
+ * Errors (KAIO_ERR_INVALID_VALUE unless noted): struct_size; dim not a multiple of 8
+ * in 8..256; negative sizes, or sizes of 2^30 or more (values of a page, and pairs times pieces of
+ * 16384 bytes of a page, too); a bad stride; a null pointer; src or dst overlapping a cache; memory
+ * of another device; KAIO_ERR_MISALIGNED (caches 16 bytes, src and dst 4). Nothing
+ * to copy returns KAIO_OK without a launch.
+ */
+typedef struct {
+  uint32_t struct_size; /* sizeof(kaio_cache_copy_args) */
+  int32_t caches, num_pages, page_size, kv_heads, dim;
+  int32_t pairs;
+  int32_t reserved; /* 0 */
+  void* const* cache;
+  const int64_t* strides;
+  const int32_t* src;
+  const int32_t* dst;
+} kaio_cache_copy_args;
+
+int kaio_cache_copy_pages(const kaio_cache_copy_args* args, kaio_stream_t stream);
+
+/*
+ * The books: page_refs i32 [num_pages] (how many places of the table hold each page;
+ * 0: free), page_table i32 [batch, max_pages] (rows table_stride apart) and kv_lens
+ * i32 [batch]. Row b holds its first ceil(kv_lens[b] / page_size) places (at most
+ * max_pages); what stands in the others means nothing and is left as it is. The
+ * operators change the books where they are, on the device, without a synchronisation;
+ * their results do not depend on timing.
+ *
+ * kaio_cache_fork: row b becomes a copy of row parents[b] (i32 [batch]), all rows at
+ *   once, with counted references; a parent outside the batch leaves its row as it
+ *   is. Pages are shared, none is copied.
+ * kaio_cache_append: row b takes n = q_starts[b + 1] - q_starts[b] positions more
+ *   (q_starts i32 [batch + 1], from 0 to tokens, not decreasing; null: one each, tokens ==
+ *   batch). The pages that the rows need, in the rows' order, are the lowest free
+ *   ones. A row with n > 0 whose last page is filled in part and held elsewhere too
+ *   takes a page instead of it: src[b] (the shared page) and dst[b] (its own), whose
+ *   contents have to be copied (kaio_cache_copy_pages), else both -1. slots i32
+ *   [tokens] gets page * page_size + place of every new position, as kaio_rope_append
+ *   takes it. A row that does not fit (its max_pages places, or the free pages that the
+ *   rows before it leave, refused ones counted too) takes nothing: its books stay, its slots are -1. So do tokens of no row.
+ * kaio_cache_truncate: row b is cut to new_lens[b] positions (i32 [batch]; below 0: 0)
+ *   where that is less than it has, and its pages behind them are given back.
+ * kaio_cache_compact: the i-th highest used page moves to the i-th lowest free one
+ *   as long as that is lower, for i < max_moves. src and dst (i32 [max_moves])
+ *   get the pairs to copy, then -1; page_refs and the table are renumbered already.
+ *   With max_moves at num_pages / 2 or more all used pages end below all free ones.
+ *
+ * page_refs has to agree with the table: a held page that it calls free may be given
+ * away. A table entry outside the pool counts for nothing.
+ * Errors (KAIO_ERR_INVALID_VALUE unless noted): struct_size; batch above 8192,
+ * num_pages above 2^23, page_size below 1, num_pages * page_size of 2^31 or more,
+ * other sizes negative or 2^30 or more (batch * max_pages too), batch > 1 with table_stride below
+ * max_pages; q_starts null with tokens != batch; a null pointer; two arrays
+ * that overlap; memory of another device; KAIO_ERR_MISALIGNED (4 bytes). batch == 0
+ * returns KAIO_OK without a launch (append needs tokens == 0 then, compact max_moves == 0).
+ * Fields that an entry does not name are not used.
+ */
+typedef struct {
+  uint32_t struct_size; /* sizeof(kaio_cache_args) */
+  int32_t batch, max_pages, num_pages, page_size;
+  int32_t tokens;    /* append */
+  int32_t max_moves; /* compact */
+  int32_t reserved;  /* 0 */
+  int64_t table_stride;
+  int32_t* page_refs;
+  int32_t* page_table;
+  int32_t* kv_lens;
+  const int32_t* parents;  /* fork */
+  const int32_t* q_starts; /* append */
+  const int32_t* new_lens; /* truncate */
+  int32_t* slots;          /* append */
+  int32_t* src;            /* append, compact */
+  int32_t* dst;            /* append, compact */
+} kaio_cache_args;
+
+int kaio_cache_fork(const kaio_cache_args* args, kaio_stream_t stream);
+int kaio_cache_append(const kaio_cache_args* args, kaio_stream_t stream);
+int kaio_cache_truncate(const kaio_cache_args* args, kaio_stream_t stream);
+int kaio_cache_compact(const kaio_cache_args* args, kaio_stream_t stream);
 
 /*
  * Dequantise packed INT4 weights to f16, exactly as the projection kernels do

@@ -26,6 +26,7 @@
 
 #include "../../include/kaio_qkv.h"
 #include "attention_internal.h"
+#include "cache_internal.h"
 #include "kaio_internal.h"
 
 namespace {
@@ -848,12 +849,15 @@ int kaio_paged_attention_workspace(uint64_t* bytes) {
 
 namespace {
 
-// wait_ns: kOwnWaitLimit, or a limit to test the tensor-core kernel with.
-int paged_attention_impl(const kaio_paged_attention_args* a, uint64_t wait_ns, cudaStream_t stream) {
+// x: what the scores and masks are besides, or null. wait_ns: kOwnWaitLimit, or a limit to
+// test the tensor-core kernel with.
+int paged_attention_impl(const kaio_paged_attention_args* a, const kaio_paged_attention_scored_args* x, uint64_t wait_ns,
+                         cudaStream_t stream) {
   if (a == nullptr) return fail(KAIO_ERR_INVALID_VALUE, "args is a null pointer");
-  if (a->struct_size != sizeof(*a))
-    return fail(KAIO_ERR_INVALID_VALUE, "struct_size %u is not sizeof(kaio_paged_attention_args) (%zu)",
-                a->struct_size, sizeof(*a));
+  const size_t block = x ? sizeof(*x) : sizeof(*a);
+  if (a->struct_size != block)
+    return fail(KAIO_ERR_INVALID_VALUE, "struct_size %u is not sizeof(kaio_paged_attention_%sargs) (%zu)",
+                a->struct_size, x ? "scored_" : "", block);
   kaio::FloatType t = kaio::FloatType::F16;
   KAIO_TRY(float16_type(a->dtype, &t));
   const int64_t T = a->tokens, H = a->heads, KH = a->kv_heads, D = a->dim, P = a->num_pages, ps = a->page_size;
@@ -871,6 +875,16 @@ int paged_attention_impl(const kaio_paged_attention_args* a, uint64_t wait_ns, c
     return fail(KAIO_ERR_INVALID_VALUE, "window (%d) and sinks (%d) must not be negative", a->window, a->sinks);
   const float scale_log2 = a->scale * 1.4426950408889634f;
   if (!std::isfinite(scale_log2)) return fail(KAIO_ERR_INVALID_VALUE, "scale (%g) must be finite, times log2(e) too", a->scale);
+  float cap_in = 0.f;
+  if (x && x->softcap != 0.f) {
+    // A score is good to 24 * 2^-24 caps (at worst; cap4 in paged_chunk.cuh): with a cap of 256 to 2^-11.4,
+    // less than what rounding a weight to f16 may cost.
+    if (!(x->softcap > 0.f && x->softcap <= 256.f))
+      return fail(KAIO_ERR_INVALID_VALUE, "softcap (%g) must be 0 or in (0, 256]", x->softcap);
+    cap_in = 2.f * std::fabs(scale_log2) / x->softcap;
+    if (!(cap_in == 0.f ? a->scale == 0.f : cap_in >= 0x1p-100f && cap_in <= 0x1p100f))
+      return fail(KAIO_ERR_INVALID_VALUE, "scale (%g) is out of range for softcap (%g)", a->scale, x->softcap);
+  }
   const int64_t rows = a->max_new * (H / KH);
   if (wait_ns != kaio::kOwnWaitLimit &&
       (rows <= kaio::kPagedDecodeRows || P == 0 || W == 0 || !kaio::paged_chunk_limit_ok(t, a->dim)))
@@ -908,6 +922,11 @@ int paged_attention_impl(const kaio_paged_attention_args* a, uint64_t wait_ns, c
                  {"workspace", a->workspace, static_cast<size_t>(a->workspace_bytes)}};
   int n_out = 2;
   if (a->lse) out[n_out++] = {"lse", a->lse, static_cast<size_t>(T * H) * 4};
+  Span more[3];
+  int n_more = 0;
+  if (x && x->slopes) more[n_more++] = {"slopes", x->slopes, static_cast<size_t>(H) * 4};
+  if (x && x->prefix_lens) more[n_more++] = {"prefix_lens", x->prefix_lens, static_cast<size_t>(B) * 4};
+  if (x && x->doc_starts) more[n_more++] = {"doc_starts", x->doc_starts, static_cast<size_t>(T) * 4};
   KAIO_TRY(check_not_null(in, n_in));
   KAIO_TRY(check_not_null(out, 2));
   KAIO_TRY(check_aligned(in, 1));
@@ -918,7 +937,9 @@ int paged_attention_impl(const kaio_paged_attention_args* a, uint64_t wait_ns, c
   }
   KAIO_TRY(check_aligned(out, 2));
   KAIO_TRY(check_aligned4(out + 2, n_out - 2));
+  KAIO_TRY(check_aligned4(more, n_more));
   KAIO_TRY(check_overlap(in, n_in, out, n_out));
+  for (int i = 0; i < n_more; ++i) KAIO_TRY(check_overlap(more + i, 1, out, n_out));
   KAIO_TRY(current_device(&dev, &info));
   const size_t need = paged_workspace_bytes(info);
   if (a->workspace_bytes < need)
@@ -926,6 +947,7 @@ int paged_attention_impl(const kaio_paged_attention_args* a, uint64_t wait_ns, c
                 static_cast<unsigned long long>(a->workspace_bytes), need);
   KAIO_TRY(check_on_device(in, n_in, dev));
   KAIO_TRY(check_on_device(out, n_out, dev));
+  KAIO_TRY(check_on_device(more, n_more, dev));
 
   kaio::PagedParams p{};
   p.q = a->q, p.kc = a->k_cache, p.vc = a->v_cache, p.out = a->out, p.lse = a->lse;
@@ -946,8 +968,17 @@ int paged_attention_impl(const kaio_paged_attention_args* a, uint64_t wait_ns, c
   // more rows are worth the tensor cores' 128-row tiles. (An empty cache has no
   // tensor map; the former handles it.)
   const bool few = rows <= kaio::kPagedDecodeRows || p.max_pages == 0;
-  const cudaError_t e = few ? kaio::launch_paged_decode(t, p, a->workspace, info.sms, stream)
-                            : kaio::launch_paged_chunk(t, p, a->workspace, info.sms, stream, wait_ns);
+  cudaError_t e;
+  if (cap_in != 0.f || n_more) {
+    p.cap_in = cap_in;
+    p.cap_log2 = x->softcap * 1.4426950408889634f;
+    p.slopes = x->slopes, p.prefix_lens = x->prefix_lens, p.doc_starts = x->doc_starts;
+    e = few ? kaio::launch_paged_decode_scored(t, p, a->workspace, info.sms, stream)
+            : kaio::launch_paged_chunk_scored(t, p, a->workspace, info.sms, stream);
+  } else {
+    e = few ? kaio::launch_paged_decode(t, p, a->workspace, info.sms, stream)
+            : kaio::launch_paged_chunk(t, p, a->workspace, info.sms, stream, wait_ns);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "paged attention kernel launch");
   return KAIO_OK;
 }
@@ -956,13 +987,178 @@ int paged_attention_impl(const kaio_paged_attention_args* a, uint64_t wait_ns, c
 
 int kaio_paged_attention(const kaio_paged_attention_args* args, kaio_stream_t stream) {
   g_last_error.clear();
-  return paged_attention_impl(args, kaio::kOwnWaitLimit, reinterpret_cast<cudaStream_t>(stream));
+  return paged_attention_impl(args, nullptr, kaio::kOwnWaitLimit, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kaio_paged_attention_scored(const kaio_paged_attention_scored_args* args, kaio_stream_t stream) {
+  g_last_error.clear();
+  return paged_attention_impl(args ? &args->base : nullptr, args, kaio::kOwnWaitLimit,
+                              reinterpret_cast<cudaStream_t>(stream));
 }
 
 int kaio_debug_paged_attention_wait_limit(const kaio_paged_attention_args* args, uint64_t wait_limit_ns,
                                           kaio_stream_t stream) {
   g_last_error.clear();
-  return paged_attention_impl(args, wait_limit_ns, reinterpret_cast<cudaStream_t>(stream));
+  return paged_attention_impl(args, nullptr, wait_limit_ns, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kaio_cache_copy_pages(const kaio_cache_copy_args* a, kaio_stream_t stream_) {
+  g_last_error.clear();
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (a == nullptr) return fail(KAIO_ERR_INVALID_VALUE, "args is a null pointer");
+  if (a->struct_size != sizeof(*a))
+    return fail(KAIO_ERR_INVALID_VALUE, "struct_size %u is not sizeof(kaio_cache_copy_args) (%zu)", a->struct_size,
+                sizeof(*a));
+  const int64_t P = a->num_pages, ps = a->page_size, KH = a->kv_heads, D = a->dim;
+  KAIO_TRY(check_sizes({{"caches", a->caches}, {"num_pages", P}, {"page_size", ps}, {"kv_heads", KH}, {"pairs", a->pairs}}));
+  if (D < 8 || D > 256 || D % 8 != 0)
+    return fail(KAIO_ERR_INVALID_VALUE, "dim (%d) must be a multiple of 8 in 8..256", a->dim);
+  const int64_t heads = std::min<int64_t>(ps * KH, kMaxSize);      // (ps * KH < 2^60)
+  KAIO_TRY(check_sizes({{"page_size * kv_heads * dim", heads * D}}));
+  const int blocks = kaio::cache_copy_blocks(static_cast<int>(heads * D / 8));
+  KAIO_TRY(check_sizes({{"pairs * pieces of a page", static_cast<int64_t>(a->pairs) * blocks}}));
+  int dev;
+  DeviceInfo info;
+  if (a->caches == 0 || a->pairs == 0 || P == 0 || heads == 0) return current_device(&dev, &info);
+  const Span lists[2] = {{"src", a->src, static_cast<size_t>(a->pairs) * 4}, {"dst", a->dst, static_cast<size_t>(a->pairs) * 4}};
+  if (a->cache == nullptr || a->strides == nullptr)
+    return fail(KAIO_ERR_INVALID_VALUE, "%s is a null pointer", a->cache ? "strides" : "cache");
+  KAIO_TRY(check_not_null(lists, 2));
+  KAIO_TRY(check_aligned4(lists, 2));
+  auto span_of = [&](int i) {
+    const int64_t* s = a->strides + 3 * i;
+    return Span{"cache", a->cache[i], extent16({{P, s[0]}, {ps, s[1]}, {KH, s[2]}}, D)};
+  };
+  for (int i = 0; i < a->caches; ++i) {
+    const int64_t* s = a->strides + 3 * i;
+    KAIO_TRY(check_strides("cache", {{P, s[0]}, {ps, s[1]}, {KH, s[2]}}, D, true));
+    const Span c = span_of(i);
+    KAIO_TRY(check_not_null(&c, 1));
+    KAIO_TRY(check_aligned(&c, 1));
+    KAIO_TRY(check_overlap(lists, 2, &c, 1));
+  }
+  KAIO_TRY(current_device(&dev, &info));
+  KAIO_TRY(check_on_device(lists, 2, dev));
+  Span spans[kaio::kCacheMaxCaches];
+  for (int first = 0; first < a->caches; first += kaio::kCacheMaxCaches) {
+    const int n = std::min(a->caches - first, kaio::kCacheMaxCaches);
+    for (int i = 0; i < n; ++i) spans[i] = span_of(first + i);
+    KAIO_TRY(check_on_device(spans, n, dev));
+  }
+  for (int first = 0; first < a->caches; first += kaio::kCacheMaxCaches) {
+    const int n = std::min(a->caches - first, kaio::kCacheMaxCaches);
+    kaio::CacheCopyParams p{};
+    bool dense = true;
+    for (int i = 0; i < n; ++i) {
+      // a page from the inside out, in pieces of 8 values: a head's, then what has the smaller stride
+      const int64_t* s = a->strides + 3 * (first + i);
+      int64_t inner = D / 8, n1 = KH, s1 = s[2] / 8, n2 = ps, s2 = s[1] / 8;
+      if (n1 <= 1 || (n2 > 1 && s2 < s1)) std::swap(n1, n2), std::swap(s1, s2);
+      if (n1 <= 1 || s1 == inner) {
+        inner *= n1, n1 = n2, s1 = s2, n2 = 1, s2 = 0;
+        if (n1 <= 1 || s1 == inner) inner *= n1, n1 = 1, s1 = 0;
+      }
+      p.cache[i] = {a->cache[first + i], P > 1 ? s[0] / 8 : 0, s1, s2, static_cast<int>(inner), static_cast<int>(n1)};
+      dense = dense && n1 == 1 && n2 == 1;
+    }
+    p.src = a->src, p.dst = a->dst;
+    p.num_pages = a->num_pages, p.pieces = static_cast<int>(heads * D / 8), p.blocks = blocks;
+    const cudaError_t e = kaio::launch_cache_copy(p, n, a->pairs, dense, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "page copy launch");
+  }
+  return KAIO_OK;
+}
+
+namespace {
+
+enum class Upkeep { kFork, kAppend, kTruncate, kCompact };
+
+int cache_impl(Upkeep op, const kaio_cache_args* a, cudaStream_t stream) {
+  if (a == nullptr) return fail(KAIO_ERR_INVALID_VALUE, "args is a null pointer");
+  if (a->struct_size != sizeof(*a))
+    return fail(KAIO_ERR_INVALID_VALUE, "struct_size %u is not sizeof(kaio_cache_args) (%zu)", a->struct_size, sizeof(*a));
+  const int64_t B = a->batch, W = a->max_pages, P = a->num_pages;
+  const int64_t T = op == Upkeep::kAppend ? a->tokens : 0, M = op == Upkeep::kCompact ? a->max_moves : 0;
+  KAIO_TRY(check_sizes({{"batch", B}, {"max_pages", W}, {"num_pages", P}, {"tokens", T}, {"max_moves", M},
+                        {"batch * max_pages", B * W}}));
+  if (B > kaio::kCacheMaxBatch)
+    return fail(KAIO_ERR_INVALID_VALUE, "batch (%d) must be at most %d", a->batch, kaio::kCacheMaxBatch);
+  if (P > kaio::kCacheMaxPages)
+    return fail(KAIO_ERR_INVALID_VALUE, "num_pages (%d) must be at most %d", a->num_pages, kaio::kCacheMaxPages);
+  if (a->page_size < 1 || P * a->page_size >= (1ll << 31))
+    return fail(KAIO_ERR_INVALID_VALUE, "page_size (%d) must be positive, and num_pages * page_size below 2^31", a->page_size);
+  if (B > 1 && (a->table_stride < W || a->table_stride >= (1ll << 40)))
+    return fail(KAIO_ERR_INVALID_VALUE, "table_stride (%lld) is out of range", static_cast<long long>(a->table_stride));
+  if (op == Upkeep::kAppend && a->q_starts == nullptr && T != B)
+    return fail(KAIO_ERR_INVALID_VALUE, "without q_starts there is one token for each sequence: tokens (%d) != batch (%d)",
+                a->tokens, a->batch);
+  int dev;
+  DeviceInfo info;
+  if (B == 0) {
+    if (T || M) return fail(KAIO_ERR_INVALID_VALUE, "tokens and max_moves must be 0 without sequences");
+    return current_device(&dev, &info);
+  }
+  Span in[1], out[6];
+  int n_in = 0, n_out = 0;
+  auto add = [](Span* to, int* n, const char* name, const void* p, int64_t count) {
+    if (count > 0) to[(*n)++] = {name, p, static_cast<size_t>(count) * 4};     // (what is empty may be null)
+  };
+  add(out, &n_out, "page_refs", a->page_refs, P);
+  add(out, &n_out, "page_table", a->page_table, W ? (B - 1) * a->table_stride + W : 0);
+  add(out, &n_out, "kv_lens", a->kv_lens, B);
+  if (op == Upkeep::kFork) add(in, &n_in, "parents", a->parents, B);
+  if (op == Upkeep::kAppend && a->q_starts) add(in, &n_in, "q_starts", a->q_starts, B + 1);
+  if (op == Upkeep::kTruncate) add(in, &n_in, "new_lens", a->new_lens, B);
+  if (op == Upkeep::kAppend) add(out, &n_out, "slots", a->slots, T);
+  if (op == Upkeep::kAppend || op == Upkeep::kCompact) {
+    add(out, &n_out, "src", a->src, op == Upkeep::kAppend ? B : M);
+    add(out, &n_out, "dst", a->dst, op == Upkeep::kAppend ? B : M);
+  }
+  KAIO_TRY(check_not_null(in, n_in));
+  KAIO_TRY(check_not_null(out, n_out));
+  KAIO_TRY(check_aligned4(in, n_in));
+  KAIO_TRY(check_aligned4(out, n_out));
+  KAIO_TRY(check_overlap(in, n_in, out, n_out));
+  KAIO_TRY(current_device(&dev, &info));
+  KAIO_TRY(check_on_device(in, n_in, dev));
+  KAIO_TRY(check_on_device(out, n_out, dev));
+
+  kaio::CacheParams p{};
+  p.page_refs = a->page_refs, p.page_table = a->page_table, p.kv_lens = a->kv_lens;
+  p.parents = a->parents, p.q_starts = a->q_starts, p.new_lens = a->new_lens;
+  p.slots = a->slots, p.src = a->src, p.dst = a->dst;
+  p.table_stride = B > 1 ? a->table_stride : 0;
+  p.batch = a->batch, p.max_pages = a->max_pages, p.num_pages = a->num_pages, p.page_size = a->page_size;
+  p.tokens = a->tokens, p.max_moves = a->max_moves;
+  p.page_div = kaio::FastDiv(static_cast<uint32_t>(a->page_size));
+  const cudaError_t e = op == Upkeep::kFork       ? kaio::launch_cache_fork(p, stream)
+                        : op == Upkeep::kAppend   ? kaio::launch_cache_append(p, stream)
+                        : op == Upkeep::kTruncate ? kaio::launch_cache_truncate(p, stream)
+                                                  : kaio::launch_cache_compact(p, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "cache upkeep launch");
+  return KAIO_OK;
+}
+
+}  // namespace
+
+int kaio_cache_fork(const kaio_cache_args* args, kaio_stream_t stream) {
+  g_last_error.clear();
+  return cache_impl(Upkeep::kFork, args, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kaio_cache_append(const kaio_cache_args* args, kaio_stream_t stream) {
+  g_last_error.clear();
+  return cache_impl(Upkeep::kAppend, args, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kaio_cache_truncate(const kaio_cache_args* args, kaio_stream_t stream) {
+  g_last_error.clear();
+  return cache_impl(Upkeep::kTruncate, args, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kaio_cache_compact(const kaio_cache_args* args, kaio_stream_t stream) {
+  g_last_error.clear();
+  return cache_impl(Upkeep::kCompact, args, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int kaio_dequant_int4_debug(const uint32_t* w, const void* s, void* out, uint32_t K, uint32_t N,
@@ -1003,10 +1199,10 @@ int kaio_device_status(void) {
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
   const unsigned err_tc = kaio::read_and_clear_tc_errors();
   const unsigned err_td = kaio::read_and_clear_tc_decode_errors();
-  const unsigned err_pc = kaio::read_and_clear_chunk_errors();
-  if (err_tc == 0xFFFFFFFFu || err_td == 0xFFFFFFFFu || err_pc == 0xFFFFFFFFu)
+  const unsigned err_pc = kaio::read_and_clear_chunk_errors(), err_ps = kaio::read_and_clear_chunk_scored_errors();
+  if (err_tc == 0xFFFFFFFFu || err_td == 0xFFFFFFFFu || err_pc == 0xFFFFFFFFu || err_ps == 0xFFFFFFFFu)
     return fail(KAIO_ERR_CUDA, "could not read the device error word");
-  const unsigned err = err_tc | err_td | err_pc;
+  const unsigned err = err_tc | err_td | err_pc | err_ps;
   if (err & kaio::kDevErrTimeoutHost)
     return fail(KAIO_ERR_DEVICE_TIMEOUT, "a kernel gave up a bounded wait (device error word 0x%x)", err);
   return KAIO_OK;

@@ -73,6 +73,11 @@ struct PagedParams {
   bool causal;
   int window, sinks;          // window 0: none; both at most kPagedMaxLen
   float scale_log2;           // softmax scale * log2(e)
+  // Of the scored kernels alone (scores that are capped or lose with distance, prefixes, documents):
+  float cap_in;               // 2 |scale| log2(e) / cap; 0: no cap
+  float cap_log2;             // cap * log2(e)
+  const float* slopes;        // [heads], may be null
+  const int *prefix_lens, *doc_starts;     // [batch], [tokens]; may be null
   float* part_o;              // [2 * ctas][rows][dim] partial outputs of split work
   float* part_l;              // [2 * ctas][rows] their log2-sum-exp2
   unsigned* counters;         // [ctas], zero between launches
@@ -84,7 +89,9 @@ constexpr int kPagedDecodeRows = 16;
 // Workspace layout: counters first, then the partial sums.
 constexpr size_t kPagedCounterBytes = KAIO_PAGED_ATTENTION_COUNTERS;
 size_t paged_decode_workspace_bytes(int num_sms);
-cudaError_t launch_paged_decode(FloatType t, PagedParams p, void* workspace, int num_sms, cudaStream_t stream);
+cudaError_t launch_paged_decode(FloatType t, const PagedParams& p, void* workspace, int num_sms, cudaStream_t stream);
+cudaError_t launch_paged_decode_scored(FloatType t, const PagedParams& p, void* workspace, int num_sms,
+                                       cudaStream_t stream);
 size_t paged_chunk_workspace_bytes(int num_sms);
 // wait_ns: limit of the pipeline's waits, kOwnWaitLimit but in a test of the path that gives
 // up, which is built for one type and width.
@@ -92,7 +99,10 @@ constexpr unsigned long long kOwnWaitLimit = ~0ull;
 constexpr bool paged_chunk_limit_ok(FloatType t, int dim) { return t == FloatType::F16 && dim > 64; }
 cudaError_t launch_paged_chunk(FloatType t, const PagedParams& p, void* workspace, int num_sms, cudaStream_t stream,
                                unsigned long long wait_ns);
+cudaError_t launch_paged_chunk_scored(FloatType t, const PagedParams& p, void* workspace, int num_sms,
+                                      cudaStream_t stream);
 unsigned read_and_clear_chunk_errors();
+unsigned read_and_clear_chunk_scored_errors();
 
 // A launch that may begin while the kernel before it in the stream still runs
 // (programmatic dependent launch): the kernel waits for it (grid_dependency_wait)

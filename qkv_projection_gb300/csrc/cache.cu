@@ -1,0 +1,441 @@
+// Upkeep of a paged cache: copies of pages, and the bookkeeping of which sequence holds
+// which (forks, appended and dropped positions, compaction).
+//
+// The books are three arrays: page_refs[p] (how many places of the table hold page p; 0:
+// free), page_table[b][i] and kv_lens[b]. Row b holds its first ceil(kv_lens[b] / page_size)
+// places. All results are integers that follow from the books alone, whatever the order in
+// which the GPU gets to them.
+//
+// What bounds the bookkeeping is latency: a step looks at some hundred rows and, to find free
+// pages, at page_refs once (2 MB for half a million pages). So each operator is one launch
+// (a fork two), and where all pages have to be counted before any can be given out, the
+// kernel is one cluster of 16 CTAs, which can wait for one another without a workspace.
+#include <algorithm>
+#include <cstdint>
+
+#include "cache_internal.h"
+#include "kaio_device.cuh"
+
+namespace kaio {
+namespace {
+
+// ------------------------------------------------------------------- copying
+// Page src[i] to page dst[i] of every cache: blocks of kCopyThreads x kCopyVecs 16-byte pieces.
+constexpr int kCopyThreads = 256, kCopyVecs = 4;
+
+template <bool kDense>
+__global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const __grid_constant__ CacheCopyParams p) {
+  allow_dependents_launch();
+  grid_dependency_wait();
+  const int pair = blockIdx.x / p.blocks, block = blockIdx.x - pair * p.blocks;
+  const int from = p.src[pair], to = p.dst[pair];
+  if (from < 0 || from >= p.num_pages || to < 0 || to >= p.num_pages || from == to) return;
+  const CacheCopyParams::Cache& c = p.cache[blockIdx.y];
+  const uint4* src = static_cast<const uint4*>(c.base) + from * c.page_stride;
+  uint4* dst = static_cast<uint4*>(c.base) + to * c.page_stride;
+  uint4 v[kCopyVecs];
+  long long at[kCopyVecs];
+#pragma unroll
+  for (int k = 0; k < kCopyVecs; ++k) {
+    const int i = (block * kCopyVecs + k) * kCopyThreads + threadIdx.x;
+    at[k] = -1;
+    if (i < p.pieces) {
+      if (kDense) {
+        at[k] = i;
+      } else {
+        const int row = i / c.inner, outer = row / c.middle;
+        at[k] = i - row * c.inner + (row - outer * c.middle) * c.middle_stride + outer * c.outer_stride;
+      }
+      v[k] = src[at[k]];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kCopyVecs; ++k)
+    if (at[k] >= 0) dst[at[k]] = v[k];
+}
+
+// --------------------------------------------------------------- bookkeeping
+// Places that a row of this length holds.
+__device__ __forceinline__ int places(const CacheParams& p, int len) {
+  len = max(len, 0);
+  const int whole = p.page_div.div(len);
+  return min(whole + (whole * p.page_size < len), p.max_pages);
+}
+__device__ __forceinline__ bool is_page(const CacheParams& p, int id) { return id >= 0 && id < p.num_pages; }
+
+// Row b becomes a copy of row parents[b], all at once: a CTA takes `cols` columns of all rows,
+// whose entries it reads before it writes any. References change only where a place does, so
+// what parent and row share already costs nothing.
+constexpr int kForkThreads = 512;
+constexpr int kNotHeld = INT32_MIN;
+
+__global__ void __launch_bounds__(kForkThreads) cache_fork_kernel(const __grid_constant__ CacheParams p, int cols_log2) {
+  extern __shared__ int tile[];                              // [batch][cols]
+  allow_dependents_launch();
+  grid_dependency_wait();
+  const int cols = 1 << cols_log2, col0 = blockIdx.x * cols, n = p.batch * cols;
+  for (int i = threadIdx.x; i < n; i += kForkThreads) {
+    const int row = i >> cols_log2, col = col0 + (i & (cols - 1));
+    tile[i] = col < places(p, p.kv_lens[row]) ? p.page_table[row * p.table_stride + col] : kNotHeld;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kForkThreads) {
+    const int row = i >> cols_log2, c = i & (cols - 1), parent = p.parents[row];
+    if (parent < 0 || parent >= p.batch) continue;
+    const int before = tile[i], now = tile[(parent << cols_log2) + c];
+    if (before == now) continue;
+    if (is_page(p, before)) atomicSub(p.page_refs + before, 1);
+    if (now != kNotHeld) p.page_table[row * p.table_stride + col0 + c] = now;
+    if (is_page(p, now)) atomicAdd(p.page_refs + now, 1);
+  }
+}
+
+// The lengths of the fork, once all places have been read by them.
+constexpr int kLensThreads = 1024;
+__global__ void __launch_bounds__(kLensThreads) cache_fork_lens_kernel(const __grid_constant__ CacheParams p) {
+  allow_dependents_launch();
+  grid_dependency_wait();
+  constexpr int kMine = kCacheMaxBatch / kLensThreads;
+  int len[kMine];
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const int row = threadIdx.x + k * kLensThreads;
+    if (row < p.batch) {
+      const int parent = p.parents[row];
+      len[k] = p.kv_lens[parent < 0 || parent >= p.batch ? row : parent];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const int row = threadIdx.x + k * kLensThreads;
+    if (row < p.batch) p.kv_lens[row] = len[k];
+  }
+}
+
+// A row is cut to new_lens[b] where that is less: a CTA for each row.
+constexpr int kCutThreads = 128;
+__global__ void __launch_bounds__(kCutThreads) cache_truncate_kernel(const __grid_constant__ CacheParams p) {
+  allow_dependents_launch();
+  grid_dependency_wait();
+  const int row = blockIdx.x, len = p.kv_lens[row], kept = max(p.new_lens[row], 0);
+  if (kept >= len) return;
+  const int end = places(p, len);
+  for (int i = places(p, kept) + threadIdx.x; i < end; i += kCutThreads) {
+    const int id = p.page_table[row * p.table_stride + i];
+    if (is_page(p, id)) atomicSub(p.page_refs + id, 1);
+  }
+  __syncthreads();                                           // all have read the length
+  if (threadIdx.x == 0) p.kv_lens[row] = kept;
+}
+
+// ------------------------------------------- one cluster over the whole pool
+constexpr int kCtas = 16, kThreads = 1024, kWarps = kThreads / 32;
+
+// Pages [first, first + 32 words) belong to one warp; which of them are free is kept in shared
+// memory, a bit each, and `before` becomes how many free ones lie before the warp's.
+struct Pool {
+  int words;            // of 32 pages, for each warp
+  int first;
+  uint32_t* mask;       // this warp's
+  int before, free;     // before this warp's pages; in the whole pool
+};
+
+struct PoolShared {
+  int warp_free[kWarps], cta_free;
+  int below;            // compaction: free pages below the line
+};
+
+// All threads of the cluster meet; what each wrote, the others see.
+__device__ __forceinline__ void meet() {
+  __syncwarp();
+  cluster_sync_all();
+}
+
+__device__ __forceinline__ int remote(const int* p, int cta) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(dsmem_map(smem_u32(p), cta)) : "memory");
+  return v;
+}
+
+// First half: counts this warp's free pages (the loads of 8 words in flight).
+__device__ __forceinline__ void pool_count(const CacheParams& p, Pool& pool, uint32_t* masks, PoolShared& sh) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, of_all = cluster_ctarank() * kWarps + warp;
+  pool.words = (p.num_pages + 32 * kCtas * kWarps - 1) / (32 * kCtas * kWarps);
+  pool.first = of_all * pool.words * 32;
+  pool.mask = masks + warp * pool.words;
+  int count = 0;
+#pragma unroll 1
+  for (int w = 0; w < pool.words; w += 8) {
+    int refs[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int id = pool.first + 32 * (w + k) + lane;
+      refs[k] = w + k < pool.words && id < p.num_pages ? p.page_refs[id] : 1;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t free = __ballot_sync(0xFFFFFFFFu, refs[k] <= 0);
+      count += __popc(free);
+      if (lane == 0 && w + k < pool.words) pool.mask[w + k] = free;
+    }
+  }
+  if (lane == 0) sh.warp_free[warp] = count;
+  __syncthreads();
+  if (warp == 0) {
+    const int all = __reduce_add_sync(0xFFFFFFFFu, sh.warp_free[lane]);
+    if (lane == 0) sh.cta_free = all;
+  }
+}
+// Second half, after the cluster has met.
+__device__ __forceinline__ void pool_places(Pool& pool, const PoolShared& sh) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = static_cast<int>(cluster_ctarank());
+  const int of_cta = lane < kCtas ? remote(&sh.cta_free, lane) : 0;
+  pool.free = __reduce_add_sync(0xFFFFFFFFu, of_cta);
+  pool.before = __reduce_add_sync(0xFFFFFFFFu, (lane < cta ? of_cta : 0) + (lane < warp ? sh.warp_free[lane] : 0));
+}
+
+// New positions for every row, in the rows' order: row b takes q_starts[b + 1] - q_starts[b].
+// The k-th page that is needed is the k-th lowest free one, so the warp that holds a free page
+// finds from its rank whose it is. A row that does not fit (its places, or what is left of the pool
+// behind the rows before it) takes nothing.
+struct AppendRow {
+  int old, n, have, want, need;
+  bool fits;
+};
+__device__ __forceinline__ AppendRow append_row(const CacheParams& p, int old, int n) {
+  AppendRow r;
+  r.old = max(old, 0), r.n = n;
+  r.fits = n > 0 && static_cast<long long>(r.old) + n <= static_cast<long long>(p.max_pages) * p.page_size;
+  r.have = places(p, r.old);
+  r.want = r.fits ? places(p, r.old + n) : r.have;
+  return r;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) cache_append_kernel(const __grid_constant__ CacheParams p) {
+  extern __shared__ int smem[];
+  __shared__ PoolShared sh;
+  __shared__ int warp_need[kWarps];
+  int* starts = smem;                                        // [batch + 1] first token of each row
+  int* before = starts + p.batch + 1;                        // [batch + 1] pages needed before it
+  int* old = before + p.batch + 1;                           // [batch]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = static_cast<int>(cluster_ctarank());
+  allow_dependents_launch();
+  grid_dependency_wait();
+  Pool pool;
+  pool_count(p, pool, reinterpret_cast<uint32_t*>(old + p.batch), sh);
+  // What each row needs; every CTA works it out for itself.
+  const int per = (p.batch + kThreads - 1) / kThreads, row0 = min(tid * per, p.batch), row1 = min(row0 + per, p.batch);
+  int mine = 0;
+  for (int row = row0; row < row1; ++row) {
+    const int s0 = p.q_starts ? min(max(p.q_starts[row], 0), p.tokens) : row;
+    const int s1 = p.q_starts ? min(max(p.q_starts[row + 1], s0), p.tokens) : row + 1;
+    const AppendRow r = append_row(p, p.kv_lens[row], s1 - s0);
+    int need = r.want - r.have;
+    if (r.fits && r.old != r.have * p.page_size) {           // a last page in part: its own, unless others hold it too
+      const int last = p.page_table[row * p.table_stride + r.have - 1];
+      need += is_page(p, last) && p.page_refs[last] > 1;
+    }
+    starts[row] = s0, old[row] = r.old, before[row] = need;
+    if (row == p.batch - 1) starts[p.batch] = s1;
+    mine += need;
+    if (cta == 0) p.src[row] = p.dst[row] = -1;
+  }
+  int upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int add = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+    if (lane >= d) upto += add;
+  }
+  if (lane == 31) warp_need[warp] = upto;
+  meet();                                        // all counts, nothing given out yet
+  pool_places(pool, sh);
+  const int of_warp = warp_need[lane];
+  const int needed = __reduce_add_sync(0xFFFFFFFFu, of_warp);
+  int at = upto - mine + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? of_warp : 0);
+  for (int row = row0; row < row1; ++row) {
+    const int need = before[row];
+    before[row] = at;
+    at += need;
+  }
+  if (tid == 0) before[p.batch] = needed;
+  __syncthreads();
+  auto granted = [&](int row, const AppendRow& r) {
+    return r.fits && (before[row + 1] == before[row] || before[row + 1] <= pool.free);
+  };
+  auto row_at = [&](int row) { return append_row(p, old[row], starts[row + 1] - starts[row]); };
+  // the last row that begins at or before x
+  auto find = [&](const int* begins, int x) {
+    int lo = 0, hi = p.batch;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (begins[mid] <= x) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  };
+  int rank0 = pool.before;
+  for (int w = 0; w < pool.words && rank0 < needed; ++w) {
+    const uint32_t free = pool.mask[w];
+    const int rank = rank0 + __popc(free & ((1u << lane) - 1));
+    rank0 += __popc(free);
+    if (!(free >> lane & 1) || rank >= needed) continue;
+    const int id = pool.first + 32 * w + lane, row = find(before, rank);
+    const AppendRow r = row_at(row);
+    if (!granted(row, r)) continue;
+    const int tail = before[row + 1] - before[row] - (r.want - r.have), k = rank - before[row];
+    int* place = p.page_table + row * p.table_stride + r.have + k - tail;
+    if (k < tail) {                                          // in place of a last page that others hold too
+      const int shared = *place;
+      p.src[row] = shared, p.dst[row] = id;
+      atomicSub(p.page_refs + shared, 1);
+    }
+    *place = id;
+    p.page_refs[id] = 1;
+  }
+  meet();                                        // the table is whole
+  if (cta == 0) {
+    for (int row = tid; row < p.batch; row += kThreads) {
+      const AppendRow r = row_at(row);
+      if (granted(row, r)) p.kv_lens[row] = r.old + r.n;
+    }
+  }
+  for (int t = cta * kThreads + tid; t < p.tokens; t += kCtas * kThreads) {
+    const int row = find(starts, t);
+    const AppendRow r = row_at(row);
+    int slot = -1;
+    if (t >= starts[row] && t < starts[row + 1] && granted(row, r)) {
+      const int pos = r.old + t - starts[row], place = p.page_div.div(pos);
+      const int id = p.page_table[row * p.table_stride + place];
+      if (is_page(p, id)) slot = id * p.page_size + pos - place * p.page_size;
+    }
+    p.slots[t] = slot;
+  }
+}
+
+// Of the U used pages those at U and above move to the free ones below U: the i-th highest of
+// them to the i-th lowest of those, up to max_moves.
+__global__ void __launch_bounds__(kThreads, 1) cache_compact_kernel(const __grid_constant__ CacheParams p) {
+  extern __shared__ uint32_t masks[];
+  __shared__ PoolShared sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = static_cast<int>(cluster_ctarank());
+  constexpr int kAll = kCtas * kThreads;
+  allow_dependents_launch();
+  grid_dependency_wait();
+  Pool pool;
+  pool_count(p, pool, masks, sh);
+  for (int i = cta * kThreads + tid; i < p.max_moves; i += kAll) p.src[i] = p.dst[i] = -1;
+  meet();
+  pool_places(pool, sh);
+  const int used = p.num_pages - pool.free;
+  int rank0 = pool.before;
+  for (int w = 0; w < pool.words; ++w) {
+    const uint32_t free = pool.mask[w];
+    const int id = pool.first + 32 * w + lane, rank = rank0 + __popc(free & ((1u << lane) - 1));
+    rank0 += __popc(free);
+    if (id >= p.num_pages) break;
+    if (id == used) sh.below = rank;
+    if (free >> lane & 1) {
+      if (id < used && rank < p.max_moves) p.dst[rank] = id;
+    } else if (id >= used) {
+      const int from_top = used - 1 - (id - rank);
+      if (from_top < p.max_moves) p.src[from_top] = id;
+    }
+  }
+  meet();                                        // both lists are whole
+  const int owner = used < p.num_pages ? used / (32 * kWarps * pool.words) : -1;
+  const int moves = owner < 0 ? 0 : min(remote(&sh.below, owner), p.max_moves);
+  meet();                                        // (no CTA leaves before it was read)
+  if (moves == 0) return;
+  for (int i = cta * kThreads + tid; i < moves; i += kAll) {
+    const int from = p.src[i];
+    p.page_refs[p.dst[i]] = p.page_refs[from];
+    p.page_refs[from] = 0;
+  }
+  // The list descends, so a place finds its page in it by halving.
+  const int lowest = p.src[moves - 1];
+  const int chunks = (p.max_pages + 127) / 128;
+  for (long long c = cta * kWarps + warp; c < static_cast<long long>(p.batch) * chunks; c += kCtas * kWarps) {
+    const int row = static_cast<int>(c / chunks), col = static_cast<int>(c - static_cast<long long>(row) * chunks) * 128;
+    const int end = places(p, p.kv_lens[row]);
+    if (col >= end) continue;
+    int* entry = p.page_table + row * p.table_stride + col + lane;
+    int id[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) id[k] = col + 32 * k + lane < end ? entry[32 * k] : -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (id[k] < lowest) continue;
+      int lo = 0, hi = moves - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (p.src[mid] <= id[k]) hi = mid;
+        else lo = mid + 1;
+      }
+      if (p.src[lo] == id[k]) entry[32 * k] = p.dst[lo];
+    }
+  }
+}
+
+// A launch of one cluster of kCtas CTAs.
+template <typename Kernel>
+cudaError_t launch_cluster(Kernel kernel, const CacheParams& p, size_t smem, cudaStream_t stream) {
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), kCacheSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kCtas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCtas, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+size_t mask_bytes(const CacheParams& p) {
+  const int per = 32 * kCtas * kWarps;
+  return static_cast<size_t>((p.num_pages + per - 1) / per) * kWarps * 4;
+}
+
+}  // namespace
+
+cudaError_t launch_cache_copy(const CacheCopyParams& p, int caches, int pairs, bool dense, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(pairs * p.blocks), static_cast<unsigned>(caches));
+  if (dense) cache_copy_kernel<true><<<grid, kCopyThreads, 0, stream>>>(p);
+  else cache_copy_kernel<false><<<grid, kCopyThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+int cache_copy_blocks(int pieces) { return (pieces + kCopyThreads * kCopyVecs - 1) / (kCopyThreads * kCopyVecs); }
+
+cudaError_t launch_cache_fork(const CacheParams& p, cudaStream_t stream) {
+  // Eight columns are a 32-byte sector of each row.
+  int cols_log2 = 3;
+  while ((static_cast<size_t>(p.batch) << cols_log2) * 4 > kCacheSmem) --cols_log2;
+  const size_t smem = (static_cast<size_t>(p.batch) << cols_log2) * 4;
+  const int ctas = (p.max_pages + (1 << cols_log2) - 1) >> cols_log2;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(cache_fork_kernel), kCacheSmem);
+  if (e == cudaSuccess && ctas > 0)
+    e = launch_dependent(cache_fork_kernel, ctas, kForkThreads, static_cast<int>(smem), stream, p, cols_log2);
+  if (e == cudaSuccess) e = launch_dependent(cache_fork_lens_kernel, 1, kLensThreads, 0, stream, p);
+  return e;
+}
+
+cudaError_t launch_cache_append(const CacheParams& p, cudaStream_t stream) {
+  return launch_cluster(cache_append_kernel, p, mask_bytes(p) + (3 * static_cast<size_t>(p.batch) + 2) * 4, stream);
+}
+
+cudaError_t launch_cache_truncate(const CacheParams& p, cudaStream_t stream) {
+  return launch_dependent(cache_truncate_kernel, p.batch, kCutThreads, 0, stream, p);
+}
+
+cudaError_t launch_cache_compact(const CacheParams& p, cudaStream_t stream) {
+  return launch_cluster(cache_compact_kernel, p, mask_bytes(p), stream);
+}
+
+}  // namespace kaio

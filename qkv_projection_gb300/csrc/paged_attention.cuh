@@ -23,11 +23,16 @@ namespace kaio {
 
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLog2e = 1.4426950408889634f;
 
+// kScored in what follows: with prefixes and documents (of the scored kernels; the others
+// have no code for them).
 struct PagedSeq {
   int q0, n, kv;     // first token, new tokens, positions in the cache
+  int prefix;        // leading positions that all its tokens see
 };
 
+template <bool kScored>
 __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
   PagedSeq s;
   if (p.q_starts) {
@@ -40,44 +45,68 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
   const long long room = static_cast<long long>(p.max_pages) << p.page_shift;
   s.kv = static_cast<int>(min(static_cast<long long>(max(p.kv_lens[b], 0)),
                               min(room, static_cast<long long>(kPagedMaxLen))));
+  s.prefix = kScored && p.prefix_lens ? min(max(p.prefix_lens[b], 0), s.kv) : 0;
   return s;
 }
 
-// Keys that the rows [r0, r1) of a sequence see: [0, first) and [lo, hi), and
-// the key tiles that hold them. The units go through the run's tiles, the one at
+// Where the document of a sequence's row r begins.
+template <bool kScored>
+__device__ __forceinline__ int paged_doc(const PagedParams& p, const PagedSeq& s, int r) {
+  return kScored && p.doc_starts ? min(max(p.doc_starts[s.q0 + p.group_div.div(r)], 0), kPagedMaxLen) : 0;
+}
+
+// Keys that the rows [r0, r1) of a sequence see: [from, first) and [lo, hi), and
+// the key tiles that hold them. `from` is the document's begin of the first row: they do
+// not decrease, so no row sees anything before it. A prefix that passes the causal end is
+// that end, and otherwise as good as sink tokens. The units go through the run's tiles, the one at
 // the window's edge last (its keys are hidden from some rows, and a poor maximum to
 // begin with would have to be renewed), and then through those of the prefix.
-template <int kKeys>
+template <int kKeys, bool kScored>
 struct PagedSpan {
-  int lo, hi, first;
+  int from, first, lo, hi;   // (an empty [from, first) is [0, 0))
   int lo_tile, run;    // the run's first tile, and its tiles
   int units;           // at least 1, so that every item is visited
-  __device__ __forceinline__ PagedSpan(const PagedParams& p, const PagedSeq& s, int r0, int r1) {
+  __device__ __forceinline__ PagedSpan(const PagedParams& p, const PagedSeq& s, int r0, int r1, int doc) {
     const int t0 = p.group_div.div(r0), t1 = p.group_div.div(r1 - 1);
     hi = p.causal ? min(max(s.kv - s.n + t1 + 1, 0), s.kv) : s.kv;
+    if (kScored) hi = max(hi, s.prefix);
     lo = p.window > 0 ? min(max(s.kv - s.n + t0 - p.window + 1, 0), hi) : 0;
-    first = min(p.sinks, lo);
+    if (kScored) lo = min(max(lo, doc), hi);
+    first = min(kScored ? max(p.sinks, s.prefix) : p.sinks, lo);
+    from = 0;
+    if (kScored) {
+      if (first > doc) from = doc;
+      else first = 0;
+      if (lo == hi && first == 0) lo = hi = 0;
+    }
     lo_tile = lo / kKeys;
     run = (hi + kKeys - 1) / kKeys - lo_tile;
-    units = max(1, run + min((first + kKeys - 1) / kKeys, lo_tile));
+    units = max(1, run + max(min((first + kKeys - 1) / kKeys, lo_tile) - from / kKeys, 0));
   }
   __device__ __forceinline__ int key0(int unit) const {
     int tile = unit + lo_tile;
     if (lo > 0) {
-      if (unit >= run) tile = unit - run;
+      if (unit >= run) tile = unit - run + (kScored ? from / kKeys : 0);
       else tile = unit + 1 < run ? tile + 1 : lo_tile;
     }
     return tile * kKeys;
   }
 };
 
-// Keys that one row sees: j < hi and (j >= lo or j < sinks).
+// Keys that one row sees: from <= j < hi and (j >= lo or j < first); pos is its own place.
+template <bool kScored>
 struct PagedRow {
-  int lo, hi;
-  __device__ __forceinline__ PagedRow(const PagedParams& p, const PagedSeq& s, int r) {
-    const int pos = s.kv - s.n + p.group_div.div(r);
+  int pos, from, first, lo, hi;
+  __device__ __forceinline__ PagedRow(const PagedParams& p, const PagedSeq& s, int r, int doc) {
+    pos = s.kv - s.n + p.group_div.div(r);
     hi = p.causal ? min(max(pos + 1, 0), s.kv) : s.kv;
+    if (kScored) hi = max(hi, s.prefix);
     lo = p.window > 0 ? min(max(pos - p.window + 1, 0), hi) : 0;
+    first = kScored ? max(p.sinks, s.prefix) : p.sinks;
+    from = kScored ? doc : 0;
+  }
+  __device__ __forceinline__ bool sees(int j) const {
+    return j < hi && (j >= lo || j < first) && (!kScored || j >= from);
   }
 };
 
@@ -113,6 +142,7 @@ struct PagedShare {
 };
 
 // A place in the line of work: an item, and a unit in it. The constants of `Work`:
+//   kScored               with prefixes and documents
 //   kRows, kKeys          rows of a tile, keys of a unit
 //   kCost, kSmallCost     length of a unit in the line; the second for items of at most
 //                         kSmallRows rows
@@ -137,6 +167,8 @@ struct PagedShare {
 //                         of 60 over 1000, 16/4 heads: 19.9 and 15.0).
 template <typename Work>
 struct PagedWalk : Work {
+  static constexpr bool kScored = Work::kScored;
+  using Span = PagedSpan<Work::kKeys, kScored>;
   using Work::kRows, Work::kFewRows, Work::kKeys, Work::kCost, Work::kSmallCost, Work::kSmallRows, Work::kItemCost;
   static_assert(kSmallCost <= kCost && kCost < 8);
   int tile_rows;              // kRows or kFewRows
@@ -152,7 +184,10 @@ struct PagedWalk : Work {
   __device__ __forceinline__ int row0() const { return tile * step(); }
   __device__ __forceinline__ int row1(const PagedParams& p) const { return min(tile * step() + step(), s.n * p.group); }
   __device__ __forceinline__ int item_units(const PagedParams& p, const PagedSeq& s, int tile) const {
-    return PagedSpan<kKeys>(p, s, tile * step(), min(tile * step() + step(), s.n * p.group)).units;
+    return item_units(p, s, tile, paged_doc<kScored>(p, s, tile * step()));
+  }
+  __device__ __forceinline__ int item_units(const PagedParams& p, const PagedSeq& s, int tile, int doc) const {
+    return Span(p, s, tile * step(), min(tile * step() + step(), s.n * p.group), doc).units;
   }
   __device__ __forceinline__ int item_cost(const PagedParams& p, const PagedSeq& s, int tile) const {
     return s.n * p.group - tile * step() <= kSmallRows || (kFewRows <= kSmallRows && step() == kFewRows) ? kSmallCost : kCost;
@@ -165,12 +200,26 @@ struct PagedWalk : Work {
   __device__ __forceinline__ long long head_length(const PagedParams& p, const PagedSeq& s, int* longest) const {   // (8 units + cost)
     long long u = 0;
     const int tiles = row_tiles(p, s);
-#pragma unroll 1
-    for (int i = 0; i < tiles; ++i) {
-      const int units = item_units(p, s, i), cost = item_cost(p, s, i);
+    auto add = [&](int i, int doc) {
+      const int units = item_units(p, s, i, doc), cost = item_cost(p, s, i);
       u += kItemCost + units * cost;
       *longest = max(*longest, 8 * units + cost);
+    };
+    if (kScored && p.doc_starts) {
+      // (eight documents' begins at a time: one after another they take a round trip each)
+#pragma unroll 1
+      for (int i = 0; i < tiles; i += 8) {
+        int doc[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) doc[k] = paged_doc<kScored>(p, s, min(i + k, tiles - 1) * step());
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (i + k < tiles) add(i + k, doc[k]);
+      }
+      return u;
     }
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i) add(i, 0);
     return u;
   }
   // The unit at which a boundary of shares cuts this item: 0 and `units` for those before and past it.
@@ -198,7 +247,7 @@ struct PagedWalk : Work {
         h = 0;
         do {
           if (++b >= p.batch) return;
-          s = paged_seq(p, b);
+          s = paged_seq<kScored>(p, b);
           tiles = row_tiles(p, s);
         } while (tiles == 0);
       }
@@ -228,7 +277,7 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
     mine = 0, total = 0, longest = 0, items = 0;
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-      const PagedSeq s = paged_seq(p, b);
+      const PagedSeq s = paged_seq<Walk::kScored>(p, b);
       mine += p.kv_heads * w.head_length(p, s, &longest);
       if (kTwoSizes) items = min(items + p.kv_heads * w.row_tiles(p, s), 1 << 20);
     }
@@ -284,7 +333,7 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
     long long left = share->begin - from;
 #pragma unroll 1
     for (w.b = b0;; ++w.b) {
-      w.s = paged_seq(p, w.b);
+      w.s = paged_seq<Walk::kScored>(p, w.b);
       const long long head = w.head_length(p, w.s, &longest);
       if (left < head * p.kv_heads) {
         w.tiles = w.row_tiles(p, w.s);
@@ -313,6 +362,11 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 

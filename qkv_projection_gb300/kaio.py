@@ -47,8 +47,14 @@ _SIGNATURES = {
     "kaio_rope": ([_vp, _vp], _i32),
     "kaio_rope_append": ([_vp, _vp], _i32),
     "kaio_paged_attention": ([_vp, _vp], _i32),
+    "kaio_paged_attention_scored": ([_vp, _vp], _i32),
     "kaio_debug_paged_attention_wait_limit": ([_vp, ctypes.c_uint64, _vp], _i32),
     "kaio_paged_attention_workspace": ([_vp], _i32),
+    "kaio_cache_copy_pages": ([_vp, _vp], _i32),
+    "kaio_cache_fork": ([_vp, _vp], _i32),
+    "kaio_cache_append": ([_vp, _vp], _i32),
+    "kaio_cache_truncate": ([_vp, _vp], _i32),
+    "kaio_cache_compact": ([_vp, _vp], _i32),
     "kaio_qkv_path": ([_u32], _i32),
     "kaio_last_error": ([], ctypes.c_char_p),
     "kaio_device_status": ([], _i32),
@@ -60,6 +66,9 @@ _SIGNATURES = {
 # field by field), filled by one pack() each.
 _ROPE_ARGS = struct.Struct("@I7i4i4i9P15q")
 _PAGED_ARGS = struct.Struct("@I13ifi9PQ11q")
+_PAGED_SCORED_ARGS = struct.Struct("@I13ifi9PQ11qfi3P")
+_CACHE_COPY_ARGS = struct.Struct("@I7i4P")
+_CACHE_ARGS = struct.Struct("@I7iq9P")
 
 
 class KaioError(RuntimeError):
@@ -589,7 +598,8 @@ def paged_attention_workspace(device=None, stream=None):
 
 def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max_new: Optional[int] = None,
                     scale: Optional[float] = None, causal: bool = True, window: int = 0, sinks: int = 0,
-                    workspace=None, out=None, return_lse: bool = False, lse=None, stream=None):
+                    workspace=None, out=None, return_lse: bool = False, lse=None, stream=None, softcap: float = 0.0,
+                    slopes=None, prefix_lens=None, doc_starts=None):
     """Attention of new tokens over a paged cache that already holds their keys
     and values. Returns out [T, H, D], or (out, lse f32 [T, H]) with return_lse.
 
@@ -602,13 +612,19 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max
     sequence (default: T, or 1 without q_starts); it chooses the kernel, so give 1 for
     a batch of single tokens with q_starts. scale defaults to D ** -0.5.
     causal: a token sees positions up to its own; window: only the last `window`
-    of them, and the first `sinks` positions besides. A token that sees nothing
-    gets zeros and lse = -inf. workspace: from ``paged_attention_workspace``;
+    of them, and the first `sinks` positions besides. prefix_lens (int32 [B]): so many
+    first positions all new tokens of the sequence see, also those that stand before them.
+    doc_starts (int32 [T], not decreasing within a sequence): a token sees nothing before
+    its document's begin. softcap (up to 256; 0: none): scores s become
+    softcap * tanh(s / softcap); slopes (f32 [H]): they then lose slopes[h] for each
+    position between token and key. A token that sees nothing gets zeros and lse = -inf.
+    workspace: from ``paged_attention_workspace``;
     without one the call makes its own. New results and that workspace belong to
     ``stream`` (default: the current one).
     """
+    scored = not (softcap == 0 and slopes is None and prefix_lens is None and doc_starts is None)
     host = _host_module or _host()
-    if host:
+    if host and not scored:
         done = host.paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts, max_new, scale, causal, window,
                                     sinks, workspace, out, return_lse, lse, stream)
         if done is not None:
@@ -654,12 +670,122 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max
         max_new = t if starts else 1
     if scale is None:
         scale = max(d, 1) ** -0.5
-    args = _pack(_PAGED_ARGS, _PAGED_ARGS.size, code, b, t, h, kh, d, page_size, pages, max_pages,
+    more = 0, 0, 0
+    if scored:
+        if slopes is not None:
+            _strides(slopes, "slopes", torch.float32, (h,))
+        if prefix_lens is not None:
+            _strides(prefix_lens, "prefix_lens", int32, (b,))
+        if doc_starts is not None:
+            _strides(doc_starts, "doc_starts", int32, (t,))
+        more = tuple(0 if m is None else m.data_ptr() for m in (slopes, prefix_lens, doc_starts))
+    fields = _PAGED_SCORED_ARGS if scored else _PAGED_ARGS
+    args = _pack(fields, fields.size, code, b, t, h, kh, d, page_size, pages, max_pages,
                  _int32(max_new, "max_new"), bool(causal), _int32(window, "window"), _int32(sinks, "sinks"),
                  ctypes.c_float(scale).value, 0,
                  q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
                  kv_lens.data_ptr(), starts, out.data_ptr(), lse_ptr, workspace.data_ptr(),
                  workspace.numel(),
-                 qs[0], qs[1], os_[0], os_[1], kc[0], kc[1], kc[2], vc[0], vc[1], vc[2], ts[0])
-    check(lib().kaio_paged_attention(args, _raw_stream(q, stream)))
+                 qs[0], qs[1], os_[0], os_[1], kc[0], kc[1], kc[2], vc[0], vc[1], vc[2], ts[0],
+                 *((ctypes.c_float(softcap).value, 0, *more) if scored else ()))
+    entry = lib().kaio_paged_attention_scored if scored else lib().kaio_paged_attention
+    check(entry(args, _raw_stream(q, stream)))
     return (out, lse) if return_lse else out
+
+
+def cache_copy_pages(caches, src, dst, stream=None):
+    """Copies page src[i] to page dst[i] of every cache, in one launch for up to 64 of them.
+
+    caches: tensors [pages, page_size, KH, D] of one type (f16 or bf16) and shape, any
+    strides with a dense last dimension: K and V of all layers. src and dst int32 [N];
+    pairs with a page outside the cache (-1) are left out; no dst may be another pair's
+    src or dst.
+    """
+    torch = _torch()
+    caches = list(caches)
+    n = _size(src, "src", torch.int32, 1, 0)
+    _strides(src, "src", torch.int32, (n,))
+    _strides(dst, "dst", torch.int32, (n,))
+    if not caches:
+        return
+    shape = getattr(caches[0], "shape", ())
+    dtype = getattr(caches[0], "dtype", None)
+    if len(shape) != 4:
+        _refuse(caches[0], "caches[0]", dtype, (None,) * 4)
+    _f16_code(dtype, "caches[0]")
+    pages, page_size, kh, d = shape
+    steps = [s for i, c in enumerate(caches) for s in _strides(c, f"caches[{i}]", dtype, shape)[:3]]
+    at = (ctypes.c_void_p * len(caches))(*(c.data_ptr() for c in caches))
+    strides = (ctypes.c_int64 * len(steps))(*steps)
+    args = _pack(_CACHE_COPY_ARGS, _CACHE_COPY_ARGS.size, len(caches), pages, page_size, kh, d, n, 0,
+                 ctypes.addressof(at), ctypes.addressof(strides), src.data_ptr(), dst.data_ptr())
+    check(lib().kaio_cache_copy_pages(args, _raw_stream(src, stream)))
+
+
+def _cache_call(entry, page_refs, page_table, kv_lens, page_size, stream, tokens=0, max_moves=0, parents=None,
+                q_starts=None, new_lens=None, slots=None, src=None, dst=None):
+    int32 = _torch().int32
+    pages = _size(page_refs, "page_refs", int32, 1, 0)
+    _strides(page_refs, "page_refs", int32, (pages,))
+    batch = _size(kv_lens, "kv_lens", int32, 1, 0)
+    _strides(kv_lens, "kv_lens", int32, (batch,))
+    width = _size(page_table, "page_table", int32, 2, 1)
+    step = _strides(page_table, "page_table", int32, (batch, width))[0]
+    for name, t, n in (("parents", parents, batch), ("q_starts", q_starts, batch + 1), ("new_lens", new_lens, batch)):
+        if t is not None:
+            _strides(t, name, int32, (n,))
+    args = _pack(_CACHE_ARGS, _CACHE_ARGS.size, batch, width, pages, _int32(page_size, "page_size"), tokens, max_moves, 0,
+                 step, page_refs.data_ptr(), page_table.data_ptr(), kv_lens.data_ptr(),
+                 *(0 if t is None else t.data_ptr() for t in (parents, q_starts, new_lens, slots, src, dst)))
+    check(entry(args, _raw_stream(page_refs, stream)))
+
+
+def cache_fork(page_refs, page_table, kv_lens, parents, page_size: int, stream=None):
+    """Row b of the books becomes a copy of row parents[b] (int32 [B]), all rows at once; a
+    parent outside the batch leaves its row as it is. Pages are shared, none is copied.
+
+    The books of a paged cache, which this and the following functions change in place:
+    page_refs int32 [pages] (how many places of the table hold each page; 0: free),
+    page_table int32 [B, P] and kv_lens int32 [B]; row b holds its first
+    ceil(kv_lens[b] / page_size) places.
+    """
+    _cache_call(lib().kaio_cache_fork, page_refs, page_table, kv_lens, page_size, stream, parents=parents)
+
+
+def cache_append(page_refs, page_table, kv_lens, q_starts, tokens: int, page_size: int, stream=None):
+    """Gives row b of the books q_starts[b + 1] - q_starts[b] new positions (int32 [B + 1],
+    from 0 to ``tokens``; None: one each), in pages that are the lowest free ones.
+    Returns (slots, src, dst): slots int32 [tokens] for ``rope_append``, and the pages
+    to copy with ``cache_copy_pages`` before anything is written: where a row's last page
+    is held elsewhere too, it gets dst[b] instead of src[b] (int32 [B]; -1: none).
+
+    A row that does not fit its places, or the pool behind the rows before it, takes nothing:
+    its slots are -1 and its books stay. New results belong to ``stream`` (default: the current one).
+    """
+    int32 = _torch().int32
+    batch = _size(kv_lens, "kv_lens", int32, 1, 0)
+    tokens = _int32(tokens, "tokens")
+    device = getattr(kv_lens, "device", None)
+    slots, src, dst = (_empty((max(n, 0),), int32, device, stream) for n in (tokens, batch, batch))
+    _cache_call(lib().kaio_cache_append, page_refs, page_table, kv_lens, page_size, stream, tokens=tokens,
+                q_starts=q_starts, slots=slots, src=src, dst=dst)
+    return slots, src, dst
+
+
+def cache_truncate(page_refs, page_table, kv_lens, new_lens, page_size: int, stream=None):
+    """Cuts row b of the books to new_lens[b] positions (int32 [B]) where it has more, and
+    gives back the pages behind them; 0 frees the row."""
+    _cache_call(lib().kaio_cache_truncate, page_refs, page_table, kv_lens, page_size, stream, new_lens=new_lens)
+
+
+def cache_compact(page_refs, page_table, kv_lens, page_size: int, max_moves: int, stream=None):
+    """Moves the highest used pages to the lowest free ones, up to ``max_moves``: renumbers the
+    books and returns (src, dst), int32 [max_moves] filled up with -1, to be copied with
+    ``cache_copy_pages``. New results belong to ``stream`` (default: the current one)."""
+    int32 = _torch().int32
+    max_moves = _int32(max_moves, "max_moves")
+    device = getattr(kv_lens, "device", None)
+    src, dst = (_empty((max(max_moves, 0),), int32, device, stream) for _ in range(2))
+    _cache_call(lib().kaio_cache_compact, page_refs, page_table, kv_lens, page_size, stream, max_moves=max_moves,
+                src=src, dst=dst)
+    return src, dst
