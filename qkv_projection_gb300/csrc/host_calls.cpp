@@ -1,4 +1,4 @@
-// Host side of the rotary and paged-attention calls: checks of the tensors, the
+// Host side of the rotary, paged-attention and cache calls: checks of the tensors, the
 // argument block, the result and the call itself, in one step from Python.
 //
 // What bounds a call on a few tokens is the host: looking at eight or nine tensors
@@ -31,6 +31,12 @@ namespace {
 int (*g_rope)(const kaio_rope_args*, void*);
 int (*g_rope_append)(const kaio_rope_args*, void*);
 int (*g_paged_attention)(const kaio_paged_attention_args*, void*);
+int (*g_paged_attention_scored)(const kaio_paged_attention_scored_args*, void*);
+int (*g_copy_pages)(const kaio_cache_copy_args*, void*);
+int (*g_fork)(const kaio_cache_args*, void*);
+int (*g_append)(const kaio_cache_args*, void*);
+int (*g_truncate)(const kaio_cache_args*, void*);
+int (*g_compact)(const kaio_cache_args*, void*);
 
 // A tensor on a GPU, dense in its last dimension, without gradient tracking.
 const at::Tensor* usable(PyObject* o, int rank) {
@@ -204,12 +210,14 @@ PyObject* rope_append(PyObject* const* v) {
 }
 
 // (q, k_cache, v_cache, page_table, kv_lens, q_starts, max_new, scale, causal, window, sinks, workspace, out,
-//  return_lse, lse, stream)
+//  return_lse, lse, stream); scored: and softcap, slopes, prefix_lens, doc_starts
+template <bool kScored>
 PyObject* paged_attention(PyObject* const* v) {
   const at::Tensor *q = usable(v[0], 3), *kc = usable(v[1], 4), *table = usable(v[3], 2), *lens = usable(v[4], 1);
   const at::Tensor* ws = usable(v[11], 1);
-  kaio_paged_attention_args a{};
-  a.struct_size = sizeof(a);
+  kaio_paged_attention_scored_args x{};
+  kaio_paged_attention_args& a = x.base;
+  a.struct_size = kScored ? sizeof(x) : sizeof(a);
   if (!q || !kc || !table || !lens || !ws || !type_code(*q, &a.dtype)) return nullptr;
   const at::ScalarType type = q->scalar_type();
   const int64_t t = q->size(0), h = q->size(1), d = q->size(2), b = lens->size(0);
@@ -260,7 +268,29 @@ PyObject* paged_attention(PyObject* const* v) {
     made_lse = new_tensor(lse_size, q->options().dtype(at::kFloat), v[15], stream);
     a.lse = static_cast<float*>(made_lse.data_ptr());
   }
-  if (!call(g_paged_attention, a, stream)) return nullptr;
+  if constexpr (kScored) {
+    if (!PyFloat_Check(v[16])) return nullptr;
+    x.softcap = static_cast<float>(PyFloat_AS_DOUBLE(v[16]));
+    const int64_t heads[1] = {h}, rows[1] = {b}, tokens[1] = {t};
+    if (v[17] != Py_None) {
+      const at::Tensor* slopes = usable(v[17], at::kFloat, heads);
+      if (!slopes) return nullptr;
+      x.slopes = static_cast<const float*>(slopes->data_ptr());
+    }
+    if (v[18] != Py_None) {
+      const at::Tensor* prefix = usable(v[18], at::kInt, rows);
+      if (!prefix) return nullptr;
+      x.prefix_lens = static_cast<const int32_t*>(prefix->data_ptr());
+    }
+    if (v[19] != Py_None) {
+      const at::Tensor* docs = usable(v[19], at::kInt, tokens);
+      if (!docs) return nullptr;
+      x.doc_starts = static_cast<const int32_t*>(docs->data_ptr());
+    }
+    if (!call(g_paged_attention_scored, x, stream)) return nullptr;
+  } else {
+    if (!call(g_paged_attention, a, stream)) return nullptr;
+  }
   PyObject* first = hand_back(v[12], made);
   if (!wants_lse || !first) return first;
   PyObject* second = hand_back(v[14], made_lse);
@@ -268,6 +298,115 @@ PyObject* paged_attention(PyObject* const* v) {
   Py_DECREF(first);
   Py_XDECREF(second);
   return both;
+}
+
+// (caches, src, dst, stream)
+PyObject* copy_pages(PyObject* const* v) {
+  const at::Tensor* src = usable(v[1], 1);
+  if (!src || src->scalar_type() != at::kInt || !fits(src->size(0)) || !(PyList_Check(v[0]) || PyTuple_Check(v[0]))) return nullptr;
+  const at::Tensor* dst = usable(v[2], at::kInt, src->sizes());
+  const Py_ssize_t n = PySequence_Fast_GET_SIZE(v[0]);
+  constexpr Py_ssize_t kMost = 512;
+  if (!dst || n < 1 || n > kMost) return nullptr;
+  void* at[kMost];
+  int64_t strides[3 * kMost];
+  const at::Tensor* first = nullptr;
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    const at::Tensor* c = usable(PySequence_Fast_GET_ITEM(v[0], i), 4);
+    if (!c) return nullptr;
+    if (!first) first = c;
+    if (c->scalar_type() != first->scalar_type() || c->sizes() != first->sizes()) return nullptr;
+    at[i] = c->data_ptr();
+    for (int k = 0; k < 3; ++k) strides[3 * i + k] = c->stride(k);
+  }
+  int32_t type;
+  kaio_cache_copy_args a{};
+  a.struct_size = sizeof(a);
+  if (!type_code(*first, &type)) return nullptr;
+  for (int k = 0; k < 4; ++k)
+    if (!fits(first->size(k))) return nullptr;
+  a.caches = static_cast<int32_t>(n), a.num_pages = static_cast<int32_t>(first->size(0));
+  a.page_size = static_cast<int32_t>(first->size(1)), a.kv_heads = static_cast<int32_t>(first->size(2));
+  a.dim = static_cast<int32_t>(first->size(3)), a.pairs = static_cast<int32_t>(src->size(0));
+  a.cache = at, a.strides = strides;
+  a.src = static_cast<const int32_t*>(src->data_ptr()), a.dst = static_cast<const int32_t*>(dst->data_ptr());
+  void* stream;
+  if (!stream_of(v[3], *src, &stream) || !call(g_copy_pages, a, stream)) return nullptr;
+  Py_RETURN_TRUE;
+}
+
+// The books: page_refs, page_table, kv_lens and a page's size.
+const at::Tensor* books(PyObject* const* v, PyObject* page_size, kaio_cache_args* a) {
+  const at::Tensor *refs = usable(v[0], 1), *table = usable(v[1], 2), *lens = usable(v[2], 1);
+  if (!refs || !table || !lens || refs->scalar_type() != at::kInt || table->scalar_type() != at::kInt ||
+      lens->scalar_type() != at::kInt || table->size(0) != lens->size(0) || !fits(refs->size(0)) || !fits(lens->size(0)) ||
+      !fits(table->size(1)) || !to_int(page_size, &a->page_size))
+    return nullptr;
+  a->struct_size = sizeof(*a);
+  a->batch = static_cast<int32_t>(lens->size(0)), a->max_pages = static_cast<int32_t>(table->size(1));
+  a->num_pages = static_cast<int32_t>(refs->size(0)), a->table_stride = table->stride(0);
+  a->page_refs = static_cast<int32_t*>(refs->data_ptr()), a->page_table = static_cast<int32_t*>(table->data_ptr());
+  a->kv_lens = static_cast<int32_t*>(lens->data_ptr());
+  return lens;
+}
+
+// (page_refs, page_table, kv_lens, parents or new_lens, page_size, stream)
+template <bool kFork>
+PyObject* fork_or_truncate(PyObject* const* v) {
+  kaio_cache_args a{};
+  const at::Tensor* lens = books(v, v[4], &a);
+  if (!lens) return nullptr;
+  const at::Tensor* rows = usable(v[3], at::kInt, lens->sizes());
+  void* stream;
+  if (!rows || !stream_of(v[5], *lens, &stream)) return nullptr;
+  (kFork ? a.parents : a.new_lens) = static_cast<const int32_t*>(rows->data_ptr());
+  if (!call(kFork ? g_fork : g_truncate, a, stream)) return nullptr;
+  Py_RETURN_TRUE;
+}
+
+PyObject* tuple_of(const at::Tensor* t, int n) {
+  PyObject* all = PyTuple_New(n);
+  for (int i = 0; all && i < n; ++i) {
+    PyObject* one = THPVariable_Wrap(t[i]);
+    if (!one) Py_CLEAR(all);
+    else PyTuple_SET_ITEM(all, i, one);
+  }
+  return all;
+}
+
+// (page_refs, page_table, kv_lens, q_starts, tokens, page_size, stream)
+PyObject* append(PyObject* const* v) {
+  kaio_cache_args a{};
+  const at::Tensor* lens = books(v, v[5], &a);
+  if (!lens || !to_int(v[4], &a.tokens) || a.tokens < 0) return nullptr;
+  if (v[3] != Py_None) {
+    const int64_t size[1] = {lens->size(0) + 1};
+    const at::Tensor* starts = usable(v[3], at::kInt, size);
+    if (!starts) return nullptr;
+    a.q_starts = static_cast<const int32_t*>(starts->data_ptr());
+  }
+  void* stream;
+  if (!stream_of(v[6], *lens, &stream)) return nullptr;
+  const int64_t size[1] = {a.tokens};
+  const at::Tensor made[3] = {new_tensor(size, lens->options(), v[6], stream),
+                              new_tensor(lens->sizes(), lens->options(), v[6], stream),
+                              new_tensor(lens->sizes(), lens->options(), v[6], stream)};
+  a.slots = static_cast<int32_t*>(made[0].data_ptr());
+  a.src = static_cast<int32_t*>(made[1].data_ptr()), a.dst = static_cast<int32_t*>(made[2].data_ptr());
+  return call(g_append, a, stream) ? tuple_of(made, 3) : nullptr;
+}
+
+// (page_refs, page_table, kv_lens, page_size, max_moves, stream)
+PyObject* compact(PyObject* const* v) {
+  kaio_cache_args a{};
+  const at::Tensor* lens = books(v, v[3], &a);
+  void* stream;
+  if (!lens || !to_int(v[4], &a.max_moves) || a.max_moves < 0 || !stream_of(v[5], *lens, &stream)) return nullptr;
+  const int64_t size[1] = {a.max_moves};
+  const at::Tensor made[2] = {new_tensor(size, lens->options(), v[5], stream),
+                              new_tensor(size, lens->options(), v[5], stream)};
+  a.src = static_cast<int32_t*>(made[0].data_ptr()), a.dst = static_cast<int32_t*>(made[1].data_ptr());
+  return call(g_compact, a, stream) ? tuple_of(made, 2) : nullptr;
 }
 
 template <PyObject* (*kCall)(PyObject* const*), Py_ssize_t kArgs>
@@ -300,13 +439,41 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+// The same of kaio_paged_attention_scored, kaio_cache_copy_pages, kaio_cache_fork,
+// kaio_cache_append, kaio_cache_truncate and kaio_cache_compact.
+PyObject* bind_more(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 6) {
+    PyErr_SetString(PyExc_TypeError, "bind_more takes six addresses");
+    return nullptr;
+  }
+  void* at[6];
+  for (int i = 0; i < 6; ++i) {
+    at[i] = PyLong_AsVoidPtr(args[i]);
+    if (PyErr_Occurred()) return nullptr;
+  }
+  g_paged_attention_scored = reinterpret_cast<decltype(g_paged_attention_scored)>(at[0]);
+  g_copy_pages = reinterpret_cast<decltype(g_copy_pages)>(at[1]);
+  g_fork = reinterpret_cast<decltype(g_fork)>(at[2]);
+  g_append = reinterpret_cast<decltype(g_append)>(at[3]);
+  g_truncate = reinterpret_cast<decltype(g_truncate)>(at[4]);
+  g_compact = reinterpret_cast<decltype(g_compact)>(at[5]);
+  Py_RETURN_NONE;
+}
+
 template <typename F> PyCFunction fast(F f) { return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)); }
 
 PyMethodDef g_methods[] = {
     {"bind", fast(bind), METH_FASTCALL, nullptr},
     {"rope", fast(entry<rope, 8>), METH_FASTCALL, nullptr},
     {"rope_append", fast(entry<rope_append, 12>), METH_FASTCALL, nullptr},
-    {"paged_attention", fast(entry<paged_attention, 16>), METH_FASTCALL, nullptr},
+    {"paged_attention", fast(entry<paged_attention<false>, 16>), METH_FASTCALL, nullptr},
+    {"bind_more", fast(bind_more), METH_FASTCALL, nullptr},
+    {"paged_attention_scored", fast(entry<paged_attention<true>, 20>), METH_FASTCALL, nullptr},
+    {"cache_copy_pages", fast(entry<copy_pages, 4>), METH_FASTCALL, nullptr},
+    {"cache_fork", fast(entry<fork_or_truncate<true>, 6>), METH_FASTCALL, nullptr},
+    {"cache_append", fast(entry<append, 7>), METH_FASTCALL, nullptr},
+    {"cache_truncate", fast(entry<fork_or_truncate<false>, 6>), METH_FASTCALL, nullptr},
+    {"cache_compact", fast(entry<compact, 6>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_host", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

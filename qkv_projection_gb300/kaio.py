@@ -495,6 +495,9 @@ def _host():
         else:
             module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                           for f in (L.kaio_rope, L.kaio_rope_append, L.kaio_paged_attention)))
+            module.bind_more(*(ctypes.cast(f, ctypes.c_void_p).value
+                               for f in (L.kaio_paged_attention_scored, L.kaio_cache_copy_pages, L.kaio_cache_fork,
+                                         L.kaio_cache_append, L.kaio_cache_truncate, L.kaio_cache_compact)))
             _host_module = module
     return _host_module
 
@@ -624,9 +627,14 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max
     """
     scored = not (softcap == 0 and slopes is None and prefix_lens is None and doc_starts is None)
     host = _host_module or _host()
-    if host and not scored:
-        done = host.paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts, max_new, scale, causal, window,
-                                    sinks, workspace, out, return_lse, lse, stream)
+    if host:
+        if scored:
+            done = host.paged_attention_scored(q, k_cache, v_cache, page_table, kv_lens, q_starts, max_new, scale, causal,
+                                               window, sinks, workspace, out, return_lse, lse, stream, softcap, slopes,
+                                               prefix_lens, doc_starts)
+        else:
+            done = host.paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts, max_new, scale, causal, window,
+                                        sinks, workspace, out, return_lse, lse, stream)
         if done is not None:
             return done
     torch = _torch()
@@ -701,6 +709,9 @@ def cache_copy_pages(caches, src, dst, stream=None):
     pairs with a page outside the cache (-1) are left out; no dst may be another pair's
     src or dst.
     """
+    host = _host_module or _host()
+    if host and host.cache_copy_pages(caches, src, dst, stream):
+        return
     torch = _torch()
     caches = list(caches)
     n = _size(src, "src", torch.int32, 1, 0)
@@ -749,7 +760,9 @@ def cache_fork(page_refs, page_table, kv_lens, parents, page_size: int, stream=N
     page_table int32 [B, P] and kv_lens int32 [B]; row b holds its first
     ceil(kv_lens[b] / page_size) places.
     """
-    _cache_call(lib().kaio_cache_fork, page_refs, page_table, kv_lens, page_size, stream, parents=parents)
+    host = _host_module or _host()
+    if not (host and host.cache_fork(page_refs, page_table, kv_lens, parents, page_size, stream)):
+        _cache_call(lib().kaio_cache_fork, page_refs, page_table, kv_lens, page_size, stream, parents=parents)
 
 
 def cache_append(page_refs, page_table, kv_lens, q_starts, tokens: int, page_size: int, stream=None):
@@ -762,6 +775,11 @@ def cache_append(page_refs, page_table, kv_lens, q_starts, tokens: int, page_siz
     A row that does not fit its places, or the pool behind the rows before it, takes nothing:
     its slots are -1 and its books stay. New results belong to ``stream`` (default: the current one).
     """
+    host = _host_module or _host()
+    if host:
+        done = host.cache_append(page_refs, page_table, kv_lens, q_starts, tokens, page_size, stream)
+        if done is not None:
+            return done
     int32 = _torch().int32
     batch = _size(kv_lens, "kv_lens", int32, 1, 0)
     tokens = _int32(tokens, "tokens")
@@ -775,13 +793,20 @@ def cache_append(page_refs, page_table, kv_lens, q_starts, tokens: int, page_siz
 def cache_truncate(page_refs, page_table, kv_lens, new_lens, page_size: int, stream=None):
     """Cuts row b of the books to new_lens[b] positions (int32 [B]) where it has more, and
     gives back the pages behind them; 0 frees the row."""
-    _cache_call(lib().kaio_cache_truncate, page_refs, page_table, kv_lens, page_size, stream, new_lens=new_lens)
+    host = _host_module or _host()
+    if not (host and host.cache_truncate(page_refs, page_table, kv_lens, new_lens, page_size, stream)):
+        _cache_call(lib().kaio_cache_truncate, page_refs, page_table, kv_lens, page_size, stream, new_lens=new_lens)
 
 
 def cache_compact(page_refs, page_table, kv_lens, page_size: int, max_moves: int, stream=None):
     """Moves the highest used pages to the lowest free ones, up to ``max_moves``: renumbers the
     books and returns (src, dst), int32 [max_moves] filled up with -1, to be copied with
     ``cache_copy_pages``. New results belong to ``stream`` (default: the current one)."""
+    host = _host_module or _host()
+    if host:
+        done = host.cache_compact(page_refs, page_table, kv_lens, page_size, max_moves, stream)
+        if done is not None:
+            return done
     int32 = _torch().int32
     max_moves = _int32(max_moves, "max_moves")
     device = getattr(kv_lens, "device", None)
