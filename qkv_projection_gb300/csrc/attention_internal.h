@@ -101,8 +101,11 @@ cudaError_t launch_paged_chunk(FloatType t, const PagedParams& p, void* workspac
                                unsigned long long wait_ns);
 cudaError_t launch_paged_chunk_scored(FloatType t, const PagedParams& p, void* workspace, int num_sms,
                                       cudaStream_t stream);
+cudaError_t launch_paged_chunk_distance(FloatType t, const PagedParams& p, void* workspace, int num_sms,
+                                        cudaStream_t stream);
 unsigned read_and_clear_chunk_errors();
-unsigned read_and_clear_chunk_scored_errors();
+unsigned read_and_clear_chunk_scored_errors();       // (of both)
+unsigned read_and_clear_chunk_distance_errors();
 
 // A launch that may begin while the kernel before it in the stream still runs
 // (programmatic dependent launch): the kernel waits for it (grid_dependency_wait)

@@ -130,12 +130,13 @@ __global__ void __launch_bounds__(kCutThreads) cache_truncate_kernel(const __gri
 }
 
 // ------------------------------------------- one cluster over the whole pool
-constexpr int kCtas = 16, kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kMaxCtas = 16, kThreads = 1024, kWarps = kThreads / 32;
+__device__ __forceinline__ int cluster_ctas() { return static_cast<int>(gridDim.x); }
 
 // Pages [first, first + 32 words) belong to one warp; which of them are free is kept in shared
 // memory, a bit each, and `before` becomes how many free ones lie before the warp's.
 struct Pool {
-  int words;            // of 32 pages, for each warp
+  int words;            // of 32 pages
   int first;
   uint32_t* mask;       // this warp's
   int before, free;     // before this warp's pages; in the whole pool
@@ -158,23 +159,24 @@ __device__ __forceinline__ int remote(const int* p, int cta) {
   return v;
 }
 
-// First half: counts this warp's free pages (the loads of 8 words in flight).
+// First half: counts this warp's free pages (the loads of 16 words in flight).
 __device__ __forceinline__ void pool_count(const CacheParams& p, Pool& pool, uint32_t* masks, PoolShared& sh) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, of_all = cluster_ctarank() * kWarps + warp;
-  pool.words = (p.num_pages + 32 * kCtas * kWarps - 1) / (32 * kCtas * kWarps);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, of_all = static_cast<int>(cluster_ctarank()) * kWarps + warp;
+  constexpr int kLoads = 16;
+  pool.words = p.warp_words;
   pool.first = of_all * pool.words * 32;
   pool.mask = masks + warp * pool.words;
   int count = 0;
 #pragma unroll 1
-  for (int w = 0; w < pool.words; w += 8) {
-    int refs[8];
+  for (int w = 0; w < pool.words; w += kLoads) {
+    int refs[kLoads];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kLoads; ++k) {
       const int id = pool.first + 32 * (w + k) + lane;
       refs[k] = w + k < pool.words && id < p.num_pages ? p.page_refs[id] : 1;
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kLoads; ++k) {
       const uint32_t free = __ballot_sync(0xFFFFFFFFu, refs[k] <= 0);
       count += __popc(free);
       if (lane == 0 && w + k < pool.words) pool.mask[w + k] = free;
@@ -190,7 +192,7 @@ __device__ __forceinline__ void pool_count(const CacheParams& p, Pool& pool, uin
 // Second half, after the cluster has met.
 __device__ __forceinline__ void pool_places(Pool& pool, const PoolShared& sh) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = static_cast<int>(cluster_ctarank());
-  const int of_cta = lane < kCtas ? remote(&sh.cta_free, lane) : 0;
+  const int of_cta = lane < cluster_ctas() ? remote(&sh.cta_free, lane) : 0;
   pool.free = __reduce_add_sync(0xFFFFFFFFu, of_cta);
   pool.before = __reduce_add_sync(0xFFFFFFFFu, (lane < cta ? of_cta : 0) + (lane < warp ? sh.warp_free[lane] : 0));
 }
@@ -251,14 +253,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_append_kernel(const __grid_
   meet();                                        // all counts, nothing given out yet
   pool_places(pool, sh);
   const int of_warp = warp_need[lane];
-  const int needed = __reduce_add_sync(0xFFFFFFFFu, of_warp);
+  const int all_need = __reduce_add_sync(0xFFFFFFFFu, of_warp);
+  const int needed = min(all_need, p.tokens);                // (no more, unless q_starts decreases)
   int at = upto - mine + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? of_warp : 0);
   for (int row = row0; row < row1; ++row) {
     const int need = before[row];
     before[row] = at;
     at += need;
   }
-  if (tid == 0) before[p.batch] = needed;
+  if (tid == 0) before[p.batch] = all_need;
   __syncthreads();
   auto granted = [&](int row, const AppendRow& r) {
     return r.fits && (before[row + 1] == before[row] || before[row + 1] <= pool.free);
@@ -274,13 +277,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_append_kernel(const __grid_
     }
     return lo;
   };
+  // The pages to give out, in their order, stand where the slots will: a row needs no more
+  // pages than it has new tokens. (Few warps hold them all, so they only list them.)
   int rank0 = pool.before;
   for (int w = 0; w < pool.words && rank0 < needed; ++w) {
     const uint32_t free = pool.mask[w];
     const int rank = rank0 + __popc(free & ((1u << lane) - 1));
     rank0 += __popc(free);
-    if (!(free >> lane & 1) || rank >= needed) continue;
-    const int id = pool.first + 32 * w + lane, row = find(before, rank);
+    if ((free >> lane & 1) && rank < needed) p.slots[rank] = pool.first + 32 * w + lane;
+  }
+  meet();
+  const int step = cluster_ctas() * kThreads;
+  for (int rank = cta * kThreads + tid; rank < min(needed, pool.free); rank += step) {
+    const int id = p.slots[rank], row = find(before, rank);
     const AppendRow r = row_at(row);
     if (!granted(row, r)) continue;
     const int tail = before[row + 1] - before[row] - (r.want - r.have), k = rank - before[row];
@@ -300,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_append_kernel(const __grid_
       if (granted(row, r)) p.kv_lens[row] = r.old + r.n;
     }
   }
-  for (int t = cta * kThreads + tid; t < p.tokens; t += kCtas * kThreads) {
+  for (int t = cta * kThreads + tid; t < p.tokens; t += step) {
     const int row = find(starts, t);
     const AppendRow r = row_at(row);
     int slot = -1;
@@ -314,17 +323,20 @@ __global__ void __launch_bounds__(kThreads, 1) cache_append_kernel(const __grid_
 }
 
 // Of the U used pages those at U and above move to the free ones below U: the i-th highest of
-// them to the i-th lowest of those, up to max_moves.
+// them to the i-th lowest of those, up to max_moves. Until the table is renumbered, a moved page's
+// count says where it went (kGone + its new place), so that a place needs one look.
+constexpr int kGone = INT32_MIN;
+
 __global__ void __launch_bounds__(kThreads, 1) cache_compact_kernel(const __grid_constant__ CacheParams p) {
   extern __shared__ uint32_t masks[];
   __shared__ PoolShared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = static_cast<int>(cluster_ctarank());
-  constexpr int kAll = kCtas * kThreads;
+  const int all = cluster_ctas() * kThreads;
   allow_dependents_launch();
   grid_dependency_wait();
   Pool pool;
   pool_count(p, pool, masks, sh);
-  for (int i = cta * kThreads + tid; i < p.max_moves; i += kAll) p.src[i] = p.dst[i] = -1;
+  for (int i = cta * kThreads + tid; i < p.max_moves; i += all) p.src[i] = p.dst[i] = -1;
   meet();
   pool_places(pool, sh);
   const int used = p.num_pages - pool.free;
@@ -342,65 +354,72 @@ __global__ void __launch_bounds__(kThreads, 1) cache_compact_kernel(const __grid
       if (from_top < p.max_moves) p.src[from_top] = id;
     }
   }
-  meet();                                        // both lists are whole
+  meet();                                                    // both lists are whole
   const int owner = used < p.num_pages ? used / (32 * kWarps * pool.words) : -1;
   const int moves = owner < 0 ? 0 : min(remote(&sh.below, owner), p.max_moves);
-  meet();                                        // (no CTA leaves before it was read)
-  if (moves == 0) return;
-  for (int i = cta * kThreads + tid; i < moves; i += kAll) {
-    const int from = p.src[i];
-    p.page_refs[p.dst[i]] = p.page_refs[from];
-    p.page_refs[from] = 0;
+  for (int i = cta * kThreads + tid; i < moves; i += all) {
+    const int from = p.src[i], to = p.dst[i];
+    p.page_refs[to] = p.page_refs[from];
+    p.page_refs[from] = kGone + to;
   }
-  // The list descends, so a place finds its page in it by halving.
-  const int lowest = p.src[moves - 1];
-  const int chunks = (p.max_pages + 127) / 128;
-  for (long long c = cta * kWarps + warp; c < static_cast<long long>(p.batch) * chunks; c += kCtas * kWarps) {
-    const int row = static_cast<int>(c / chunks), col = static_cast<int>(c - static_cast<long long>(row) * chunks) * 128;
-    const int end = places(p, p.kv_lens[row]);
-    if (col >= end) continue;
-    int* entry = p.page_table + row * p.table_stride + col + lane;
-    int id[4];
+  meet();
+  if (moves > 0) {
+    constexpr int kEach = 8;                                 // entries of a lane in flight
+    const int lowest = p.src[moves - 1], chunks = (p.max_pages + 32 * kEach - 1) / (32 * kEach);
+    for (int c = cta * kWarps + warp; c < p.batch * chunks; c += cluster_ctas() * kWarps) {
+      const int row = c / chunks, col = (c - row * chunks) * 32 * kEach + lane;
+      const int end = places(p, p.kv_lens[row]);
+      int* entry = p.page_table + row * p.table_stride + col;
+      int id[kEach], to[kEach];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) id[k] = col + 32 * k + lane < end ? entry[32 * k] : -1;
+      for (int k = 0; k < kEach; ++k) id[k] = col + 32 * k < end ? entry[32 * k] : -1;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (id[k] < lowest) continue;
-      int lo = 0, hi = moves - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (p.src[mid] <= id[k]) hi = mid;
-        else lo = mid + 1;
-      }
-      if (p.src[lo] == id[k]) entry[32 * k] = p.dst[lo];
+      for (int k = 0; k < kEach; ++k) to[k] = id[k] >= lowest && id[k] < p.num_pages ? p.page_refs[id[k]] : 0;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k)
+        if (to[k] < kGone + p.num_pages) entry[32 * k] = to[k] - kGone;
     }
   }
+  meet();
+  for (int i = cta * kThreads + tid; i < moves; i += all) p.page_refs[p.src[i]] = 0;
 }
 
-// A launch of one cluster of kCtas CTAs.
-template <typename Kernel>
-cudaError_t launch_cluster(Kernel kernel, const CacheParams& p, size_t smem, cudaStream_t stream) {
-  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), kCacheSmem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+// A launch of one cluster.
+template <void (*kKernel)(CacheParams)>
+cudaError_t launch_cluster(CacheParams p, int ctas, size_t smem, cudaStream_t stream) {
+  // (set once for a device; 16 CTAs are more than every device of the architecture takes)
+  thread_local uint64_t allowed = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev >= 64 || !(allowed >> dev & 1))) {
+    e = ensure_smem_limit(reinterpret_cast<const void*>(kKernel), kCacheSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && dev < 64) allowed |= 1ull << dev;
+  }
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kCtas);
+  const int per = 32 * ctas * kWarps;
+  p.warp_words = (p.num_pages + per - 1) / per;              // of 32 pages
+  smem += static_cast<size_t>(p.warp_words) * kWarps * 4;
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kCtas, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ctas), attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cudaLaunchKernelEx(&cfg, kKernel, p);
 }
 
-size_t mask_bytes(const CacheParams& p) {
-  const int per = 32 * kCtas * kWarps;
-  return static_cast<size_t>((p.num_pages + per - 1) / per) * kWarps * 4;
+// How many CTAs share `pieces` of work of which a CTA takes `each` at a time.
+int ctas_for(long long pieces, int each) {
+  int ctas = 1;
+  while (ctas < kMaxCtas && pieces > static_cast<long long>(ctas) * each) ctas *= 2;
+  return ctas;
 }
 
 }  // namespace
@@ -427,7 +446,8 @@ cudaError_t launch_cache_fork(const CacheParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_cache_append(const CacheParams& p, cudaStream_t stream) {
-  return launch_cluster(cache_append_kernel, p, mask_bytes(p) + (3 * static_cast<size_t>(p.batch) + 2) * 4, stream);
+  const int ctas = ctas_for(std::max(p.num_pages / 4, p.tokens), kThreads);
+  return launch_cluster<cache_append_kernel>(p, ctas, (3 * static_cast<size_t>(p.batch) + 2) * 4, stream);
 }
 
 cudaError_t launch_cache_truncate(const CacheParams& p, cudaStream_t stream) {
@@ -435,7 +455,8 @@ cudaError_t launch_cache_truncate(const CacheParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_cache_compact(const CacheParams& p, cudaStream_t stream) {
-  return launch_cluster(cache_compact_kernel, p, mask_bytes(p), stream);
+  const int ctas = ctas_for(std::max<long long>(p.num_pages, static_cast<long long>(p.batch) * p.max_pages) / 4, kThreads);
+  return launch_cluster<cache_compact_kernel>(p, ctas, 0, stream);
 }
 
 }  // namespace kaio

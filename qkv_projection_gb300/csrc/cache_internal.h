@@ -39,6 +39,7 @@ struct CacheParams {
   int batch, max_pages, num_pages, page_size;
   int tokens, max_moves;
   FastDiv page_div;
+  int warp_words;       // set by the launch: words of 32 pages that a warp looks after
 };
 cudaError_t launch_cache_fork(const CacheParams& p, cudaStream_t stream);
 cudaError_t launch_cache_append(const CacheParams& p, cudaStream_t stream);

@@ -66,6 +66,8 @@ struct PagedSpan {
   int from, first, lo, hi;   // (an empty [from, first) is [0, 0))
   int lo_tile, run;    // the run's first tile, and its tiles
   int units;           // at least 1, so that every item is visited
+  bool nearest_first;  // (scored) scores lose with distance: the run's tiles in reverse, or every tile would raise the maximum
+  __device__ __forceinline__ bool back() const { return kScored && nearest_first; }
   __device__ __forceinline__ PagedSpan(const PagedParams& p, const PagedSeq& s, int r0, int r1, int doc) {
     const int t0 = p.group_div.div(r0), t1 = p.group_div.div(r1 - 1);
     hi = p.causal ? min(max(s.kv - s.n + t1 + 1, 0), s.kv) : s.kv;
@@ -79,13 +81,16 @@ struct PagedSpan {
       else first = 0;
       if (lo == hi && first == 0) lo = hi = 0;
     }
+    nearest_first = kScored && p.slopes != nullptr;
     lo_tile = lo / kKeys;
     run = (hi + kKeys - 1) / kKeys - lo_tile;
     units = max(1, run + max(min((first + kKeys - 1) / kKeys, lo_tile) - from / kKeys, 0));
   }
   __device__ __forceinline__ int key0(int unit) const {
     int tile = unit + lo_tile;
-    if (lo > 0) {
+    if (back()) {
+      tile = unit < run ? lo_tile + run - 1 - unit : unit - run + from / kKeys;
+    } else if (lo > 0) {
       if (unit >= run) tile = unit - run + (kScored ? from / kKeys : 0);
       else tile = unit + 1 < run ? tile + 1 : lo_tile;
     }

@@ -9,7 +9,7 @@ size_t paged_chunk_workspace_bytes(int num_sms) {
 
 cudaError_t launch_paged_chunk(FloatType t, const PagedParams& p, void* workspace, int num_sms, cudaStream_t stream,
                                unsigned long long wait_ns) {
-  return launch_chunk<false>(t, p, workspace, num_sms, stream, wait_ns);
+  return launch_chunk<Form::kPlain>(t, p, workspace, num_sms, stream, wait_ns);
 }
 
 unsigned read_and_clear_chunk_errors() { return read_and_clear_errors(); }

@@ -69,6 +69,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "paged_attention.cuh"
 
@@ -264,12 +265,18 @@ struct ChunkParams {
   unsigned long long wait_ns;         // limit of a wait; used where kLimited
 };
 
-// kScored: with capped scores, slopes, prefixes and documents. kLimited: waits are limited to
-// wait_ns (a test of the path that gives up).
-template <typename T, int kDim, bool kScored, bool kLimited>
+// What the scores and masks are: kPlain has no prefixes and documents, the others do. Each
+// is a kernel of its own, since the loop over a row's scores leaves no register to spare.
+enum class Form : int { kPlain, kMasks, kCapped, kDistance, kCappedDistance };
+
+// kLimited: waits are limited to wait_ns (a test of the path that gives up).
+template <typename T, int kDim, Form kForm, bool kLimited>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                        const __grid_constant__ ChunkParams cp) {
+  constexpr bool kScored = kForm != Form::kPlain;
+  constexpr bool kCapped = kForm == Form::kCapped || kForm == Form::kCappedDistance;
+  constexpr bool kDistance = kForm == Form::kDistance || kForm == Form::kCappedDistance;
   using S = Shape<kDim>;
   using Walk = PagedWalk<Work<kScored>>;
   using Span = typename Walk::Span;
@@ -387,10 +394,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int h0 = row0 + (rows > kHalf ? kHalf * half : 0), h1 = min(h0 + kHalf, row0 + rows) - 1;
               const Row top(p, w.s, h0, 0), bottom(p, w.s, h1, paged_doc<kScored>(p, w.s, h1));
               const int all_hi = top.hi, all_lo = max(bottom.lo, bottom.from);
-              // tiles [t0, t1) are seen whole; in units, the run's first tile comes last
+              // tiles [t0, t1) are seen whole; in units, the run's first tile comes last (or all in reverse)
               const int t0 = (all_lo + kKeys - 1) / kKeys - span.lo_tile, t1 = min(all_hi / kKeys - span.lo_tile, span.run);
-              job.plain0[half] = span.lo > 0 ? max(t0, 1) - 1 : t0;
-              job.plain1[half] = span.lo > 0 ? t1 - 1 : t1;
+              job.plain0[half] = span.back() ? span.run - t1 : span.lo > 0 ? max(t0, 1) - 1 : t0;
+              job.plain1[half] = span.back() ? span.run - t0 : span.lo > 0 ? t1 - 1 : t1;
             }
             if (job.split) {
               job.c0 = w.first_owner(ctl.share);
@@ -613,9 +620,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // positive: a negative one turns Q's signs, a zero makes Q zero.
     // (Scored: of what the passes over the scores below leave in their place.)
     const float raw_scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
-    const bool cap = kScored && p.cap_in != 0.f, distance = kScored && p.slopes != nullptr;
-    const float cap_scale = cap ? 2.f * p.cap_log2 : raw_scale;
-    const float scale = distance ? 1.f : cap_scale;
+    const float cap_scale = kCapped ? 2.f * p.cap_log2 : raw_scale;
+    const float scale = kDistance ? 1.f : cap_scale;
+    const float most = kCapped ? kCapRange / p.cap_in : 0.f;
     // What a row's scores, times the scale, get added as exponents of its weights. Rounded
     // down, so that no weight is above 2^(kLazy + kShift) at any size of the reference.
     constexpr int kShift = Type<T>::kShift;
@@ -698,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kScored) {
         const int r = w.row0 + min(my_row, rows - 1);
         doc = paged_doc<kScored>(p, w.s, r);
-        if (distance) slope = p.slopes[w.h * p.group + r - p.group_div.div(r) * p.group] * kLog2e;
+        if (kDistance) slope = p.slopes[w.h * p.group + r - p.group_div.div(r) * p.group] * kLog2e;
       }
       if (works(mode)) {
         if (!q_sent) {
@@ -721,70 +728,80 @@ __global__ void __launch_bounds__(kThreads, 1)
             q_next = ok && works(nx.mode);
             if (q_next) fetch_q(nx);
           }
+          // Of 32 keys from `at` on: bits of those that this row sees, and the others' scores to -inf.
+          const bool masked = u < plain0 || u >= plain1;
+          auto hide = [&](const Row& vis, int at, uint32_t (&x)[32]) {
+            auto below = [&](int x) { return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1; };
+            uint32_t seen = below(vis.hi - at) & (~below(vis.lo - at) | below(vis.first - at));
+            if (kScored) seen &= ~below(vis.from - at);
+            if (__all_sync(0xFFFFFFFFu, seen == 0xFFFFFFFFu)) return;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(seen >> e & 1)) x[e] = __float_as_uint(kNegInf);
+          };
+          auto row_here = [&] { return Row(p, w.s, w.row0 + min(my_row, rows - 1), doc); };
           uint32_t s[4][32];
 #pragma unroll
           for (int i = 0; i < 4; ++i) tmem_ld32(s_tmem + 32 * i, s[i]);
           tmem_ld_wait();
-          // Bits of the visible ones of these 32 keys.
-          const bool masked = u < plain0 || u >= plain1;
-          auto hide = [&] {
-            const Row vis(p, w.s, w.row0 + min(my_row, rows - 1), doc);
-            const int k0 = w.span.key0(u);
+          const int key0 = w.span.key0(u);
+          auto hide_all = [&] {
+            const Row vis = row_here();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int at = k0 + 32 * i;
-              auto below = [&](int x) { return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1; };
-              uint32_t seen = below(vis.hi - at) & (~below(vis.lo - at) | below(vis.first - at));
-              if (kScored) seen &= ~below(vis.from - at);
-              if (__all_sync(0xFFFFFFFFu, seen == 0xFFFFFFFFu)) continue;
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(seen >> e & 1)) s[i][e] = __float_as_uint(kNegInf);
-            }
+            for (int i = 0; i < 4; ++i) hide(vis, key0 + 32 * i, s[i]);
           };
           auto top_of = [&] {
             float top8[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) top8[i] = fmaxf(__uint_as_float(s[0][2 * i]), __uint_as_float(s[0][2 * i + 1]));
 #pragma unroll
-            for (int i = 8; i < 64; ++i)
+            for (int i = 8; i < 16 * 4; ++i)
               top8[i & 7] = max3(top8[i & 7], __uint_as_float(s[i >> 4][2 * i & 31]), __uint_as_float(s[i >> 4][(2 * i & 31) + 1]));
             return fmaxf(max3(top8[0], top8[1], top8[2]), max3(max3(top8[3], top8[4], top8[5]), top8[6], top8[7]));
           };
-          if (masked) hide();
-          if (cap) {
-            if (__any_sync(0xFFFFFFFFu, top_of() * p.cap_in > kCapRange)) {
-              const float most = kCapRange / p.cap_in;
+          if (masked) hide_all();
+          float top = kNegInf;
+          if constexpr (kCapped) {
+            // (the largest result is that of the largest score)
+            top = top_of();
+            if (__any_sync(0xFFFFFFFFu, top > most)) {
+              top = fminf(top, most);
 #pragma unroll
-              for (int e = 0; e < 128; ++e) s[e >> 5][e & 31] = __float_as_uint(min_nan(__uint_as_float(s[e >> 5][e & 31]), most));
+              for (int e = 0; e < 32 * 4; ++e)
+                s[e >> 5][e & 31] = __float_as_uint(min_nan(__uint_as_float(s[e >> 5][e & 31]), most));
             }
+            if (kForm == Form::kCapped && top != kNegInf) top = -rcp_fast(1.f + exp2_fast(top * p.cap_in));
+            if constexpr (kDistance) {
 #pragma unroll
-            for (int e = 0; e < 128; e += 4) cap4(&s[e >> 5][e & 31], p.cap_in);
-            if (masked) hide();                            // (what was hidden before came out as -1)
+              for (int e = 0; e < 128; e += 4) cap4(&s[e >> 5][e & 31], p.cap_in);
+              if (masked) hide_all();                      // (what was hidden before came out as -1)
+            }
           }
-          if (distance) {
-            const int first_key = w.span.key0(u) - (w.s.kv - w.s.n + p.group_div.div(w.row0 + min(my_row, rows - 1)));
+          if constexpr (kDistance) {
+            const int first_key = key0 - (w.s.kv - w.s.n + p.group_div.div(w.row0 + min(my_row, rows - 1)));
+            if (__all_sync(0xFFFFFFFFu, first_key <= -127)) {      // left of it the bias grows evenly with the key
+              const uint64_t scale2 = pair(cap_scale, cap_scale), step2 = pair(4.f * slope, 4.f * slope);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int at = first_key + 32 * i;           // of the 32 keys, relative to the row's own position
-              const float base = static_cast<float>(at);
-              if (__all_sync(0xFFFFFFFFu, at <= -31)) {
-                const uint64_t scale2 = pair(cap_scale, cap_scale), step2 = pair(2.f * slope, 2.f * slope);
-                uint64_t lin2 = pair(slope * base, slope * (base + 1.f));
+              for (int i = 0; i < 4; ++i) {
+                const float base = static_cast<float>(first_key + 32 * i);
+                uint64_t bias2[2] = {pair(slope * base, slope * (base + 1.f)), pair(slope * (base + 2.f), slope * (base + 3.f))};
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                  const float2 x = unpair(fma2(pair(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])), scale2, lin2));
+                  uint64_t& b = bias2[e >> 1 & 1];
+                  const float2 x = unpair(fma2(pair(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])), scale2, b));
                   s[i][e] = __float_as_uint(x.x), s[i][e + 1] = __float_as_uint(x.y);
-                  lin2 = add2(lin2, step2);
+                  if (e < 28) b = add2(b, step2);
                 }
-              } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  s[i][e] = __float_as_uint(fmaf(__uint_as_float(s[i][e]), cap_scale, -slope * fabsf(base + e)));
               }
+            } else {
+              const float base = static_cast<float>(first_key);
+#pragma unroll
+              for (int e = 0; e < 128; ++e)
+                s[e >> 5][e & 31] =
+                    __float_as_uint(fmaf(__uint_as_float(s[e >> 5][e & 31]), cap_scale, -slope * fabsf(base + e)));
             }
           }
-          const float top = top_of();
+          if constexpr (kForm != Form::kCapped) top = top_of();
           // (the first finite maximum after none needs no rescaling: O and l are zero)
           const bool renew = top > m && (m == kNegInf || (top - m) * scale > kLazy);
           if (__any_sync(0xFFFFFFFFu, renew)) {
@@ -812,22 +829,87 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float add = addend(m);
           const uint64_t scale2 = pair(scale, scale), addend2 = pair(add, add);
           uint64_t sum2[2] = {};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          auto give = [&](int of) {                        // 64 keys of P are complete
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0 && ok) mbar_arrive(&ctl.p_full[half][of]);
+          };
+          if (kForm == Form::kCapped && !masked) {
+            // Sixteen scores a step, four steps in work at a time: what one waits for (the exponentials,
+            // the reciprocal) the others' work covers.
+            constexpr int kSteps = 8;
+            uint64_t both[2][4];
+            float inv[2][4];
             uint32_t packed[16];
+            auto at = [&](int e) -> uint32_t& { return s[e >> 5][e & 31]; };
+            auto get = [&](int e) { return pair(__uint_as_float(at(e)), __uint_as_float(at(e + 1))); };
+            auto set = [&](int e, uint64_t v) {
+              const float2 x = unpair(v);
+              at(e) = __float_as_uint(x.x), at(e + 1) = __float_as_uint(x.y);
+            };
+            const uint64_t c2 = pair(p.cap_in, p.cap_in), minus1 = pair(-1.f, -1.f);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 x = unpair(fma2(pair(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])), scale2, addend2));
-              const float a = exp2_fast(x.x), b = exp2_fast(x.y);
-              sum2[i & 1] = add2(sum2[i & 1], pair(a, b));
-              packed[e >> 1] = Type<T>::pack(a, b);
+            for (int b = 0; b < kSteps + 3; ++b) {
+              if (b < kSteps) {
+#pragma unroll
+                for (int e = 16 * b; e < 16 * b + 16; e += 2) {
+                  const float2 y = unpair(mul2(get(e), c2));
+                  set(e, pair(exp2_fast(y.x), exp2_fast(y.y)));
+                }
+              }
+              if (b >= 1 && b < kSteps + 1) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int e = 16 * (b - 1) + 4 * k;
+                  set(e, fma2(get(e), minus1, minus1));
+                  set(e + 2, fma2(get(e + 2), minus1, minus1));
+                  both[(b - 1) & 1][k] = mul2(get(e), get(e + 2));
+                  const float2 x = unpair(both[(b - 1) & 1][k]);
+                  inv[(b - 1) & 1][k] = rcp_fast(x.x * x.y);
+                }
+              }
+              if (b >= 2 && b < kSteps + 2) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int e = 16 * (b - 2) + 4 * k;
+                  const float2 x = unpair(both[b & 1][k]);
+                  const float r = inv[b & 1][k];
+                  const uint64_t of_both = pair(r * x.y, r * x.x), first = get(e);
+                  set(e, fma2(mul2(of_both, get(e + 2)), scale2, addend2));
+                  set(e + 2, fma2(mul2(of_both, first), scale2, addend2));
+                }
+              }
+              if (b >= 3) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const int e = 16 * (b - 3) + 2 * k;
+                  const float x = exp2_fast(__uint_as_float(at(e))), y = exp2_fast(__uint_as_float(at(e + 1)));
+                  sum2[b & 1] = add2(sum2[b & 1], pair(x, y));
+                  packed[8 * ((b - 3) & 1) + k] = Type<T>::pack(x, y);
+                }
+                if ((b - 3) & 1) tmem_st16(s_tmem + 16 * ((b - 3) >> 1), packed);
+                if (((b - 3) & 3) == 3) give((b - 3) >> 2);
+              }
             }
-            tmem_st16(s_tmem + 16 * i, packed);
-            if (i & 1) {                                   // 64 keys of P are complete
-              tmem_st_wait();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0 && ok) mbar_arrive(&ctl.p_full[half][i >> 1]);
+          } else {
+            if constexpr (kForm == Form::kCapped) {
+#pragma unroll
+              for (int e = 0; e < 128; e += 4) cap4(&s[e >> 5][e & 31], p.cap_in);
+              hide_all();                                  // (what was hidden before came out as -1)
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t packed[16];
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float2 x = unpair(fma2(pair(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])), scale2, addend2));
+                const float a = exp2_fast(x.x), b = exp2_fast(x.y);
+                sum2[i & 1] = add2(sum2[i & 1], pair(a, b));
+                packed[e >> 1] = Type<T>::pack(a, b);
+              }
+              tmem_st16(s_tmem + 16 * i, packed);
+              if (i & 1) give(i >> 1);
             }
           }
           const float2 sa = unpair(sum2[0]), sb = unpair(sum2[1]);
@@ -840,7 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Results of this thread's row: O / l and reference + log2 l (nothing seen: zeros, -inf).
       const bool none = l == 0.f;                          // (a NaN score leaves l NaN)
       float lse2 = none ? kNegInf : (kShift - addend(m)) + log2f(l * (1.f / (1 << kShift)));
-      if (cap) lse2 += p.cap_log2;                         // (left out of every score)
+      if (kCapped) lse2 += p.cap_log2;                         // (left out of every score)
       float mul = none ? 0.f : 1.f / l, mul_other = 0.f;
       const bool paired = mode == Mode::kPair, split = w.split;
       const bool real = mine && my_row < rows;
@@ -1149,16 +1231,16 @@ cudaError_t encode_cache(CUtensorMap* map, int* heads_first, const void* base, F
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <typename T, int kDim, bool kScored, bool kLimited = false>
+template <typename T, int kDim, Form kForm, bool kLimited = false>
 cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const ChunkParams& cp, int ctas, cudaStream_t stream) {
-  constexpr int kBytes = kSmem<kDim, kScored>;
+  constexpr int kBytes = kSmem<kDim, kForm != Form::kPlain>;
   const cudaError_t e =
-      ensure_smem_limit(reinterpret_cast<const void*>(paged_chunk_kernel<T, kDim, kScored, kLimited>), kBytes);
+      ensure_smem_limit(reinterpret_cast<const void*>(paged_chunk_kernel<T, kDim, kForm, kLimited>), kBytes);
   if (e != cudaSuccess) return e;
-  return launch_dependent(paged_chunk_kernel<T, kDim, kScored, kLimited>, ctas, kThreads, kBytes, stream, km, vm, cp);
+  return launch_dependent(paged_chunk_kernel<T, kDim, kForm, kLimited>, ctas, kThreads, kBytes, stream, km, vm, cp);
 }
 
-template <bool kScored>
+template <Form kForm>
 cudaError_t launch_chunk(FloatType t, const PagedParams& params, void* workspace, int num_sms, cudaStream_t stream,
                          unsigned long long wait_ns) {
   ChunkParams cp{};
@@ -1177,16 +1259,16 @@ cudaError_t launch_chunk(FloatType t, const PagedParams& params, void* workspace
   cudaError_t e = encode_cache(&km, &cp.k_heads_first, p.kc, t, p, p.k_ps, p.k_ss, p.k_hs);
   if (e == cudaSuccess) e = encode_cache(&vm, &cp.v_heads_first, p.vc, t, p, p.v_ps, p.v_ss, p.v_hs);
   if (e != cudaSuccess) return e;
-  if constexpr (!kScored) {
+  if constexpr (kForm == Form::kPlain) {
     if (wait_ns != kOwnWaitLimit)
-      return paged_chunk_limit_ok(t, p.dim) ? launch<__half, 128, false, true>(km, vm, cp, ctas, stream)
+      return paged_chunk_limit_ok(t, p.dim) ? launch<__half, 128, Form::kPlain, true>(km, vm, cp, ctas, stream)
                                             : cudaErrorNotSupported;
   }
   if (t == FloatType::BF16)
-    return p.dim <= 64 ? launch<__nv_bfloat16, 64, kScored>(km, vm, cp, ctas, stream)
-                       : launch<__nv_bfloat16, 128, kScored>(km, vm, cp, ctas, stream);
-  return p.dim <= 64 ? launch<__half, 64, kScored>(km, vm, cp, ctas, stream)
-                     : launch<__half, 128, kScored>(km, vm, cp, ctas, stream);
+    return p.dim <= 64 ? launch<__nv_bfloat16, 64, kForm>(km, vm, cp, ctas, stream)
+                       : launch<__nv_bfloat16, 128, kForm>(km, vm, cp, ctas, stream);
+  return p.dim <= 64 ? launch<__half, 64, kForm>(km, vm, cp, ctas, stream)
+                     : launch<__half, 128, kForm>(km, vm, cp, ctas, stream);
 }
 
 unsigned read_and_clear_errors() {
