@@ -63,25 +63,36 @@ __device__ __forceinline__ int places(const CacheParams& p, int len) {
 }
 __device__ __forceinline__ bool is_page(const CacheParams& p, int id) { return id >= 0 && id < p.num_pages; }
 
-// Row b becomes a copy of row parents[b], all at once: a CTA takes `cols` columns of all rows,
+// Row b becomes a copy of row parents[b], all at once: a CTA takes a few columns of all rows,
 // whose entries it reads before it writes any. References change only where a place does, so
 // what parent and row share already costs nothing.
 constexpr int kForkThreads = 512;
 constexpr int kNotHeld = INT32_MIN;
 
 __global__ void __launch_bounds__(kForkThreads) cache_fork_kernel(const __grid_constant__ CacheParams p, int cols_log2) {
-  extern __shared__ int tile[];                              // [batch][cols]
+  extern __shared__ int smem[];
+  int* held = smem;                                          // [batch] places
+  int* parents = held + p.batch;                             // [batch] -1: the row stays
+  int* tile = parents + p.batch;                             // [batch][cols]
+  const int cols = 1 << cols_log2, col0 = blockIdx.x * cols, n = p.batch * cols;
   allow_dependents_launch();
   grid_dependency_wait();
-  const int cols = 1 << cols_log2, col0 = blockIdx.x * cols, n = p.batch * cols;
-  for (int i = threadIdx.x; i < n; i += kForkThreads) {
-    const int row = i >> cols_log2, col = col0 + (i & (cols - 1));
-    tile[i] = col < places(p, p.kv_lens[row]) ? p.page_table[row * p.table_stride + col] : kNotHeld;
+  for (int row = threadIdx.x; row < p.batch; row += kForkThreads) {
+    const int parent = p.parents[row];
+    held[row] = places(p, p.kv_lens[row]);
+    parents[row] = parent < 0 || parent >= p.batch ? -1 : parent;
   }
   __syncthreads();
+#pragma unroll 4
   for (int i = threadIdx.x; i < n; i += kForkThreads) {
-    const int row = i >> cols_log2, c = i & (cols - 1), parent = p.parents[row];
-    if (parent < 0 || parent >= p.batch) continue;
+    const int row = i >> cols_log2, col = col0 + (i & (cols - 1));
+    tile[i] = col < held[row] ? p.page_table[row * p.table_stride + col] : kNotHeld;
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n; i += kForkThreads) {
+    const int row = i >> cols_log2, c = i & (cols - 1), parent = parents[row];
+    if (parent < 0) continue;
     const int before = tile[i], now = tile[(parent << cols_log2) + c];
     if (before == now) continue;
     if (is_page(p, before)) atomicSub(p.page_refs + before, 1);
@@ -406,20 +417,20 @@ cudaError_t launch_cluster(CacheParams p, int ctas, size_t smem, cudaStream_t st
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(ctas), attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(ctas), attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kKernel, p);
 }
 
-// How many CTAs share `pieces` of work of which a CTA takes `each` at a time.
-int ctas_for(long long pieces, int each) {
-  int ctas = 1;
-  while (ctas < kMaxCtas && pieces > static_cast<long long>(ctas) * each) ctas *= 2;
-  return ctas;
+// One CTA as long as it needs few rounds for the pages (16 a thread), table entries (8) and
+// tokens (1); else a cluster of 16.
+int ctas_for(const CacheParams& p, long long entries, int tokens) {
+  const long long rounds = p.num_pages / (16 * kThreads) + entries / (8 * kThreads) + tokens / kThreads;
+  return rounds <= 3 ? 1 : kMaxCtas;
 }
 
 }  // namespace
@@ -433,10 +444,11 @@ cudaError_t launch_cache_copy(const CacheCopyParams& p, int caches, int pairs, b
 int cache_copy_blocks(int pieces) { return (pieces + kCopyThreads * kCopyVecs - 1) / (kCopyThreads * kCopyVecs); }
 
 cudaError_t launch_cache_fork(const CacheParams& p, cudaStream_t stream) {
-  // Eight columns are a 32-byte sector of each row.
+  // A CTA takes eight columns, a 32-byte sector of each row.
+  const size_t rows = 2 * static_cast<size_t>(p.batch);
   int cols_log2 = 3;
-  while ((static_cast<size_t>(p.batch) << cols_log2) * 4 > kCacheSmem) --cols_log2;
-  const size_t smem = (static_cast<size_t>(p.batch) << cols_log2) * 4;
+  while ((rows + (static_cast<size_t>(p.batch) << cols_log2)) * 4 > kCacheSmem) --cols_log2;
+  const size_t smem = (rows + (static_cast<size_t>(p.batch) << cols_log2)) * 4;
   const int ctas = (p.max_pages + (1 << cols_log2) - 1) >> cols_log2;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(cache_fork_kernel), kCacheSmem);
   if (e == cudaSuccess && ctas > 0)
@@ -446,7 +458,7 @@ cudaError_t launch_cache_fork(const CacheParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_cache_append(const CacheParams& p, cudaStream_t stream) {
-  const int ctas = ctas_for(std::max(p.num_pages / 4, p.tokens), kThreads);
+  const int ctas = ctas_for(p, 0, p.tokens);
   return launch_cluster<cache_append_kernel>(p, ctas, (3 * static_cast<size_t>(p.batch) + 2) * 4, stream);
 }
 
@@ -455,7 +467,7 @@ cudaError_t launch_cache_truncate(const CacheParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_cache_compact(const CacheParams& p, cudaStream_t stream) {
-  const int ctas = ctas_for(std::max<long long>(p.num_pages, static_cast<long long>(p.batch) * p.max_pages) / 4, kThreads);
+  const int ctas = ctas_for(p, static_cast<long long>(p.batch) * p.max_pages, 0);
   return launch_cluster<cache_compact_kernel>(p, ctas, 0, stream);
 }
 

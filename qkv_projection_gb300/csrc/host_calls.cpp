@@ -19,6 +19,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <array>
 #include <cmath>
 #include <cstdint>
 #include <limits>
@@ -364,9 +365,31 @@ PyObject* fork_or_truncate(PyObject* const* v) {
   Py_RETURN_TRUE;
 }
 
-PyObject* tuple_of(const at::Tensor* t, int n) {
+// n dense int32 tensors of these sizes in one piece of memory (an allocation takes 0.9 us, a
+// tensor on what is there 0.2).
+template <int n>
+std::array<at::Tensor, n> new_ints(const std::array<int64_t, n>& sizes, const at::TensorOptions& options, PyObject* given_stream,
+                                   void* stream) {
+  int64_t total = 0;
+  for (int64_t size : sizes) total += size;
+  const int64_t whole[1] = {total};
+  const at::Tensor memory = new_tensor(whole, options, given_stream, stream);
+  std::array<at::Tensor, n> made;
+  int64_t at = 0;
+  for (int i = 0; i < n; ++i) {
+    made[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(memory.storage()), memory.key_set(), memory.dtype());
+    const int64_t size[1] = {sizes[i]};
+    made[i].unsafeGetTensorImpl()->set_storage_offset(at);
+    made[i].unsafeGetTensorImpl()->set_sizes_contiguous(size);
+    at += sizes[i];
+  }
+  return made;
+}
+
+template <size_t n>
+PyObject* tuple_of(const std::array<at::Tensor, n>& t) {
   PyObject* all = PyTuple_New(n);
-  for (int i = 0; all && i < n; ++i) {
+  for (size_t i = 0; all && i < n; ++i) {
     PyObject* one = THPVariable_Wrap(t[i]);
     if (!one) Py_CLEAR(all);
     else PyTuple_SET_ITEM(all, i, one);
@@ -387,13 +410,10 @@ PyObject* append(PyObject* const* v) {
   }
   void* stream;
   if (!stream_of(v[6], *lens, &stream)) return nullptr;
-  const int64_t size[1] = {a.tokens};
-  const at::Tensor made[3] = {new_tensor(size, lens->options(), v[6], stream),
-                              new_tensor(lens->sizes(), lens->options(), v[6], stream),
-                              new_tensor(lens->sizes(), lens->options(), v[6], stream)};
+  const auto made = new_ints<3>({a.tokens, a.batch, a.batch}, lens->options(), v[6], stream);
   a.slots = static_cast<int32_t*>(made[0].data_ptr());
   a.src = static_cast<int32_t*>(made[1].data_ptr()), a.dst = static_cast<int32_t*>(made[2].data_ptr());
-  return call(g_append, a, stream) ? tuple_of(made, 3) : nullptr;
+  return call(g_append, a, stream) ? tuple_of(made) : nullptr;
 }
 
 // (page_refs, page_table, kv_lens, page_size, max_moves, stream)
@@ -402,11 +422,9 @@ PyObject* compact(PyObject* const* v) {
   const at::Tensor* lens = books(v, v[3], &a);
   void* stream;
   if (!lens || !to_int(v[4], &a.max_moves) || a.max_moves < 0 || !stream_of(v[5], *lens, &stream)) return nullptr;
-  const int64_t size[1] = {a.max_moves};
-  const at::Tensor made[2] = {new_tensor(size, lens->options(), v[5], stream),
-                              new_tensor(size, lens->options(), v[5], stream)};
+  const auto made = new_ints<2>({a.max_moves, a.max_moves}, lens->options(), v[5], stream);
   a.src = static_cast<int32_t*>(made[0].data_ptr()), a.dst = static_cast<int32_t*>(made[1].data_ptr());
-  return call(g_compact, a, stream) ? tuple_of(made, 2) : nullptr;
+  return call(g_compact, a, stream) ? tuple_of(made) : nullptr;
 }
 
 template <PyObject* (*kCall)(PyObject* const*), Py_ssize_t kArgs>
