@@ -170,14 +170,16 @@ __device__ __forceinline__ int remote(const int* p, int cta) {
   return v;
 }
 
-// First half: counts this warp's free pages (the loads of 16 words in flight).
-__device__ __forceinline__ void pool_count(const CacheParams& p, Pool& pool, uint32_t* masks, PoolShared& sh) {
+// First half: counts this warp's free pages (the loads of 16 words in flight, `meanwhile` behind the first).
+template <typename F>
+__device__ __forceinline__ void pool_count(const CacheParams& p, Pool& pool, uint32_t* masks, PoolShared& sh, F meanwhile) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, of_all = static_cast<int>(cluster_ctarank()) * kWarps + warp;
   constexpr int kLoads = 16;
   pool.words = p.warp_words;
   pool.first = of_all * pool.words * 32;
   pool.mask = masks + warp * pool.words;
   int count = 0;
+  if (pool.words == 0) meanwhile();
 #pragma unroll 1
   for (int w = 0; w < pool.words; w += kLoads) {
     int refs[kLoads];
@@ -186,6 +188,7 @@ __device__ __forceinline__ void pool_count(const CacheParams& p, Pool& pool, uin
       const int id = pool.first + 32 * (w + k) + lane;
       refs[k] = w + k < pool.words && id < p.num_pages ? p.page_refs[id] : 1;
     }
+    if (w == 0) meanwhile();
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {
       const uint32_t free = __ballot_sync(0xFFFFFFFFu, refs[k] <= 0);
@@ -199,6 +202,21 @@ __device__ __forceinline__ void pool_count(const CacheParams& p, Pool& pool, uin
     const int all = __reduce_add_sync(0xFFFFFFFFu, sh.warp_free[lane]);
     if (lane == 0) sh.cta_free = all;
   }
+}
+// The free pages of a lane's word of 32, and how many are free before it: word w0 + lane of
+// this warp's; *rank0 steps over all 32.
+__device__ __forceinline__ uint32_t pool_word(const Pool& pool, int w0, int* rank0, int* before) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t free = w0 + lane < pool.words ? pool.mask[w0 + lane] : 0u;
+  int upto = __popc(free);
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int add = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+    if (lane >= d) upto += add;
+  }
+  *before = *rank0 + upto - __popc(free);
+  *rank0 += __shfl_sync(0xFFFFFFFFu, upto, 31);
+  return free;
 }
 // Second half, after the cluster has met.
 __device__ __forceinline__ void pool_places(Pool& pool, const PoolShared& sh) {
@@ -235,20 +253,35 @@ __global__ void __launch_bounds__(kThreads, 1) cache_append_kernel(const __grid_
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = static_cast<int>(cluster_ctarank());
   allow_dependents_launch();
   grid_dependency_wait();
-  Pool pool;
-  pool_count(p, pool, reinterpret_cast<uint32_t*>(old + p.batch), sh);
-  // What each row needs; every CTA works it out for itself.
+  // What each row needs; every CTA works it out for itself. A thread's first row (most have no
+  // other) is looked up while the pool is: length and tokens, last page, who else holds it.
   const int per = (p.batch + kThreads - 1) / kThreads, row0 = min(tid * per, p.batch), row1 = min(row0 + per, p.batch);
+  int s0 = 0, s1 = 0, len = 0, last = -1;
+  AppendRow r{};
+  auto look = [&](int row) {
+    s0 = p.q_starts ? p.q_starts[row] : row;
+    s1 = p.q_starts ? p.q_starts[row + 1] : row + 1;
+    len = p.kv_lens[row];
+  };
+  auto look_at_table = [&](int row) {
+    s0 = min(max(s0, 0), p.tokens);
+    s1 = min(max(s1, s0), p.tokens);
+    r = append_row(p, len, s1 - s0);
+    const bool in_part = r.fits && r.old != r.have * p.page_size;      // the last page is the row's own, unless others hold it too
+    last = in_part ? p.page_table[row * p.table_stride + r.have - 1] : -1;
+  };
+  if (row0 < row1) look(row0);
+  Pool pool;
+  pool_count(p, pool, reinterpret_cast<uint32_t*>(old + p.batch), sh, [&] {
+    if (row0 < row1) look_at_table(row0);
+  });
   int mine = 0;
   for (int row = row0; row < row1; ++row) {
-    const int s0 = p.q_starts ? min(max(p.q_starts[row], 0), p.tokens) : row;
-    const int s1 = p.q_starts ? min(max(p.q_starts[row + 1], s0), p.tokens) : row + 1;
-    const AppendRow r = append_row(p, p.kv_lens[row], s1 - s0);
-    int need = r.want - r.have;
-    if (r.fits && r.old != r.have * p.page_size) {           // a last page in part: its own, unless others hold it too
-      const int last = p.page_table[row * p.table_stride + r.have - 1];
-      need += is_page(p, last) && p.page_refs[last] > 1;
+    if (row > row0) {
+      look(row);
+      look_at_table(row);
     }
+    const int need = r.want - r.have + (is_page(p, last) && p.page_refs[last] > 1);
     starts[row] = s0, old[row] = r.old, before[row] = need;
     if (row == p.batch - 1) starts[p.batch] = s1;
     mine += need;
@@ -267,42 +300,36 @@ __global__ void __launch_bounds__(kThreads, 1) cache_append_kernel(const __grid_
   const int all_need = __reduce_add_sync(0xFFFFFFFFu, of_warp);
   const int needed = min(all_need, p.tokens);                // (no more, unless q_starts decreases)
   int at = upto - mine + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? of_warp : 0);
+  // From here old is -1 for rows that take nothing.
   for (int row = row0; row < row1; ++row) {
     const int need = before[row];
+    const AppendRow r = append_row(p, old[row], starts[row + 1] - starts[row]);
     before[row] = at;
     at += need;
+    if (!r.fits || (need > 0 && at > pool.free)) old[row] = -1;
+    else if (cta == 0) p.kv_lens[row] = r.old + r.n;       // (every CTA has its own copy of the old ones)
   }
   if (tid == 0) before[p.batch] = all_need;
-  __syncthreads();
-  auto granted = [&](int row, const AppendRow& r) {
-    return r.fits && (before[row + 1] == before[row] || before[row + 1] <= pool.free);
-  };
-  auto row_at = [&](int row) { return append_row(p, old[row], starts[row + 1] - starts[row]); };
-  // the last row that begins at or before x
-  auto find = [&](const int* begins, int x) {
-    int lo = 0, hi = p.batch;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (begins[mid] <= x) lo = mid;
-      else hi = mid;
-    }
-    return lo;
-  };
   // The pages to give out, in their order, stand where the slots will: a row needs no more
   // pages than it has new tokens. (Few warps hold them all, so they only list them.)
   int rank0 = pool.before;
-  for (int w = 0; w < pool.words && rank0 < needed; ++w) {
-    const uint32_t free = pool.mask[w];
-    const int rank = rank0 + __popc(free & ((1u << lane) - 1));
-    rank0 += __popc(free);
-    if ((free >> lane & 1) && rank < needed) p.slots[rank] = pool.first + 32 * w + lane;
+  for (int w = 0; w < pool.words && rank0 < needed; w += 32) {
+    int rank;
+    uint32_t free = pool_word(pool, w, &rank0, &rank);
+    for (; free != 0 && rank < needed; free &= free - 1) p.slots[rank++] = pool.first + 32 * (w + lane) + __ffs(free) - 1;
   }
   meet();
+  // The last row that begins at or before x, of `begins`: as many steps for everyone.
+  int top = 1;
+  while (2 * top < p.batch) top *= 2;
   const int step = cluster_ctas() * kThreads;
   for (int rank = cta * kThreads + tid; rank < min(needed, pool.free); rank += step) {
-    const int id = p.slots[rank], row = find(before, rank);
-    const AppendRow r = row_at(row);
-    if (!granted(row, r)) continue;
+    const int id = p.slots[rank];
+    int row = 0;
+    for (int d = top; d > 0; d >>= 1)
+      if (row + d < p.batch && before[row + d] <= rank) row += d;
+    if (old[row] < 0) continue;
+    const AppendRow r = append_row(p, old[row], starts[row + 1] - starts[row]);
     const int tail = before[row + 1] - before[row] - (r.want - r.have), k = rank - before[row];
     int* place = p.page_table + row * p.table_stride + r.have + k - tail;
     if (k < tail) {                                          // in place of a last page that others hold too
@@ -313,23 +340,27 @@ __global__ void __launch_bounds__(kThreads, 1) cache_append_kernel(const __grid_
     *place = id;
     p.page_refs[id] = 1;
   }
-  meet();                                        // the table is whole
-  if (cta == 0) {
-    for (int row = tid; row < p.batch; row += kThreads) {
-      const AppendRow r = row_at(row);
-      if (granted(row, r)) p.kv_lens[row] = r.old + r.n;
+  meet();                                                    // the table is whole
+  constexpr int kEach = 4;                                   // tokens of a thread in work at a time
+  for (int t0 = cta * kThreads + tid; t0 < p.tokens; t0 += kEach * step) {
+    int row[kEach] = {}, pos[kEach], place[kEach], id[kEach];
+    for (int d = top; d > 0; d >>= 1) {
+#pragma unroll
+      for (int k = 0; k < kEach; ++k)
+        if (row[k] + d < p.batch && starts[row[k] + d] <= t0 + k * step) row[k] += d;
     }
-  }
-  for (int t = cta * kThreads + tid; t < p.tokens; t += step) {
-    const int row = find(starts, t);
-    const AppendRow r = row_at(row);
-    int slot = -1;
-    if (t >= starts[row] && t < starts[row + 1] && granted(row, r)) {
-      const int pos = r.old + t - starts[row], place = p.page_div.div(pos);
-      const int id = p.page_table[row * p.table_stride + place];
-      if (is_page(p, id)) slot = id * p.page_size + pos - place * p.page_size;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int t = t0 + k * step, was = old[row[k]];
+      const bool taken = t >= starts[row[k]] && t < starts[row[k] + 1] && was >= 0;
+      pos[k] = taken ? was + t - starts[row[k]] : 0;
+      place[k] = p.page_div.div(pos[k]);
+      id[k] = taken ? p.page_table[row[k] * p.table_stride + place[k]] : -1;
     }
-    p.slots[t] = slot;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+      if (t0 + k * step < p.tokens)
+        p.slots[t0 + k * step] = is_page(p, id[k]) ? id[k] * p.page_size + pos[k] - place[k] * p.page_size : -1;
   }
 }
 
@@ -346,23 +377,29 @@ __global__ void __launch_bounds__(kThreads, 1) cache_compact_kernel(const __grid
   allow_dependents_launch();
   grid_dependency_wait();
   Pool pool;
-  pool_count(p, pool, masks, sh);
+  pool_count(p, pool, masks, sh, [] {});
   for (int i = cta * kThreads + tid; i < p.max_moves; i += all) p.src[i] = p.dst[i] = -1;
   meet();
   pool_places(pool, sh);
   const int used = p.num_pages - pool.free;
   int rank0 = pool.before;
-  for (int w = 0; w < pool.words; ++w) {
-    const uint32_t free = pool.mask[w];
-    const int id = pool.first + 32 * w + lane, rank = rank0 + __popc(free & ((1u << lane) - 1));
-    rank0 += __popc(free);
-    if (id >= p.num_pages) break;
-    if (id == used) sh.below = rank;
-    if (free >> lane & 1) {
-      if (id < used && rank < p.max_moves) p.dst[rank] = id;
-    } else if (id >= used) {
-      const int from_top = used - 1 - (id - rank);
-      if (from_top < p.max_moves) p.src[from_top] = id;
+  for (int w = 0; w < pool.words; w += 32) {
+    // A lane takes a word of 32 pages: `rank` are free before it, `first - rank` used.
+    int rank;
+    const uint32_t free = pool_word(pool, w, &rank0, &rank);
+    const int first = pool.first + 32 * (w + lane), count = w + lane < pool.words ? min(max(p.num_pages - first, 0), 32) : 0;
+    auto below = [&](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1; };
+    const uint32_t low = below(used - first), here = below(count);
+    if (used >= first && used < first + count) sh.below = rank + __popc(free & low);
+    int to = rank;
+    for (uint32_t left = free & low; left != 0 && to < p.max_moves; left &= left - 1) p.dst[to++] = first + __ffs(left) - 1;
+    // the used ones from U on, from the highest down
+    uint32_t left = here & ~free & ~low;
+    int from = used - (first + count - rank - __popc(free));   // used ones behind this word
+    for (; left != 0 && from < p.max_moves; ++from) {
+      const int bit = 31 - __clz(left);
+      p.src[from] = first + bit;
+      left ^= 1u << bit;
     }
   }
   meet();                                                    // both lists are whole
