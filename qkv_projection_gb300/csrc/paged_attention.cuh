@@ -269,19 +269,37 @@ struct PagedWalk : Work {
 template <int kThreads, typename Walk>
 __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* sums, Walk* place,
                             PagedShare* share) {
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int per = (p.batch + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
   constexpr int kWarps = kThreads / 32;
+  // Few sequences with documents: a warp takes each, its lanes the row tiles (three prompts of 2500
+  // tokens, a thread each: the first tile is found after 21000-28000 cycles, so after half of it).
+  const bool by_warps = Walk::kScored && Walk::kRows > 32 && p.batch <= kWarps;
   constexpr bool kTwoSizes = Walk::kFewRows < Walk::kRows;
   Walk w;
-  long long mine, upto, total;
+  long long mine, upto, total, head = 0;
   int longest, items;
 #pragma unroll 1
   for (w.tile_rows = Walk::kRows;; w.tile_rows = Walk::kFewRows) {
     mine = 0, total = 0, longest = 0, items = 0;
+    if (by_warps && (tid >> 5) < p.batch) {
+      w.s = paged_seq<Walk::kScored>(p, tid >> 5);
+      w.tiles = w.row_tiles(p, w.s);
 #pragma unroll 1
-    for (int b = b0; b < b1; ++b) {
+      for (int i = lane; i < w.tiles; i += 32) {
+        const int units = w.item_units(p, w.s, i), cost = w.item_cost(p, w.s, i);
+        mine += Walk::kItemCost + units * cost;
+        longest = max(longest, 8 * units + cost);
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, d);
+      head = mine;
+      mine = lane == 0 ? mine * p.kv_heads : 0;
+      if (kTwoSizes) items = lane == 0 ? min(p.kv_heads * w.tiles, 1 << 20) : 0;
+    }
+#pragma unroll 1
+    for (int b = by_warps ? b1 : b0; b < b1; ++b) {
       const PagedSeq s = paged_seq<Walk::kScored>(p, b);
       mine += p.kv_heads * w.head_length(p, s, &longest);
       if (kTwoSizes) items = min(items + p.kv_heads * w.row_tiles(p, s), 1 << 20);
@@ -333,6 +351,41 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
   share->snap = min(Walk::kSnap, (each + 1) / 2);
   share->begin = cta * share->each + min(cta, share->more);
   share->end = share->begin + share->each + (cta < share->more ? 1 : 0);
+  if (by_warps) {
+    const long long from = upto - head * p.kv_heads;
+    if ((tid >> 5) < p.batch && share->begin >= from && share->begin < upto) {
+      long long left = share->begin - from;
+      w.b = tid >> 5;
+#pragma unroll 1
+      for (w.h = 0; left >= head; ++w.h) left -= head;
+#pragma unroll 1
+      for (int t0 = 0;; t0 += 32) {
+        const int t = min(t0 + lane, w.tiles - 1);
+        w.units = w.item_units(p, w.s, t);
+        w.cost = w.item_cost(p, w.s, t);
+        long long end = t0 + lane < w.tiles ? w.length() : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long add = __shfl_up_sync(0xFFFFFFFFu, end, d);
+          if (lane >= d) end += add;
+        }
+        const unsigned past = __ballot_sync(0xFFFFFFFFu, end > left);
+        if (past != 0) {
+          if (lane == __ffs(past) - 1) {
+            w.tile = t;
+            w.at = share->begin - (left - (end - w.length()));
+            w.unit = w.cut(share->begin, *share);
+            if (w.unit == w.units) w.next_item(p);
+            *place = w;
+          }
+          break;
+        }
+        left -= __shfl_sync(0xFFFFFFFFu, end, 31);
+      }
+    }
+    __syncthreads();
+    return true;
+  }
   const long long from = upto - mine;
   if (share->begin >= from && share->begin < upto) {
     long long left = share->begin - from;

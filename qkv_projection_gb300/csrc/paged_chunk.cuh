@@ -246,6 +246,51 @@ __device__ __forceinline__ void cap4(uint32_t* s, float c) {
   s[0] = __float_as_uint(u.x), s[1] = __float_as_uint(u.y);
   s[2] = __float_as_uint(v.x), s[3] = __float_as_uint(v.y);
 }
+// The same of 128, sixteen a step and three steps in work at a time: what one waits for (the
+// exponentials, the reciprocal) the others' work covers.
+__device__ __forceinline__ void cap128(uint32_t (&s)[4][32], float c) {
+  uint64_t ab[2][4];
+  float inv[2][4];
+  auto at = [&](int e) -> uint32_t& { return s[e >> 5][e & 31]; };
+  auto get = [&](int e) { return pair(__uint_as_float(at(e)), __uint_as_float(at(e + 1))); };
+  auto set = [&](int e, uint64_t v) {
+    const float2 x = unpair(v);
+    at(e) = __float_as_uint(x.x), at(e + 1) = __float_as_uint(x.y);
+  };
+  const uint64_t c2 = pair(c, c), minus1 = pair(-1.f, -1.f);
+#pragma unroll
+  for (int b = 0; b < 10; ++b) {
+    if (b < 8) {
+#pragma unroll
+      for (int e = 16 * b; e < 16 * b + 16; e += 2) {
+        const float2 y = unpair(mul2(get(e), c2));
+        set(e, pair(exp2_fast(y.x), exp2_fast(y.y)));
+      }
+    }
+    if (b >= 1 && b < 9) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int e = 16 * (b - 1) + 4 * k;
+        set(e, fma2(get(e), minus1, minus1));
+        set(e + 2, fma2(get(e + 2), minus1, minus1));
+        ab[(b - 1) & 1][k] = mul2(get(e), get(e + 2));
+        const float2 x = unpair(ab[(b - 1) & 1][k]);
+        inv[(b - 1) & 1][k] = rcp_fast(x.x * x.y);
+      }
+    }
+    if (b >= 2) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int e = 16 * (b - 2) + 4 * k;
+        const float2 x = unpair(ab[b & 1][k]);
+        const float r = inv[b & 1][k];
+        const uint64_t of_both = pair(r * x.y, r * x.x), first = get(e);
+        set(e, mul2(of_both, get(e + 2)));
+        set(e + 2, mul2(of_both, first));
+      }
+    }
+  }
+}
 // 32 bytes to global memory; half of them at a time where they may not be aligned.
 __device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8], bool aligned) {
   if (aligned) {
@@ -701,10 +746,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       float m = kNegInf, l = 0.f;                          // the row's reference (in units of S) and sum
       int doc = 0;                                         // of this thread's row: its document's begin,
+      int my_pos = 0;                                      // its place,
       float slope = 0.f;                                   // and what a score gains with each position to the right
       if (kScored) {
         const int r = w.row0 + min(my_row, rows - 1);
         doc = paged_doc<kScored>(p, w.s, r);
+        my_pos = w.s.kv - w.s.n + p.group_div.div(r);
         if (kDistance) slope = p.slopes[w.h * p.group + r - p.group_div.div(r) * p.group] * kLog2e;
       }
       if (works(mode)) {
@@ -741,49 +788,70 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           auto row_here = [&] { return Row(p, w.s, w.row0 + min(my_row, rows - 1), doc); };
           uint32_t s[4][32];
+          const int key0 = w.span.key0(u);
+          // Units with hidden keys, and those that a bias does not fall evenly over, go 32 keys at a time through one
+          // short loop, in place in tensor memory, before the rest: few units, and each instruction of an item's
+          // code that is fetched anew takes 5 cycles.
+          bool slow = kScored && masked;
+          if constexpr (kDistance) slow = slow || __any_sync(0xFFFFFFFFu, key0 + 127 > my_pos);
+          if (slow) {
+            const Row vis = row_here();
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              uint32_t x[32];
+              tmem_ld32(s_tmem + 32 * i, x);
+              tmem_ld_wait();
+              const int at = key0 + 32 * i;
+              hide(vis, at, x);
+              if constexpr (kCapped) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(min_nan(__uint_as_float(x[e]), most));
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) cap4(&x[e], p.cap_in);
+              }
+              if constexpr (kDistance) {
+                const float base = static_cast<float>(at - my_pos);
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  x[e] = __float_as_uint(fmaf(__uint_as_float(x[e]), cap_scale, -slope * fabsf(base + e)));
+              }
+              if constexpr (kCapped) hide(vis, at, x);     // (what was hidden before came out as -1)
+              tmem_st32(s_tmem + 32 * i, x);
+            }
+            tmem_st_wait();
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) tmem_ld32(s_tmem + 32 * i, s[i]);
           tmem_ld_wait();
-          const int key0 = w.span.key0(u);
-          auto hide_all = [&] {
+          if (!kScored && masked) {
             const Row vis = row_here();
 #pragma unroll
             for (int i = 0; i < 4; ++i) hide(vis, key0 + 32 * i, s[i]);
-          };
+          }
           auto top_of = [&] {
             float top8[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) top8[i] = fmaxf(__uint_as_float(s[0][2 * i]), __uint_as_float(s[0][2 * i + 1]));
 #pragma unroll
-            for (int i = 8; i < 16 * 4; ++i)
+            for (int i = 8; i < 64; ++i)
               top8[i & 7] = max3(top8[i & 7], __uint_as_float(s[i >> 4][2 * i & 31]), __uint_as_float(s[i >> 4][(2 * i & 31) + 1]));
             return fmaxf(max3(top8[0], top8[1], top8[2]), max3(max3(top8[3], top8[4], top8[5]), top8[6], top8[7]));
           };
-          if (masked) hide_all();
-          float top = kNegInf;
-          if constexpr (kCapped) {
-            // (the largest result is that of the largest score)
-            top = top_of();
-            if (__any_sync(0xFFFFFFFFu, top > most)) {
-              top = fminf(top, most);
+          if constexpr (kForm == Form::kCappedDistance) {
+            if (!slow) {
+              if (__any_sync(0xFFFFFFFFu, top_of() > most)) {
 #pragma unroll
-              for (int e = 0; e < 32 * 4; ++e)
-                s[e >> 5][e & 31] = __float_as_uint(min_nan(__uint_as_float(s[e >> 5][e & 31]), most));
-            }
-            if (kForm == Form::kCapped && top != kNegInf) top = -rcp_fast(1.f + exp2_fast(top * p.cap_in));
-            if constexpr (kDistance) {
-#pragma unroll
-              for (int e = 0; e < 128; e += 4) cap4(&s[e >> 5][e & 31], p.cap_in);
-              if (masked) hide_all();                      // (what was hidden before came out as -1)
+                for (int e = 0; e < 128; ++e) s[e >> 5][e & 31] = __float_as_uint(min_nan(__uint_as_float(s[e >> 5][e & 31]), most));
+              }
+              cap128(s, p.cap_in);
             }
           }
           if constexpr (kDistance) {
-            const int first_key = key0 - (w.s.kv - w.s.n + p.group_div.div(w.row0 + min(my_row, rows - 1)));
-            if (__all_sync(0xFFFFFFFFu, first_key <= -127)) {      // left of it the bias grows evenly with the key
+            if (!slow) {                                   // left of the row's place the bias grows evenly with the key
               const uint64_t scale2 = pair(cap_scale, cap_scale), step2 = pair(4.f * slope, 4.f * slope);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const float base = static_cast<float>(first_key + 32 * i);
+                const float base = static_cast<float>(key0 - my_pos + 32 * i);
                 uint64_t bias2[2] = {pair(slope * base, slope * (base + 1.f)), pair(slope * (base + 2.f), slope * (base + 3.f))};
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
@@ -793,15 +861,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                   if (e < 28) b = add2(b, step2);
                 }
               }
-            } else {
-              const float base = static_cast<float>(first_key);
-#pragma unroll
-              for (int e = 0; e < 128; ++e)
-                s[e >> 5][e & 31] =
-                    __float_as_uint(fmaf(__uint_as_float(s[e >> 5][e & 31]), cap_scale, -slope * fabsf(base + e)));
             }
           }
-          if constexpr (kForm != Form::kCapped) top = top_of();
+          float top = top_of();
+          if constexpr (kForm == Form::kCapped) {
+            if (!slow) {
+              if (__any_sync(0xFFFFFFFFu, top > most)) {
+                top = fminf(top, most);
+#pragma unroll
+                for (int e = 0; e < 128; ++e) s[e >> 5][e & 31] = __float_as_uint(min_nan(__uint_as_float(s[e >> 5][e & 31]), most));
+              }
+              // (the largest result is that of the largest score)
+              if (top != kNegInf) top = -rcp_fast(1.f + exp2_fast(top * p.cap_in));
+              cap128(s, p.cap_in);
+            }
+          }
           // (the first finite maximum after none needs no rescaling: O and l are zero)
           const bool renew = top > m && (m == kNegInf || (top - m) * scale > kLazy);
           if (__any_sync(0xFFFFFFFFu, renew)) {
@@ -835,82 +909,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0 && ok) mbar_arrive(&ctl.p_full[half][of]);
           };
-          if (kForm == Form::kCapped && !masked) {
-            // Sixteen scores a step, four steps in work at a time: what one waits for (the exponentials,
-            // the reciprocal) the others' work covers.
-            constexpr int kSteps = 8;
-            uint64_t both[2][4];
-            float inv[2][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
             uint32_t packed[16];
-            auto at = [&](int e) -> uint32_t& { return s[e >> 5][e & 31]; };
-            auto get = [&](int e) { return pair(__uint_as_float(at(e)), __uint_as_float(at(e + 1))); };
-            auto set = [&](int e, uint64_t v) {
-              const float2 x = unpair(v);
-              at(e) = __float_as_uint(x.x), at(e + 1) = __float_as_uint(x.y);
-            };
-            const uint64_t c2 = pair(p.cap_in, p.cap_in), minus1 = pair(-1.f, -1.f);
 #pragma unroll
-            for (int b = 0; b < kSteps + 3; ++b) {
-              if (b < kSteps) {
-#pragma unroll
-                for (int e = 16 * b; e < 16 * b + 16; e += 2) {
-                  const float2 y = unpair(mul2(get(e), c2));
-                  set(e, pair(exp2_fast(y.x), exp2_fast(y.y)));
-                }
-              }
-              if (b >= 1 && b < kSteps + 1) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const int e = 16 * (b - 1) + 4 * k;
-                  set(e, fma2(get(e), minus1, minus1));
-                  set(e + 2, fma2(get(e + 2), minus1, minus1));
-                  both[(b - 1) & 1][k] = mul2(get(e), get(e + 2));
-                  const float2 x = unpair(both[(b - 1) & 1][k]);
-                  inv[(b - 1) & 1][k] = rcp_fast(x.x * x.y);
-                }
-              }
-              if (b >= 2 && b < kSteps + 2) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const int e = 16 * (b - 2) + 4 * k;
-                  const float2 x = unpair(both[b & 1][k]);
-                  const float r = inv[b & 1][k];
-                  const uint64_t of_both = pair(r * x.y, r * x.x), first = get(e);
-                  set(e, fma2(mul2(of_both, get(e + 2)), scale2, addend2));
-                  set(e + 2, fma2(mul2(of_both, first), scale2, addend2));
-                }
-              }
-              if (b >= 3) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const int e = 16 * (b - 3) + 2 * k;
-                  const float x = exp2_fast(__uint_as_float(at(e))), y = exp2_fast(__uint_as_float(at(e + 1)));
-                  sum2[b & 1] = add2(sum2[b & 1], pair(x, y));
-                  packed[8 * ((b - 3) & 1) + k] = Type<T>::pack(x, y);
-                }
-                if ((b - 3) & 1) tmem_st16(s_tmem + 16 * ((b - 3) >> 1), packed);
-                if (((b - 3) & 3) == 3) give((b - 3) >> 2);
-              }
+            for (int e = 0; e < 32; e += 2) {
+              const float2 x = unpair(fma2(pair(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])), scale2, addend2));
+              const float a = exp2_fast(x.x), b = exp2_fast(x.y);
+              sum2[i & 1] = add2(sum2[i & 1], pair(a, b));
+              packed[e >> 1] = Type<T>::pack(a, b);
             }
-          } else {
-            if constexpr (kForm == Form::kCapped) {
-#pragma unroll
-              for (int e = 0; e < 128; e += 4) cap4(&s[e >> 5][e & 31], p.cap_in);
-              hide_all();                                  // (what was hidden before came out as -1)
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t packed[16];
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const float2 x = unpair(fma2(pair(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])), scale2, addend2));
-                const float a = exp2_fast(x.x), b = exp2_fast(x.y);
-                sum2[i & 1] = add2(sum2[i & 1], pair(a, b));
-                packed[e >> 1] = Type<T>::pack(a, b);
-              }
-              tmem_st16(s_tmem + 16 * i, packed);
-              if (i & 1) give(i >> 1);
-            }
+            tmem_st16(s_tmem + 16 * i, packed);
+            if (i & 1) give(i >> 1);
           }
           const float2 sa = unpair(sum2[0]), sb = unpair(sum2[1]);
           l += (sa.x + sa.y) + (sb.x + sb.y);
