@@ -794,6 +794,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           // code that is fetched anew takes 5 cycles.
           bool slow = kScored && masked;
           if constexpr (kDistance) slow = slow || __any_sync(0xFFFFFFFFu, key0 + 127 > my_pos);
+          auto load = [&] {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tmem_ld32(s_tmem + 32 * i, s[i]);
+            tmem_ld_wait();
+          };
+          auto top_of = [&] {
+            float top8[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top8[i] = fmaxf(__uint_as_float(s[0][2 * i]), __uint_as_float(s[0][2 * i + 1]));
+#pragma unroll
+            for (int i = 8; i < 64; ++i)
+              top8[i & 7] = max3(top8[i & 7], __uint_as_float(s[i >> 4][2 * i & 31]), __uint_as_float(s[i >> 4][(2 * i & 31) + 1]));
+            return fmaxf(max3(top8[0], top8[1], top8[2]), max3(max3(top8[3], top8[4], top8[5]), top8[6], top8[7]));
+          };
+          float top = kNegInf;
+          if constexpr (kCapped) {                         // (and those with a score that is many caps)
+            if (!slow) {
+              load();
+              top = top_of();
+              slow = __any_sync(0xFFFFFFFFu, top > most);
+            }
+          }
           if (slow) {
             const Row vis = row_here();
 #pragma unroll 1
@@ -820,31 +842,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_st_wait();
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32(s_tmem + 32 * i, s[i]);
-          tmem_ld_wait();
+          if (!kCapped || slow) load();
           if (!kScored && masked) {
             const Row vis = row_here();
 #pragma unroll
             for (int i = 0; i < 4; ++i) hide(vis, key0 + 32 * i, s[i]);
           }
-          auto top_of = [&] {
-            float top8[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top8[i] = fmaxf(__uint_as_float(s[0][2 * i]), __uint_as_float(s[0][2 * i + 1]));
-#pragma unroll
-            for (int i = 8; i < 64; ++i)
-              top8[i & 7] = max3(top8[i & 7], __uint_as_float(s[i >> 4][2 * i & 31]), __uint_as_float(s[i >> 4][(2 * i & 31) + 1]));
-            return fmaxf(max3(top8[0], top8[1], top8[2]), max3(max3(top8[3], top8[4], top8[5]), top8[6], top8[7]));
-          };
           if constexpr (kForm == Form::kCappedDistance) {
-            if (!slow) {
-              if (__any_sync(0xFFFFFFFFu, top_of() > most)) {
-#pragma unroll
-                for (int e = 0; e < 128; ++e) s[e >> 5][e & 31] = __float_as_uint(min_nan(__uint_as_float(s[e >> 5][e & 31]), most));
-              }
-              cap128(s, p.cap_in);
-            }
+            if (!slow) cap128(s, p.cap_in);
           }
           if constexpr (kDistance) {
             if (!slow) {                                   // left of the row's place the bias grows evenly with the key
@@ -863,18 +868,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          float top = top_of();
           if constexpr (kForm == Form::kCapped) {
-            if (!slow) {
-              if (__any_sync(0xFFFFFFFFu, top > most)) {
-                top = fminf(top, most);
-#pragma unroll
-                for (int e = 0; e < 128; ++e) s[e >> 5][e & 31] = __float_as_uint(min_nan(__uint_as_float(s[e >> 5][e & 31]), most));
-              }
-              // (the largest result is that of the largest score)
+            if (!slow) {                                   // (the largest result is that of the largest score)
               if (top != kNegInf) top = -rcp_fast(1.f + exp2_fast(top * p.cap_in));
               cap128(s, p.cap_in);
+            } else {
+              top = top_of();
             }
+          } else {
+            top = top_of();
           }
           // (the first finite maximum after none needs no rescaling: O and l are zero)
           const bool renew = top > m && (m == kNegInf || (top - m) * scale > kLazy);
