@@ -1,12 +1,13 @@
 """Attention with quantised projections over a paged cache: prompts in chunks, then
-token by token, each step one projection, one rotation with its cache write and one
-attention.
+token by token, each step pages for the new tokens, one projection, one rotation with its
+cache write and one attention.
 
     python examples/attention_steps.py
 
 Runs a batch of prompts of unlike lengths through one layer's attention on the
 current GPU (synthetic weights), in chunks of at most 256 tokens, then generates a
-few tokens for every sequence, and prints the time of a step.
+few tokens for every sequence, forks one into all rows, cuts what was drafted, compacts
+the cache, and prints the time of a step.
 """
 import math
 import os
@@ -22,17 +23,18 @@ from qkv_projection_gb300 import kaio  # noqa: E402
 class PagedLayer:
     """One layer's attention: W4A16 projections, rotary positions, a paged cache.
 
-    The projections give as many K/V heads as query heads. Pages are handed out in
-    the order in which sequences grow into them.
+    The projections give as many K/V heads as query heads. Which sequence holds which
+    pages is kept on the GPU (page_refs, page_table, kv_lens); `lengths` follows on the host.
+    softcap and slopes (f32 [heads]) are those of ``kaio.paged_attention``.
     """
 
     def __init__(self, columns, heads, head_dim, sequences, pages, page_size=16, theta=10000.0, window=0, sinks=0,
-                 seed=0):
+                 seed=0, softcap=0.0, slopes=None):
         g = torch.Generator(device="cuda").manual_seed(seed)
         dev = dict(device="cuda")
         n = heads * head_dim
         self.heads, self.head_dim, self.page_size = heads, head_dim, page_size
-        self.window, self.sinks = window, sinks
+        self.window, self.sinks, self.softcap, self.slopes = window, sinks, softcap, slopes
         self.weights = [torch.randint(-2**31, 2**31 - 1, (columns // 8, n), dtype=torch.int32, generator=g, **dev)
                         for _ in range(3)]
         self.scales = [torch.full((columns // 128, n), 0.2 / math.sqrt(columns), dtype=torch.float16, **dev)
@@ -40,33 +42,52 @@ class PagedLayer:
         self.inv_freq = (theta ** (-torch.arange(0, head_dim, 2, dtype=torch.float64) / head_dim)).float().cuda()
         shape = (pages, page_size, heads, head_dim)
         self.k_cache, self.v_cache = (torch.empty(shape, dtype=torch.float16, **dev) for _ in range(2))
+        self.page_refs = torch.zeros(pages, dtype=torch.int32, **dev)
         self.page_table = torch.full((sequences, pages), -1, dtype=torch.int32, **dev)
-        self.free = list(range(pages))[::-1]
+        self.kv_lens = torch.zeros(sequences, dtype=torch.int32, **dev)
         self.lengths = [0] * sequences
         self.workspace = kaio.paged_attention_workspace()
 
     def step(self, x, new):
         """x f16 [sum(new), columns]: the next new[b] tokens of each sequence b, in order.
         Returns their attention outputs f16 [sum(new), heads * head_dim]."""
-        positions, slots, starts = [], [], [0]
+        positions, starts = [], [0]
         for b, n in enumerate(new):
-            for p in range(self.lengths[b], self.lengths[b] + n):
-                if p % self.page_size == 0:
-                    self.page_table[b, p // self.page_size] = self.free.pop()
             positions += range(self.lengths[b], self.lengths[b] + n)
             self.lengths[b] += n
             starts.append(starts[-1] + n)
         ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
-        positions, starts, lengths = ints(positions), ints(starts), ints(self.lengths)
-        owner = torch.repeat_interleave(torch.arange(len(new), device="cuda"), (starts[1:] - starts[:-1]).long())
-        slots = self.page_table[owner, positions // self.page_size] * self.page_size + positions % self.page_size
+        positions, starts = ints(positions), ints(starts)
+        # pages for the new tokens; where a last page is shared, its row gets a copy of its own
+        slots, src, dst = kaio.cache_append(*self.books(), starts, x.shape[0], self.page_size)
+        kaio.cache_copy_pages((self.k_cache, self.v_cache), src, dst)
 
         rows = (x.shape[0], self.heads, self.head_dim)
         q, k, v = (t.view(rows) for t in kaio.qkv_project_int4(x, *self.weights, *self.scales))
         kaio.rope_append(q, k, v, positions, self.inv_freq, self.k_cache, self.v_cache, slots, q_out=q)
-        out = kaio.paged_attention(q, self.k_cache, self.v_cache, self.page_table, lengths, starts, max_new=max(new),
-                                   window=self.window, sinks=self.sinks, workspace=self.workspace)
+        out = kaio.paged_attention(q, self.k_cache, self.v_cache, self.page_table, self.kv_lens, starts, max_new=max(new),
+                                   window=self.window, sinks=self.sinks, workspace=self.workspace, softcap=self.softcap,
+                                   slopes=self.slopes)
         return out.view(x.shape[0], -1)
+
+    def books(self):
+        return self.page_refs, self.page_table, self.kv_lens
+
+    def fork(self, parents):
+        """Row b goes on from where row parents[b] stands; they share their pages."""
+        kaio.cache_fork(*self.books(), torch.tensor(parents, dtype=torch.int32, device="cuda"), self.page_size)
+        self.lengths = [self.lengths[p] for p in parents]
+
+    def truncate(self, lengths):
+        """Drops what each row has past these lengths (drafts that were refused; 0: the sequence is done)."""
+        kaio.cache_truncate(*self.books(), torch.tensor(lengths, dtype=torch.int32, device="cuda"), self.page_size)
+        self.lengths = [min(a, max(b, 0)) for a, b in zip(self.lengths, lengths)]
+
+    def compact(self):
+        """Moves all pages in use to the beginning of the cache."""
+        pages = self.page_refs.numel()
+        src, dst = kaio.cache_compact(*self.books(), self.page_size, (pages + 1) // 2)
+        kaio.cache_copy_pages((self.k_cache, self.v_cache), src, dst)
 
 
 def main():
@@ -90,7 +111,17 @@ def main():
     end.record()
     kaio.device_status()
     print(f"one token for each of {len(prompts)} sequences of {layer.lengths} positions: "
-          f"{begin.elapsed_time(end) / 20 * 1e3:.0f} us a step (with the bookkeeping on the host)")
+          f"{begin.elapsed_time(end) / 20 * 1e3:.0f} us a step (positions counted on the host)")
+
+    layer.fork([0] * len(prompts))                         # four samples of the longest prompt
+    layer.step(x, ones)
+    layer.step(torch.cat([x] * 4), [4] * len(prompts))     # four drafted tokens each, of which one to four stay
+    layer.truncate([n - b for b, n in enumerate(layer.lengths)])
+    layer.compact()
+    out = layer.step(x, ones)
+    kaio.device_status()
+    print(f"forked, drafted, cut and compacted: {layer.lengths} positions in {int((layer.page_refs > 0).sum())} pages, "
+          f"output {tuple(out.shape)}")
 
 
 if __name__ == "__main__":

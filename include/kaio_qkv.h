@@ -523,8 +523,9 @@ int kaio_cache_copy_pages(const kaio_cache_copy_args* args, kaio_stream_t stream
  *   takes a page instead of it: src[b] (the shared page) and dst[b] (its own), whose
  *   contents have to be copied (kaio_cache_copy_pages), else both -1. slots i32
  *   [tokens] gets page * page_size + place of every new position, as kaio_rope_append
- *   takes it. A row that does not fit (its max_pages places, or the free pages that the
- *   rows before it leave, refused ones counted too) takes nothing: its books stay, its slots are -1. So do tokens of no row.
+ *   takes it. A row that does not fit (its max_pages places, 2^31 - 1
+ *   positions, or the free pages that the rows before it leave, refused ones counted too) takes
+ *   nothing: its books stay, its slots are -1. Tokens of no row get -1, too.
  * kaio_cache_truncate: row b is cut to new_lens[b] positions (i32 [batch]; below 0: 0)
  *   where that is less than it has, and its pages behind them are given back.
  * kaio_cache_compact: the i-th highest used page moves to the i-th lowest free one

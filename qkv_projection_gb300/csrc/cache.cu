@@ -237,7 +237,8 @@ struct AppendRow {
 __device__ __forceinline__ AppendRow append_row(const CacheParams& p, int old, int n) {
   AppendRow r;
   r.old = max(old, 0), r.n = n;
-  r.fits = n > 0 && static_cast<long long>(r.old) + n <= static_cast<long long>(p.max_pages) * p.page_size;
+  const long long room = min(static_cast<long long>(p.max_pages) * p.page_size, static_cast<long long>(INT32_MAX));
+  r.fits = n > 0 && static_cast<long long>(r.old) + n <= room;
   r.have = places(p, r.old);
   r.want = r.fits ? places(p, r.old + n) : r.have;
   return r;
