@@ -63,32 +63,41 @@ __device__ __forceinline__ int places(const CacheParams& p, int len) {
 }
 __device__ __forceinline__ bool is_page(const CacheParams& p, int id) { return id >= 0 && id < p.num_pages; }
 
+// All threads of the cluster meet; what each wrote, the others see.
+__device__ __forceinline__ void cluster_meet() {
+  __syncwarp();
+  cluster_sync_all();
+}
+
 // Row b becomes a copy of row parents[b], all at once: a CTA takes a few columns of all rows,
 // whose entries it reads before it writes any. References change only where a place does, so
-// what parent and row share already costs nothing.
+// what parent and row share already costs nothing. Lengths may be written once every CTA has
+// read them: by the kernel itself where its CTAs are one cluster (kOne), by another one otherwise.
 constexpr int kForkThreads = 512;
 constexpr int kNotHeld = INT32_MIN;
 
+template <bool kOne>
 __global__ void __launch_bounds__(kForkThreads) cache_fork_kernel(const __grid_constant__ CacheParams p, int cols_log2) {
   extern __shared__ int smem[];
-  int* held = smem;                                          // [batch] places
-  int* parents = held + p.batch;                             // [batch] -1: the row stays
+  int* lens = smem;                                          // [batch]
+  int* parents = lens + p.batch;                             // [batch] -1: the row stays
   int* tile = parents + p.batch;                             // [batch][cols]
   const int cols = 1 << cols_log2, col0 = blockIdx.x * cols, n = p.batch * cols;
   allow_dependents_launch();
   grid_dependency_wait();
   for (int row = threadIdx.x; row < p.batch; row += kForkThreads) {
     const int parent = p.parents[row];
-    held[row] = places(p, p.kv_lens[row]);
+    lens[row] = p.kv_lens[row];
     parents[row] = parent < 0 || parent >= p.batch ? -1 : parent;
   }
   __syncthreads();
 #pragma unroll 4
   for (int i = threadIdx.x; i < n; i += kForkThreads) {
     const int row = i >> cols_log2, col = col0 + (i & (cols - 1));
-    tile[i] = col < held[row] ? p.page_table[row * p.table_stride + col] : kNotHeld;
+    tile[i] = col < places(p, lens[row]) ? p.page_table[row * p.table_stride + col] : kNotHeld;
   }
-  __syncthreads();
+  if (kOne) cluster_meet();
+  else __syncthreads();
 #pragma unroll 4
   for (int i = threadIdx.x; i < n; i += kForkThreads) {
     const int row = i >> cols_log2, c = i & (cols - 1), parent = parents[row];
@@ -98,6 +107,10 @@ __global__ void __launch_bounds__(kForkThreads) cache_fork_kernel(const __grid_c
     if (is_page(p, before)) atomicSub(p.page_refs + before, 1);
     if (now != kNotHeld) p.page_table[row * p.table_stride + col0 + c] = now;
     if (is_page(p, now)) atomicAdd(p.page_refs + now, 1);
+  }
+  if (kOne && blockIdx.x == 0) {
+    for (int row = threadIdx.x; row < p.batch; row += kForkThreads)
+      if (parents[row] >= 0) p.kv_lens[row] = lens[parents[row]];
   }
 }
 
@@ -157,12 +170,6 @@ struct PoolShared {
   int warp_free[kWarps], cta_free;
   int below;            // compaction: free pages below the line
 };
-
-// All threads of the cluster meet; what each wrote, the others see.
-__device__ __forceinline__ void meet() {
-  __syncwarp();
-  cluster_sync_all();
-}
 
 __device__ __forceinline__ int remote(const int* p, int cta) {
   int v;
@@ -295,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_append_kernel(const __grid_
     if (lane >= d) upto += add;
   }
   if (lane == 31) warp_need[warp] = upto;
-  meet();                                        // all counts, nothing given out yet
+  cluster_meet();                                        // all counts, nothing given out yet
   pool_places(pool, sh);
   const int of_warp = warp_need[lane];
   const int all_need = __reduce_add_sync(0xFFFFFFFFu, of_warp);
@@ -319,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_append_kernel(const __grid_
     uint32_t free = pool_word(pool, w, &rank0, &rank);
     for (; free != 0 && rank < needed; free &= free - 1) p.slots[rank++] = pool.first + 32 * (w + lane) + __ffs(free) - 1;
   }
-  meet();
+  cluster_meet();
   // The last row that begins at or before x, of `begins`: as many steps for everyone.
   int top = 1;
   while (2 * top < p.batch) top *= 2;
@@ -341,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_append_kernel(const __grid_
     *place = id;
     p.page_refs[id] = 1;
   }
-  meet();                                                    // the table is whole
+  cluster_meet();                                                    // the table is whole
   constexpr int kEach = 4;                                   // tokens of a thread in work at a time
   for (int t0 = cta * kThreads + tid; t0 < p.tokens; t0 += kEach * step) {
     int row[kEach] = {}, pos[kEach], place[kEach], id[kEach];
@@ -380,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_compact_kernel(const __grid
   Pool pool;
   pool_count(p, pool, masks, sh, [] {});
   for (int i = cta * kThreads + tid; i < p.max_moves; i += all) p.src[i] = p.dst[i] = -1;
-  meet();
+  cluster_meet();
   pool_places(pool, sh);
   const int used = p.num_pages - pool.free;
   int rank0 = pool.before;
@@ -403,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_compact_kernel(const __grid
       left ^= 1u << bit;
     }
   }
-  meet();                                                    // both lists are whole
+  cluster_meet();                                                    // both lists are whole
   const int owner = used < p.num_pages ? used / (32 * kWarps * pool.words) : -1;
   const int moves = owner < 0 ? 0 : min(remote(&sh.below, owner), p.max_moves);
   for (int i = cta * kThreads + tid; i < moves; i += all) {
@@ -411,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_compact_kernel(const __grid
     p.page_refs[to] = p.page_refs[from];
     p.page_refs[from] = kGone + to;
   }
-  meet();
+  cluster_meet();
   if (moves > 0) {
     constexpr int kEach = 8;                                 // entries of a lane in flight
     const int lowest = p.src[moves - 1], chunks = (p.max_pages + 32 * kEach - 1) / (32 * kEach);
@@ -429,13 +436,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_compact_kernel(const __grid
         if (to[k] < kGone + p.num_pages) entry[32 * k] = to[k] - kGone;
     }
   }
-  meet();
+  cluster_meet();
   for (int i = cta * kThreads + tid; i < moves; i += all) p.page_refs[p.src[i]] = 0;
 }
 
-// A launch of one cluster.
-template <void (*kKernel)(CacheParams)>
-cudaError_t launch_cluster(CacheParams p, int ctas, size_t smem, cudaStream_t stream) {
+// A launch as one cluster of `ctas` CTAs (one CTA: as it is), which may begin while the kernel
+// before it runs, and waits for it.
+template <auto kKernel, typename... Args>
+cudaError_t launch_cluster(int ctas, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
   // (set once for a device; 16 CTAs are more than every device of the architecture takes)
   thread_local uint64_t allowed = 0;
   int dev = 0;
@@ -447,11 +455,8 @@ cudaError_t launch_cluster(CacheParams p, int ctas, size_t smem, cudaStream_t st
   }
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  const int per = 32 * ctas * kWarps;
-  p.warp_words = (p.num_pages + per - 1) / per;              // of 32 pages
-  smem += static_cast<size_t>(p.warp_words) * kWarps * 4;
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -461,7 +466,15 @@ cudaError_t launch_cluster(CacheParams p, int ctas, size_t smem, cudaStream_t st
   attr[1].val.clusterDim.x = static_cast<unsigned>(ctas), attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = ctas > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kKernel, p);
+  return cudaLaunchKernelEx(&cfg, kKernel, args...);
+}
+
+// A kernel over the whole pool, of which every warp looks after as many words of 32 pages.
+template <auto kKernel>
+cudaError_t launch_pool(CacheParams p, int ctas, size_t smem, cudaStream_t stream) {
+  const int per = 32 * ctas * kWarps;
+  p.warp_words = (p.num_pages + per - 1) / per;
+  return launch_cluster<kKernel>(ctas, kThreads, smem + static_cast<size_t>(p.warp_words) * kWarps * 4, stream, p);
 }
 
 // One CTA as long as it needs few rounds for the pages (16 a thread), table entries (8) and
@@ -482,22 +495,31 @@ cudaError_t launch_cache_copy(const CacheCopyParams& p, int caches, int pairs, b
 int cache_copy_blocks(int pieces) { return (pieces + kCopyThreads * kCopyVecs - 1) / (kCopyThreads * kCopyVecs); }
 
 cudaError_t launch_cache_fork(const CacheParams& p, cudaStream_t stream) {
-  // A CTA takes eight columns, a 32-byte sector of each row.
+  // Up to sixteen places for a thread of sixteen CTAs: those are one cluster, in one launch. Otherwise a CTA
+  // takes eight columns, a 32-byte sector of each row, and a second launch writes the lengths (64 rows of 252 places:
+  // 11.5 us among others with two launches, bound by the host).
   const size_t rows = 2 * static_cast<size_t>(p.batch);
+  auto bytes = [&](int cols_log2) { return (rows + (static_cast<size_t>(p.batch) << cols_log2)) * 4; };
   int cols_log2 = 3;
-  while ((rows + (static_cast<size_t>(p.batch) << cols_log2)) * 4 > kCacheSmem) --cols_log2;
-  const size_t smem = (rows + (static_cast<size_t>(p.batch) << cols_log2)) * 4;
+  while (kMaxCtas << cols_log2 < p.max_pages) ++cols_log2;
+  if (static_cast<size_t>(p.batch) << cols_log2 <= 16 * kForkThreads) {
+    int ctas = 1;
+    while (ctas << cols_log2 < p.max_pages) ctas *= 2;
+    return launch_cluster<cache_fork_kernel<true>>(ctas, kForkThreads, bytes(cols_log2), stream, p, cols_log2);
+  }
+  cols_log2 = 3;
+  while (bytes(cols_log2) > kCacheSmem) --cols_log2;
   const int ctas = (p.max_pages + (1 << cols_log2) - 1) >> cols_log2;
-  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(cache_fork_kernel), kCacheSmem);
-  if (e == cudaSuccess && ctas > 0)
-    e = launch_dependent(cache_fork_kernel, ctas, kForkThreads, static_cast<int>(smem), stream, p, cols_log2);
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(cache_fork_kernel<false>), kCacheSmem);
+  if (e == cudaSuccess)
+    e = launch_dependent(cache_fork_kernel<false>, ctas, kForkThreads, static_cast<int>(bytes(cols_log2)), stream, p, cols_log2);
   if (e == cudaSuccess) e = launch_dependent(cache_fork_lens_kernel, 1, kLensThreads, 0, stream, p);
   return e;
 }
 
 cudaError_t launch_cache_append(const CacheParams& p, cudaStream_t stream) {
   const int ctas = ctas_for(p, 0, p.tokens);
-  return launch_cluster<cache_append_kernel>(p, ctas, (3 * static_cast<size_t>(p.batch) + 2) * 4, stream);
+  return launch_pool<cache_append_kernel>(p, ctas, (3 * static_cast<size_t>(p.batch) + 2) * 4, stream);
 }
 
 cudaError_t launch_cache_truncate(const CacheParams& p, cudaStream_t stream) {
@@ -506,7 +528,7 @@ cudaError_t launch_cache_truncate(const CacheParams& p, cudaStream_t stream) {
 
 cudaError_t launch_cache_compact(const CacheParams& p, cudaStream_t stream) {
   const int ctas = ctas_for(p, static_cast<long long>(p.batch) * p.max_pages, 0);
-  return launch_cluster<cache_compact_kernel>(p, ctas, 0, stream);
+  return launch_pool<cache_compact_kernel>(p, ctas, 0, stream);
 }
 
 }  // namespace kaio
