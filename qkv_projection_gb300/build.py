@@ -23,8 +23,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libkaio_qkv.so")
 SOURCES = ["api.cu", "decode_w4a16.cu", "tc_decode.cu", "tc_kernels.cu", "dequant_group.cu",
-           "rope.cu", "paged_decode.cu", "paged_decode_scored.cu", "paged_chunk.cu", "paged_chunk_scored.cu", "paged_chunk_distance.cu",
-           "cache.cu"]
+           "rope.cu", "paged_decode.cu", "paged_decode_scored.cu", "paged_decode_distance.cu",
+           "paged_chunk.cu", "paged_chunk_scored.cu", "paged_chunk_distance.cu", "cache.cu"]
 HOST_SOURCE = os.path.join(CSRC, "host_calls.cpp")
 HOST_LIB = os.path.join(HERE, "_host.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -92,6 +92,8 @@ size_t paged_decode_workspace_bytes(int num_sms);
 cudaError_t launch_paged_decode(FloatType t, const PagedParams& p, void* workspace, int num_sms, cudaStream_t stream);
 cudaError_t launch_paged_decode_scored(FloatType t, const PagedParams& p, void* workspace, int num_sms,
                                        cudaStream_t stream);
+cudaError_t launch_paged_decode_distance(FloatType t, const PagedParams& p, void* workspace, int num_sms,
+                                         cudaStream_t stream);
 size_t paged_chunk_workspace_bytes(int num_sms);
 // wait_ns: limit of the pipeline's waits, kOwnWaitLimit but in a test of the path that gives
 // up, which is built for one type and width.

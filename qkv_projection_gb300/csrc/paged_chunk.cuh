@@ -310,18 +310,12 @@ struct ChunkParams {
   unsigned long long wait_ns;         // limit of a wait; used where kLimited
 };
 
-// What the scores and masks are: kPlain has no prefixes and documents, the others do. Each
-// is a kernel of its own, since the loop over a row's scores leaves no register to spare.
-enum class Form : int { kPlain, kMasks, kCapped, kDistance, kCappedDistance };
-
 // kLimited: waits are limited to wait_ns (a test of the path that gives up).
 template <typename T, int kDim, Form kForm, bool kLimited>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                        const __grid_constant__ ChunkParams cp) {
-  constexpr bool kScored = kForm != Form::kPlain;
-  constexpr bool kCapped = kForm == Form::kCapped || kForm == Form::kCappedDistance;
-  constexpr bool kDistance = kForm == Form::kDistance || kForm == Form::kCappedDistance;
+  constexpr bool kScored = kForm != Form::kPlain, kCapped = is_capped(kForm), kDistance = has_distance(kForm);
   using S = Shape<kDim>;
   using Walk = PagedWalk<Work<kScored>>;
   using Span = typename Walk::Span;

@@ -9,7 +9,7 @@ size_t paged_decode_workspace_bytes(int num_sms) {
 }
 
 cudaError_t launch_paged_decode(FloatType t, const PagedParams& p, void* workspace, int num_sms, cudaStream_t stream) {
-  return launch_decode<false>(t, p, workspace, num_sms, stream);
+  return launch_decode<Form::kPlain>(t, p, workspace, num_sms, stream);
 }
 
 }  // namespace kaio

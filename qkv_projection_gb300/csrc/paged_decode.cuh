@@ -135,9 +135,10 @@ __device__ __forceinline__ float capped(float s, float c, float cap_log2) {
 // Shared memory of a CTA: a ring for each warp. Between items the first stage
 // already takes the next item's first keys; the others hold what the warps and CTAs
 // tell each other (kScratch floats of each warp's are used as one array).
-template <typename T, int kDim, bool kScored>
+template <typename T, int kDim, Form kForm>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(const __grid_constant__ PagedParams p) {
   using S = Shape<kDim>;
+  constexpr bool kScored = kForm != Form::kPlain;
   using Walk = PagedWalk<Work<kScored>>;
   using Span = typename Walk::Span;
   using Row = PagedRow<kScored>;
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     const int all_hi = Row(p, seq, row0, 0).hi, all_lo = last_row.lo, all_from = last_row.from, leading = last_row.first;
     // what a score loses for each position between key and query, for this lane's rows
     float slope_a = 0.f, slope_b = 0.f;
-    if (kScored && p.slopes) {
+    if (has_distance(kForm)) {
       const int ra = row0 + min(row_a, rows - 1), rb = row0 + min(row_b, rows - 1);
       slope_a = p.slopes[head0 + ra - p.group_div.div(ra) * p.group] * kLog2e;
       slope_b = p.slopes[head0 + rb - p.group_div.div(rb) * p.group] * kLog2e;
@@ -299,16 +300,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       }
       const bool whole = k0 + kStepKeys <= all_hi && (k0 >= all_lo || k0 + kStepKeys <= leading) &&
                          (!kScored || k0 >= all_from);
+      // this lane's first key, relative to its rows' places
+      const float off_a = has_distance(kForm) ? static_cast<float>(k0 + 2 * (lane & 3) - vis_a.pos) : 0.f;
+      const float off_b = has_distance(kForm) ? static_cast<float>(k0 + 2 * (lane & 3) - vis_b.pos) : 0.f;
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int j = k0 + 8 * n + 2 * (lane & 3) + (e & 1);
           const Row& v = e < 2 ? vis_a : vis_b;
-          if (kScored && p.cap_in != 0.f) s[n][e] = capped(s[n][e], p.scale_log2 < 0.f ? -p.cap_in : p.cap_in, p.cap_log2);
+          if (is_capped(kForm)) s[n][e] = capped(s[n][e], p.scale_log2 < 0.f ? -p.cap_in : p.cap_in, p.cap_log2);
           else s[n][e] *= p.scale_log2;
-          if (kScored && p.slopes)
-            s[n][e] = fmaf(-(e < 2 ? slope_a : slope_b), fabsf(static_cast<float>(v.pos - j)), s[n][e]);
+          if (has_distance(kForm))
+            s[n][e] = fmaf(-(e < 2 ? slope_a : slope_b), fabsf((e < 2 ? off_a : off_b) + (8 * n + (e & 1))), s[n][e]);
           if (!whole && !v.sees(j)) s[n][e] = kNegInf;
         }
       const float top_a = fmaxf(m_a, quad_max(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]))));
@@ -496,15 +500,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   }
 }
 
-template <typename T, int kDim, bool kScored>
+template <typename T, int kDim, Form kForm>
 cudaError_t launch(const PagedParams& p, int ctas, cudaStream_t stream) {
-  const void* kernel = reinterpret_cast<const void*>(paged_decode_kernel<T, kDim, kScored>);
+  const void* kernel = reinterpret_cast<const void*>(paged_decode_kernel<T, kDim, kForm>);
   const cudaError_t e = ensure_smem_limit(kernel, Shape<kDim>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(paged_decode_kernel<T, kDim, kScored>, ctas, kThreads, Shape<kDim>::kSmem, stream, p);
+  return launch_dependent(paged_decode_kernel<T, kDim, kForm>, ctas, kThreads, Shape<kDim>::kSmem, stream, p);
 }
 
-template <bool kScored>
+template <Form kForm>
 cudaError_t launch_decode(FloatType t, PagedParams p, void* workspace, int num_sms, cudaStream_t stream) {
   // No more CTAs than counters, and than there can be units.
   const long long most = static_cast<long long>(p.max_pages) << p.page_shift;
@@ -516,9 +520,9 @@ cudaError_t launch_decode(FloatType t, PagedParams p, void* workspace, int num_s
   p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kPagedCounterBytes);
   p.part_l = p.part_o + static_cast<size_t>(2) * ctas * kRows * (p.dim <= 64 ? 64 : 128);
   if (t == FloatType::BF16)
-    return p.dim <= 64 ? launch<__nv_bfloat16, 64, kScored>(p, ctas, stream)
-                       : launch<__nv_bfloat16, 128, kScored>(p, ctas, stream);
-  return p.dim <= 64 ? launch<__half, 64, kScored>(p, ctas, stream) : launch<__half, 128, kScored>(p, ctas, stream);
+    return p.dim <= 64 ? launch<__nv_bfloat16, 64, kForm>(p, ctas, stream)
+                       : launch<__nv_bfloat16, 128, kForm>(p, ctas, stream);
+  return p.dim <= 64 ? launch<__half, 64, kForm>(p, ctas, stream) : launch<__half, 128, kForm>(p, ctas, stream);
 }
 
 }  // namespace
