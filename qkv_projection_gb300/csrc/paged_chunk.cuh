@@ -769,8 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             q_next = ok && works(nx.mode);
             if (q_next) fetch_q(nx);
           }
-          // Of 32 keys from `at` on: bits of those that this row sees, and the others' scores to -inf.
-          const bool masked = u < plain0 || u >= plain1;
+          // Bits of those of 32 keys from `at` on that a row sees, and the others' scores to -inf.
           auto hide = [&](const Row& vis, int at, uint32_t (&x)[32]) {
             auto below = [&](int x) { return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1; };
             uint32_t seen = below(vis.hi - at) & (~below(vis.lo - at) | below(vis.first - at));
@@ -780,14 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 32; ++e)
               if (!(seen >> e & 1)) x[e] = __float_as_uint(kNegInf);
           };
-          auto row_here = [&] { return Row(p, w.s, w.row0 + min(my_row, rows - 1), doc); };
           uint32_t s[4][32];
-          const int key0 = w.span.key0(u);
-          // Units with hidden keys, and those that a bias does not fall evenly over, go 32 keys at a time through one
-          // short loop, in place in tensor memory, before the rest: few units, and each instruction of an item's
-          // code that is fetched anew takes 5 cycles.
-          bool slow = kScored && masked;
-          if constexpr (kDistance) slow = slow || __any_sync(0xFFFFFFFFu, key0 + 127 > my_pos);
           auto load = [&] {
 #pragma unroll
             for (int i = 0; i < 4; ++i) tmem_ld32(s_tmem + 32 * i, s[i]);
@@ -803,74 +795,88 @@ __global__ void __launch_bounds__(kThreads, 1)
             return fmaxf(max3(top8[0], top8[1], top8[2]), max3(max3(top8[3], top8[4], top8[5]), top8[6], top8[7]));
           };
           float top = kNegInf;
-          if constexpr (kCapped) {                         // (and those with a score that is many caps)
-            if (!slow) {
-              load();
-              top = top_of();
-              slow = __any_sync(0xFFFFFFFFu, top > most);
+          if constexpr (!kScored) {
+            load();
+            if (u < plain0 || u >= plain1) {
+              const Row vis(p, w.s, w.row0 + min(my_row, rows - 1), 0);
+              const int k0 = w.span.key0(u);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) hide(vis, k0 + 32 * i, s[i]);
             }
-          }
-          if (slow) {
-            const Row vis = row_here();
+            top = top_of();
+          } else {
+            const bool masked = u < plain0 || u >= plain1;
+            const int key0 = kDistance ? w.span.key0(u) : 0;
+            // Units with hidden keys, and those that a bias does not fall evenly over, go 32 keys at a time through one
+            // short loop, in place in tensor memory, before the rest: few units, and each instruction of an item's
+            // code that is fetched anew takes 5 cycles.
+            bool slow = masked;
+            if constexpr (kDistance) slow = slow || __any_sync(0xFFFFFFFFu, key0 + 127 > my_pos);
+            if constexpr (kCapped) {                         // (and those with a score that is many caps)
+              if (!slow) {
+                load();
+                top = top_of();
+                slow = __any_sync(0xFFFFFFFFu, top > most);
+              }
+            }
+            if (slow) {
+              const Row vis = Row(p, w.s, w.row0 + min(my_row, rows - 1), doc);
+              const int first_key = kDistance ? key0 : w.span.key0(u);
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-              uint32_t x[32];
-              tmem_ld32(s_tmem + 32 * i, x);
-              tmem_ld_wait();
-              const int at = key0 + 32 * i;
-              hide(vis, at, x);
-              if constexpr (kCapped) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(min_nan(__uint_as_float(x[e]), most));
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) cap4(&x[e], p.cap_in);
-              }
-              if constexpr (kDistance) {
-                const float base = static_cast<float>(at - my_pos);
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  x[e] = __float_as_uint(fmaf(__uint_as_float(x[e]), cap_scale, -slope * fabsf(base + e)));
-              }
-              if constexpr (kCapped) hide(vis, at, x);     // (what was hidden before came out as -1)
-              tmem_st32(s_tmem + 32 * i, x);
-            }
-            tmem_st_wait();
-          }
-          if (!kCapped || slow) load();
-          if (!kScored && masked) {
-            const Row vis = row_here();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) hide(vis, key0 + 32 * i, s[i]);
-          }
-          if constexpr (kForm == Form::kCappedDistance) {
-            if (!slow) cap128(s, p.cap_in);
-          }
-          if constexpr (kDistance) {
-            if (!slow) {                                   // left of the row's place the bias grows evenly with the key
-              const uint64_t scale2 = pair(cap_scale, cap_scale), step2 = pair(4.f * slope, 4.f * slope);
-#pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const float base = static_cast<float>(key0 - my_pos + 32 * i);
-                uint64_t bias2[2] = {pair(slope * base, slope * (base + 1.f)), pair(slope * (base + 2.f), slope * (base + 3.f))};
+                uint32_t x[32];
+                tmem_ld32(s_tmem + 32 * i, x);
+                tmem_ld_wait();
+                const int at = first_key + 32 * i;
+                hide(vis, at, x);
+                if constexpr (kCapped) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                  uint64_t& b = bias2[e >> 1 & 1];
-                  const float2 x = unpair(fma2(pair(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])), scale2, b));
-                  s[i][e] = __float_as_uint(x.x), s[i][e + 1] = __float_as_uint(x.y);
-                  if (e < 28) b = add2(b, step2);
+                  for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(min_nan(__uint_as_float(x[e]), most));
+#pragma unroll
+                  for (int e = 0; e < 32; e += 4) cap4(&x[e], p.cap_in);
+                }
+                if constexpr (kDistance) {
+                  const float base = static_cast<float>(at - my_pos);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    x[e] = __float_as_uint(fmaf(__uint_as_float(x[e]), cap_scale, -slope * fabsf(base + e)));
+                }
+                if constexpr (kCapped) hide(vis, at, x);     // (what was hidden before came out as -1)
+                tmem_st32(s_tmem + 32 * i, x);
+              }
+              tmem_st_wait();
+            }
+            if (!kCapped || slow) load();
+            if constexpr (kForm == Form::kCappedDistance) {
+              if (!slow) cap128(s, p.cap_in);
+            }
+            if constexpr (kDistance) {
+              if (!slow) {                                   // left of the row's place the bias grows evenly with the key
+                const uint64_t scale2 = pair(cap_scale, cap_scale), step2 = pair(4.f * slope, 4.f * slope);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float base = static_cast<float>(key0 - my_pos + 32 * i);
+                  uint64_t bias2[2] = {pair(slope * base, slope * (base + 1.f)), pair(slope * (base + 2.f), slope * (base + 3.f))};
+#pragma unroll
+                  for (int e = 0; e < 32; e += 2) {
+                    uint64_t& b = bias2[e >> 1 & 1];
+                    const float2 x = unpair(fma2(pair(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])), scale2, b));
+                    s[i][e] = __float_as_uint(x.x), s[i][e + 1] = __float_as_uint(x.y);
+                    if (e < 28) b = add2(b, step2);
+                  }
                 }
               }
             }
-          }
-          if constexpr (kForm == Form::kCapped) {
-            if (!slow) {                                   // (the largest result is that of the largest score)
-              if (top != kNegInf) top = -rcp_fast(1.f + exp2_fast(top * p.cap_in));
-              cap128(s, p.cap_in);
+            if constexpr (kForm == Form::kCapped) {
+              if (!slow) {                                   // (the largest result is that of the largest score)
+                if (top != kNegInf) top = -rcp_fast(1.f + exp2_fast(top * p.cap_in));
+                cap128(s, p.cap_in);
+              } else {
+                top = top_of();
+              }
             } else {
               top = top_of();
             }
-          } else {
-            top = top_of();
           }
           // (the first finite maximum after none needs no rescaling: O and l are zero)
           const bool renew = top > m && (m == kNegInf || (top - m) * scale > kLazy);
