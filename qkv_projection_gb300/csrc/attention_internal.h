@@ -1,5 +1,5 @@
 // Host-side interface of the rotary and paged-attention kernels (rope.cu,
-// paged_decode.cu, paged_chunk.cu), beside kaio_internal.h.
+// paged_decode*.cu, paged_chunk*.cu), beside kaio_internal.h.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -7,9 +7,14 @@
 // which the GPU gets to them.
 //
 // What bounds the bookkeeping is latency: a step looks at some hundred rows and, to find free
-// pages, at page_refs once (2 MB for half a million pages). So each operator is one launch
-// (a fork two), and where all pages have to be counted before any can be given out, the
-// kernel is one cluster of 16 CTAs, which can wait for one another without a workspace.
+// pages, at page_refs once (2 MB for half a million pages: 0.3 us). So each operator is one launch
+// (the fork of a large table two), and where all pages have to be counted before any can be given
+// out, the kernel is one CTA, or one cluster of 16, whose CTAs can wait for one another without a workspace.
+// Of the GPU's time (in a graph) a step of 62 sequences takes 7.5 us (pages and slots 5, the cut 2.5), 256
+// sequences with 52000 new positions in a pool of 250000 pages 15, a compaction of half a million pages 14-17
+// (4700 cycles to count, 5000 for the table, 1000-2500 each time the cluster meets), a fork of 64 rows 2.9, of 512 rows
+// with 960000 places 6.6. Among others, not in a graph, a call is bound by the host: 2.3 us for a cut, 4.5 where
+// results are made.
 #include <algorithm>
 #include <cstdint>
 
@@ -20,7 +25,10 @@ namespace kaio {
 namespace {
 
 // ------------------------------------------------------------------- copying
-// Page src[i] to page dst[i] of every cache: blocks of kCopyThreads x kCopyVecs 16-byte pieces.
+// Page src[i] to page dst[i] of every cache: blocks of kCopyThreads x kCopyVecs 16-byte pieces, four
+// loads of a thread in flight. Bound by memory: 500 pages of 64 KB in 16 caches, 1.05 GB, take 155.6 us, 6.74
+// TB/s, what a plain copy reaches; 4 pages in 64 caches 3.1 us of the GPU and 6.4 of the host, which
+// looks at 64 tensors.
 constexpr int kCopyThreads = 256, kCopyVecs = 4;
 
 template <bool kDense>

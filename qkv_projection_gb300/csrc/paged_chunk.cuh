@@ -7,10 +7,10 @@
 //   S = Q K^T          tcgen05.mma, Q and K in shared memory, S (f32) in TMEM
 //   P = exp2(c S - m)  one thread per row: S from TMEM, P (16 bit) over S in TMEM
 //   O += P V           tcgen05.mma, P from TMEM, V in shared memory, O (f32) in TMEM
-// with the online softmax of paged_decode.cu in its lazy form: the reference m of
+// with the online softmax of paged_decode.cuh in its lazy form: the reference m of
 // a row is renewed, and O and the sum rescaled, only when the maximum has grown
 // by more than 2^8, so a renewal is rare; sums are of the unrounded f32 weights. In f16
-// the exponents are raised by 7 (for the reason in paged_decode.cu): the largest weight
+// the exponents are raised by 7 (for the reason in paged_decode.cuh): the largest weight
 // of a row lies between 2^7 and 2^15, of the 65504 that fit, and what is lost 2^-32 or
 // more below it.
 //
@@ -44,6 +44,23 @@
 // the memory's rate. Such a unit counts 3 in the line of work, one of 256 rows 4 (a mixed
 // step of 31 single tokens and 512 new ones: 136 us with equal counts, 121 us so, 114 with
 // the cost of an item).
+//
+// Scores of other forms (a cap, a bias that grows with distance, documents, prefixes; each a
+// kernel of its own): what a row's scores go through happens in the same registers, between the
+// load from TMEM and the maximum. The chain of a half is longer by it, so these are bound by the softmax warps:
+// - a cap costs a second exponential and a quarter of a reciprocal a score. The exponential unit takes 4 cycles
+//   a warp's exponential, 8 a reciprocal: 10 cycles a score where 4.5 were, 11 measured for the whole sequence alone, 12.3 with one
+//   warp; two halves' 128 scores then fill 2800 of a unit's 5000 cycles. 4096 tokens over 16384: 1050 us, 0.92 PFLOP/s.
+// - a bias makes the nearest keys the heaviest, so the tiles of its kernels run from the last to the first: from the
+//   first on, most tiles would raise a steep head's maximum and rescale O (1100 us so, 788 in reverse).
+// - units with hidden keys, and those a bias does not fall evenly over (the row's own place lies inside), go
+//   through one short loop of 32 keys at a time, in place in TMEM, before the rest. Unrolled over 128 in registers it cost a
+//   prompt of documents 147 us, rolled 128: such items have two to four units, and code that is fetched anew runs at 5 cycles an
+//   instruction. With a cap the loop also takes scores of more than 10 caps.
+// Measured and not kept: the weights through shared memory, so that the next product of Q and K runs behind the
+// softmax (no wait for it left, but 400 cycles more for each 64 keys' stores and fence, and the issuing thread late: with a cap
+// 1214 us, with slopes 970); units in parts of 64 keys with a product each (1262); two threads a row (1200); halves held half a
+// unit's time apart (1160); a fraction of the waits polled (1233).
 //
 // Warps 0-3 and 4-7: the softmax of the halves; 8, 9: their MMAs; 10: works out the
 // jobs (items, or this CTA's part of one) a few ahead and loads K; 11: loads V. Tiles

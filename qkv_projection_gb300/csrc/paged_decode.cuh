@@ -23,6 +23,10 @@
 // (0.95-0.98 of a measured copy); one token over 131071: 90-91 us (0.87); 16 tokens of 64
 // heads with a window of 4096: 52-54 us (0.75; 5 us of it before the first keys arrive).
 //
+// Scores that are capped or lose with distance cost a few instructions a score, documents and
+// prefixes a comparison in the tiles at their edges; the bytes still bound (64 tokens over contexts of up to
+// 8192 with a cap: 207-209 us, 6.5 TB/s; one token over 1037 keys of 32 heads with slopes: 13.2 us).
+//
 // Short calls are bound by what surrounds the units. One token over 1037 keys, 32 heads
 // (12.0 us): 4 us from the launch to the first copies (the shares, then page ids, then
 // keys: three round trips, in code that is fetched for the first time), 2 us for two

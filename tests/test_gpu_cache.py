@@ -242,3 +242,49 @@ def test_captured_steps_on_another_stream():
     want += cache.compact(b.refs, b.table, b.lens, 4, 9)
     assert [t.tolist() for t in made] == list(want)
     b.same()
+
+
+def test_two_books_at_once_on_streams_of_their_own():
+    """Kernels of one cluster and of one CTA side by side, many times."""
+    import torch
+    books = [Books(40, 300, 40000, 4, seed=21), Books(5, 30, 200, 4, seed=22)]
+    streams = [torch.cuda.Stream() for _ in books]
+    torch.cuda.synchronize()
+    r = random.Random(5)
+    results = [[] for _ in books]
+    for _ in range(15):
+        new = [[r.randint(0, 60 // (1 + k)) for _ in range(b.batch)] for k, b in enumerate(books)]
+        kept = [[r.randint(0, 200) for _ in range(b.batch)] for b in books]
+        parents = [[r.randrange(b.batch) for _ in range(b.batch)] for b in books]
+        args = [[dev(v) for v in (([sum(n[:i]) for i in range(len(n) + 1)]), k, p)] for n, k, p in zip(new, kept, parents)]
+        torch.cuda.synchronize()
+        for k, (b, s, (starts, cut, par)) in enumerate(zip(books, streams, args)):
+            got = kaio.cache_append(*b.books(), starts, sum(new[k]), 4, stream=s)
+            kaio.cache_fork(*b.books(), par, 4, stream=s)
+            kaio.cache_truncate(*b.books(), cut, 4, stream=s)
+            got += kaio.cache_compact(*b.books(), 4, 50, stream=s)
+            results[k].append((new[k], parents[k], kept[k], got))
+    torch.cuda.synchronize()
+    for b, steps in zip(books, results):
+        for new, parents, kept, got in steps:
+            starts = [sum(new[:i]) for i in range(len(new) + 1)]
+            want = cache.append(b.refs, b.table, b.lens, starts, starts[-1], 4)
+            cache.fork(b.refs, b.table, b.lens, parents, 4)
+            cache.truncate(b.refs, b.table, b.lens, kept, 4)
+            want += cache.compact(b.refs, b.table, b.lens, 4, 50)
+            assert [g.tolist() for g in got] == list(want)
+        b.same()
+
+
+def test_results_of_a_call_that_ended_long_ago_are_its_own():
+    """slots, src and dst of one call share memory with each other, and with no later call's."""
+    b = Books(4, 8, 64, 4, seed=23)
+    first = kaio.cache_append(*b.books(), dev([0, 3, 3, 9, 10]), 10, 4)
+    kept = [t.clone() for t in first]
+    for _ in range(5):
+        kaio.cache_append(*b.books(), None, 4, 4)
+        kaio.cache_compact(*b.books(), 4, 7)
+    assert all((x == y).all() for x, y in zip(first, kept))
+    assert first[0].is_contiguous() and first[0].shape == (10,) and first[1].shape == first[2].shape == (4,)
+    first[0].zero_()
+    assert (first[1] == kept[1]).all()

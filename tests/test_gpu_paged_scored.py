@@ -223,3 +223,33 @@ def test_many_tiles_in_documents():
     p = Scored([(700, 900), (1, 2000), (300, 300)], 8, 1, 64, 16, "bfloat16", seed=13)
     p.verify(**extras(p, "cap slopes prefix docs", 9))
     p.verify(**extras(p, "docs", 10))
+
+
+@pytest.mark.parametrize("n", [1, 60])
+def test_rows_behind_the_last_sequence_stay(n):
+    """A padded batch: more rows of q, documents and results than the sequences have tokens."""
+    import torch
+    p = Scored([(n, 200), (n, 90)], 4, 2, 64, 16, seed=14)
+    kw = extras(p, "cap slopes prefix docs", 6)
+    want = p.run(**kw)
+    pad = lambda t, v: torch.cat((t, torch.full((5, *t.shape[1:]), v, dtype=t.dtype, device="cuda")))  # noqa: E731
+    out, lse = torch.full((2 * n + 5, 4, 64), 7.0, device="cuda").half(), torch.full((2 * n + 5, 4), 7.0, device="cuda")
+    wide = dict(kw, doc_starts=pad(kw["doc_starts"], -1))
+    p.run(q=pad(p.q, float("nan")), out=out, lse=lse, **wide)
+    assert (out[:2 * n] == want[0]).all() and (lse[:2 * n] == want[1]).all()
+    assert (out[2 * n:] == 7).all() and (lse[2 * n:] == 7).all()
+
+
+def test_two_calls_at_once_on_streams_of_their_own():
+    import torch
+    a, b = Scored([(70, 900)], 8, 2, 64, 16, seed=15), Scored([(1, 3000), (1, 40)], 8, 2, 64, 16, seed=16)
+    kws = [extras(p, "cap slopes docs", 7) for p in (a, b)]
+    want = [p.run(**kw) for p, kw in zip((a, b), kws)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [kaio.paged_attention_workspace() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [p.run(workspace=ws, stream=s, **kw) for p, kw, ws, s in zip((a, b), kws, spaces, streams)]
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert all((i == j).all() for i, j in zip(x, y))
