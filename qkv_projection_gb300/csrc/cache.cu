@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_append_kernel(const __grid_
     if (lane >= d) upto += add;
   }
   if (lane == 31) warp_need[warp] = upto;
-  cluster_meet();                                        // all counts, nothing given out yet
+  cluster_meet();                                            // all counts, nothing given out yet
   pool_places(pool, sh);
   const int of_warp = warp_need[lane];
   const int all_need = __reduce_add_sync(0xFFFFFFFFu, of_warp);
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_append_kernel(const __grid_
     *place = id;
     p.page_refs[id] = 1;
   }
-  cluster_meet();                                                    // the table is whole
+  cluster_meet();                                            // the table is whole
   constexpr int kEach = 4;                                   // tokens of a thread in work at a time
   for (int t0 = cta * kThreads + tid; t0 < p.tokens; t0 += kEach * step) {
     int row[kEach] = {}, pos[kEach], place[kEach], id[kEach];
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_compact_kernel(const __grid
       left ^= 1u << bit;
     }
   }
-  cluster_meet();                                                    // both lists are whole
+  cluster_meet();                                            // both lists are whole
   const int owner = used < p.num_pages ? used / (32 * kWarps * pool.words) : -1;
   const int moves = owner < 0 ? 0 : min(remote(&sh.below, owner), p.max_moves);
   for (int i = cta * kThreads + tid; i < moves; i += all) {

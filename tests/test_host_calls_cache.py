@@ -47,7 +47,7 @@ def test_scored_attention_the_same_either_way(host, monkeypatch):  # noqa: F811
         same(*both(monkeypatch, lambda: kaio.paged_attention(a["q"], a["kc"], a["vc"], a["table"], a["lens"], a["starts"],
                                                              max_new=4, return_lse=True, workspace=ws, **kw)))
     for error, match, kw in ((ValueError, "slopes", dict(slopes=slopes[:2])), (TypeError, "doc_starts", dict(doc_starts=docs.long())),
-                             (kaio.KaioError, "softcap", dict(softcap=-1.0)), (TypeError, "", dict(softcap="x"))):
+                             (kaio.KaioError, "softcap", dict(softcap=-1.0)), (TypeError, None, dict(softcap="x"))):
         for hold in (False, True):
             with monkeypatch.context() as m, pytest.raises(error, match=match):
                 if hold:
