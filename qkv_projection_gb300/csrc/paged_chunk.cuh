@@ -48,15 +48,16 @@
 // Scores of other forms (a cap, a bias that grows with distance, documents, prefixes; each a
 // kernel of its own): what a row's scores go through happens in the same registers, between the
 // load from TMEM and the maximum. The chain of a half is longer by it, so these are bound by the softmax warps:
-// - a cap costs a second exponential and a quarter of a reciprocal a score. The exponential unit takes 4 cycles
-//   a warp's exponential, 8 a reciprocal: 10 cycles a score where 4.5 were, 11 measured for the whole sequence alone, 12.3 with one
-//   warp; two halves' 128 scores then fill 2800 of a unit's 5000 cycles. 4096 tokens over 16384: 1050 us, 0.92 PFLOP/s.
+// - a cap costs a second exponential and an eighth of a reciprocal a score. The exponential unit takes 4 cycles
+//   a warp's exponential, 9 a reciprocal: 9 cycles a score where 4 were (a quarter: 10, and 11 measured for the whole sequence
+//   alone, 12.3 with one warp); two halves' 128 scores then fill half of a unit's 5000 cycles. 4096 tokens over 16384: 1050
+//   us with a quarter, 1031 with an eighth, 0.93 PFLOP/s.
 // - a bias makes the nearest keys the heaviest, so the tiles of its kernels run from the last to the first: from the
 //   first on, most tiles would raise a steep head's maximum and rescale O (1100 us so, 788 in reverse).
 // - units with hidden keys, and those a bias does not fall evenly over (the row's own place lies inside), go
 //   through one short loop of 32 keys at a time, in place in TMEM, before the rest. Unrolled over 128 in registers it cost a
 //   prompt of documents 147 us, rolled 128: such items have two to four units, and code that is fetched anew runs at 5 cycles an
-//   instruction. With a cap the loop also takes scores of more than 10 caps.
+//   instruction. With a cap the loop also takes scores of more than 5 caps.
 // Measured and not kept: the weights through shared memory, so that the next product of Q and K runs behind the
 // softmax (no wait for it left, but 400 cycles more for each 64 keys' stores and fence, and the issuing thread late: with a cap
 // 1214 us, with slopes 970); units in parts of 64 keys with a product each (1262); two threads a row (1200); halves held half a
@@ -248,8 +249,8 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 // scale / cap. The factor 2 cap goes into what follows, the constant cap into the log-sum. The four
 // share a reciprocal (1/a = bcd / abcd), so c s is at most kCapRange, where the tanh is 1 - 2^-29.
 // Errors, in 2^-23: of exp2 (approximate to 2^-22.5, its argument rounded twice) 0.8 after the
-// quotient's slope of at most a quarter, of the reciprocal, the sum and the products 3.5; so a score is off by at most
-// 24 * 2^-24 caps, and far less where it is large, since the results are small there.
+// quotient's slope of at most a quarter, of the reciprocal, the sum and the products 3.5 (4.5 where eight share one); so a
+// score is off by at most 24 * 2^-24 caps, and far less where it is large, since the results are small there.
 constexpr float kCapRange = 30.f;
 __device__ __forceinline__ void cap4(uint32_t* s, float c) {
   const uint64_t c2 = pair(c, c), minus1 = pair(-1.f, -1.f);
@@ -264,11 +265,11 @@ __device__ __forceinline__ void cap4(uint32_t* s, float c) {
   s[0] = __float_as_uint(u.x), s[1] = __float_as_uint(u.y);
   s[2] = __float_as_uint(v.x), s[3] = __float_as_uint(v.y);
 }
-// The same of 128, sixteen a step and three steps in work at a time: what one waits for (the
-// exponentials, the reciprocal) the others' work covers.
+// The same of 128 scores of at most kCapRange / 2, of which eight share a reciprocal. Sixteen a
+// step and three steps in work at a time: what one waits for (the exponentials, the reciprocal) the others' work covers.
 __device__ __forceinline__ void cap128(uint32_t (&s)[4][32], float c) {
-  uint64_t ab[2][4];
-  float inv[2][4];
+  uint64_t ab[2][4], abcd[2][2];
+  float inv[2][2];
   auto at = [&](int e) -> uint32_t& { return s[e >> 5][e & 31]; };
   auto get = [&](int e) { return pair(__uint_as_float(at(e)), __uint_as_float(at(e + 1))); };
   auto set = [&](int e, uint64_t v) {
@@ -286,25 +287,34 @@ __device__ __forceinline__ void cap128(uint32_t (&s)[4][32], float c) {
       }
     }
     if (b >= 1 && b < 9) {
+      const int now = (b - 1) & 1;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int e = 16 * (b - 1) + 4 * k;
         set(e, fma2(get(e), minus1, minus1));
         set(e + 2, fma2(get(e + 2), minus1, minus1));
-        ab[(b - 1) & 1][k] = mul2(get(e), get(e + 2));
-        const float2 x = unpair(ab[(b - 1) & 1][k]);
-        inv[(b - 1) & 1][k] = rcp_fast(x.x * x.y);
+        ab[now][k] = mul2(get(e), get(e + 2));
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        abcd[now][k] = mul2(ab[now][2 * k], ab[now][2 * k + 1]);
+        const float2 x = unpair(abcd[now][k]);
+        inv[now][k] = rcp_fast(x.x * x.y);
       }
     }
     if (b >= 2) {
+      const int now = b & 1;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int e = 16 * (b - 2) + 4 * k;
-        const float2 x = unpair(ab[b & 1][k]);
-        const float r = inv[b & 1][k];
-        const uint64_t of_both = pair(r * x.y, r * x.x), first = get(e);
-        set(e, mul2(of_both, get(e + 2)));
-        set(e + 2, mul2(of_both, first));
+      for (int k = 0; k < 2; ++k) {
+        const float2 x = unpair(abcd[now][k]);
+        const uint64_t of_all = pair(inv[now][k] * x.y, inv[now][k] * x.x);
+        const uint64_t of_ab = mul2(of_all, ab[now][2 * k + 1]), of_cd = mul2(of_all, ab[now][2 * k]);
+        const int e = 16 * (b - 2) + 8 * k;
+        const uint64_t first = get(e), third = get(e + 4);
+        set(e, mul2(of_ab, get(e + 2)));
+        set(e + 2, mul2(of_ab, first));
+        set(e + 4, mul2(of_cd, get(e + 6)));
+        set(e + 6, mul2(of_cd, third));
       }
     }
   }
@@ -834,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!slow) {
                 load();
                 top = top_of();
-                slow = __any_sync(0xFFFFFFFFu, top > most);
+                slow = __any_sync(0xFFFFFFFFu, top > 0.5f * most);
               }
             }
             if (slow) {
