@@ -1038,12 +1038,11 @@ int kaio_cache_copy_pages(const kaio_cache_copy_args* a, kaio_stream_t stream_) 
     KAIO_TRY(check_overlap(lists, 2, &c, 1));
   }
   KAIO_TRY(current_device(&dev, &info));
-  KAIO_TRY(check_on_device(lists, 2, dev));
-  Span spans[kaio::kCacheMaxCaches];
+  Span spans[2 + kaio::kCacheMaxCaches] = {lists[0], lists[1]};
   for (int first = 0; first < a->caches; first += kaio::kCacheMaxCaches) {
     const int n = std::min(a->caches - first, kaio::kCacheMaxCaches);
-    for (int i = 0; i < n; ++i) spans[i] = span_of(first + i);
-    KAIO_TRY(check_on_device(spans, n, dev));
+    for (int i = 0; i < n; ++i) spans[2 + i] = span_of(first + i);
+    KAIO_TRY(check_on_device(spans, 2 + n, dev));
   }
   for (int first = 0; first < a->caches; first += kaio::kCacheMaxCaches) {
     const int n = std::min(a->caches - first, kaio::kCacheMaxCaches);
@@ -1098,7 +1097,7 @@ int cache_impl(Upkeep op, const kaio_cache_args* a, cudaStream_t stream) {
     if (T || M) return fail(KAIO_ERR_INVALID_VALUE, "tokens and max_moves must be 0 without sequences");
     return current_device(&dev, &info);
   }
-  Span in[1], out[6];
+  Span in[1], out[7];
   int n_in = 0, n_out = 0;
   auto add = [](Span* to, int* n, const char* name, const void* p, int64_t count) {
     if (count > 0) to[(*n)++] = {name, p, static_cast<size_t>(count) * 4};     // (what is empty may be null)
@@ -1120,7 +1119,7 @@ int cache_impl(Upkeep op, const kaio_cache_args* a, cudaStream_t stream) {
   KAIO_TRY(check_aligned4(out, n_out));
   KAIO_TRY(check_overlap(in, n_in, out, n_out));
   KAIO_TRY(current_device(&dev, &info));
-  KAIO_TRY(check_on_device(in, n_in, dev));
+  for (int i = 0; i < n_in; ++i) out[n_out++] = in[i];       // (one query for each allocation of either)
   KAIO_TRY(check_on_device(out, n_out, dev));
 
   kaio::CacheParams p{};

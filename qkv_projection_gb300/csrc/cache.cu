@@ -382,7 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_append_kernel(const __grid_
 
 // Of the U used pages those at U and above move to the free ones below U: the i-th highest of
 // them to the i-th lowest of those, up to max_moves. Until the table is renumbered, a moved page's
-// count says where it went (kGone + its new place), so that a place needs one look.
+// count says where it went (kGone + its new place), so that a place needs one look (halving in the list of moved
+// pages instead, from shared memory: two meetings fewer, but 24.9 us for half a million pages, and 17.5 so).
 constexpr int kGone = INT32_MIN;
 
 __global__ void __launch_bounds__(kThreads, 1) cache_compact_kernel(const __grid_constant__ CacheParams p) {

@@ -288,3 +288,23 @@ def test_results_of_a_call_that_ended_long_ago_are_its_own():
     assert first[0].is_contiguous() and first[0].shape == (10,) and first[1].shape == first[2].shape == (4,)
     first[0].zero_()
     assert (first[1] == kept[1]).all()
+
+
+@pytest.mark.parametrize("pages,moves", [(70000, 33000), (70000, 32768), (40000, 32769), (5000, 5000), (100, 1)])
+def test_compactions_of_many_pages(pages, moves):
+    """Long lists; only the upper pages are in use."""
+    import torch
+    width = pages // 8
+    b = Books(4, width, pages, 2, seed=pages)
+    at = pages - 4 * (width - 1)
+    for row in range(4):
+        ids = list(range(at + row, pages, 4))[:width - 1]
+        b.r.shuffle(ids)
+        b.table[row][:len(ids)] = ids
+        b.lens[row] = 2 * len(ids) - row % 2
+    b.refs[:] = cache.count(b.table, b.lens, 2, pages)
+    b.d_table.copy_(dev(b.table)), b.d_lens.copy_(dev(b.lens)), b.d_refs.copy_(dev(b.refs))
+    b.compact(moves)
+    b.fork([3, 2, 1, 0])
+    b.compact(pages)
+    assert torch.equal(b.d_refs > 0, torch.arange(pages, device="cuda") < int((b.d_refs > 0).sum()))
