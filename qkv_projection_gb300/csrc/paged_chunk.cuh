@@ -61,8 +61,9 @@
 // Measured and not kept: the weights through shared memory, so that the next product of Q and K runs behind the
 // softmax (no wait for it left, but 400 cycles more for each 64 keys' stores and fence, and the issuing thread late: with a cap
 // 1214 us, with slopes 970); units in parts of 64 keys with a product each (1262); two threads a row (1200); halves held half a
-// unit's time apart (1160); waits polled (1233); the next unit's first 64 scores computed behind this one's softmax, in
-// the half of the scores' place that the weights leave free (1103, with slopes 813: one more product, wait and commit).
+// unit's time apart (1160); waits polled (1233); the next unit's scores in two products of 64 keys, the first behind
+// this one's softmax or between its two products (1103 to 1155, with slopes 813 to 846: a product of 64 keys takes the tensor
+// cores about as long as one of 128).
 //
 // Warps 0-3 and 4-7: the softmax of the halves; 8, 9: their MMAs; 10: works out the
 // jobs (items, or this CTA's part of one) a few ahead and loads K; 11: loads V. Tiles
