@@ -9,7 +9,7 @@
 // What bounds the bookkeeping is latency: a step looks at some hundred rows and, to find free
 // pages, at page_refs once (2 MB for half a million pages: 0.3 us). So each operator is one launch
 // (the fork of a large table two), and where all pages have to be counted before any can be given
-// out, the kernel is one CTA, or one cluster of 16, whose CTAs can wait for one another without a workspace.
+// out, the kernel is one CTA, or one cluster of up to 16, whose CTAs can wait for one another without a workspace.
 // Of the GPU's time (in a graph) a step of 62 sequences takes 7.5 us (pages and slots 5, the cut 2.5), 256
 // sequences with 52000 new positions in a pool of 250000 pages 15, a compaction of half a million pages 14-17
 // (4700 cycles to count, 5000 for the table, 1000-2500 each time the cluster meets), a fork of 64 rows 2.9, of 512 rows
@@ -486,11 +486,14 @@ cudaError_t launch_pool(CacheParams p, int ctas, size_t smem, cudaStream_t strea
   return launch_cluster<kKernel>(ctas, kThreads, smem + static_cast<size_t>(p.warp_words) * kWarps * 4, stream, p);
 }
 
-// One CTA as long as it needs few rounds for the pages (16 a thread), table entries (8) and
-// tokens (1); else a cluster of 16.
+// CTAs by pages, table entries (read once: a quarter of a page's work) and tokens (four). Of the GPU's time in
+// a graph, with 1, 4, 8 and 16 CTAs: a token each for 16 rows in 5200 pages 6.8, 8.4, 8.6, 9.6 us; for 31 in 20400
+// 10.2, 10.2, 10.5, 11.5; 62 in 40400 11.8, 9.8, 10.0, 10.9; 124 in 80500 16.0, 12.1, 10.5, 11.3; 124 in 160900 26.6, 15.2,
+// 13.5, 12.5. 2593 tokens in 20400 pages 11.3, 10.9, 11.1, 11.9. Compaction of 20400 pages, 16000 entries 8.4,
+// 9.0, 9.2, 9.9; 40400 and 32000 11.9, 9.0, 9.0, 10.4; 80500 and 64000 18.0, 10.4, 8.7, 10.0; 160900 and 128000 29, 14.4, 10.6, 10.0.
 int ctas_for(const CacheParams& p, long long entries, int tokens) {
-  const long long rounds = p.num_pages / (16 * kThreads) + entries / (8 * kThreads) + tokens / kThreads;
-  return rounds <= 3 ? 1 : kMaxCtas;
+  const long long work = p.num_pages + entries / 4 + 4ll * tokens;
+  return work <= 28 * 1024 ? 1 : work <= 64 * 1024 ? 4 : work <= 128 * 1024 ? 8 : kMaxCtas;
 }
 
 }  // namespace
@@ -504,14 +507,15 @@ cudaError_t launch_cache_copy(const CacheCopyParams& p, int caches, int pairs, b
 int cache_copy_blocks(int pieces) { return (pieces + kCopyThreads * kCopyVecs - 1) / (kCopyThreads * kCopyVecs); }
 
 cudaError_t launch_cache_fork(const CacheParams& p, cudaStream_t stream) {
-  // Up to sixteen places for a thread of sixteen CTAs: those are one cluster, in one launch. Otherwise a CTA
-  // takes eight columns, a 32-byte sector of each row, and a second launch writes the lengths (64 rows of 252 places:
-  // 11.5 us among others with two launches, bound by the host).
+  // Up to eight places for a thread of sixteen CTAs: those are one cluster, in one launch. Otherwise a CTA
+  // takes eight columns, a 32-byte sector of each row, and a second launch writes the lengths. One launch and two, of the GPU in
+  // a graph and among others, where the host bounds: 16200 places 2.9 and 3.5 us, 9-11 and 12.4; 64400 places 5.9 and
+  // 3.9, 9-11 and 13; 128800 places 9.4 and 4.5, 12.5 and 12.5.
   const size_t rows = 2 * static_cast<size_t>(p.batch);
   auto bytes = [&](int cols_log2) { return (rows + (static_cast<size_t>(p.batch) << cols_log2)) * 4; };
   int cols_log2 = 3;
   while (kMaxCtas << cols_log2 < p.max_pages) ++cols_log2;
-  if (static_cast<size_t>(p.batch) << cols_log2 <= 16 * kForkThreads) {
+  if (static_cast<size_t>(p.batch) << cols_log2 <= 8 * kForkThreads) {
     int ctas = 1;
     while (ctas << cols_log2 < p.max_pages) ctas *= 2;
     return launch_cluster<cache_fork_kernel<true>>(ctas, kForkThreads, bytes(cols_log2), stream, p, cols_log2);
