@@ -53,7 +53,8 @@
 //   alone, 12.3 with one warp); two halves' 128 scores then fill half of a unit's 5000 cycles. 4096 tokens over 16384: 1050
 //   us with a quarter, 1031 with an eighth, 0.93 PFLOP/s.
 // - a bias makes the nearest keys the heaviest, so the tiles of its kernels run from the last to the first: from the
-//   first on, most tiles would raise a steep head's maximum and rescale O (1100 us so, 788 in reverse).
+//   first on, most tiles would raise a steep head's maximum and rescale O (4096 tokens over 16384: 1100 us so, 788 in reverse,
+//   775 since pieces that a warp sees nothing of are not worked on).
 // - units with hidden keys, and those a bias does not fall evenly over (the row's own place lies inside), go
 //   through one short loop of 32 keys at a time, in place in TMEM, before the rest. Unrolled over 128 in registers it cost a
 //   prompt of documents 147 us, rolled 128: such items have two to four units, and code that is fetched anew runs at 5 cycles an
@@ -493,7 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           int id = p.num_pages;                             // out of range: the box is filled with zeros
           if (lane < boxes && u < u1) {
             const int k0 = span.key0(u) + lane * box_keys;
-            if (k0 < span.hi && (k0 + box_keys > span.lo || (k0 < span.first && (!kScored || k0 + box_keys > span.from)))) id = table[k0 >> p.page_shift];
+            const bool in_first = k0 < span.first && (!kScored || k0 + box_keys > span.from);
+            if (k0 < span.hi && (k0 + box_keys > span.lo || in_first)) id = table[k0 >> p.page_shift];
             if (id < 0 || id > p.num_pages) id = p.num_pages;
           }
           return id;
@@ -798,11 +800,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             q_next = ok && works(nx.mode);
             if (q_next) fetch_q(nx);
           }
-          // Bits of those of 32 keys from `at` on that a row sees, and the others' scores to -inf.
-          auto hide = [&](const Row& vis, int at, uint32_t (&x)[32]) {
+          // Bits of those of 32 keys from `at` on that a row sees; the others' scores to -inf.
+          auto seen_of = [&](const Row& vis, int at) {
             auto below = [&](int x) { return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1; };
             uint32_t seen = below(vis.hi - at) & (~below(vis.lo - at) | below(vis.first - at));
             if (kScored) seen &= ~below(vis.from - at);
+            return seen;
+          };
+          auto hide = [&](uint32_t seen, uint32_t (&x)[32]) {
             if (__all_sync(0xFFFFFFFFu, seen == 0xFFFFFFFFu)) return;
 #pragma unroll
             for (int e = 0; e < 32; ++e)
@@ -830,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const Row vis(p, w.s, w.row0 + min(my_row, rows - 1), 0);
               const int k0 = w.span.key0(u);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) hide(vis, k0 + 32 * i, s[i]);
+              for (int i = 0; i < 4; ++i) hide(seen_of(vis, k0 + 32 * i), s[i]);
             }
             top = top_of();
           } else {
@@ -854,10 +859,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
               for (int i = 0; i < 4; ++i) {
                 uint32_t x[32];
+                const int at = first_key + 32 * i;
+                const uint32_t seen = seen_of(vis, at);
+                if ((kCapped || kDistance) && __all_sync(0xFFFFFFFFu, seen == 0)) {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(kNegInf);
+                  tmem_st32(s_tmem + 32 * i, x);
+                  continue;
+                }
                 tmem_ld32(s_tmem + 32 * i, x);
                 tmem_ld_wait();
-                const int at = first_key + 32 * i;
-                hide(vis, at, x);
+                hide(seen, x);
                 if constexpr (kCapped) {
 #pragma unroll
                   for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(min_nan(__uint_as_float(x[e]), most));
@@ -870,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   for (int e = 0; e < 32; ++e)
                     x[e] = __float_as_uint(fmaf(__uint_as_float(x[e]), cap_scale, -slope * fabsf(base + e)));
                 }
-                if constexpr (kCapped) hide(vis, at, x);     // (what was hidden before came out as -1)
+                if constexpr (kCapped) hide(seen, x);     // (what was hidden before came out as -1)
                 tmem_st32(s_tmem + 32 * i, x);
               }
               tmem_st_wait();
