@@ -82,7 +82,7 @@ __device__ __forceinline__ void cluster_meet() {
 // what parent and row share already costs nothing. Lengths may be written once every CTA has
 // read them: by the kernel itself where its CTAs are one cluster (kOne), by another one otherwise.
 constexpr int kForkThreads = 512;
-constexpr int kNotHeld = INT32_MIN;
+constexpr int kNotHeld = INT32_MIN;                          // (what stands in a held place may be that, too: no page)
 
 template <bool kOne>
 __global__ void __launch_bounds__(kForkThreads) cache_fork_kernel(const __grid_constant__ CacheParams p, int cols_log2) {
@@ -111,9 +111,9 @@ __global__ void __launch_bounds__(kForkThreads) cache_fork_kernel(const __grid_c
     const int row = i >> cols_log2, c = i & (cols - 1), parent = parents[row];
     if (parent < 0) continue;
     const int before = tile[i], now = tile[(parent << cols_log2) + c];
-    if (before == now) continue;
+    if (before == now && now != kNotHeld) continue;
     if (is_page(p, before)) atomicSub(p.page_refs + before, 1);
-    if (now != kNotHeld) p.page_table[row * p.table_stride + col0 + c] = now;
+    if (now != kNotHeld || col0 + c < places(p, lens[parent])) p.page_table[row * p.table_stride + col0 + c] = now;
     if (is_page(p, now)) atomicAdd(p.page_refs + now, 1);
   }
   if (kOne && blockIdx.x == 0) {

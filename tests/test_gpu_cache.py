@@ -165,6 +165,23 @@ def test_lengths_and_entries_that_make_no_sense():
     b.truncate([1, 0, 2, 7])
 
 
+@pytest.mark.parametrize("batch", [3, 700])
+def test_forks_of_entries_of_every_value(batch):
+    """A held entry outside the pool is copied as it stands, and what stood there before it is gone."""
+    b = Books(batch, 12, 40, 4, seed=7)
+    odd = (-2 ** 31, -2 ** 31 + 1, -1, 40, 2 ** 31 - 1)
+    for i in range(batch):
+        b.lens[i] = (13, 30, 0)[i % 3]
+        b.table[i] = [odd[(i + j) % 5] if i % 3 else 7 for j in range(12)]
+    b.d_lens.copy_(dev(b.lens))
+    b.d_table.copy_(dev(b.table))
+    b.refs[7] = 4 * len(b.lens[::3])
+    b.d_refs.copy_(dev(b.refs))
+    r = random.Random(batch)
+    b.fork([1, 2, 1] + [r.randint(-1, batch) for _ in range(batch - 3)])
+    b.fork([r.randint(-1, batch) for _ in range(batch)])
+
+
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
 @pytest.mark.parametrize("layout", ["slots_first", "heads_first", "one_buffer", "padded", "sliced"])
 @pytest.mark.parametrize("page,kv_heads,d,caches", [(16, 2, 64, 2), (1, 1, 8, 3), (32, 8, 128, 5), (24, 3, 72, 70), (1024, 1, 256, 1)])
