@@ -893,17 +893,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if constexpr (kDistance) {
               if (!slow) {                                   // left of the row's place the bias grows evenly with the key
-                const uint64_t scale2 = pair(cap_scale, cap_scale), step2 = pair(4.f * slope, 4.f * slope);
+                // From the nearest of 32 keys outwards: each sum is then off by 2^-24 of at most its own key's bias, where sums that
+                // began at the far end would carry that end's roundings to keys whose bias is next to nothing.
+                const uint64_t scale2 = pair(cap_scale, cap_scale), step2 = pair(-4.f * slope, -4.f * slope);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  const float base = static_cast<float>(key0 - my_pos + 32 * i);
+                  const float base = static_cast<float>(key0 - my_pos + 32 * i + 28);
                   uint64_t bias2[2] = {pair(slope * base, slope * (base + 1.f)), pair(slope * (base + 2.f), slope * (base + 3.f))};
 #pragma unroll
-                  for (int e = 0; e < 32; e += 2) {
+                  for (int e = 30; e >= 0; e -= 2) {
                     uint64_t& b = bias2[e >> 1 & 1];
                     const float2 x = unpair(fma2(pair(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])), scale2, b));
                     s[i][e] = __float_as_uint(x.x), s[i][e + 1] = __float_as_uint(x.y);
-                    if (e < 28) b = add2(b, step2);
+                    if (e >= 4) b = add2(b, step2);
                   }
                 }
               }
