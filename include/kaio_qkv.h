@@ -436,7 +436,8 @@ int kaio_paged_attention(const kaio_paged_attention_args* args, kaio_stream_t st
  *
  *   softcap     0: none; else in (0, 256], with 2 log2(e) |scale| / softcap in 2^-100..2^100
  *               (or scale 0). Scores are then good to 24 * 2^-24 softcap.
- *   slopes      f32 [heads], finite, of either sign; null: none
+ *   slopes      f32 [heads], finite, of either sign; null: none. (A key whose bias passes f32's range
+ *               is as good as hidden; with a slope below zero it makes the token's results NaN.)
  *   prefix_lens i32 [batch]; null: none. The first prefix_lens[b] positions (cut to 0..kv_lens[b])
  *               are seen by all new tokens, also by those before them.
  *   doc_starts  i32 [tokens]; null: 0. The position where the document of each token begins (below 0: 0),

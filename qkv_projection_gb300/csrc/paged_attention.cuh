@@ -30,6 +30,7 @@ __host__ __device__ constexpr bool is_capped(Form f) { return f == Form::kCapped
 __host__ __device__ constexpr bool has_distance(Form f) { return f == Form::kDistance || f == Form::kCappedDistance; }
 
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kMaxFloat = 3.4028234663852886e38f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -423,6 +424,13 @@ __device__ bool paged_share(const PagedParams& p, int cta, int grid, long long* 
   }
   __syncthreads();
   return true;
+}
+
+// A slope times log2(e). Where that passes f32's range it is the largest number: the token's own key, at a
+// distance of zero, then keeps a bias of zero.
+__device__ __forceinline__ float slope_log2(float slope) {
+  const float s = slope * kLog2e;
+  return fabsf(s) <= kMaxFloat ? s : copysignf(kMaxFloat, s) + 0.f * slope;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {

@@ -777,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = w.row0 + min(my_row, rows - 1);
         doc = paged_doc<kScored>(p, w.s, r);
         my_pos = w.s.kv - w.s.n + p.group_div.div(r);
-        if (kDistance) slope = p.slopes[w.h * p.group + r - p.group_div.div(r) * p.group] * kLog2e;
+        if (kDistance) slope = slope_log2(p.slopes[w.h * p.group + r - p.group_div.div(r) * p.group]);
       }
       if (works(mode)) {
         if (!q_sent) {

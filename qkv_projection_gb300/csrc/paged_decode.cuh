@@ -272,8 +272,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     float slope_a = 0.f, slope_b = 0.f;
     if (has_distance(kForm)) {
       const int ra = row0 + min(row_a, rows - 1), rb = row0 + min(row_b, rows - 1);
-      slope_a = p.slopes[head0 + ra - p.group_div.div(ra) * p.group] * kLog2e;
-      slope_b = p.slopes[head0 + rb - p.group_div.div(rb) * p.group] * kLog2e;
+      slope_a = slope_log2(p.slopes[head0 + ra - p.group_div.div(ra) * p.group]);
+      slope_b = slope_log2(p.slopes[head0 + rb - p.group_div.div(rb) * p.group]);
     }
 
     float o[kDim / 8][4];
