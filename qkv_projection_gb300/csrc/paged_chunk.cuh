@@ -912,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if constexpr (kForm == Form::kCapped) {
               if (!slow) {                                   // (the largest result is that of the largest score)
-                if (top != kNegInf) top = -rcp_fast(1.f + exp2_fast(top * p.cap_in));
+                top = -rcp_fast(1.f + exp2_fast(top * p.cap_in));   // (of an infinite one, too)
                 cap128(s, p.cap_in);
               } else {
                 top = top_of();
