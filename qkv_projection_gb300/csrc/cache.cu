@@ -522,7 +522,7 @@ cudaError_t launch_cache_fork(const CacheParams& p, cudaStream_t stream) {
   }
   cols_log2 = 3;
   while (bytes(cols_log2) > kCacheSmem) --cols_log2;
-  const int ctas = (p.max_pages + (1 << cols_log2) - 1) >> cols_log2;
+  const int ctas = std::max(1, (p.max_pages + (1 << cols_log2) - 1) >> cols_log2);     // (without columns: for the lengths)
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(cache_fork_kernel<false>), kCacheSmem);
   if (e == cudaSuccess)
     e = launch_dependent(cache_fork_kernel<false>, ctas, kForkThreads, static_cast<int>(bytes(cols_log2)), stream, p, cols_log2);
