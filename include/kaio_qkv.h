@@ -542,6 +542,8 @@ int kaio_cache_copy_pages(const kaio_cache_copy_args* args, kaio_stream_t stream
  * max_pages; q_starts null with tokens != batch; a null pointer; two arrays
  * that overlap; memory of another device; KAIO_ERR_MISALIGNED (4 bytes). batch == 0
  * returns KAIO_OK without a launch (append needs tokens == 0 then, compact max_moves == 0).
+ * KAIO_ERR_CUDA where the device places fewer than 16 thread blocks as one cluster and the pages
+ * do not fit in the shared memory of those: with 8, above some 5400 rows of an append next to 2^23 pages.
  * Fields that an entry does not name are not used.
  */
 typedef struct {
@@ -566,6 +568,13 @@ int kaio_cache_fork(const kaio_cache_args* args, kaio_stream_t stream);
 int kaio_cache_append(const kaio_cache_args* args, kaio_stream_t stream);
 int kaio_cache_truncate(const kaio_cache_args* args, kaio_stream_t stream);
 int kaio_cache_compact(const kaio_cache_args* args, kaio_stream_t stream);
+
+/*
+ * Test entry: kaio_cache_fork (op 0), kaio_cache_append (1) or kaio_cache_compact (2) on a
+ * device that places no more than `most` (1 or more) thread blocks as one cluster. Further error
+ * (KAIO_ERR_INVALID_VALUE): another op, most below 1.
+ */
+int kaio_debug_cache_cluster_limit(int op, const kaio_cache_args* args, int32_t most, kaio_stream_t stream);
 
 /*
  * Dequantise packed INT4 weights to f16, exactly as the projection kernels do

@@ -1072,7 +1072,7 @@ namespace {
 
 enum class Upkeep { kFork, kAppend, kTruncate, kCompact };
 
-int cache_impl(Upkeep op, const kaio_cache_args* a, cudaStream_t stream) {
+int cache_impl(Upkeep op, const kaio_cache_args* a, cudaStream_t stream, int most_ctas = 0) {
   if (a == nullptr) return fail(KAIO_ERR_INVALID_VALUE, "args is a null pointer");
   if (a->struct_size != sizeof(*a))
     return fail(KAIO_ERR_INVALID_VALUE, "struct_size %u is not sizeof(kaio_cache_args) (%zu)", a->struct_size, sizeof(*a));
@@ -1130,10 +1130,14 @@ int cache_impl(Upkeep op, const kaio_cache_args* a, cudaStream_t stream) {
   p.batch = a->batch, p.max_pages = a->max_pages, p.num_pages = a->num_pages, p.page_size = a->page_size;
   p.tokens = a->tokens, p.max_moves = a->max_moves;
   p.page_div = kaio::FastDiv(static_cast<uint32_t>(a->page_size));
+  p.most_ctas = most_ctas;
   const cudaError_t e = op == Upkeep::kFork       ? kaio::launch_cache_fork(p, stream)
                         : op == Upkeep::kAppend   ? kaio::launch_cache_append(p, stream)
                         : op == Upkeep::kTruncate ? kaio::launch_cache_truncate(p, stream)
                                                   : kaio::launch_cache_compact(p, stream);
+  if (e == cudaErrorNotSupported)
+    return fail(KAIO_ERR_CUDA, "%d pages and %d sequences need more thread blocks side by side than this device places", a->num_pages,
+                a->batch);
   if (e != cudaSuccess) return cuda_fail(e, "cache upkeep launch");
   return KAIO_OK;
 }
@@ -1158,6 +1162,14 @@ int kaio_cache_truncate(const kaio_cache_args* args, kaio_stream_t stream) {
 int kaio_cache_compact(const kaio_cache_args* args, kaio_stream_t stream) {
   g_last_error.clear();
   return cache_impl(Upkeep::kCompact, args, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kaio_debug_cache_cluster_limit(int op, const kaio_cache_args* args, int32_t most, kaio_stream_t stream) {
+  g_last_error.clear();
+  const Upkeep ops[] = {Upkeep::kFork, Upkeep::kAppend, Upkeep::kCompact};
+  if (op < 0 || op > 2) return fail(KAIO_ERR_INVALID_VALUE, "op (%d) must be in 0..2", op);
+  if (most < 1) return fail(KAIO_ERR_INVALID_VALUE, "most (%d) must be positive", most);
+  return cache_impl(ops[op], args, reinterpret_cast<cudaStream_t>(stream), most);
 }
 
 int kaio_dequant_int4_debug(const uint32_t* w, const void* s, void* out, uint32_t K, uint32_t N,

@@ -451,39 +451,68 @@ __global__ void __launch_bounds__(kThreads, 1) cache_compact_kernel(const __grid
 
 // A launch as one cluster of `ctas` CTAs (one CTA: as it is), which may begin while the kernel
 // before it runs, and waits for it.
-template <auto kKernel, typename... Args>
-cudaError_t launch_cluster(int ctas, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
-  // (set once for a device; 16 CTAs are more than every device of the architecture takes)
-  thread_local uint64_t allowed = 0;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess && (dev >= 64 || !(allowed >> dev & 1))) {
-    e = ensure_smem_limit(reinterpret_cast<const void*>(kKernel), kCacheSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess && dev < 64) allowed |= 1ull << dev;
-  }
-  if (e != cudaSuccess) return e;
+cudaLaunchConfig_t cluster_config(int ctas, int threads, size_t smem, cudaStream_t stream, cudaLaunchAttribute (&attr)[2]) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = static_cast<unsigned>(ctas), attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = ctas > 1 ? 2 : 1;
+  return cfg;
+}
+
+// How many CTAs of a kernel the current device places as one cluster, up to kMaxCtas. 8 are portable; 16 need as
+// many SMs of one group, which a part of a device or another of the architecture may not have. Asked once for a device.
+template <auto kKernel>
+cudaError_t cluster_limit(int threads, int* most) {
+  constexpr int kDevices = 64;
+  thread_local int known[kDevices] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < kDevices && known[dev] > 0) {
+    *most = known[dev];
+    return cudaSuccess;
+  }
+  e = ensure_smem_limit(reinterpret_cast<const void*>(kKernel), kCacheSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = cluster_config(kMaxCtas, threads, kCacheSmem, nullptr, attr);
+  int size = 0;
+  e = cudaOccupancyMaxPotentialClusterSize(&size, kKernel, &cfg);
+  if (e != cudaSuccess) return e;
+  *most = std::clamp(size, 1, kMaxCtas);
+  if (dev < kDevices) known[dev] = *most;
+  return cudaSuccess;
+}
+
+template <auto kKernel, typename... Args>
+cudaError_t launch_cluster(int ctas, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = cluster_config(ctas, threads, smem, stream, attr);
   return cudaLaunchKernelEx(&cfg, kKernel, args...);
 }
 
-// A kernel over the whole pool, of which every warp looks after as many words of 32 pages.
+// A kernel over the whole pool, of which every warp looks after as many words of 32 pages, in
+// `ctas` CTAs or as many as can be placed. (Fewer hold more words each: 8 take 2^23 pages, but
+// not beside what an append of some 5400 rows or more keeps.)
 template <auto kKernel>
 cudaError_t launch_pool(CacheParams p, int ctas, size_t smem, cudaStream_t stream) {
+  int most = 0;
+  const cudaError_t e = cluster_limit<kKernel>(kThreads, &most);
+  if (e != cudaSuccess) return e;
+  ctas = std::min(ctas, p.most_ctas > 0 ? std::min(p.most_ctas, most) : most);
   const int per = 32 * ctas * kWarps;
   p.warp_words = (p.num_pages + per - 1) / per;
-  return launch_cluster<kKernel>(ctas, kThreads, smem + static_cast<size_t>(p.warp_words) * kWarps * 4, stream, p);
+  smem += static_cast<size_t>(p.warp_words) * kWarps * 4;
+  if (smem > kCacheSmem) return cudaErrorNotSupported;
+  return launch_cluster<kKernel>(ctas, kThreads, smem, stream, p);
 }
 
 // CTAs by pages, table entries (read once: a quarter of a page's work) and tokens (four). Of the GPU's time in
@@ -507,7 +536,7 @@ cudaError_t launch_cache_copy(const CacheCopyParams& p, int caches, int pairs, b
 int cache_copy_blocks(int pieces) { return (pieces + kCopyThreads * kCopyVecs - 1) / (kCopyThreads * kCopyVecs); }
 
 cudaError_t launch_cache_fork(const CacheParams& p, cudaStream_t stream) {
-  // Up to eight places for a thread of sixteen CTAs: those are one cluster, in one launch. Otherwise a CTA
+  // Up to eight places for a thread of sixteen CTAs: those are one cluster, in one launch, if they can be placed. Otherwise a CTA
   // takes eight columns, a 32-byte sector of each row, and a second launch writes the lengths. One launch and two, of the GPU in
   // a graph and among others, where the host bounds: 16200 places 2.9 and 3.5 us, 9-11 and 12.4; 64400 places 5.9 and
   // 3.9, 9-11 and 13; 128800 places 9.4 and 4.5, 12.5 and 12.5.
@@ -516,9 +545,12 @@ cudaError_t launch_cache_fork(const CacheParams& p, cudaStream_t stream) {
   int cols_log2 = 3;
   while (kMaxCtas << cols_log2 < p.max_pages) ++cols_log2;
   if (static_cast<size_t>(p.batch) << cols_log2 <= 8 * kForkThreads) {
-    int ctas = 1;
+    int ctas = 1, most = 0;
     while (ctas << cols_log2 < p.max_pages) ctas *= 2;
-    return launch_cluster<cache_fork_kernel<true>>(ctas, kForkThreads, bytes(cols_log2), stream, p, cols_log2);
+    const cudaError_t e = cluster_limit<cache_fork_kernel<true>>(kForkThreads, &most);
+    if (e != cudaSuccess) return e;
+    if (ctas <= (p.most_ctas > 0 ? std::min(p.most_ctas, most) : most))
+      return launch_cluster<cache_fork_kernel<true>>(ctas, kForkThreads, bytes(cols_log2), stream, p, cols_log2);
   }
   cols_log2 = 3;
   while (bytes(cols_log2) > kCacheSmem) --cols_log2;

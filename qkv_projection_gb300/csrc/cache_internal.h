@@ -39,8 +39,10 @@ struct CacheParams {
   int batch, max_pages, num_pages, page_size;
   int tokens, max_moves;
   FastDiv page_div;
+  int most_ctas;        // limit of a cluster; 0: the device's
   int warp_words;       // set by the launch: words of 32 pages that a warp looks after
 };
+// cudaErrorNotSupported: the pool's words do not fit in the shared memory of as many CTAs as can be placed.
 cudaError_t launch_cache_fork(const CacheParams& p, cudaStream_t stream);
 cudaError_t launch_cache_append(const CacheParams& p, cudaStream_t stream);
 cudaError_t launch_cache_truncate(const CacheParams& p, cudaStream_t stream);

@@ -55,6 +55,7 @@ _SIGNATURES = {
     "kaio_cache_append": ([_vp, _vp], _i32),
     "kaio_cache_truncate": ([_vp, _vp], _i32),
     "kaio_cache_compact": ([_vp, _vp], _i32),
+    "kaio_debug_cache_cluster_limit": ([_i32, _vp, _i32, _vp], _i32),
     "kaio_qkv_path": ([_u32], _i32),
     "kaio_last_error": ([], ctypes.c_char_p),
     "kaio_device_status": ([], _i32),
