@@ -272,6 +272,7 @@ PyObject* paged_attention(PyObject* const* v) {
   if constexpr (kScored) {
     if (!PyFloat_Check(v[16])) return nullptr;
     x.softcap = static_cast<float>(PyFloat_AS_DOUBLE(v[16]));
+    if (x.softcap == 0.f && PyFloat_AS_DOUBLE(v[16]) != 0.) return nullptr;
     const int64_t heads[1] = {h}, rows[1] = {b}, tokens[1] = {t};
     if (v[17] != Py_None) {
       const at::Tensor* slopes = usable(v[17], at::kFloat, heads);

@@ -638,6 +638,9 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max
                                         sinks, workspace, out, return_lse, lse, stream)
         if done is not None:
             return done
+    cap = ctypes.c_float(softcap).value
+    if cap == 0 and softcap != 0:
+        raise ValueError(f"softcap ({softcap}) is zero in 32 bits: it must be 0 or in (0, 256]")
     torch = _torch()
     int32 = torch.int32
     code, dtype, shape = _rank3(q, "q")
@@ -696,7 +699,7 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max
                  kv_lens.data_ptr(), starts, out.data_ptr(), lse_ptr, workspace.data_ptr(),
                  workspace.numel(),
                  qs[0], qs[1], os_[0], os_[1], kc[0], kc[1], kc[2], vc[0], vc[1], vc[2], ts[0],
-                 *((ctypes.c_float(softcap).value, 0, *more) if scored else ()))
+                 *((cap, 0, *more) if scored else ()))
     entry = lib().kaio_paged_attention_scored if scored else lib().kaio_paged_attention
     check(entry(args, _raw_stream(q, stream)))
     return (out, lse) if return_lse else out
