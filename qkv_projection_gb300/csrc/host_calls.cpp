@@ -69,6 +69,12 @@ bool to_int(PyObject* o, int32_t* v) {
   return true;
 }
 
+bool to_double(PyObject* o, double* v) {
+  if (!PyFloat_Check(o) && !PyLong_Check(o)) return false;
+  *v = PyFloat_AsDouble(o);
+  return !PyErr_Occurred();
+}
+
 bool fits(int64_t n) { return n <= std::numeric_limits<int32_t>::max(); }
 
 bool to_flag(PyObject* o, int32_t* v) {
@@ -270,9 +276,10 @@ PyObject* paged_attention(PyObject* const* v) {
     a.lse = static_cast<float*>(made_lse.data_ptr());
   }
   if constexpr (kScored) {
-    if (!PyFloat_Check(v[16])) return nullptr;
-    x.softcap = static_cast<float>(PyFloat_AS_DOUBLE(v[16]));
-    if (x.softcap == 0.f && PyFloat_AS_DOUBLE(v[16]) != 0.) return nullptr;
+    double cap;
+    if (!to_double(v[16], &cap)) return nullptr;
+    x.softcap = static_cast<float>(cap);
+    if (x.softcap == 0.f && cap != 0.) return nullptr;
     const int64_t heads[1] = {h}, rows[1] = {b}, tokens[1] = {t};
     if (v[17] != Py_None) {
       const at::Tensor* slopes = usable(v[17], at::kFloat, heads);
