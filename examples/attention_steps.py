@@ -12,6 +12,7 @@ the cache, and prints the time of a step.
 import math
 import os
 import sys
+from collections import Counter
 
 import torch
 
@@ -24,7 +25,10 @@ class PagedLayer:
     """One layer's attention: W4A16 projections, rotary positions, a paged cache.
 
     The projections give as many K/V heads as query heads. Which sequence holds which
-    pages is kept on the GPU (page_refs, page_table, kv_lens); `lengths` follows on the host.
+    pages is kept on the GPU (page_refs, page_table, kv_lens). `lengths` follows on the host, and so does
+    how many pages are left, under numbers of the host's own (`held`: the pages of each row, `holders`: how
+    many hold each): a step for which there is no room is refused before anything is sent, since on
+    the GPU a row that does not fit takes nothing, silently.
     softcap and slopes (f32 [heads]) are those of ``kaio.paged_attention``.
     """
 
@@ -46,11 +50,13 @@ class PagedLayer:
         self.page_table = torch.full((sequences, pages), -1, dtype=torch.int32, **dev)
         self.kv_lens = torch.zeros(sequences, dtype=torch.int32, **dev)
         self.lengths = [0] * sequences
+        self.held, self.holders, self.named = [[] for _ in range(sequences)], Counter(), 0
         self.workspace = kaio.paged_attention_workspace()
 
     def step(self, x, new):
         """x f16 [sum(new), columns]: the next new[b] tokens of each sequence b, in order.
         Returns their attention outputs f16 [sum(new), heads * head_dim]."""
+        self.take(new)
         positions, starts = [], [0]
         for b, n in enumerate(new):
             positions += range(self.lengths[b], self.lengths[b] + n)
@@ -70,6 +76,28 @@ class PagedLayer:
                                    slopes=self.slopes)
         return out.view(x.shape[0], -1)
 
+    def take(self, new):
+        """Pages for new[b] more tokens of each row, as cache_append gives them out."""
+        places = lambda n: -(-n // self.page_size)  # noqa: E731
+        own = [int(n > 0 and self.lengths[b] % self.page_size > 0 and self.holders[self.held[b][-1]] > 1)
+               for b, n in enumerate(new)]                 # a shared last page is replaced
+        more = [places(self.lengths[b] + n) - len(self.held[b]) for b, n in enumerate(new)]
+        pages, rows = self.page_refs.numel(), self.page_table.shape[1]
+        if sum(own) + sum(more) > pages - len(self.holders) or any(m + len(h) > rows for m, h in zip(more, self.held)):
+            raise RuntimeError(f"the cache is full: {sum(own) + sum(more)} pages more, {pages - len(self.holders)} of {pages} left")
+        for row, o, m in zip(self.held, own, more):
+            if o:
+                self.holders[row.pop()] -= 1
+            made = range(self.named, self.named + o + m)
+            row += made
+            self.holders.update(made)
+            self.named = made.stop
+        if any(own):
+            self.holders = +self.holders                   # (without those that nobody holds any more)
+
+    def count(self):
+        self.holders = Counter(p for row in self.held for p in row)
+
     def books(self):
         return self.page_refs, self.page_table, self.kv_lens
 
@@ -77,11 +105,15 @@ class PagedLayer:
         """Row b goes on from where row parents[b] stands; they share their pages."""
         kaio.cache_fork(*self.books(), torch.tensor(parents, dtype=torch.int32, device="cuda"), self.page_size)
         self.lengths = [self.lengths[p] for p in parents]
+        self.held = [list(self.held[p]) for p in parents]
+        self.count()
 
     def truncate(self, lengths):
         """Drops what each row has past these lengths (drafts that were refused; 0: the sequence is done)."""
         kaio.cache_truncate(*self.books(), torch.tensor(lengths, dtype=torch.int32, device="cuda"), self.page_size)
         self.lengths = [min(a, max(b, 0)) for a, b in zip(self.lengths, lengths)]
+        self.held = [row[:-(-n // self.page_size)] for row, n in zip(self.held, self.lengths)]
+        self.count()
 
     def compact(self):
         """Moves all pages in use to the beginning of the cache."""

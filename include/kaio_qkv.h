@@ -526,7 +526,11 @@ int kaio_cache_copy_pages(const kaio_cache_copy_args* args, kaio_stream_t stream
  *   [tokens] gets page * page_size + place of every new position, as kaio_rope_append
  *   takes it. A row that does not fit (its max_pages places, 2^31 - 1
  *   positions, or the free pages that the rows before it leave, refused ones counted too) takes
- *   nothing: its books stay, its slots are -1. Tokens of no row get -1, too.
+ *   nothing: its books stay, its slots are -1. Tokens of no row get -1, too. Nothing else tells:
+ *   kaio_rope_append does not store such a row's tokens and kaio_paged_attention takes them for the last ones of the
+ *   old length, so their outputs mean nothing, and lengths kept elsewhere must not count them. (Know
+ *   the room before, or read the slots back.) Of rows that share a filled part of a page and
+ *   all take positions in one call, each takes a page of its own, the last one, too.
  * kaio_cache_truncate: row b is cut to new_lens[b] positions (i32 [batch]; below 0: 0)
  *   where that is less than it has, and its pages behind them are given back.
  * kaio_cache_compact: the i-th highest used page moves to the i-th lowest free one

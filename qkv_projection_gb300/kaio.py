@@ -777,7 +777,9 @@ def cache_append(page_refs, page_table, kv_lens, q_starts, tokens: int, page_siz
     is held elsewhere too, it gets dst[b] instead of src[b] (int32 [B]; -1: none).
 
     A row that does not fit its places, or the pool behind the rows before it, takes nothing:
-    its slots are -1 and its books stay. New results belong to ``stream`` (default: the current one).
+    its slots are -1 and its books stay. Nothing raises then, and what ``paged_attention`` gives for its tokens
+    means nothing: know the room before, or read slots (or kv_lens) back and leave the row out. New
+    results belong to ``stream`` (default: the current one).
     """
     host = _host_module or _host()
     if host:
