@@ -102,8 +102,9 @@ class PagedLayer:
         return self.page_refs, self.page_table, self.kv_lens
 
     def fork(self, parents):
-        """Row b goes on from where row parents[b] stands; they share their pages."""
+        """Row b goes on from where row parents[b] stands; they share their pages. A parent that is no row leaves its row."""
         kaio.cache_fork(*self.books(), torch.tensor(parents, dtype=torch.int32, device="cuda"), self.page_size)
+        parents = [p if 0 <= p < len(self.lengths) else b for b, p in enumerate(parents)]
         self.lengths = [self.lengths[p] for p in parents]
         self.held = [list(self.held[p]) for p in parents]
         self.count()
