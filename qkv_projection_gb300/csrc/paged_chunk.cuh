@@ -22,7 +22,8 @@
 // wait and one commit of 150-300 cycles each. TMEM is full (two S and two O of 128
 // columns), so there is no third half to fill the gap. 4096 tokens over 16384 keys,
 // 32 heads on 8 of 128: 726-750 us with the power limit, 1.28-1.33 PFLOP/s, 0.66-0.68 of
-// what the measured library product reaches in a burst, 0.74-0.77 of it sustained.
+// what the measured library product reaches in a burst, 0.74-0.77 of it sustained
+// (680-690 us on a GPU that kept a higher clock, beside which the figures of other forms below were taken).
 //
 // Registers: the softmax warps rescale O and write the results themselves (both are
 // rare), so eight of twelve warps share nearly all registers (216 a thread, 72 for the
@@ -50,14 +51,18 @@
 // load from TMEM and the maximum. The chain of a half is longer by it, so these are bound by the softmax warps:
 // - a cap costs a second exponential and an eighth of a reciprocal a score. The exponential unit takes 4 cycles
 //   a warp's exponential, 9 a reciprocal: 9 cycles a score where 4 were (a quarter: 10, and 11 measured for the whole sequence
-//   alone, 12.3 with one warp); two halves' 128 scores then fill half of a unit's 5000 cycles. 4096 tokens over 16384: 1050
-//   us with a quarter, 1031 with an eighth, 0.93 PFLOP/s.
+//   alone, 12.3 with one warp); two halves' 128 scores then fill 2330 of a unit's 5000 cycles, 1280 more than without a cap. The
+//   unit takes 1700 more; what the rest is (36-40 bytes a thread that spill, halves that compute at the same
+//   time) has not been told apart. 4096 tokens over 16384: 1050 us with a quarter, 1033-1040 with an eighth, 0.93 PFLOP/s; with
+//   a window of 4096 365 us, and 235 without a cap.
 // - a bias makes the nearest keys the heaviest, so the tiles of its kernels run from the last to the first: from the
 //   first on, most tiles would raise a steep head's maximum and rescale O (4096 tokens over 16384: 1100 us so, 788 in reverse,
-//   775 since pieces that a warp sees nothing of are not worked on).
+//   773-784 since pieces that a warp sees nothing of are not worked on). Slopes below zero, whose heaviest keys are the
+//   farthest, meet their tiles from that wrong end: 923-939 us. Without causal order what lies right of a row goes through the
+//   short loop below: 1020 us, and 740 without slopes. With a cap, too, 1228 us; 76-84 bytes a thread spill there.
 // - units with hidden keys, and those a bias does not fall evenly over (the row's own place lies inside), go
 //   through one short loop of 32 keys at a time, in place in TMEM, before the rest. Unrolled over 128 in registers it cost a
-//   prompt of documents 147 us, rolled 128: such items have two to four units, and code that is fetched anew runs at 5 cycles an
+//   prompt of documents 147 us, rolled 128-130: such items have five units on average, and code that is fetched anew runs at 5 cycles an
 //   instruction. With a cap the loop also takes scores of more than 5 caps.
 // Measured and not kept: the weights through shared memory, so that the next product of Q and K runs behind the
 // softmax (no wait for it left, but 400 cycles more for each 64 keys' stores and fence, and the issuing thread late: with a cap
@@ -249,7 +254,7 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 }
 // cap tanh(x) = cap - 2 cap / (1 + exp(2x)): four scores become -1 / (1 + exp2(c s)), c = 2 log2(e)
 // scale / cap. The factor 2 cap goes into what follows, the constant cap into the log-sum. The four
-// share a reciprocal (1/a = bcd / abcd), so c s is at most kCapRange, where the tanh is 1 - 2^-29.
+// share a reciprocal (1/a = bcd / abcd, known as batch inversion), so c s is at most kCapRange, where the tanh is 1 - 2^-29.
 // Errors, in 2^-23: of exp2 (approximate to 2^-22.5, its argument rounded twice) 0.8 after the
 // quotient's slope of at most a quarter, of the reciprocal, the sum and the products 3.5 (4.5 where eight share one); so a
 // score is off by at most 24 * 2^-24 caps, and far less where it is large, since the results are small there.
